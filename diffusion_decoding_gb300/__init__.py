@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(HERE, "libdllm.so")
 
 DLLM_OK, DLLM_ERR_INVALID_ARG, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA, DLLM_ERR_TIMEOUT = range(5)
 DLLM_F32, DLLM_BF16 = 0, 1
+DLLM_ROPE_LINEAR, DLLM_ROPE_BANDS = 0, 1
 
 _c_i32, _c_i64, _c_f32, _c_vp, _c_sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                                         ctypes.c_void_p, ctypes.c_size_t)
@@ -48,6 +49,25 @@ class dllm_stats(ctypes.Structure):
 class dllm_shard_stats(ctypes.Structure):
     _fields_ = [("stats", dllm_stats), ("vocab_offset", _c_i64)]
 
+
+class dllm_heads(ctypes.Structure):
+    _fields_ = [("data", _c_vp), ("heads", _c_i32), ("dtype", _c_i32), ("batch_stride", _c_i64),
+                ("token_stride", _c_i64), ("head_stride", _c_i64)]
+
+
+class dllm_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", _c_i32), ("scaling", _c_i32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("slow_turns", ctypes.c_double), ("fast_turns", ctypes.c_double)]
+
+
+class dllm_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", _c_vp), ("k_params", _c_vp), ("v_codes", _c_vp), ("v_params", _c_vp),
+                ("page_table", _c_vp), ("pages", _c_i32), ("heads", _c_i32),
+                ("page_size", _c_i32), ("head_dim", _c_i32), ("table_stride", _c_i32)]
+
+
+_P_HEADS, _P_CACHE = ctypes.POINTER(dllm_heads), ctypes.POINTER(dllm_kv4_cache)
 
 _SIGS = {
     "dllm_last_error": (ctypes.c_char_p, []),
@@ -96,6 +116,18 @@ _SIGS = {
                                         _c_vp, _c_i32, _c_vp]),
     "dllm_kv_refresh_mask": (_c_i32, [ctypes.POINTER(dllm_block_state), _c_i32, _c_i32, _c_i32,
                                       _c_i32, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "dllm_rope_phases": (_c_i32, [ctypes.POINTER(dllm_rope), _c_vp, _c_vp]),
+    "dllm_qk_norm_rope": (_c_i32, [_P_HEADS, _P_HEADS, _P_HEADS, _P_HEADS, _c_i32, _c_i32, _c_i32,
+                                   _c_vp, _c_i64, _c_vp, _c_i32, _c_i32, _c_f32, _c_i32, _c_vp,
+                                   _c_vp, _c_f32, _c_vp]),
+    "dllm_kv4_write": (_c_i32, [_P_CACHE, _P_HEADS, _P_HEADS, _c_i32, _c_i32, _c_vp, _c_i64,
+                                _c_vp]),
+    "dllm_kv4_read": (_c_i32, [_P_CACHE, _P_HEADS, _P_HEADS, _c_i32, _c_i32, _c_vp, _c_i64,
+                               _c_vp]),
+    "dllm_attention_kv4_workspace_bytes": (_c_sz, [_P_CACHE, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "dllm_attention_kv4": (_c_i32, [_P_HEADS, _P_CACHE, _c_vp, _c_i32, _c_vp, _c_i64, _c_f32,
+                                    _c_i32, _P_HEADS, _c_vp, _c_i32, _c_i32, _c_vp, _c_sz,
+                                    _c_vp]),
     "dllm_get_status": (_c_i32, [_c_vp, _c_vp, ctypes.POINTER(_c_i32)]),
     "dllm_merge_shard_stats": (_c_i32, [ctypes.POINTER(dllm_shard_stats), _c_i32, _c_i64,
                                         ctypes.POINTER(dllm_stats), _c_vp]),
@@ -203,6 +235,68 @@ class BlockState:
     def reset(self, stream=None) -> None:
         """A new block, by one kernel (dllm_block_state_reset), credit slots included."""
         dllm_block_state_reset(self, stream=stream)
+
+
+class Kv4Cache:
+    """Device arrays of a paged 4-bit key/value cache (format: include/dllm.h) and its page table.
+
+    pages: pages in the pool; table: [B, pages per sequence] int32 page ids (a word outside
+    [0, pages) is an absent page).  The table may be changed between calls; codes and params need
+    no initial values."""
+
+    def __init__(self, pages: int, heads: int, page_size: int, head_dim: int, B: int,
+                 pages_per_seq: int, device=None):
+        dev = device or torch.device("cuda")
+        codes, params = (pages, heads, page_size, head_dim // 2), (pages, heads, page_size,
+                                                                   head_dim // 32)
+        self._set(torch.empty(codes, dtype=torch.uint8, device=dev),
+                  torch.empty(params, dtype=torch.int16, device=dev),
+                  torch.empty(codes, dtype=torch.uint8, device=dev),
+                  torch.empty(params, dtype=torch.int16, device=dev),
+                  torch.full((B, pages_per_seq), -1, dtype=torch.int32, device=dev))
+
+    @classmethod
+    def of(cls, k_codes, k_params, v_codes, v_params, table) -> "Kv4Cache":
+        """A cache over existing contiguous device tensors (shapes as the constructor makes)."""
+        self = cls.__new__(cls)
+        pages, heads, page_size, half = k_codes.shape
+        for name, t, shape, es in (("k_codes", k_codes, k_codes.shape, 1),
+                                   ("v_codes", v_codes, k_codes.shape, 1),
+                                   ("k_params", k_params, (pages, heads, page_size, half // 16), 2),
+                                   ("v_params", v_params, (pages, heads, page_size, half // 16), 2),
+                                   ("table", table, (table.shape[0], table.shape[-1]), 4)):
+            if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.element_size() != es:
+                raise ValueError(f"{name} must be contiguous, {tuple(shape)}, {es} bytes a value")
+        self._set(k_codes, k_params, v_codes, v_params, table)
+        return self
+
+    def _set(self, k_codes, k_params, v_codes, v_params, table) -> None:
+        self.k_codes, self.k_params = k_codes, k_params
+        self.v_codes, self.v_params = v_codes, v_params
+        self.table = table
+        pages, heads, page_size, half = k_codes.shape
+        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
+        self._c = dllm_kv4_cache(_ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params),
+                                 _ptr(table), pages, heads, page_size, 2 * half, table.shape[1])
+
+    def c(self) -> dllm_kv4_cache:
+        return self._c
+
+
+def heads_of(t: torch.Tensor) -> dllm_heads:
+    """Descriptor of a [B, n, heads, head_dim] bf16 or fp32 tensor with contiguous channels."""
+    if t.dim() != 4:
+        raise ValueError("need a [B, n, heads, head_dim] tensor")
+    sb, st, sh, sc = t.stride()
+    if sc != 1 and t.shape[3] != 1:
+        raise ValueError("channels must be contiguous")
+    if t.dtype == torch.bfloat16:
+        dt = DLLM_BF16
+    elif t.dtype == torch.float32:
+        dt = DLLM_F32
+    else:
+        raise TypeError("need bfloat16 or float32")
+    return dllm_heads(t.data_ptr(), t.shape[2], dt, sb, st, sh)
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -357,6 +451,104 @@ def dllm_commit_threshold_static(logits, shape, stats: StatsBuffers, state: Bloc
                                               ctypes.byref(st), ctypes.byref(bs), tau, eos_id,
                                               _stream(stream)),
            "dllm_commit_threshold_static")
+
+
+def dllm_rope_phases(rotary_dim: int, phases: torch.Tensor, base: float = 10000.0,
+                     factor: float = 1.0, scaling: int = DLLM_ROPE_LINEAR,
+                     original_len: float = 0.0, slow_turns: float = 1.0, fast_turns: float = 32.0,
+                     stream=None) -> None:
+    """Fill phases ([rotary_dim / 2] int64) with each pair's turns per position in 2^-64."""
+    if phases.dtype != torch.int64 or phases.numel() < rotary_dim // 2:
+        raise ValueError("phases must hold rotary_dim / 2 int64 words")
+    r = dllm_rope(rotary_dim, scaling, base, factor, original_len, slow_turns, fast_turns)
+    _check(lib().dllm_rope_phases(ctypes.byref(r), _ptr(phases), _stream(stream)),
+           "dllm_rope_phases")
+
+
+def _pos_stride(pos, B: int, n: int) -> int:
+    if pos is None:
+        return 0
+    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[0] != B or pos.shape[1] < n \
+            or (pos.stride(1) != 1 and pos.shape[1] != 1):
+        raise ValueError("pos must be [B, >= n] int32 with contiguous rows")
+    return pos.stride(0)
+
+
+def dllm_qk_norm_rope(q, k, q_out, k_out, pos, phases, q_weight=None, k_weight=None,
+                      eps: float = 1e-6, interleaved: bool = False, magnitude: float = 1.0,
+                      norm: bool = True, stream=None) -> None:
+    """q, k and their outputs: [B, n, heads, head_dim] (any strides with contiguous channels; q or
+    k with its output may be None); pos: [B, >= n] int32, < 0: token skipped; phases: the
+    dllm_rope_phases table, two channels per entry are rotated (None: no rotation)."""
+    x = q if q is not None else k
+    B, n, _, D = x.shape
+    for t in (q, k, q_out, k_out):
+        if t is not None and (t.shape[0] != B or t.shape[1] != n or t.shape[3] != D):
+            raise ValueError("the tensors differ in B, n or head_dim")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.numel() != D or w.dtype != x.dtype or not w.is_contiguous()):
+            raise ValueError("weights must be contiguous, [head_dim], of the tensors' dtype")
+    hs = [None if t is None else ctypes.byref(heads_of(t)) for t in (q, q_out, k, k_out)]
+    rotary = 0 if phases is None else 2 * phases.numel()
+    _check(lib().dllm_qk_norm_rope(*hs, B, n, D, _ptr(pos), _pos_stride(pos, B, n), _ptr(phases),
+                                   rotary, int(interleaved), magnitude, int(norm), _ptr(q_weight),
+                                   _ptr(k_weight), eps, _stream(stream)), "dllm_qk_norm_rope")
+
+
+def _check_rows(cache: Kv4Cache, k, v) -> None:
+    if k.shape != v.shape or k.shape[3] != cache.head_dim or k.shape[0] != cache.table.shape[0]:
+        raise ValueError("k and v must be [B, n, heads, head_dim] of the cache")
+
+
+def dllm_kv4_write(cache: Kv4Cache, k, v, pos, stream=None) -> None:
+    """Quantise k, v ([B, n, heads, head_dim]) into the entries pos ([B, >= n] int32, < 0: skip)."""
+    _check_rows(cache, k, v)
+    _check(lib().dllm_kv4_write(ctypes.byref(cache.c()), ctypes.byref(heads_of(k)),
+                                ctypes.byref(heads_of(v)), k.shape[0], k.shape[1], _ptr(pos),
+                                _pos_stride(pos, k.shape[0], k.shape[1]), _stream(stream)),
+           "dllm_kv4_write")
+
+
+def dllm_kv4_read(cache: Kv4Cache, k, v, pos=None, stream=None) -> None:
+    """Read the entries pos (None: 0 .. n-1) back into k, v ([B, n, heads, head_dim])."""
+    _check_rows(cache, k, v)
+    _check(lib().dllm_kv4_read(ctypes.byref(cache.c()), ctypes.byref(heads_of(k)),
+                               ctypes.byref(heads_of(v)), k.shape[0], k.shape[1], _ptr(pos),
+                               _pos_stride(pos, k.shape[0], k.shape[1]), _stream(stream)),
+           "dllm_kv4_read")
+
+
+def dllm_attention_kv4_workspace_bytes(cache: Kv4Cache, B: int, n: int, q_heads: int,
+                                       max_len: int) -> int:
+    return int(lib().dllm_attention_kv4_workspace_bytes(ctypes.byref(cache.c()), B, n, q_heads,
+                                                        max_len))
+
+
+def dllm_attention_kv4(q, cache: Kv4Cache, lens, max_len: int, out, ws, lse=None, key_mask=None,
+                       scale: float | None = None, causal: bool = False, stream=None) -> None:
+    """q, out: [B, n, heads, head_dim] bf16; lens: [B] int32 (None: max_len everywhere); lse:
+    [B, heads, n] fp32 or None; key_mask: [B, >= max_len] uint8 or bool, 0 = hidden; scale: None
+    for head_dim ** -0.5."""
+    B, n, H, D = q.shape
+    if out.shape != q.shape or D != cache.head_dim or B != cache.table.shape[0]:
+        raise ValueError("q and out must be [B, n, heads, head_dim] of the cache")
+    if lens is not None and (lens.dtype != torch.int32 or lens.numel() != B
+                             or not lens.is_contiguous()):
+        raise ValueError("lens must be [B] int32, contiguous")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, n)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be [B, heads, n] float32, contiguous")
+    if key_mask is not None and (key_mask.element_size() != 1 or key_mask.dim() != 2
+                                 or key_mask.shape[0] != B or key_mask.shape[1] < max_len
+                                 or key_mask.stride(1) != 1):
+        raise ValueError("key_mask must be [B, >= max_len] uint8 or bool with contiguous rows")
+    _check(lib().dllm_attention_kv4(ctypes.byref(heads_of(q)), ctypes.byref(cache.c()),
+                                    _ptr(lens), max_len, _ptr(key_mask),
+                                    0 if key_mask is None else key_mask.stride(0),
+                                    D ** -0.5 if scale is None else scale, int(causal),
+                                    ctypes.byref(heads_of(out)), _ptr(lse), B, n, _ptr(ws),
+                                    ws.numel(), _stream(stream)),
+           "dllm_attention_kv4")
 
 
 def dllm_capture_condition(default_value: int = 0, stream=None) -> int:

@@ -6,6 +6,9 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <cmath>
+
+#include "attention.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -146,6 +149,78 @@ dllm_status commit_common(const void* logits, const dllm_shape* shape, const dll
   }
   if (e != cudaSuccess) return cuda_fail(e, name);
   return ok();
+}
+
+// Rows of heads: pointer, dtype and alignment to the element size.
+dllm_status check_heads(const dllm_heads* h, const char* what) {
+  if (!h || !h->data) return fail(DLLM_ERR_INVALID_ARG, "%s or its data is null", what);
+  if (h->dtype != DLLM_F32 && h->dtype != DLLM_BF16)
+    return fail(DLLM_ERR_UNSUPPORTED, "%s: dtype %d is not fp32 (0) or bf16 (1)", what, h->dtype);
+  if (h->heads < 1 || h->heads > 65536)
+    return fail(DLLM_ERR_INVALID_ARG, "%s: heads=%d outside [1, 65536]", what, h->heads);
+  if (!aligned(h->data, h->dtype == DLLM_BF16 ? 2 : 4))
+    return fail(DLLM_ERR_INVALID_ARG, "%s must be aligned to the element size", what);
+  return DLLM_OK;
+}
+
+dllm_status check_tokens(int32_t B, int32_t n) {
+  if (B < 1 || n < 1) return fail(DLLM_ERR_INVALID_ARG, "need B, n >= 1 (B=%d n=%d)", B, n);
+  if (static_cast<int64_t>(B) * n > (int64_t{1} << 20))
+    return fail(DLLM_ERR_UNSUPPORTED, "B*n=%lld exceeds 2^20", static_cast<long long>(B) * n);
+  return DLLM_OK;
+}
+
+dllm_status check_cache(const dllm_kv4_cache* c) {
+  if (!c || !c->k_codes || !c->k_params || !c->v_codes || !c->v_params || !c->page_table)
+    return fail(DLLM_ERR_INVALID_ARG, "cache or one of its arrays is null");
+  if (c->pages < 1 || c->heads < 1 || c->table_stride < 1)
+    return fail(DLLM_ERR_INVALID_ARG, "need pages, heads, table_stride >= 1 (%d, %d, %d)", c->pages,
+                c->heads, c->table_stride);
+  if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16 != 0)
+    return fail(DLLM_ERR_UNSUPPORTED, "page_size=%d is not a multiple of 16 in [16, 65536]",
+                c->page_size);
+  if (c->head_dim < 32 || c->head_dim > 512 || c->head_dim % 32 != 0)
+    return fail(DLLM_ERR_UNSUPPORTED, "head_dim=%d is not a multiple of 32 in [32, 512]",
+                c->head_dim);
+  if (c->heads > 65536) return fail(DLLM_ERR_UNSUPPORTED, "heads=%d exceeds 65536", c->heads);
+  if (static_cast<int64_t>(c->table_stride) * c->page_size >= (int64_t{1} << 31))
+    return fail(DLLM_ERR_UNSUPPORTED, "table_stride * page_size exceeds 2^31 - 1");
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_params, 4) ||
+      !aligned(c->v_params, 4) || !aligned(c->page_table, 4))
+    return fail(DLLM_ERR_INVALID_ARG, "codes must be 16-byte, params and page_table 4-byte aligned");
+  return DLLM_OK;
+}
+
+// Shared checks of the cache's write and read.
+dllm_status check_cache_rows(const dllm_kv4_cache* cache, const dllm_heads* k, const dllm_heads* v,
+                             int32_t B, int32_t n) {
+  DLLM_TRY(check_cache(cache));
+  DLLM_TRY(check_heads(k, "k"));
+  DLLM_TRY(check_heads(v, "v"));
+  DLLM_TRY(check_tokens(B, n));
+  if (k->dtype != v->dtype) return fail(DLLM_ERR_INVALID_ARG, "k and v differ in dtype");
+  if (k->heads != cache->heads || v->heads != cache->heads)
+    return fail(DLLM_ERR_INVALID_ARG, "k has %d heads and v %d, the cache %d", k->heads, v->heads,
+                cache->heads);
+  return DLLM_OK;
+}
+
+dllm_status check_attention(const dllm_kv4_cache* cache, int32_t B, int32_t n, int32_t q_heads,
+                            int32_t max_len) {
+  DLLM_TRY(check_cache(cache));
+  DLLM_TRY(check_tokens(B, n));
+  if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 192 &&
+      cache->head_dim != 256)
+    return fail(DLLM_ERR_UNSUPPORTED, "head_dim=%d is not 64, 128, 192 or 256", cache->head_dim);
+  if (q_heads < 1 || q_heads > 65536 || q_heads % cache->heads != 0)
+    return fail(DLLM_ERR_INVALID_ARG, "%d query heads are no multiple of the cache's %d", q_heads,
+                cache->heads);
+  if (max_len < 0 ||
+      max_len > static_cast<int64_t>(cache->table_stride) * cache->page_size)
+    return fail(DLLM_ERR_INVALID_ARG, "max_len=%d outside [0, table_stride * page_size]", max_len);
+  if (static_cast<int64_t>(B) * n * q_heads > (int64_t{1} << 30))
+    return fail(DLLM_ERR_UNSUPPORTED, "B * n * heads exceeds 2^30");
+  return DLLM_OK;
 }
 
 }  // namespace
@@ -589,6 +664,162 @@ dllm_status dllm_merge_shard_stats(const dllm_shard_stats* shards, int32_t n, in
   cudaError_t e = dllm::launch_merge_shard_stats(shards, n, rows, *out,
                                                  reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dllm_merge_shard_stats");
+  return ok();
+}
+
+dllm_status dllm_rope_phases(const dllm_rope* rope, int64_t* phases, dllm_stream_t stream) {
+  CallRange range_("dllm_rope_phases");
+  if (!rope || !phases) return fail(DLLM_ERR_INVALID_ARG, "rope and phases must not be null");
+  if (!aligned(phases, 8)) return fail(DLLM_ERR_INVALID_ARG, "phases must be 8-byte aligned");
+  if (rope->rotary_dim < 2 || rope->rotary_dim % 2 != 0)
+    return fail(DLLM_ERR_INVALID_ARG, "rotary_dim=%d must be even and positive", rope->rotary_dim);
+  if (rope->rotary_dim > 1024)
+    return fail(DLLM_ERR_UNSUPPORTED, "rotary_dim=%d exceeds 1024", rope->rotary_dim);
+  if (rope->scaling != DLLM_ROPE_LINEAR && rope->scaling != DLLM_ROPE_BANDS)
+    return fail(DLLM_ERR_UNSUPPORTED, "scaling %d is not LINEAR (0) or BANDS (1)", rope->scaling);
+  if (!(rope->base > 1.0) || !std::isfinite(rope->base) || !(rope->factor >= 1.0) ||
+      !std::isfinite(rope->factor))
+    return fail(DLLM_ERR_INVALID_ARG, "need a finite base > 1 and factor >= 1");
+  if (rope->scaling == DLLM_ROPE_BANDS &&
+      (!(rope->original_len > 0.0) || !std::isfinite(rope->original_len) ||
+       !(rope->slow_turns >= 0.0) || !(rope->fast_turns > rope->slow_turns) ||
+       !std::isfinite(rope->fast_turns)))
+    return fail(DLLM_ERR_INVALID_ARG,
+                "need original_len > 0 and 0 <= slow_turns < fast_turns, all finite");
+  cudaError_t e = dllm::launch_rope_phases(*rope, phases, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_rope_phases");
+  return ok();
+}
+
+dllm_status dllm_qk_norm_rope(const dllm_heads* q, const dllm_heads* q_out, const dllm_heads* k,
+                              const dllm_heads* k_out, int32_t B, int32_t n, int32_t head_dim,
+                              const int32_t* pos, int64_t pos_stride, const int64_t* phases,
+                              int32_t rotary_dim, int32_t interleaved, float magnitude,
+                              int32_t norm, const void* q_weight, const void* k_weight, float eps,
+                              dllm_stream_t stream) {
+  CallRange range_("dllm_qk_norm_rope");
+  if (!q != !q_out || !k != !k_out || (!q && !k))
+    return fail(DLLM_ERR_INVALID_ARG, "need q with q_out, or k with k_out, or both pairs");
+  int dtype = -1;
+  const dllm_heads* in[2] = {q, k};
+  const dllm_heads* out[2] = {q_out, k_out};
+  for (int j = 0; j < 2; ++j) {
+    if (!in[j]) continue;
+    DLLM_TRY(check_heads(in[j], j ? "k" : "q"));
+    DLLM_TRY(check_heads(out[j], j ? "k_out" : "q_out"));
+    if (in[j]->heads != out[j]->heads)
+      return fail(DLLM_ERR_INVALID_ARG, "%s and its output differ in heads", j ? "k" : "q");
+    if (dtype < 0) dtype = in[j]->dtype;
+    if (in[j]->dtype != dtype || out[j]->dtype != dtype)
+      return fail(DLLM_ERR_INVALID_ARG, "the tensors differ in dtype");
+  }
+  DLLM_TRY(check_tokens(B, n));
+  if (head_dim < 1 || head_dim > 1024)
+    return fail(head_dim < 1 ? DLLM_ERR_INVALID_ARG : DLLM_ERR_UNSUPPORTED,
+                "head_dim=%d outside [1, 1024]", head_dim);
+  if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > head_dim)
+    return fail(DLLM_ERR_INVALID_ARG, "rotary_dim=%d must be even and in [0, head_dim=%d]",
+                rotary_dim, head_dim);
+  if (rotary_dim > 0 && (!pos || !phases))
+    return fail(DLLM_ERR_INVALID_ARG, "a rotation needs pos and phases");
+  if (rotary_dim == 0 && !norm)
+    return fail(DLLM_ERR_INVALID_ARG, "neither a norm nor a rotation is asked for");
+  if (norm && !(eps >= 0.f)) return fail(DLLM_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!norm && (q_weight || k_weight))
+    return fail(DLLM_ERR_INVALID_ARG, "weights without a norm");
+  const size_t es = dtype == DLLM_BF16 ? 2 : 4;
+  if (!aligned(q_weight, es) || !aligned(k_weight, es) || !aligned(pos, 4) || !aligned(phases, 8))
+    return fail(DLLM_ERR_INVALID_ARG, "weights, pos and phases must be aligned to their elements");
+  cudaError_t e = dllm::launch_norm_rope(
+      q, q_out, k, k_out, B, n, head_dim, pos, pos_stride, phases, rotary_dim, interleaved != 0,
+      magnitude, norm != 0, q_weight, k_weight, eps, sm_count(),
+      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_qk_norm_rope");
+  return ok();
+}
+
+dllm_status dllm_kv4_write(const dllm_kv4_cache* cache, const dllm_heads* k, const dllm_heads* v,
+                           int32_t B, int32_t n, const int32_t* pos, int64_t pos_stride,
+                           dllm_stream_t stream) {
+  CallRange range_("dllm_kv4_write");
+  DLLM_TRY(check_cache_rows(cache, k, v, B, n));
+  if (!pos || !aligned(pos, 4))
+    return fail(DLLM_ERR_INVALID_ARG, "pos must not be null and 4-byte aligned");
+  cudaError_t e = dllm::launch_kv4_write(*cache, *k, *v, B, n, pos, pos_stride, sm_count(),
+                                         reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_kv4_write");
+  return ok();
+}
+
+dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, const dllm_heads* v,
+                          int32_t B, int32_t n, const int32_t* pos, int64_t pos_stride,
+                          dllm_stream_t stream) {
+  CallRange range_("dllm_kv4_read");
+  DLLM_TRY(check_cache_rows(cache, k, v, B, n));
+  if (!aligned(pos, 4)) return fail(DLLM_ERR_INVALID_ARG, "pos must be 4-byte aligned");
+  cudaError_t e = dllm::launch_kv4_read(*cache, *k, *v, B, n, pos, pos_stride, sm_count(),
+                                        reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_kv4_read");
+  return ok();
+}
+
+size_t dllm_attention_kv4_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t n,
+                                          int32_t q_heads, int32_t max_len) {
+  if (check_attention(cache, B, n, q_heads, max_len) != DLLM_OK) return 0;
+  return dllm::attention_ws_bytes(B, n, q_heads, cache->heads, cache->head_dim, max_len,
+                                  sm_count());
+}
+
+dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
+                               const int32_t* lens, int32_t max_len, const uint8_t* key_mask,
+                               int64_t mask_stride, float scale, int32_t causal,
+                               const dllm_heads* out, float* lse, int32_t B, int32_t n, void* ws,
+                               size_t ws_bytes, dllm_stream_t stream) {
+  CallRange range_("dllm_attention_kv4");
+  DLLM_TRY(check_heads(q, "q"));
+  DLLM_TRY(check_heads(out, "out"));
+  DLLM_TRY(check_attention(cache, B, n, q->heads, max_len));
+  DLLM_TRY(check_ws(ws));
+  if (q->dtype != DLLM_BF16 || out->dtype != DLLM_BF16)
+    return fail(DLLM_ERR_UNSUPPORTED, "q and out must be bf16");
+  if (q->heads != out->heads)
+    return fail(DLLM_ERR_INVALID_ARG, "q has %d heads, out %d", q->heads, out->heads);
+  if (!std::isfinite(scale)) return fail(DLLM_ERR_INVALID_ARG, "scale is not finite");
+  if (key_mask && mask_stride < max_len)
+    return fail(DLLM_ERR_INVALID_ARG, "mask_stride %lld < max_len %d",
+                static_cast<long long>(mask_stride), max_len);
+  if (!aligned(lens, 4) || !aligned(lse, 4))
+    return fail(DLLM_ERR_INVALID_ARG, "lens and lse must be 4-byte aligned");
+  const size_t need = dllm::attention_ws_bytes(B, n, q->heads, cache->heads, cache->head_dim,
+                                               max_len, sm_count());
+  if (ws_bytes < need)
+    return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed",
+                ws_bytes, need);
+  dllm::AttnParams p{};
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.qb = q->batch_stride, p.qt = q->token_stride, p.qh = q->head_stride;
+  p.out = static_cast<uint16_t*>(out->data);
+  p.ob = out->batch_stride, p.ot = out->token_stride, p.oh = out->head_stride;
+  p.lse = lse;
+  p.k_codes = cache->k_codes, p.k_params = cache->k_params;
+  p.v_codes = cache->v_codes, p.v_params = cache->v_params;
+  p.table = cache->page_table;
+  p.table_stride = cache->table_stride;
+  p.pages = cache->pages;
+  p.page_size = cache->page_size;
+  p.heads = cache->heads;
+  p.G = q->heads / cache->heads;
+  p.lens = lens;
+  p.max_len = max_len;
+  p.key_mask = key_mask;
+  p.mask_stride = mask_stride;
+  p.scale_log2 = scale * dllm::kLog2e;
+  p.causal = causal != 0;
+  p.B = B;
+  p.n = n;
+  cudaError_t e = dllm::launch_attention(p, cache->head_dim, ws, sm_count(),
+                                         reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_attention_kv4");
   return ok();
 }
 

@@ -137,6 +137,20 @@ cudaError_t launch_merge_shard_stats(const dllm_shard_stats* shards, int n, int6
 cudaError_t launch_wait_timeout_selftest(int32_t* status, uint64_t limit_ns,
                                          cudaStream_t stream);
 
+// Refresh operators: norm + rotation, the 4-bit cache (attention: attention.h).
+cudaError_t launch_rope_phases(const dllm_rope& rope, int64_t* phases, cudaStream_t stream);
+cudaError_t launch_norm_rope(const dllm_heads* q, const dllm_heads* q_out, const dllm_heads* k,
+                             const dllm_heads* k_out, int B, int n, int D, const int32_t* pos,
+                             int64_t pos_stride, const int64_t* phases, int R, bool interleaved,
+                             float magnitude, bool norm, const void* q_weight, const void* k_weight,
+                             float eps, int sm_count, cudaStream_t stream);
+cudaError_t launch_kv4_write(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_heads& v,
+                             int B, int n, const int32_t* pos, int64_t pos_stride, int sm_count,
+                             cudaStream_t stream);
+cudaError_t launch_kv4_read(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_heads& v,
+                            int B, int n, const int32_t* pos, int64_t pos_stride, int sm_count,
+                            cudaStream_t stream);
+
 // Record a message for dllm_last_error() on this thread (with a CUDA error string if e != 0).
 void set_last_error(const char* msg, cudaError_t e);
 

@@ -1,0 +1,345 @@
+// The 4-bit key/value cache: quantising entries as they are written, and reading them back (dInfer
+// explainer, KV-cache manager: refreshed entries replace the stale ones in the cache).  The format
+// is described in kv4.cuh and include/dllm.h.
+//
+// Both kernels are HBM-bound (bf16: 2 bytes of values and 9/16 bytes of cache per value).  A lane
+// handles eight channels, so a warp reads or writes 512 contiguous bytes of bf16 values per access
+// and 128 of codes; the four lanes of a group find its extremes with two shuffles.  A warp takes
+// up to kItems such pieces of one token and issues all their loads before it uses the first.
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace dllm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = 4;
+
+struct Kv4Params {
+  char* x[2];  // keys, values; strides in bytes
+  int64_t xb[2], xt[2], xh[2];
+  uint8_t* codes[2];
+  uint16_t* params[2];
+  const int32_t* table;
+  int table_stride, pages, heads, page_size, D;
+  const int32_t* pos;
+  int64_t pos_stride;
+  int n;
+  int64_t tokens;
+  int segs;  // warps per token and tensor
+};
+
+// One warp's work: a token, keys or values, and pieces [first, first + 32 * ITEMS) of its heads.
+struct Unit {
+  int b, i, side, first;
+  int entry;  // cache entry, -1: none
+  bool valid;
+};
+
+__device__ __forceinline__ Unit unit_of(const Kv4Params& p, int items) {
+  const int64_t warp = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  const int64_t row = warp / p.segs;  // token * 2 + side
+  Unit u;
+  u.first = static_cast<int>(warp - row * p.segs) * 32 * items;
+  u.side = static_cast<int>(row & 1);
+  const int64_t token = row >> 1;
+  u.valid = token < p.tokens;
+  u.b = static_cast<int>(token / p.n);
+  u.i = static_cast<int>(token - static_cast<int64_t>(u.b) * p.n);
+  u.entry = -1;
+  if (u.valid) u.entry = p.pos ? p.pos[u.b * p.pos_stride + u.i] : u.i;
+  return u;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_min_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Step from the extremes (lo <= 0 <= hi): (hi - lo) / 15 rounded up to three significant bits; 0
+// when it is tiny, NaN when the group is not finite.  15 * s has seven significant bits, so the
+// comparison that settles the rounding is exact.
+__device__ __forceinline__ float kv4_step(float lo, float hi) {
+  const float d = hi - lo;
+  const float t = d * (1.f / 15.f) * 0.99999904632568359375f;  // 1 - 2^-20: never above d / 15
+  float s = __uint_as_float((__float_as_uint(t) + 0x1FFFFFu) & ~0x1FFFFFu);
+  if (15.f * s < d) s = __uint_as_float(__float_as_uint(s) + 0x200000u);
+  if (!(d >= 15.f * 7.7037197775489434e-34f)) s = 0.f;  // 2^-110
+  if (!(s <= 5.316911983139663e36f)) s = __uint_as_float(kKv4NaNParam << 16);  // 2^122
+  return d != d ? __uint_as_float(kKv4NaNParam << 16) : s;
+}
+
+// kAligned: rows on 16-byte boundaries; otherwise values are read one by one.
+template <int DT, bool kAligned, int ITEMS>
+__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_constant__ Kv4Params p) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const Unit u = unit_of(p, ITEMS);
+  if (!u.valid || u.entry < 0) return;
+  const int page = kv4_page(p.table + static_cast<int64_t>(u.b) * p.table_stride, p.table_stride,
+                            p.pages, p.page_size, u.entry);
+  if (page < 0) return;
+  const int slot = u.entry % p.page_size;
+  const int cpr = p.D / 8, pieces = p.heads * cpr;
+  const char* x = p.x[u.side] + u.b * p.xb[u.side] + u.i * p.xt[u.side];
+  const int64_t xh = p.xh[u.side];
+  uint8_t* codes = p.codes[u.side];
+  uint16_t* params = p.params[u.side];
+
+  uint32_t raw[ITEMS][DT == DLLM_BF16 ? 4 : 8];
+#pragma unroll
+  for (int t = 0; t < ITEMS; ++t) {
+    const int c = u.first + t * 32 + lane;
+#pragma unroll
+    for (int e = 0; e < (DT == DLLM_BF16 ? 4 : 8); ++e) raw[t][e] = 0u;
+    if (c >= pieces) continue;
+    const int h = c / cpr;
+    const char* src = x + h * xh + (c - h * cpr) * (DT == DLLM_BF16 ? 16 : 32);
+    if constexpr (kAligned) {
+      const uint4 a = ld_stream_v4(src);
+      raw[t][0] = a.x, raw[t][1] = a.y, raw[t][2] = a.z, raw[t][3] = a.w;
+      if constexpr (DT == DLLM_F32) {
+        const uint4 d = ld_stream_v4(src + 16);
+        raw[t][4] = d.x, raw[t][5] = d.y, raw[t][6] = d.z, raw[t][7] = d.w;
+      }
+    } else if constexpr (DT == DLLM_BF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        raw[t][e] = reinterpret_cast<const uint16_t*>(src)[2 * e] |
+                    static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[2 * e + 1]) << 16;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) raw[t][e] = reinterpret_cast<const uint32_t*>(src)[e];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < ITEMS; ++t) {
+    const int c = u.first + t * 32 + lane;
+    float hi, lo;
+    if constexpr (DT == DLLM_BF16) {
+      // extremes in packed bf16; the maximum and the negated minimum share a word
+      uint32_t mx = raw[t][0], mn = raw[t][0];
+#pragma unroll
+      for (int e = 1; e < 4; ++e) {
+        mx = bf2_max_nan(mx, raw[t][e]);
+        mn = bf2_min_nan(mn, raw[t][e]);
+      }
+      mn ^= 0x80008000u;
+      uint32_t both = bf2_max_nan(__byte_perm(mx, mn, 0x5410), __byte_perm(mx, mn, 0x7632));
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) both = bf2_max_nan(both, __shfl_xor_sync(kFull, both, o));
+      both = bf2_max_nan(both, 0u);
+      hi = bf16lo(both);
+      lo = -bf16hi(both);
+    } else {
+      hi = 0.f, lo = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        hi = max_nan(hi, __uint_as_float(raw[t][e]));
+        lo = max_nan(lo, -__uint_as_float(raw[t][e]));
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
+        lo = max_nan(lo, __shfl_xor_sync(kFull, lo, o));
+      }
+      lo = -lo;
+    }
+    float s;
+    uint32_t z, w = 0u;
+    if constexpr (DT == DLLM_BF16) {
+      s = kv4_step(lo, hi);
+      // x / s has at most eight and three significant bits: apart from exact ties it is no nearer
+      // than 2^-9 to a tie, so a product with 1 / s enlarged by 2^-16 rounds ties away from zero
+      // and everything else to the nearest.  Adding 1.5 * 2^23 rounds to an integer in the low
+      // bits.
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+      inv = s > 0.f ? inv * 1.0000152587890625f : 0.f;
+      z = __float_as_uint(fmaf(-lo, inv, 12582912.f)) & 15u;
+      const float base = 12582912.f + static_cast<float>(z);
+#pragma unroll
+      for (int e = 7; e >= 0; --e) {
+        const float v = e & 1 ? bf16hi(raw[t][e >> 1]) : bf16lo(raw[t][e >> 1]);
+        const uint32_t n = min(__float_as_uint(fmaf(v, inv, base)), 0x4B40000Fu);
+        w = w * 16u + (n - 0x4B400000u);
+      }
+    } else {
+      const float d = hi - lo;
+      s = __fdiv_rn(d, 15.f);
+      const bool finite = d < INFINITY;
+      s = s < 7.7037197775489434e-34f ? 0.f
+                                      : __uint_as_float((__float_as_uint(s) + 0x1FFFFFu) & ~0x1FFFFFu);
+      if (!finite || s > 5.316911983139663e36f) s = __uint_as_float(kKv4NaNParam << 16);
+      const float den = s > 0.f ? s : 1.f;
+      z = static_cast<uint32_t>(fminf(floorf(__fadd_rn(__fdiv_rn(-lo, den), 0.5f)), 15.f));
+#pragma unroll
+      for (int e = 7; e >= 0; --e) {
+        const float r = __fdiv_rn(__uint_as_float(raw[t][e]), den);
+        const float k = s > 0.f ? copysignf(floorf(__fadd_rn(fabsf(r), 0.5f)), r) : 0.f;
+        const float nf = fminf(fmaxf(k + static_cast<float>(z), 0.f), 15.f);
+        w = w * 16u + static_cast<uint32_t>(nf);
+      }
+    }
+    if (c >= pieces) continue;
+    if (s != s) z = 0u;
+    const int h = c / cpr, cc = c - h * cpr;
+    const int64_t row = (static_cast<int64_t>(page) * p.heads + h) * p.page_size + slot;
+    *reinterpret_cast<uint32_t*>(codes + row * (p.D / 2) + cc * 4) = w;
+    if ((cc & 3) == 0)
+      params[row * (p.D / kKv4Group) + (cc >> 2)] =
+          static_cast<uint16_t>((__float_as_uint(s) >> 16) | z);
+  }
+}
+
+template <int DT, bool kAligned, int ITEMS>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ Kv4Params p) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const Unit u = unit_of(p, ITEMS);
+  if (!u.valid) return;
+  const int page = u.entry < 0 ? -1
+                               : kv4_page(p.table + static_cast<int64_t>(u.b) * p.table_stride,
+                                          p.table_stride, p.pages, p.page_size, u.entry);
+  const int slot = u.entry % p.page_size;
+  const int cpr = p.D / 8, pieces = p.heads * cpr;
+  char* x = p.x[u.side] + u.b * p.xb[u.side] + u.i * p.xt[u.side];
+  const int64_t xh = p.xh[u.side];
+  uint32_t w[ITEMS], pp[ITEMS];
+#pragma unroll
+  for (int t = 0; t < ITEMS; ++t) {
+    const int c = u.first + t * 32 + lane;
+    w[t] = pp[t] = 0u;
+    if (page < 0 || c >= pieces) continue;
+    const int h = c / cpr, cc = c - h * cpr;
+    const int64_t row = (static_cast<int64_t>(page) * p.heads + h) * p.page_size + slot;
+    w[t] = __ldg(reinterpret_cast<const uint32_t*>(p.codes[u.side] + row * (p.D / 2) + cc * 4));
+    pp[t] = __ldg(p.params[u.side] + row * (p.D / kKv4Group) + (cc >> 2));
+  }
+#pragma unroll
+  for (int t = 0; t < ITEMS; ++t) {
+    const int c = u.first + t * 32 + lane;
+    if (c >= pieces) continue;
+    const int h = c / cpr, cc = c - h * cpr;
+    const Kv4Scale sc = kv4_scale(__byte_perm(pp[t], pp[t], 0x1010));
+    // pairs of channels (j, j + 4), put back side by side
+    const uint32_t a = kv4_pair<0>(w[t], sc), b = kv4_pair<1>(w[t], sc), d = kv4_pair<2>(w[t], sc),
+                   e = kv4_pair<3>(w[t], sc);
+    const uint32_t v[4] = {__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410),
+                           __byte_perm(a, b, 0x7632), __byte_perm(d, e, 0x7632)};
+    char* dst = x + h * xh + cc * (DT == DLLM_BF16 ? 16 : 32);
+    if constexpr (DT == DLLM_BF16) {
+      if constexpr (kAligned) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          reinterpret_cast<uint16_t*>(dst)[k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
+      }
+    } else {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[2 * k] = bf16lo(v[k]);
+        f[2 * k + 1] = bf16hi(v[k]);
+      }
+      if constexpr (kAligned) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) reinterpret_cast<float*>(dst)[k] = f[k];
+      }
+    }
+  }
+}
+
+bool aligned16(const dllm_heads& h) {
+  const int es = h.dtype == DLLM_BF16 ? 2 : 4;
+  return (reinterpret_cast<uintptr_t>(h.data) | static_cast<uintptr_t>(h.batch_stride * es) |
+          static_cast<uintptr_t>(h.token_stride * es) | static_cast<uintptr_t>(h.head_stride * es)) %
+             16 == 0;
+}
+
+template <bool kWrite, int DT, bool kAligned>
+cudaError_t launch_items(Kv4Params& p, int sm_count, cudaStream_t stream) {
+  const int pieces = p.heads * (p.D / 8);
+  auto run = [&](auto kern, int items) {
+    p.segs = (pieces + 32 * items - 1) / (32 * items);
+    const int64_t warps = p.tokens * 2 * p.segs;
+    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+  };
+  // Four pieces a warp hide more of the load latency and share the page lookup; one piece a warp
+  // when the call has too few warps to fill the SMs.
+  const bool few = p.tokens * 2 * ((pieces + 127) / 128) < static_cast<int64_t>(sm_count) * 16;
+  if constexpr (kWrite)
+    return few ? run(kv4_write_kernel<DT, kAligned, 1>, 1)
+               : run(kv4_write_kernel<DT, kAligned, kItems>, kItems);
+  else
+    return few ? run(kv4_read_kernel<DT, kAligned, 1>, 1)
+               : run(kv4_read_kernel<DT, kAligned, kItems>, kItems);
+}
+
+template <bool kWrite>
+cudaError_t launch(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_heads& v, int B,
+                   int n, const int32_t* pos, int64_t pos_stride, int sm_count,
+                   cudaStream_t stream) {
+  Kv4Params p{};
+  const dllm_heads* x[2] = {&k, &v};
+  const int es = k.dtype == DLLM_BF16 ? 2 : 4;
+  for (int j = 0; j < 2; ++j) {
+    p.x[j] = static_cast<char*>(x[j]->data);
+    p.xb[j] = x[j]->batch_stride * es;
+    p.xt[j] = x[j]->token_stride * es;
+    p.xh[j] = x[j]->head_stride * es;
+  }
+  p.codes[0] = cache.k_codes, p.codes[1] = cache.v_codes;
+  p.params[0] = cache.k_params, p.params[1] = cache.v_params;
+  p.table = cache.page_table;
+  p.table_stride = cache.table_stride;
+  p.pages = cache.pages;
+  p.heads = cache.heads;
+  p.page_size = cache.page_size;
+  p.D = cache.head_dim;
+  p.pos = pos;
+  p.pos_stride = pos_stride;
+  p.n = n;
+  p.tokens = static_cast<int64_t>(B) * n;
+  const bool al = aligned16(k) && aligned16(v);
+  if (k.dtype == DLLM_BF16)
+    return al ? launch_items<kWrite, DLLM_BF16, true>(p, sm_count, stream)
+              : launch_items<kWrite, DLLM_BF16, false>(p, sm_count, stream);
+  return al ? launch_items<kWrite, DLLM_F32, true>(p, sm_count, stream)
+            : launch_items<kWrite, DLLM_F32, false>(p, sm_count, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_heads& v,
+                             int B, int n, const int32_t* pos, int64_t pos_stride, int sm_count,
+                             cudaStream_t stream) {
+  return launch<true>(cache, k, v, B, n, pos, pos_stride, sm_count, stream);
+}
+
+cudaError_t launch_kv4_read(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_heads& v,
+                            int B, int n, const int32_t* pos, int64_t pos_stride, int sm_count,
+                            cudaStream_t stream) {
+  return launch<false>(cache, k, v, B, n, pos, pos_stride, sm_count, stream);
+}
+
+}  // namespace dllm

@@ -1,0 +1,370 @@
+// Norm of each query and key head and rotation to its position, in one pass (dInfer explainer,
+// KV-cache manager: the keys of refreshed entries are recomputed at their positions):
+//   y = x * (mean(x^2) + eps)^(-1/2) * w;  pairs (a, c) -> m * (a cos t - c sin t, c cos t + a sin t).
+//
+// The phase of pair i at position p is p * u_i modulo 2^64 in units of 2^-64 turns (u_i holds the
+// frequency): the upper 32 bits of that product, as a signed number, are the phase within half a
+// turn, at any position.  Products in fp32 would lose 2^-24 of the whole angle instead, 8e-3
+// radians at position 131072.  The hardware sine and cosine then see |angle| <= pi, where their
+// error is at most 2^-21.
+//
+// HBM-bound: 2 * heads * head_dim values move per token and ~8 instructions are spent per value.
+// A group of head_dim / 16 lanes (padded to a power of two) owns a head, each lane 16 channels as
+// two 16-byte pieces that hold whole pairs, so the mean is a shuffle sum over the group and the
+// rotation stays in the lane.  A lane keeps the same channels for every head of its token: the
+// eight sines and cosines are computed once per warp and used for all the heads it loops over.
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace dllm {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Side {  // one tensor pair; strides in bytes
+  const char* x;
+  char* y;
+  const char* w;
+  int heads;
+  int64_t xb, xt, xh, yb, yt, yh;
+};
+
+struct NormRopeParams {
+  Side s[2];
+  const int32_t* pos;
+  int64_t pos_stride;
+  const int64_t* phases;
+  int n;
+  int64_t tokens;  // B * n
+  int D, R, interleaved, norm;
+  float magnitude, eps;
+  int chunks;  // warps per token
+  int units;   // head groups per warp
+};
+
+// cos and sin of p * u turns-in-2^-64, times m
+__device__ __forceinline__ void phase_sincos(int p, int64_t u, float m, float& c, float& s) {
+  const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(p)) * static_cast<uint64_t>(u);
+  const float a = static_cast<float>(static_cast<int32_t>(t >> 32)) * (6.283185307179586f / 4294967296.f);
+  c = __cosf(a) * m;
+  s = __sinf(a) * m;
+}
+
+template <int DT>
+struct Piece {  // eight channels
+  uint4 r[DT == DLLM_BF16 ? 1 : 2];
+};
+
+template <int DT>
+__device__ __forceinline__ Piece<DT> load_piece(const char* p) {
+  Piece<DT> v;
+  v.r[0] = *reinterpret_cast<const uint4*>(p);
+  if constexpr (DT == DLLM_F32) v.r[1] = *reinterpret_cast<const uint4*>(p + 16);
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack(const Piece<DT>& v, float (&x)[8]) {
+  if constexpr (DT == DLLM_BF16) {
+    const uint32_t w[4] = {v.r[0].x, v.r[0].y, v.r[0].z, v.r[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16lo(w[i]);
+      x[2 * i + 1] = bf16hi(w[i]);
+    }
+  } else {
+    const uint32_t w[8] = {v.r[0].x, v.r[0].y, v.r[0].z, v.r[0].w,
+                           v.r[1].x, v.r[1].y, v.r[1].z, v.r[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_piece(char* p, const float (&x)[8]) {
+  if constexpr (DT == DLLM_BF16) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf2_pack(x[0], x[1]), bf2_pack(x[2], x[3]),
+                                              bf2_pack(x[4], x[5]), bf2_pack(x[6], x[7]));
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// GL lanes per head (a power of two >= D / 16); D % 16 == 0, R % 16 == 0, 16-byte aligned rows.
+template <int DT, int GL>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int ES = DT == DLLM_BF16 ? 2 : 4;
+  constexpr int HPW = 32 / GL;  // heads a warp holds at once
+  const int64_t warp = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t token = warp / p.chunks;
+  if (token >= p.tokens) return;
+  const int chunk = static_cast<int>(warp - token * p.chunks);
+  const int b = static_cast<int>(token / p.n), i = static_cast<int>(token - static_cast<int64_t>(b) * p.n);
+  const int pos = p.pos ? p.pos[b * p.pos_stride + i] : 0;
+  if (pos < 0) return;
+
+  const int sub = lane % GL, slot = lane / GL;
+  const bool active = sub < p.D / 16;
+  const bool turns = sub < p.R / 16;
+  int o0, o1;
+  if (!turns) {
+    o0 = 16 * sub;  // = R + 16 * (sub - R / 16)
+    o1 = o0 + 8;
+  } else if (p.interleaved) {
+    o0 = 16 * sub;
+    o1 = o0 + 8;
+  } else {
+    o0 = 8 * sub;
+    o1 = p.R / 2 + 8 * sub;
+  }
+  float cs[8], sn[8];
+  if (turns) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      phase_sincos(pos, __ldg(p.phases + 8 * sub + e), p.magnitude, cs[e], sn[e]);
+  }
+  const int nq = p.s[0].heads, total = nq + p.s[1].heads;
+  Piece<DT> wq0{}, wq1{}, wk0{}, wk1{};
+  if (active) {
+    if (p.s[0].w) {
+      wq0 = load_piece<DT>(p.s[0].w + o0 * ES);
+      wq1 = load_piece<DT>(p.s[0].w + o1 * ES);
+    }
+    if (p.s[1].w) {
+      wk0 = load_piece<DT>(p.s[1].w + o0 * ES);
+      wk1 = load_piece<DT>(p.s[1].w + o1 * ES);
+    }
+  }
+  const char* xq = p.s[0].x + b * p.s[0].xb + i * p.s[0].xt;
+  const char* xk = p.s[1].x + b * p.s[1].xb + i * p.s[1].xt;
+  char* yq = p.s[0].y + b * p.s[0].yb + i * p.s[0].yt;
+  char* yk = p.s[1].y + b * p.s[1].yb + i * p.s[1].yt;
+  const float inv_d = 1.f / static_cast<float>(p.D);
+
+  auto src = [&](int h) {
+    return h < nq ? xq + h * p.s[0].xh : xk + (h - nq) * p.s[1].xh;
+  };
+  const int h0 = chunk * p.units * HPW + slot;
+  Piece<DT> a0{}, a1{};
+  if (active && h0 < total) {
+    a0 = load_piece<DT>(src(h0) + o0 * ES);
+    a1 = load_piece<DT>(src(h0) + o1 * ES);
+  }
+  for (int u = 0; u < p.units; ++u) {
+    const int h = h0 + u * HPW;
+    const bool mine = active && h < total;
+    float v0[8], v1[8];
+    unpack<DT>(a0, v0);
+    unpack<DT>(a1, v1);
+    if (u + 1 < p.units && active && h + HPW < total) {  // the next heads are on their way
+      a0 = load_piece<DT>(src(h + HPW) + o0 * ES);
+      a1 = load_piece<DT>(src(h + HPW) + o1 * ES);
+    }
+    if (p.norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v0[e], v0[e], fmaf(v1[e], v1[e], ss));
+      if (!active) ss = 0.f;
+#pragma unroll
+      for (int o = GL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      const float r = rsqrtf(ss * inv_d + p.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v0[e] *= r;
+        v1[e] *= r;
+      }
+      if (h < nq ? p.s[0].w != nullptr : p.s[1].w != nullptr) {
+        float w0[8], w1[8];
+        unpack<DT>(h < nq ? wq0 : wk0, w0);
+        unpack<DT>(h < nq ? wq1 : wk1, w1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v0[e] *= w0[e];
+          v1[e] *= w1[e];
+        }
+      }
+    }
+    if (turns) {
+      if (p.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a = v0[2 * e], c = v0[2 * e + 1];
+          v0[2 * e] = a * cs[e] - c * sn[e];
+          v0[2 * e + 1] = c * cs[e] + a * sn[e];
+          a = v1[2 * e], c = v1[2 * e + 1];
+          v1[2 * e] = a * cs[4 + e] - c * sn[4 + e];
+          v1[2 * e + 1] = c * cs[4 + e] + a * sn[4 + e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = v0[e], c = v1[e];
+          v0[e] = a * cs[e] - c * sn[e];
+          v1[e] = c * cs[e] + a * sn[e];
+        }
+      }
+    }
+    if (mine) {
+      char* y = h < nq ? yq + h * p.s[0].yh : yk + (h - nq) * p.s[1].yh;
+      store_piece<DT>(y + o0 * ES, v0);
+      store_piece<DT>(y + o1 * ES, v1);
+    }
+  }
+}
+
+__device__ __forceinline__ void store_value(char* p, int dtype, float v) {
+  if (dtype == DLLM_F32)
+    *reinterpret_cast<float*>(p) = v;
+  else
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(bf2_pack(v, 0.f));
+}
+
+// Any layout, one warp per head, element by element.
+__global__ void __launch_bounds__(kThreads)
+    norm_rope_any_kernel(const __grid_constant__ NormRopeParams p, int dtype) {
+  const int es = dtype == DLLM_BF16 ? 2 : 4;
+  const int64_t warp = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int total = p.s[0].heads + p.s[1].heads;
+  const int64_t token = warp / total;
+  if (token >= p.tokens) return;
+  const int h = static_cast<int>(warp - token * total);
+  const int b = static_cast<int>(token / p.n), i = static_cast<int>(token - static_cast<int64_t>(b) * p.n);
+  const int pos = p.pos ? p.pos[b * p.pos_stride + i] : 0;
+  if (pos < 0) return;
+  const Side& s = p.s[h < p.s[0].heads ? 0 : 1];
+  const int hl = h < p.s[0].heads ? h : h - p.s[0].heads;
+  const char* x = s.x + b * s.xb + i * s.xt + hl * s.xh;
+  char* y = s.y + b * s.yb + i * s.yt + hl * s.yh;
+  float r = 1.f;
+  if (p.norm) {
+    float ss = 0.f;
+    for (int c = lane; c < p.D; c += 32) {
+      const float v = load_logit(x, dtype, c);
+      ss = fmaf(v, v, ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    r = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
+  }
+  const bool weighted = p.norm && s.w;
+  auto value = [&](int c) {
+    float v = load_logit(x, dtype, c);
+    if (p.norm) v *= r;
+    return weighted ? v * load_logit(s.w, dtype, c) : v;
+  };
+  // a lane reads the channels it writes before it writes them: in place is safe
+  for (int j = lane; j < p.R / 2; j += 32) {
+    const int ca = p.interleaved ? 2 * j : j, cc = p.interleaved ? 2 * j + 1 : j + p.R / 2;
+    float cs, sn;
+    phase_sincos(pos, __ldg(p.phases + j), p.magnitude, cs, sn);
+    const float a = value(ca), c = value(cc);
+    store_value(y + static_cast<int64_t>(ca) * es, dtype, a * cs - c * sn);
+    store_value(y + static_cast<int64_t>(cc) * es, dtype, c * cs + a * sn);
+  }
+  for (int c = p.R + lane; c < p.D; c += 32) store_value(y + static_cast<int64_t>(c) * es, dtype, value(c));
+}
+
+__global__ void rope_phases_kernel(dllm_rope r, int64_t* phases) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  pdl_wait();
+  if (i >= r.rotary_dim / 2) return;
+  const double two_pi = 6.283185307179586476925;
+  const double g = pow(r.base, -2.0 * i / r.rotary_dim);
+  double f = g / r.factor;
+  if (r.scaling == DLLM_ROPE_BANDS) {
+    const double turns = r.original_len * g / two_pi;
+    const double w = fmin(1.0, fmax(0.0, (turns - r.slow_turns) / (r.fast_turns - r.slow_turns)));
+    f = (1.0 - w) * f + w * g;
+  }
+  phases[i] = __double2ll_rn(f / two_pi * 18446744073709551616.0);
+}
+
+bool rows_aligned(const Side& s) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(s.x) | reinterpret_cast<uintptr_t>(s.y) |
+                         reinterpret_cast<uintptr_t>(s.w) | static_cast<uintptr_t>(s.xb) |
+                         static_cast<uintptr_t>(s.xt) | static_cast<uintptr_t>(s.xh) |
+                         static_cast<uintptr_t>(s.yb) | static_cast<uintptr_t>(s.yt) |
+                         static_cast<uintptr_t>(s.yh);
+  return s.heads == 0 || bits % 16 == 0;
+}
+
+template <int DT, int GL>
+cudaError_t launch_vec(NormRopeParams& p, int sm_count, cudaStream_t stream) {
+  const int groups = (p.s[0].heads + p.s[1].heads + 32 / GL - 1) / (32 / GL);
+  // A warp takes as many of its token's head groups as still leave 32 warps per SM: the sines and
+  // cosines and the weights are then used for more heads; fewer tokens spread over more warps.
+  const int64_t spare = p.tokens * groups / (static_cast<int64_t>(sm_count) * 32);
+  p.units = static_cast<int>(spare < 1 ? 1 : spare > groups ? groups : spare);
+  p.chunks = (groups + p.units - 1) / p.units;
+  const int64_t warps = p.tokens * p.chunks;
+  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  return launch_dependent(norm_rope_kernel<DT, GL>, dim3(static_cast<unsigned>(blocks)),
+                          dim3(kThreads), 0, stream, p);
+}
+
+template <int DT>
+cudaError_t launch_vec_dt(NormRopeParams& p, int sm_count, cudaStream_t stream) {
+  const int lanes = p.D / 16;
+  if (lanes <= 1) return launch_vec<DT, 1>(p, sm_count, stream);
+  if (lanes <= 2) return launch_vec<DT, 2>(p, sm_count, stream);
+  if (lanes <= 4) return launch_vec<DT, 4>(p, sm_count, stream);
+  if (lanes <= 8) return launch_vec<DT, 8>(p, sm_count, stream);
+  if (lanes <= 16) return launch_vec<DT, 16>(p, sm_count, stream);
+  return launch_vec<DT, 32>(p, sm_count, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const dllm_heads* q, const dllm_heads* q_out, const dllm_heads* k,
+                             const dllm_heads* k_out, int B, int n, int D, const int32_t* pos,
+                             int64_t pos_stride, const int64_t* phases, int R, bool interleaved,
+                             float magnitude, bool norm, const void* q_weight, const void* k_weight,
+                             float eps, int sm_count, cudaStream_t stream) {
+  NormRopeParams p{};
+  const dllm_heads* in[2] = {q, k};
+  const dllm_heads* out[2] = {q_out, k_out};
+  const void* w[2] = {q_weight, k_weight};
+  int dtype = DLLM_F32;
+  for (int j = 0; j < 2; ++j) {
+    if (!in[j]) continue;
+    dtype = in[j]->dtype;
+    const int es = dtype == DLLM_BF16 ? 2 : 4;
+    p.s[j] = Side{static_cast<const char*>(in[j]->data), static_cast<char*>(out[j]->data),
+                  static_cast<const char*>(w[j]), in[j]->heads,
+                  in[j]->batch_stride * es, in[j]->token_stride * es, in[j]->head_stride * es,
+                  out[j]->batch_stride * es, out[j]->token_stride * es, out[j]->head_stride * es};
+  }
+  p.pos = pos;
+  p.pos_stride = pos_stride;
+  p.phases = phases;
+  p.n = n;
+  p.tokens = static_cast<int64_t>(B) * n;
+  p.D = D;
+  p.R = R;
+  p.interleaved = interleaved;
+  p.norm = norm;
+  p.magnitude = magnitude;
+  p.eps = eps;
+  if (D % 16 == 0 && D <= 512 && R % 16 == 0 && rows_aligned(p.s[0]) && rows_aligned(p.s[1]))
+    return dtype == DLLM_BF16 ? launch_vec_dt<DLLM_BF16>(p, sm_count, stream)
+                              : launch_vec_dt<DLLM_F32>(p, sm_count, stream);
+  const int64_t warps = p.tokens * (p.s[0].heads + p.s[1].heads);
+  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  return launch_dependent(norm_rope_any_kernel, dim3(static_cast<unsigned>(blocks)),
+                          dim3(kThreads), 0, stream, p, dtype);
+}
+
+cudaError_t launch_rope_phases(const dllm_rope& rope, int64_t* phases, cudaStream_t stream) {
+  return launch_dependent(rope_phases_kernel, dim3((rope.rotary_dim / 2 + 127) / 128), dim3(128), 0,
+                          stream, rope, phases);
+}
+
+}  // namespace dllm

@@ -379,6 +379,148 @@ dllm_status dllm_loop_continue(const dllm_block_state* state, int32_t B, int32_t
                                uint64_t handle, dllm_stream_t stream);
 
 /*
+ * What a refresh runs through (dInfer explainer, KV-cache manager: the entries of a changed region
+ * and its neighbours are recomputed).  dllm_kv_refresh_mask lists the entries; their new keys (and
+ * the block's queries) are normalised per head and rotated to their positions
+ * (dllm_qk_norm_rope), keys and values are stored in a cache of 4-bit codes (dllm_kv4_write) and
+ * the block's queries attend over that cache (dllm_attention_kv4).  The index list of
+ * dllm_kv_refresh_mask serves as `pos` of the calls below as it is: entries of -1 are skipped.
+ *
+ * dllm_heads describes rows of heads: channel c of head h of token i of sequence b is element
+ *   data[b*batch_stride + i*token_stride + h*head_stride + c]
+ * (strides in elements, so queries, keys and values may be slices of one projection's output).
+ * Any strides and any pointer aligned to the element size are accepted; rows that all start on
+ * 16-byte boundaries are read and written with 16-byte accesses, others element by element.
+ */
+typedef struct {
+  void* data;
+  int32_t heads;
+  int32_t dtype; /* dllm_dtype */
+  int64_t batch_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+} dllm_heads;
+
+/*
+ * Rotary frequencies: pair i of rotary_dim / 2 turns by f_i radians per position,
+ *   g_i = base^(-2i / rotary_dim),
+ *   DLLM_ROPE_LINEAR: f_i = g_i / factor  (factor 1: no scaling);
+ *   DLLM_ROPE_BANDS:  with r_i = original_len * g_i / 2pi, the turns of pair i over the original
+ *     context, and w = clamp((r_i - slow_turns) / (fast_turns - slow_turns), 0, 1):
+ *     f_i = (1 - w) * g_i / factor + w * g_i   (pairs that turn often keep their frequency, slow
+ *     ones are interpolated: the "by parts" rule of the YaRN paper, arXiv 2309.00071, section 3.2).
+ * dllm_rope_phases writes phases[i] = round(f_i / 2pi * 2^64), rotary_dim / 2 device words: the
+ * fraction of a turn per position in units of 2^-64, so that position * phases[i] modulo 2^64 is
+ * the phase without a loss at long positions.  Run it once per model.  rotary_dim even,
+ * 2 <= rotary_dim <= 1024; base > 1; factor >= 1; for BANDS original_len > 0 and
+ * 0 <= slow_turns < fast_turns.
+ */
+typedef enum { DLLM_ROPE_LINEAR = 0, DLLM_ROPE_BANDS = 1 } dllm_rope_scaling;
+typedef struct {
+  int32_t rotary_dim;
+  int32_t scaling; /* dllm_rope_scaling */
+  double base;
+  double factor;
+  double original_len;
+  double slow_turns;
+  double fast_turns;
+} dllm_rope;
+dllm_status dllm_rope_phases(const dllm_rope* rope, int64_t* phases, dllm_stream_t stream);
+
+/*
+ * Norm of each head of queries and keys and rotation to the token's position, in one pass.  Per
+ * token (b, i) with p = pos[b*pos_stride + i] >= 0 (tokens with p < 0 are skipped: their output
+ * is left as it is), per head x of head_dim channels:
+ *   y = norm ? x * (mean(x^2) + eps)^(-1/2) * weight : x       (weight NULL: ones)
+ *   each pair (a, c) = (y[i], y[i + rotary_dim/2]) or, interleaved, (y[2i], y[2i+1]), i <
+ *   rotary_dim/2:  (a cos t - c sin t, c cos t + a sin t) * magnitude,  t = 2pi * p*phases[i]/2^64;
+ *   the other channels are y.
+ * All in fp32, rounded once to the output.  q and q_out (k and k_out) have the same number of
+ * heads; they may be the same memory with the same strides, and must not overlap otherwise.
+ * q, q_out or k, k_out may be NULL (both of a pair): only the other is done.  One dtype for all
+ * tensors and weights (fp32 or bf16).  1 <= head_dim <= 1024; rotary_dim even, <= head_dim, 0: no
+ * rotation (phases may be NULL, and pos too: every token is done).  B, n >= 1, B*n <= 2^20.
+ */
+dllm_status dllm_qk_norm_rope(const dllm_heads* q, const dllm_heads* q_out, const dllm_heads* k,
+                              const dllm_heads* k_out, int32_t B, int32_t n, int32_t head_dim,
+                              const int32_t* pos, int64_t pos_stride, const int64_t* phases,
+                              int32_t rotary_dim, int32_t interleaved, float magnitude,
+                              int32_t norm, const void* q_weight, const void* k_weight, float eps,
+                              dllm_stream_t stream);
+
+/*
+ * A cache of keys and values in 4-bit codes, in pages.  Entry p of sequence b is slot
+ * p % page_size of page page_table[b*table_stride + p / page_size]; a table word outside
+ * [0, pages) means that the page is absent.  32 channels of one entry of one head are a group with
+ * a step s (fp32 value with three significant bits) and a zero point z in 0..15; code n stands
+ * for s * (n - z), which bf16 holds exactly.  codes: [pages, heads, page_size, head_dim / 2]
+ * bytes, channel 2c in the low nibble of byte c.  params: [pages, heads, page_size, head_dim / 32]
+ * 16-bit words, the bf16 bits of s with z in the low four.  4.5 bits a value.
+ * page_size a multiple of 16 in [16, 65536]; head_dim a multiple of 32 in [32, 512]; codes 16-byte
+ * and params 4-byte aligned.  The caller owns all arrays; nothing has to be initialised.
+ */
+typedef struct {
+  uint8_t* k_codes;
+  uint16_t* k_params;
+  uint8_t* v_codes;
+  uint16_t* v_params;
+  const int32_t* page_table;
+  int32_t pages;
+  int32_t heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t table_stride; /* words (pages) of a sequence in page_table */
+} dllm_kv4_cache;
+
+/*
+ * Quantise keys and values as they are written: token (b, i) goes to entry pos[b*pos_stride + i]
+ * of sequence b.  Entries < 0, beyond the page table or on an absent page are skipped; the entries
+ * of one call must differ from each other.  Per group x of 32 channels, in fp32:
+ *   lo = min(0, min x), hi = max(0, max x), s = (hi - lo) / 15 rounded up to three significant
+ *   bits (0 if below 2^-110), z = floor(-lo / s + 1/2),
+ *   n = min(15, round(x / s) + z), round half away from zero: |x - s (n - z)| <= s / 2.
+ * A group that holds a NaN or an infinity, or whose s exceeds 2^122, reads back as NaN.
+ * k, v: cache->heads heads, one dtype (fp32 or bf16).  B, n >= 1, B*n <= 2^20.
+ */
+dllm_status dllm_kv4_write(const dllm_kv4_cache* cache, const dllm_heads* k, const dllm_heads* v,
+                           int32_t B, int32_t n, const int32_t* pos, int64_t pos_stride,
+                           dllm_stream_t stream);
+
+/*
+ * Read entries back: k and v of token (b, i) receive the values of entry pos[b*pos_stride + i]
+ * (pos NULL: entry i), exact in both dtypes; entries < 0, beyond the table or on an absent page
+ * read as 0.  Limits as dllm_kv4_write.
+ */
+dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, const dllm_heads* v,
+                          int32_t B, int32_t n, const int32_t* pos, int64_t pos_stride,
+                          dllm_stream_t stream);
+
+/*
+ * Attention of n queries per sequence over the cache (a block of positions being decoded, a single
+ * token, a piece of a prompt).  Query head h reads key/value head h / (q->heads / cache->heads).
+ * Query i of sequence b sees entry j when
+ *   j < len_b = min(lens[b], max_len)  (lens NULL: max_len),  key_mask[b*mask_stride + j] != 0
+ *   (key_mask NULL: all),  its page is present, and, with `causal`, j <= len_b - n + i;
+ *   lse = ln sum_j exp(scale * q.K_j),  out = sum_j exp(scale * q.K_j - lse) V_j.
+ * A query that sees nothing gets out = 0 and lse = -inf.  Entries that no query sees are never
+ * used, whatever their codes, params and mask neighbours hold.  Scores, the softmax statistics and
+ * sums are fp32; the weights exp(.) are rounded to bf16 for their product with V, which is exact
+ * bf16, and out is rounded once to bf16.  The order of all sums is fixed: repeated calls agree
+ * bit for bit.
+ * q, out: bf16, same heads (a multiple of cache->heads).  lse: [B, q->heads, n] fp32 or NULL.
+ * head_dim 64, 128, 192 or 256; 0 <= max_len <= table_stride * page_size; scale finite; B*n <= 2^20.
+ * ws: dllm_attention_kv4_workspace_bytes(...) bytes (0 on invalid sizes); max_len is the bound the
+ * split of the entries over the GPU is planned from, lens are read on the device.
+ */
+size_t dllm_attention_kv4_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t n,
+                                          int32_t q_heads, int32_t max_len);
+dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
+                               const int32_t* lens, int32_t max_len, const uint8_t* key_mask,
+                               int64_t mask_stride, float scale, int32_t causal,
+                               const dllm_heads* out, float* lse, int32_t B, int32_t n, void* ws,
+                               size_t ws_bytes, dllm_stream_t stream);
+
+/*
  * Self-test of failure detection (no counterpart in the pages): runs the bounded wait the
  * smoothing GEMM uses on a barrier that nothing ever completes.  After limit_us microseconds
  * (1 .. 2,000,000) the wait gives up and records DLLM_ERR_TIMEOUT in the status word of `ws`
