@@ -218,6 +218,7 @@ dllm_status check_attention(const dllm_kv4_cache* cache, int32_t B, int32_t n, i
   if (max_len < 0 ||
       max_len > static_cast<int64_t>(cache->table_stride) * cache->page_size)
     return fail(DLLM_ERR_INVALID_ARG, "max_len=%d outside [0, table_stride * page_size]", max_len);
+  if (max_len > (1 << 30)) return fail(DLLM_ERR_UNSUPPORTED, "max_len=%d exceeds 2^30", max_len);
   if (static_cast<int64_t>(B) * n * q_heads > (int64_t{1} << 30))
     return fail(DLLM_ERR_UNSUPPORTED, "B * n * heads exceeds 2^30");
   return DLLM_OK;

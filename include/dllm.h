@@ -508,7 +508,8 @@ dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, cons
  * bf16, and out is rounded once to bf16.  The order of all sums is fixed: repeated calls agree
  * bit for bit.
  * q, out: bf16, same heads (a multiple of cache->heads).  lse: [B, q->heads, n] fp32 or NULL.
- * head_dim 64, 128, 192 or 256; 0 <= max_len <= table_stride * page_size; scale finite; B*n <= 2^20.
+ * head_dim 64, 128, 192 or 256; 0 <= max_len <= table_stride * page_size and 2^30; scale finite;
+ * B*n <= 2^20, B*n*heads <= 2^30.
  * ws: dllm_attention_kv4_workspace_bytes(...) bytes (0 on invalid sizes); max_len is the bound the
  * split of the entries over the GPU is planned from, lens are read on the device.
  */
