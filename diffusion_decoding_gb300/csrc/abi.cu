@@ -185,9 +185,9 @@ dllm_status check_cache(const dllm_kv4_cache* c) {
   if (c->heads > 65536) return fail(DLLM_ERR_UNSUPPORTED, "heads=%d exceeds 65536", c->heads);
   if (static_cast<int64_t>(c->table_stride) * c->page_size >= (int64_t{1} << 31))
     return fail(DLLM_ERR_UNSUPPORTED, "table_stride * page_size exceeds 2^31 - 1");
-  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_params, 4) ||
-      !aligned(c->v_params, 4) || !aligned(c->page_table, 4))
-    return fail(DLLM_ERR_INVALID_ARG, "codes must be 16-byte, params and page_table 4-byte aligned");
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_params, 16) ||
+      !aligned(c->v_params, 16) || !aligned(c->page_table, 4))
+    return fail(DLLM_ERR_INVALID_ARG, "codes and params must be 16-byte, page_table 4-byte aligned");
   return DLLM_OK;
 }
 
@@ -767,8 +767,7 @@ dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, cons
 size_t dllm_attention_kv4_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t n,
                                           int32_t q_heads, int32_t max_len) {
   if (check_attention(cache, B, n, q_heads, max_len) != DLLM_OK) return 0;
-  return dllm::attention_ws_bytes(B, n, q_heads, cache->heads, cache->head_dim, max_len,
-                                  sm_count());
+  return dllm::attention_ws_bytes(n, q_heads / cache->heads, cache->head_dim, max_len, sm_count());
 }
 
 dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
@@ -791,8 +790,8 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
                 static_cast<long long>(mask_stride), max_len);
   if (!aligned(lens, 4) || !aligned(lse, 4))
     return fail(DLLM_ERR_INVALID_ARG, "lens and lse must be 4-byte aligned");
-  const size_t need = dllm::attention_ws_bytes(B, n, q->heads, cache->heads, cache->head_dim,
-                                               max_len, sm_count());
+  const size_t need = dllm::attention_ws_bytes(n, q->heads / cache->heads, cache->head_dim, max_len,
+                                               sm_count());
   if (ws_bytes < need)
     return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed",
                 ws_bytes, need);

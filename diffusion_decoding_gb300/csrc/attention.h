@@ -30,8 +30,8 @@ struct AttnParams {
   int B, n;
 };
 
-size_t attention_ws_bytes(int B, int n, int q_heads, int heads, int D, int max_len, int sm_count);
+size_t attention_ws_bytes(int n, int G, int D, int max_len, int sm_count);
 
-cudaError_t launch_attention(AttnParams p, int D, void* ws, int sm_count, cudaStream_t stream);
+cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream);
 
 }  // namespace dllm

@@ -43,7 +43,9 @@ __device__ __forceinline__ Kv4Scale kv4_scale(uint32_t pp) {
 template <int J>
 __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, const Kv4Scale& sc) {
   const uint32_t t = J == 0 ? (w << 3) : (w >> (4 * J - 3 < 0 ? 0 : 4 * J - 3));
-  return bf2_fma((t & 0x00780078u) | 0x41804180u, sc.step, sc.offset);
+  uint32_t n;  // (t & mask) | bits of 16, one instruction
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(n) : "r"(t), "r"(0x00780078u), "r"(0x41804180u));
+  return bf2_fma(n, sc.step, sc.offset);
 }
 
 // Page of entry p of one sequence's table row, -1 when absent (p within the table).
