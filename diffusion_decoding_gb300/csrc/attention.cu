@@ -39,7 +39,7 @@ struct FewPlan {
   int row_tiles;
   int q_aligned;    // query rows on 16-byte boundaries
   float* part_o;    // [2 * CTAs, rows of a tile, D]
-  float2* part_ml;  // [2 * CTAs, rows of a tile]: maximum (base 2) and sum
+  float2* part_ml;  // [2 * CTAs, rows of a tile]: reference (base 2) and sum of weights
   int ctas;
 };
 
@@ -198,45 +198,71 @@ struct Tile {
   uint32_t k[2][KW], v[4][VW];
   uint32_t kp[2][kSpread ? 6 : D == 256 ? 2 : 1], vp[4][kSpread ? 3 : 1];
 
-  __device__ __forceinline__ void read_k(uint32_t at, int c, int g) {
+  // What a lane reads, as bytes from the tile's start: K words of row g (row g + 8 is 8 rows
+  // further; head_dim 256: also the next piece), V words of rows 2c and 2c + 1, and their params.
+  struct Lane {
+    uint32_t k, k2, kp, v0, v1, vp;
+    __device__ __forceinline__ Lane(uint32_t ring, int c, int g) {
+      const int entry = (g >> 1) + 4 * (g & 1);
+      constexpr int LANES = kSpread ? 4 : 4 / VW;  // lanes of a V piece
+      k2 = 0u;
+      if constexpr (kSpread) {
+        k = place(g, 0) + 4 * c;
+        kp = entry * (D / 16);
+      } else if constexpr (D == 256) {
+        k = place(g, 2 * c);
+        k2 = ring + place(g, 2 * c + 1);
+        kp = entry * (D / 16) + 4 * c;
+      } else if constexpr (D == 128) {
+        k = place(g, c);
+        kp = entry * (D / 16) + 2 * c;
+      } else {
+        k = place(g, c >> 1) + 8 * (c & 1);
+        kp = entry * (D / 16) + 2 * (c >> 1);
+      }
+      const int in = kSpread ? 4 * (g & 3) : (g % LANES) * VW * 4;
+      v0 = ring + kV + place(2 * c, g / LANES) + in;
+      v1 = ring + kV + place(2 * c + 1, g / LANES) + in;
+      vp = ring + kVp + c * (D / 16) + 2 * (kSpread ? g >> 2 : g * VW / 4);
+      k += ring;
+      kp += ring + kKp;
+    }
+  };
+
+  // `at`: bytes of the stage from the ring's start
+  __device__ __forceinline__ void read_k(const Lane& l, uint32_t at) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = g + 8 * e, entry = (g >> 1) + 4 * (g & 1) + 8 * e;
-      const uint32_t par = at + kKp + entry * (D / 16);
+      const uint32_t row = at + 8 * ROW * e, par = l.kp + at + 8 * (D / 16) * e;
       if constexpr (kSpread) {
 #pragma unroll
-        for (int i = 0; i < KW; ++i) lds_words<1>(at + place(r, i) + 4 * c, &k[e][i]);
+        for (int i = 0; i < KW; ++i) lds_words<1>(l.k + row + 16 * i, &k[e][i]);
 #pragma unroll
         for (int i = 0; i < 6; ++i) kp[e][i] = lds_u16(par + 2 * i);
       } else if constexpr (D == 256) {
-        lds_words<4>(at + place(r, 2 * c), &k[e][0]);
-        lds_words<4>(at + place(r, 2 * c + 1), &k[e][4]);
-        kp[e][0] = lds_u16(par + 4 * c);
-        kp[e][1] = lds_u16(par + 4 * c + 2);
-      } else if constexpr (D == 128) {
-        lds_words<4>(at + place(r, c), &k[e][0]);
-        kp[e][0] = lds_u16(par + 2 * c);
+        lds_words<4>(l.k + row, &k[e][0]);
+        lds_words<4>(l.k2 + row, &k[e][4]);
+        kp[e][0] = lds_u16(par);
+        kp[e][1] = lds_u16(par + 2);
       } else {
-        lds_words<2>(at + place(r, c >> 1) + 8 * (c & 1), &k[e][0]);
-        kp[e][0] = lds_u16(par + 2 * (c >> 1));
+        lds_words<KW>(l.k + row, &k[e][0]);
+        kp[e][0] = lds_u16(par);
       }
     }
   }
-  __device__ __forceinline__ void read_v(uint32_t at, int c, int g) {
+  __device__ __forceinline__ void read_v(const Lane& l, uint32_t at) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 2 * c + (e & 1) + 8 * (e >> 1), entry = c + 4 * e;
-      const uint32_t par = at + kVp + entry * (D / 16);
+      const uint32_t row = (e & 1 ? l.v1 : l.v0) + at + 8 * ROW * (e >> 1);
+      const uint32_t par = l.vp + at + 4 * (D / 16) * e;
       if constexpr (kSpread) {
 #pragma unroll
-        for (int i = 0; i < VW; ++i)
-          lds_words<1>(at + kV + place(r, 2 * i + (g >> 2)) + 4 * (g & 3), &v[e][i]);
+        for (int i = 0; i < VW; ++i) lds_words<1>(row + 32 * i, &v[e][i]);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) vp[e][i] = lds_u16(par + 2 * (2 * i + (g >> 2)));
+        for (int i = 0; i < 3; ++i) vp[e][i] = lds_u16(par + 4 * i);
       } else {
-        constexpr int LANES = 4 / VW;  // lanes of a piece
-        lds_words<VW>(at + kV + place(r, g / LANES) + (g % LANES) * VW * 4, &v[e][0]);
-        vp[e][0] = lds_u16(par + 2 * (g * VW / 4));
+        lds_words<VW>(row, &v[e][0]);
+        vp[e][0] = lds_u16(par);
       }
     }
   }
@@ -247,6 +273,10 @@ struct Tile {
   }
   __device__ __forceinline__ uint32_t v_param(int e, int i) const { return vp[e][kSpread ? i : 0]; }
 };
+
+// A weight may reach 2^kSlack before the reference moves: sums of 2^30 of them stay far inside fp32,
+// and bf16 keeps the same relative precision at every magnitude.
+constexpr float kSlack = 8.f;
 
 // CTAs of the one resident wave per SM: what the registers allow (checked with -Xptxas -v).
 constexpr int few_ctas_per_sm(int D, int NT) {
@@ -292,8 +322,13 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
 #pragma unroll
   for (int i = 0; i < R::PIECES; ++i) {
     const int piece = lane + 32 * i;
-    dst[i] = R::place(R::row_of(piece / (D / 32)), piece % (D / 32));
+    dst[i] = ring + R::place(R::row_of(piece / (D / 32)), piece % (D / 32));
   }
+  const uint32_t dst_par = ring + (lane < 16 ? R::kKp : R::kVp) + (lane & 15) * 16;
+  const uint16_t* par_of_lane = (lane < 16 ? p.k_params : p.v_params) + (lane & 15) * 8;
+  const uint8_t* k_of_lane = p.k_codes + lane * 16;
+  const uint8_t* v_of_lane = p.v_codes + lane * 16;
+  const typename R::Lane at_lane(ring, c, g);
 
   for (int64_t u = u0; u < u1;) {
     const int piece = static_cast<int>(min(static_cast<int64_t>(units - k0), u1 - u));
@@ -355,25 +390,20 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
       return pg >= 0 && pg < p.pages ? pg : -1;
     };
     int page = page_ahead();
-    uint32_t present = 0;  // bit s: the tile in stage s is there
-    // copy the next tile into stage `s` and look the page after it up
-    auto copy = [&](int s) {
-      present &= ~(1u << s);
-      if (page >= 0) {
-        present |= 1u << s;
+    // copy the next tile into the stage at byte `at` of the ring and look the page after it up;
+    // whether the tile was there
+    auto copy = [&](uint32_t at) {
+      const bool there = page >= 0;
+      if (there) {
         const int64_t row = (static_cast<int64_t>(page) * p.heads + h) * p.page_size + slot_ahead;
-        const uint32_t at = ring + s * R::kBytes;
-        const uint8_t* ks = p.k_codes + row * (D / 2) + lane * 16;
-        const uint8_t* vs = p.v_codes + row * (D / 2) + lane * 16;
+        const uint8_t* ks = k_of_lane + row * (D / 2);
+        const uint8_t* vs = v_of_lane + row * (D / 2);
 #pragma unroll
         for (int i = 0; i < R::PIECES; ++i) {
-          cp_async16(at + dst[i], ks + 512 * i);
-          cp_async16(at + R::kV + dst[i], vs + 512 * i);
+          cp_async16(dst[i] + at, ks + 512 * i);
+          cp_async16(dst[i] + at + R::kV, vs + 512 * i);
         }
-        if ((lane & 15) < D / 16) {
-          const uint16_t* par = (lane < 16 ? p.k_params : p.v_params) + row * (D / 32);
-          cp_async16(at + (lane < 16 ? R::kKp : R::kVp) + (lane & 15) * 16, par + (lane & 15) * 8);
-        }
+        if ((lane & 15) < D / 16) cp_async16(dst_par + at, par_of_lane + row * (D / 32));
       }
       cp_async_commit();
       j_ahead += kStep;
@@ -384,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
         ++t_ahead;
       }
       page = page_ahead();
+      return there;
     };
 
     auto compute = [&](uint32_t at, int j) {
@@ -396,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
         vis = __ballot_sync(kFull, e < end && (!mask || __ldg(mask + e) != 0)) & 0xffffu;
         if (vis == 0u) return;
       }
-      cur.read_k(at, c, g);
+      cur.read_k(at_lane, at);
       float s[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
@@ -437,10 +468,11 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) above |= fmaxf(s[t][x], s[t][x + 2]) > m[t][x];
+        for (int x = 0; x < 2; ++x) above |= fmaxf(s[t][x], s[t][x + 2]) > m[t][x] + kSlack;
       }
-      // the running maximum moves rarely after the first tiles: only then is it reduced over the
-      // lanes and what was summed so far rescaled
+      // m is a reference that no score exceeds by more than kSlack, not the maximum itself: it
+      // moves rarely after the first tile, and only then are the scores reduced over the lanes and
+      // what was summed so far rescaled
       if (__any_sync(kFull, above)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -474,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
         pt[t][0] = transpose8x8(bf2_pack(p0, p1));
         pt[t][1] = transpose8x8(bf2_pack(p2, p3));
       }
-      cur.read_v(at, c, g);
+      cur.read_v(at_lane, at);
       if (vis != 0xffffu) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -509,15 +541,18 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
       }
     };
 
+    uint32_t there = 0;  // bit k: the tile k steps ahead is there
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) copy(k);
-    int stage = 0;
+    for (int k = 0; k < kStages - 1; ++k) there |= copy(k * R::kBytes) ? 1u << k : 0u;
+    uint32_t at = 0, into = (kStages - 1) * R::kBytes;
     for (int j = j0; j < end; j += kStep) {
       cp_async_wait_group<kStages - 2>();
-      __syncwarp();  // every lane's pieces have landed, and all lanes are done with the stage before
-      copy(stage == 0 ? kStages - 1 : stage - 1);
-      if (present >> stage & 1u) compute(ring + stage * R::kBytes, j);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
+      __syncwarp();  // every lane's pieces have landed, and all are done with the stage before
+      there |= copy(into) ? 1u << (kStages - 1) : 0u;
+      if (there & 1u) compute(at, j);
+      there >>= 1;
+      into = at;
+      at = at == (kStages - 1) * R::kBytes ? 0u : at + R::kBytes;
     }
     cp_async_wait_all();
     __syncthreads();  // the rings become the buffers of the join
