@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdllm.so")
 SOURCES = ["stats_commit.cu", "stats_probs.cu", "scan.cu", "smooth.cu", "norm_rope.cu",
-           "kv4_cache.cu", "attention.cu", "abi.cu", "static_ws.cu"]
+           "kv4_cache.cu", "attention.cu", "attention_tc.cu", "abi.cu", "static_ws.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

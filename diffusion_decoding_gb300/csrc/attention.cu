@@ -10,16 +10,13 @@
 // lanes that the fragments want them in; nothing is transposed (P^T comes out of S^T by
 // movmatrix).  The order of channels inside a product is free, so the lane's words are contiguous.
 //
-// The grid is one wave of resident CTAs that share the work evenly whatever the lengths: all
-// (sequence, head, row tile) segments, cut into units of 16 entries per warp, form one line, and
-// CTA k takes the k-th equal stretch of it.  A segment inside one stretch is written straight to
-// the output; of the others each CTA leaves a partial result (at most two a CTA: the segments its
-// stretch begins and ends in), which attention_join_kernel adds in order.
+// The grid is one wave of resident CTAs that share the work evenly (attention_line.cuh).
 //
 // HBM-bound: an entry of one head costs 9/8 * head_dim bytes.  Each warp keeps kStages - 1 tiles on
 // their way into a ring of its own in shared memory (16-byte asynchronous copies, no block
 // barrier), and page ids one tile further ahead.
 #include "attention.h"
+#include "attention_line.cuh"
 
 #include "common.cuh"
 #include "internal.h"
@@ -31,106 +28,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-
 constexpr int kStep = 16 * kWarps;  // entries that the warps take together
-
-struct FewPlan {
-  int unit;         // entries of a unit, a multiple of kStep
-  int row_tiles;
-  int q_aligned;    // query rows on 16-byte boundaries
-  float* part_o;    // [2 * CTAs, rows of a tile, D]
-  float2* part_ml;  // [2 * CTAs, rows of a tile]: reference (base 2) and sum of weights
-  int ctas;
-};
-
-__device__ __forceinline__ int length_of(const AttnParams& p, int b) {
-  return p.lens ? max(0, min(__ldg(p.lens + b), p.max_len)) : p.max_len;
-}
-__device__ __forceinline__ int units_of(int len, int unit) {
-  return max(1, (len + unit - 1) / unit);
-}
-
-// The line of units: sequences in order, each with `segs` segments of units_of(length) units, cut
-// into f.ctas stretches that differ by one unit at most.  Built and asked by whole warps.
-struct Line {
-  int64_t total, each, longer;  // units; units of a stretch; stretches with one unit more
-  int64_t own, upto;            // this lane's sequence (of the first 32): its units, and all up to it
-
-  __device__ __forceinline__ void build(const AttnParams& p, int segs, int unit, int ctas) {
-    const int lane = threadIdx.x & 31;
-    own = lane < p.B ? static_cast<int64_t>(segs) * units_of(length_of(p, lane), unit) : 0;
-    upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(kFull, upto, o);
-      if (lane >= o) upto += v;
-    }
-    total = __shfl_sync(kFull, upto, 31);
-    if (p.B > 32) {
-      if (!p.lens) {
-        total = static_cast<int64_t>(p.B) * segs * units_of(p.max_len, unit);
-      } else {
-        int64_t sum = 0;
-        for (int b = 32 + lane; b < p.B; b += 32) sum += units_of(length_of(p, b), unit);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        total += sum * segs;
-      }
-    }
-    if (total >> 32)
-      each = total / ctas;
-    else
-      each = static_cast<uint32_t>(total) / static_cast<uint32_t>(ctas);
-    longer = total - each * ctas;
-  }
-  // first unit of CTA c's stretch
-  __device__ __forceinline__ int64_t start(int64_t c) const {
-    return each * c + (c < longer ? c : longer);
-  }
-  // CTA whose stretch holds unit u
-  __device__ __forceinline__ int64_t holder(int64_t u) const {
-    const int64_t head = longer * (each + 1);
-    return u < head ? u / (each + 1) : longer + (u - head) / each;
-  }
-  // sequence that holds unit `at` (< total), and the units before that sequence
-  __device__ __forceinline__ int find(const AttnParams& p, int segs, int unit, int64_t at,
-                                      int64_t* before) const {
-    const int lane = threadIdx.x & 31;
-    if (p.B > 32 && !p.lens) {
-      const int64_t per = static_cast<int64_t>(segs) * units_of(p.max_len, unit);
-      *before = at / per * per;
-      return static_cast<int>(at / per);
-    }
-    int64_t base = 0, mine = own, incl = upto;
-    for (int b0 = 0;;) {
-      const unsigned hit = __ballot_sync(kFull, base + incl > at);
-      if (hit != 0u || b0 + 32 >= p.B) {
-        const int l = hit ? __ffs(hit) - 1 : 31;
-        *before = base + __shfl_sync(kFull, incl - mine, l);
-        return min(b0 + l, p.B - 1);
-      }
-      base += __shfl_sync(kFull, incl, 31);
-      b0 += 32;
-      mine = b0 + lane < p.B ? static_cast<int64_t>(segs) * units_of(length_of(p, b0 + lane), unit) : 0;
-      incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-    }
-  }
-  // units before sequence b
-  __device__ __forceinline__ int64_t before(const AttnParams& p, int segs, int unit, int b) const {
-    if (b < 32) return __shfl_sync(kFull, upto - own, b);
-    if (!p.lens) return static_cast<int64_t>(b) * segs * units_of(p.max_len, unit);
-    int64_t sum = 0;
-    for (int k = 32 + (threadIdx.x & 31); k < b; k += 32) sum += units_of(length_of(p, k), unit);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    return sum * segs + __shfl_sync(kFull, upto, 31);
-  }
-};
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -292,7 +190,7 @@ constexpr size_t few_smem() {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
-    attention_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewPlan f) {
+    attention_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
   using R = Tile<D>;
   constexpr int KW = R::KW, VW = R::VW, MT = D / 16, ROWS = 8 * NT;
   extern __shared__ float4 smem_raw[];
@@ -301,18 +199,15 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int rows = p.n * p.G, segs = p.heads * f.row_tiles;
+  const int rows = p.n * p.G;
   pdl_wait();
   pdl_trigger();
-  Line line;
-  line.build(p, segs, f.unit, f.ctas);
+  Line<ROWS> line;
+  line.build(p, f);
   const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
   if (u0 >= u1) return;
-  int64_t before;
-  int b = line.find(p, segs, f.unit, u0, &before);
-  int len = length_of(p, b), units = units_of(len, f.unit);
-  int seg = static_cast<int>((u0 - before) / units);
-  int k0 = static_cast<int>((u0 - before) - static_cast<int64_t>(seg) * units);
+  Segment<ROWS> sg;
+  sg.find(p, f, line, u0);
 
   const int t0 = (g >> 1) + (g & 1) * 4;  // entry of fragment row g
   const int step_pages = kStep / p.page_size, step_slots = kStep % p.page_size;
@@ -331,14 +226,10 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
   const typename R::Lane at_lane(ring, c, g);
 
   for (int64_t u = u0; u < u1;) {
-    const int piece = static_cast<int>(min(static_cast<int64_t>(units - k0), u1 - u));
-    const int h = seg / f.row_tiles, r0 = (seg - h * f.row_tiles) * ROWS;
-    // causal: row r sees the entries below len - n + i + 1, i = r / G; the last row of the tile
-    // the most
-    const int i_last = (min(r0 + ROWS, rows) - 1) / p.G;
-    const int seen_last = p.causal ? min(len, len - p.n + i_last + 1) : len;
-    const int seen_first = p.causal ? min(len, len - p.n + r0 / p.G + 1) : len;
-    const int end = min(seen_last, (k0 + piece) * f.unit);
+    const int piece = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), u1 - u));
+    const int b = sg.b, h = sg.h, len = sg.len, r0 = sg.rt * ROWS, k0 = sg.k0;
+    const int seen_first = rows_see(p, len, r0);  // what the tile's first row sees
+    const int end = min(sg.seen, (k0 + piece) * f.unit);
 
     // queries: channel pairs (j, j + 4) of the lane's words, as the K fragments hold them
     uint32_t q[NT][2 * KW][2];
@@ -459,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
           for (int e = 0; e < 4; ++e) {
             const int entry = t0 + (e >> 1) * 8;
             const int r = r0 + t * 8 + 2 * c + (e & 1);
-            const int bound = p.causal ? len - p.n + r / p.G + 1 : len;
+            const int bound = rows_see(p, len, r);
             if (!(vis >> entry & 1u) || j + entry >= bound) s[t][e] = -INFINITY;
           }
         }
@@ -595,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
       }
     }
     __syncthreads();
-    const bool direct = piece == units;
+    const bool direct = piece == sg.units;
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
     for (int e = threadIdx.x; e < ROWS * (D / 2); e += kThreads) {
       const int r = e / (D / 2), ch = e - r * (D / 2);
@@ -620,102 +511,21 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
       } else {
         const int i = (r0 + r) / p.G, hq = h * p.G + (r0 + r) - i * p.G;
         uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + 2 * ch;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const uint32_t w = bf2_pack(acc.x * inv, acc.y * inv);
         dst[0] = static_cast<uint16_t>(w);
         dst[1] = static_cast<uint16_t>(w >> 16);
         if (ch == 0 && p.lse)
           p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
-              sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+              sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
     }
     u += piece;
-    k0 = 0;
     if (u < u1) {
       __syncthreads();  // the buffers are reused
-      if (++seg == segs) {
-        seg = 0;
-        len = length_of(p, ++b);
-        units = units_of(len, f.unit);
-      }
+      sg.next(p, f);
     }
   }
-}
-
-// Join the parts of the segments that several CTAs share, in order of their entries:
-//   out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
-// One CTA per row of a segment; each warp takes every fourth part.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads)
-    attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewPlan f) {
-  constexpr int ROWS = 8 * NT, V = D / 64;
-  __shared__ float2 acc_s[kWarps][D / 2];
-  __shared__ float sum_s[kWarps], max_s[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = p.n * p.G, segs = p.heads * f.row_tiles;
-  const int r = blockIdx.x % rows;
-  const int h = blockIdx.x / rows % p.heads, b = blockIdx.x / rows / p.heads;
-  pdl_wait();
-  pdl_trigger();
-  const int units = units_of(length_of(p, b), f.unit);
-  if (units == 1) return;
-  Line line;
-  line.build(p, segs, f.unit, f.ctas);
-  const int64_t first = line.before(p, segs, f.unit, b) +
-                        (static_cast<int64_t>(h) * f.row_tiles + r / ROWS) * units;
-  const int64_t c0 = line.holder(first), c1 = line.holder(first + units - 1);
-  if (c0 == c1) return;  // written by its one CTA
-  // a CTA's part: its first one unless its stretch began in a segment before
-  auto part_of = [&](int64_t c) { return 2 * c + (line.start(c) >= first ? 0 : 1); };
-  float mx = -INFINITY;
-  for (int64_t c = c0 + threadIdx.x; c <= c1; c += kThreads) {
-    mx = fmaxf(mx, f.part_ml[part_of(c) * ROWS + r % ROWS].x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-  if (lane == 0) max_s[warp] = mx;
-  __syncthreads();
-  mx = max_s[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, max_s[w]);
-  float2 acc[V] = {};
-  float sum = 0.f;
-#pragma unroll 4
-  for (int64_t c = c0 + warp; c <= c1; c += kWarps) {
-    const int64_t part = part_of(c);
-    const float2 v = f.part_ml[part * ROWS + r % ROWS];
-    const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
-    sum = fmaf(v.y, keep, sum);
-    const float* src = f.part_o + (part * ROWS + r % ROWS) * D;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float2 x = *reinterpret_cast<const float2*>(src + 64 * k + 2 * lane);
-      acc[k].x = fmaf(x.x, keep, acc[k].x);
-      acc[k].y = fmaf(x.y, keep, acc[k].y);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < V; ++k) acc_s[warp][32 * k + lane] = acc[k];
-  if (lane == 0) sum_s[warp] = sum;
-  __syncthreads();
-  sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
-  const int i = r / p.G, hq = h * p.G + r - i * p.G;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  for (int e = threadIdx.x; e < D / 2; e += kThreads) {
-    float2 a = acc_s[0][e];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      a.x += acc_s[w][e].x;
-      a.y += acc_s[w][e].y;
-    }
-    const uint32_t w = bf2_pack(a.x * inv, a.y * inv);
-    uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + 2 * e;
-    dst[0] = static_cast<uint16_t>(w);
-    dst[1] = static_cast<uint16_t>(w >> 16);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
-        sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 struct FewSizes {
@@ -742,7 +552,7 @@ FewSizes few_sizes(int n, int G, int D, int max_len, int sm_count) {
 }
 
 template <int D, int NT>
-cudaError_t launch_few(const AttnParams& p, const FewPlan& f, bool split, cudaStream_t stream) {
+cudaError_t launch_few(const AttnParams& p, const AttnPlan& f, bool split, cudaStream_t stream) {
   constexpr size_t smem = few_smem<D, NT>();
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024)
@@ -752,25 +562,29 @@ cudaError_t launch_few(const AttnParams& p, const FewPlan& f, bool split, cudaSt
   e = launch_dependent(attention_few_kernel<D, NT>, dim3(f.ctas), dim3(kThreads), smem,
                                    stream, p, f);
   if (e != cudaSuccess || !split) return e;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.heads * p.n * p.G;
-  return launch_dependent(attention_join_kernel<D, NT>, dim3(static_cast<unsigned>(rows)),
-                          dim3(kThreads), 0, stream, p, f);
+  return launch_join<D, 8 * NT>(p, f, stream);
 }
 
 }  // namespace
 
+bool attention_rows_aligned(const void* x, int64_t sb, int64_t st, int64_t sh) {
+  return (reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(sb * 2) |
+          static_cast<uintptr_t>(st * 2) | static_cast<uintptr_t>(sh * 2)) % 16 == 0;
+}
+
 size_t attention_ws_bytes(int n, int G, int D, int max_len, int sm_count) {
-  return few_sizes(n, G, D, max_len, sm_count).bytes;
+  return attention_tc_takes(n, G, D) ? attention_tc_ws_bytes(D, sm_count)
+                                     : few_sizes(n, G, D, max_len, sm_count).bytes;
 }
 
 cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream) {
+  if (attention_tc_takes(p.n, p.G, D)) return launch_attention_tc(p, D, ws, sm_count, stream);
   const FewSizes s = few_sizes(p.n, p.G, D, p.max_len, sm_count);
-  FewPlan f{};
+  AttnPlan f{};
   f.row_tiles = s.row_tiles;
   f.ctas = s.ctas;
   f.unit = s.unit;
-  f.q_aligned = (reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.qb * 2) |
-                 static_cast<uintptr_t>(p.qt * 2) | static_cast<uintptr_t>(p.qh * 2)) % 16 == 0;
+  f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + s.off_ml);
   switch (D * 10 + s.nt) {

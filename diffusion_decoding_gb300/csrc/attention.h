@@ -34,4 +34,13 @@ size_t attention_ws_bytes(int n, int G, int D, int max_len, int sm_count);
 
 cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream);
 
+// Many rows per cache head (attention_tc.cu): head_dim 64 or 128.
+bool attention_tc_takes(int n, int G, int D);
+size_t attention_tc_ws_bytes(int D, int sm_count);
+cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
+                                cudaStream_t stream);
+
+// Rows of a bf16 tensor (strides in elements) all start on 16-byte boundaries.
+bool attention_rows_aligned(const void* x, int64_t sb, int64_t st, int64_t sh);
+
 }  // namespace dllm

@@ -1,0 +1,253 @@
+// How the attention's work is shared out, and the kernel that joins what was split.
+//
+// Rows are the n * G queries of a sequence that share a cache head, row r = i * G + g; a row tile
+// is ROWS of them.  A segment is one (sequence, row tile, head); the entries it has to look at are
+// cut into units.  All segments form one line of units, and CTA k of a single resident wave takes
+// the k-th equal stretch of it, whatever the lengths.  A segment inside one stretch is written
+// straight to the output; of the others each CTA leaves a partial result (at most two a CTA: the
+// segments its stretch begins and ends in), which attention_join_kernel adds in order.
+#pragma once
+
+#include "attention.h"
+#include "common.cuh"
+#include "kv4.cuh"
+
+namespace dllm {
+
+struct AttnPlan {
+  int unit;         // entries of a unit
+  int row_tiles;
+  int q_aligned;    // query rows on 16-byte boundaries
+  int out_aligned;  // output rows too
+  float* part_o;    // [2 * CTAs, rows of a tile, D]
+  float2* part_ml;  // [2 * CTAs, rows of a tile]: reference (base 2) and sum of weights
+  int ctas;
+  int32_t* status;
+};
+
+namespace {
+
+__device__ __forceinline__ int length_of(const AttnParams& p, int b) {
+  return p.lens ? max(0, min(__ldg(p.lens + b), p.max_len)) : p.max_len;
+}
+__device__ __forceinline__ int units_of(int entries, int unit) {
+  return max(1, (entries + unit - 1) / unit);
+}
+// Row r sees the entries below this (if its mask and the pages let it).
+__device__ __forceinline__ int rows_see(const AttnParams& p, int len, int r) {
+  return p.causal ? min(len, len - p.n + r / p.G + 1) : len;
+}
+// The last row of a tile sees the most.
+template <int ROWS>
+__device__ __forceinline__ int tile_sees(const AttnParams& p, int len, int rt) {
+  return rows_see(p, len, min((rt + 1) * ROWS, p.n * p.G) - 1);
+}
+
+// The line of units: items (sequence, row tile) in order, each with the same units for every head,
+// cut into f.ctas stretches that differ by one unit at most.  Built and asked by whole warps.
+template <int ROWS>
+struct Line {
+  int64_t total, each, longer;  // units; units of a stretch; stretches with one unit more
+  int64_t own, upto;            // this lane's item (of the first 32): its units, and all up to it
+  int items;
+  bool equal;
+
+  __device__ __forceinline__ int64_t weight(const AttnParams& p, const AttnPlan& f, int item) const {
+    if (item >= items) return 0;
+    const int b = item / f.row_tiles, rt = item - b * f.row_tiles;
+    return static_cast<int64_t>(p.heads) * units_of(tile_sees<ROWS>(p, length_of(p, b), rt), f.unit);
+  }
+  static __device__ __forceinline__ int64_t scan(int64_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
+  }
+  // sum of the weights of items [32, upto)
+  __device__ __forceinline__ int64_t sum_from_32(const AttnParams& p, const AttnPlan& f, int to) const {
+    int64_t sum = 0;
+    for (int k = 32 + (threadIdx.x & 31); k < to; k += 32) sum += weight(p, f, k);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    return sum;
+  }
+  __device__ __forceinline__ void build(const AttnParams& p, const AttnPlan& f) {
+    items = p.B * f.row_tiles;
+    equal = !p.lens && !p.causal;
+    own = weight(p, f, threadIdx.x & 31);
+    upto = scan(own);
+    total = __shfl_sync(kFull, upto, 31);
+    if (items > 32) total = equal ? weight(p, f, 0) * items : total + sum_from_32(p, f, items);
+    if (total >> 32)
+      each = total / f.ctas;
+    else
+      each = static_cast<uint32_t>(total) / static_cast<uint32_t>(f.ctas);
+    longer = total - each * f.ctas;
+  }
+  // first unit of CTA c's stretch
+  __device__ __forceinline__ int64_t start(int64_t c) const {
+    return each * c + (c < longer ? c : longer);
+  }
+  // CTA whose stretch holds unit u
+  __device__ __forceinline__ int64_t holder(int64_t u) const {
+    const int64_t head = longer * (each + 1);
+    return u < head ? u / (each + 1) : longer + (u - head) / each;
+  }
+  // item that holds unit `at` (< total), and the units before that item
+  __device__ __forceinline__ int find(const AttnParams& p, const AttnPlan& f, int64_t at,
+                                      int64_t* before) const {
+    const int lane = threadIdx.x & 31;
+    if (items > 32 && equal) {
+      const int64_t per = weight(p, f, 0);
+      *before = at / per * per;
+      return static_cast<int>(at / per);
+    }
+    int64_t base = 0, mine = own, incl = upto;
+    for (int i0 = 0;;) {
+      const unsigned hit = __ballot_sync(kFull, base + incl > at);
+      if (hit != 0u || i0 + 32 >= items) {
+        const int l = hit ? __ffs(hit) - 1 : 31;
+        *before = base + __shfl_sync(kFull, incl - mine, l);
+        return min(i0 + l, items - 1);
+      }
+      base += __shfl_sync(kFull, incl, 31);
+      i0 += 32;
+      mine = weight(p, f, i0 + lane);
+      incl = scan(mine);
+    }
+  }
+  // units before an item
+  __device__ __forceinline__ int64_t before(const AttnParams& p, const AttnPlan& f, int item) const {
+    if (item < 32) return __shfl_sync(kFull, upto - own, item);
+    if (equal) return weight(p, f, 0) * item;
+    return sum_from_32(p, f, item) + __shfl_sync(kFull, upto, 31);
+  }
+};
+
+// Where a CTA is on the line: a segment and the unit in it.
+template <int ROWS>
+struct Segment {
+  int item, b, rt, h;
+  int len;    // of the sequence
+  int seen;   // entries the tile's last row sees
+  int units;  // of the segment
+  int k0;     // first unit to do
+
+  __device__ __forceinline__ void at_item(const AttnParams& p, const AttnPlan& f) {
+    b = item / f.row_tiles;
+    rt = item - b * f.row_tiles;
+    len = length_of(p, b);
+    seen = tile_sees<ROWS>(p, len, rt);
+    units = units_of(seen, f.unit);
+  }
+  __device__ __forceinline__ void find(const AttnParams& p, const AttnPlan& f, const Line<ROWS>& line,
+                                       int64_t u) {
+    int64_t before;
+    item = line.find(p, f, u, &before);
+    at_item(p, f);
+    const int64_t in = u - before;
+    h = static_cast<int>(in >> 32 ? in / units
+                                  : static_cast<uint32_t>(in) / static_cast<uint32_t>(units));
+    k0 = static_cast<int>(in - static_cast<int64_t>(h) * units);
+  }
+  __device__ __forceinline__ void next(const AttnParams& p, const AttnPlan& f) {
+    k0 = 0;
+    if (++h == p.heads) {
+      h = 0;
+      ++item;
+      at_item(p, f);
+    }
+  }
+};
+
+constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = 32 * kJoinWarps;
+
+// Join the parts of the segments that several CTAs share, in order of their entries:
+//   out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
+// One CTA per row of a segment; each warp takes every fourth part.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads)
+    attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
+  constexpr int V = D / 64;
+  __shared__ float2 acc_s[kJoinWarps][D / 2];
+  __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = p.n * p.G;
+  const int r = blockIdx.x % rows;
+  const int h = blockIdx.x / rows % p.heads, b = blockIdx.x / rows / p.heads;
+  pdl_wait();
+  pdl_trigger();
+  const int rt = r / ROWS;
+  const int units = units_of(tile_sees<ROWS>(p, length_of(p, b), rt), f.unit);
+  if (units == 1) return;
+  Line<ROWS> line;
+  line.build(p, f);
+  const int64_t first = line.before(p, f, b * f.row_tiles + rt) + static_cast<int64_t>(h) * units;
+  const int64_t c0 = line.holder(first), c1 = line.holder(first + units - 1);
+  if (c0 == c1) return;  // written by its one CTA
+  // a CTA's part: its first one unless its stretch began in a segment before
+  auto part_of = [&](int64_t c) { return 2 * c + (line.start(c) >= first ? 0 : 1); };
+  float mx = -INFINITY;
+  for (int64_t c = c0 + threadIdx.x; c <= c1; c += kJoinThreads) {
+    mx = fmaxf(mx, f.part_ml[part_of(c) * ROWS + r % ROWS].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+  if (lane == 0) max_s[warp] = mx;
+  __syncthreads();
+  mx = max_s[0];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
+  float2 acc[V] = {};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps) {
+    const int64_t part = part_of(c);
+    const float2 v = f.part_ml[part * ROWS + r % ROWS];
+    const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
+    sum = fmaf(v.y, keep, sum);
+    const float* src = f.part_o + (part * ROWS + r % ROWS) * D;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float2 x = *reinterpret_cast<const float2*>(src + 64 * k + 2 * lane);
+      acc[k].x = fmaf(x.x, keep, acc[k].x);
+      acc[k].y = fmaf(x.y, keep, acc[k].y);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc_s[warp][32 * k + lane] = acc[k];
+  if (lane == 0) sum_s[warp] = sum;
+  __syncthreads();
+  sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int e = threadIdx.x; e < D / 2; e += kJoinThreads) {
+    float2 a = acc_s[0][e];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+      a.x += acc_s[w][e].x;
+      a.y += acc_s[w][e].y;
+    }
+    const uint32_t w = bf2_pack(a.x * inv, a.y * inv);
+    uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + 2 * e;
+    dst[0] = static_cast<uint16_t>(w);
+    dst[1] = static_cast<uint16_t>(w >> 16);
+  }
+  if (p.lse && threadIdx.x == 0)
+    p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
+        sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+template <int D, int ROWS>
+cudaError_t launch_join(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.B) * p.heads * p.n * p.G;
+  return launch_dependent(attention_join_kernel<D, ROWS>, dim3(static_cast<unsigned>(rows)),
+                          dim3(kJoinThreads), 0, stream, p, f);
+}
+
+}  // namespace
+}  // namespace dllm

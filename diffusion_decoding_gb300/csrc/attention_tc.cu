@@ -1,0 +1,525 @@
+// Attention over the 4-bit cache for many query rows per cache head (blocks, pieces of prompts), on
+// the 5th-generation tensor cores.
+//
+// A row tile is 128 rows; entries are taken 64 at a time:
+//   S [128 x 64] = Q K^T,   O [128 x D] += P V     (tcgen05.mma, fp32 accumulators in TMEM)
+// Q and P are left operands in TMEM, so shared memory only carries K and V: per 64 entries and
+// D = 128 it is written and read 32 KB each, as many cycles as the two products take.  TMEM columns:
+// Q [0, D/2), S [D/2, D/2 + 64) with P over it, O at 128: 256 columns, so that two CTAs share an SM
+// and one's products run while the other is in its softmax.
+//
+// Warps 0-3, one thread per row: softmax (no shuffles), the rescaling of O when the reference moves
+// (rarely: attention.cu's kSlack), and the output.  Warps 4-7: codes to bf16, into a ring of K/V
+// stages in the 128-byte swizzled layout; a lane turns 32 channels (one group) of one entry, eight
+// lanes of the same group store to eight different bank groups.  Warp 8: one thread issues the
+// products; each stage's release and each score tile's arrival are tcgen05.commit's.
+// The eight channels of a code word come out as pairs (j, j + 4): Q's channels are put in the same
+// order (the scores do not depend on it), and the output's are put back.
+#include "attention.h"
+#include "attention_line.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "mbarrier.cuh"
+#include "vec_math.cuh"
+
+namespace dllm {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTile = 64;  // entries of a step
+constexpr int kStages = 3;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 2;
+constexpr int kTmemCols = 256;
+constexpr int kOCol = 128;
+constexpr float kSlack = 8.f;  // as in attention.cu
+
+// ---- tcgen05, one CTA
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// D [128 x N] (+)= A [128 x 16] B [16 x N], A in TMEM, B in shared memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` once every tcgen05.mma issued so far by this thread has completed.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory descriptors, 128-byte swizzle: rows of 128 bytes (64 channels of one entry), the
+// 16-byte piece c of row i at i * 128 + ((c ^ (i & 7)) * 16), 8-row groups 1024 bytes apart, 64
+// channels further 64 rows on.  K is K-major (the product runs over the channels of a row); V is
+// MN-major (it runs over the rows): its leading offset steps to the next 64 channels.
+__device__ __forceinline__ uint64_t sw128(uint32_t saddr, uint32_t leading) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(leading >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
+         static_cast<uint64_t>(2) << 61;
+}
+// D fp32, A and B bf16, M = 128; b_mn: B is MN-major
+__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <int D>
+struct Smem {
+  static constexpr uint32_t kTensor = kTile * D * 2;  // K (or V) of a stage
+  static constexpr uint32_t kStage = 2 * kTensor;
+  static constexpr size_t kBytes = kStages * kStage + 1024;  // and room to align
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    attention_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
+  using M = Smem<D>;
+  constexpr int SLABS = D / 64;
+  constexpr uint32_t SLAB = kTile * 128;
+  extern __shared__ uint8_t dyn[];
+  __shared__ uint64_t bars[2 * kStages + 4];
+  __shared__ uint32_t visible[kStages][2];  // of the stage's 64 entries: bit per entry
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kStages]);
+  const uint32_t q_bar = smem_u32(&bars[2 * kStages]);  // Q is in TMEM, O may be overwritten
+  const uint32_t s_bar = smem_u32(&bars[2 * kStages + 1]);
+  const uint32_t p_bar = smem_u32(&bars[2 * kStages + 2]);
+  const uint32_t o_bar = smem_u32(&bars[2 * kStages + 3]);
+
+  // nothing of this CTA, its tensor memory included, is taken before the kernels it depends on are
+  // done: one of them may be waiting for tensor memory
+  pdl_wait();
+  pdl_trigger();
+  Line<kRows> line;
+  line.build(p, f);
+  const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
+  if (u0 >= u1) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 4);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(q_bar, 4);
+    mbar_init(s_bar, 1);
+    mbar_init(p_bar, 4);
+    mbar_init(o_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_v = &abort_flag;
+  const int rows = p.n * p.G;
+
+  Segment<kRows> sg;
+  sg.find(p, f, line, u0);
+  int step = 0;   // K/V tiles so far: stage step % kStages
+  int piece_no = 0, o_no = 0;  // segments so far, and those with tiles
+  for (int64_t u = u0; u < u1; ++piece_no) {
+    const int piece = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), u1 - u));
+    const int j0 = sg.k0 * f.unit;
+    const int end = min(sg.seen, j0 + piece * f.unit);
+    const int tiles = end > j0 ? (end - j0 + kTile - 1) / kTile : 0;
+    const int b = sg.b, h = sg.h;
+
+    if (warp < 4) {
+      // ---------------------------------------------------------------- softmax, one row a thread
+      const bool issuer = threadIdx.x == 0;
+      // scores of tile k (counted over all segments) once its K is there
+      auto scores = [&](int k) {
+        const int st = k % kStages;
+        if (!wait_bar(full0 + 8 * st, (k / kStages) & 1, abort_v, f.status)) return;
+        tc_after();
+        const uint32_t sk = sbase + st * M::kStage;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma_ts(tmem + D / 2, tmem + x * 8, sw128(sk + (x >> 2) * SLAB + (x & 3) * 32, 16),
+                 idesc(kTile, false), x > 0);
+        mma_commit(s_bar);
+      };
+      // the weights of tile k times its V, once all rows' weights are there
+      auto values = [&](int k, bool first) {
+        const int st = k % kStages;
+        if (!wait_bar(p_bar, k & 1, abort_v, f.status)) return;
+        tc_after();
+        const uint32_t sv = sbase + st * M::kStage + M::kTensor;
+#pragma unroll
+        for (int x = 0; x < kTile / 16; ++x)
+          mma_ts(tmem + kOCol, tmem + D / 2 + x * 8, sw128(sv + x * 2048, SLABS > 1 ? SLAB : 16),
+                 idesc(D, true), !first || x > 0);
+        mma_commit(empty0 + 8 * st);
+      };
+      const int r = sg.rt * kRows + threadIdx.x;
+      const int i = r / p.G, hq = h * p.G + r - i * p.G;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      const uint32_t t_s = lanes + D / 2, t_o = lanes + kOCol;
+      const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+      {
+        const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const uint32_t q_keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
+        const uint16_t* src = p.q + b * p.qb + i * p.qt + hq * p.qh;
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t x[4] = {0u, 0u, 0u, 0u};
+            if (r < rows) {
+              const uint16_t* s8 = src + half * 64 + k * 8;
+              if (f.q_aligned) {
+                const uint4 v = *reinterpret_cast<const uint4*>(s8);
+                x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  x[e] = s8[2 * e] | static_cast<uint32_t>(s8[2 * e + 1]) << 16;
+              }
+            }
+            // a negative scale turns the sign of Q, one of zero makes Q zero: both exact
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = (x[e] ^ q_flip) & q_keep;
+            w[4 * k] = __byte_perm(x[0], x[2], 0x5410);
+            w[4 * k + 1] = __byte_perm(x[0], x[2], 0x7632);
+            w[4 * k + 2] = __byte_perm(x[1], x[3], 0x5410);
+            w[4 * k + 3] = __byte_perm(x[1], x[3], 0x7632);
+          }
+          tmem_st32(lanes + half * 32, w);
+        }
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_bar);
+        // every phase of q_bar is waited for, of segments without tiles too
+        if (issuer && wait_bar(q_bar, piece_no & 1, abort_v, f.status) && tiles > 0) scores(step);
+        __syncwarp();
+      }
+      const int bound = rows_see(p, sg.len, r);                    // entries this row sees
+      const int all_see = rows_see(p, sg.len, sg.rt * kRows);      // what every row of the tile sees
+      float m = -INFINITY;
+      float l = 0.f;
+      bool ok = true;
+      for (int t = 0; t < tiles; ++t) {
+        const int k = step + t, st = k % kStages;
+        // the mask words of the stage, and the scores
+        ok = ok && wait_bar(full0 + 8 * st, (k / kStages) & 1, abort_v, f.status);
+        ok = __all_sync(kFull, ok && wait_bar(s_bar, k & 1, abort_v, f.status));
+        if (!ok) break;
+        tc_after();
+        float s[kTile];
+        tmem_ld32(t_s, s);
+        tmem_ld32(t_s + 32, s + 32);
+        const uint32_t vis0 = visible[st][0], vis1 = visible[st][1];
+        tmem_wait_ld();
+        const int j = j0 + t * kTile;
+        if ((vis0 & vis1) != 0xffffffffu || j + kTile > all_see) {
+          const int left = bound - j;  // entries of the tile below the bound
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) {
+            const bool v = ((e < 32 ? vis0 : vis1) >> (e & 31) & 1u) && e < left;
+            s[e] = v ? s[e] : -INFINITY;
+          }
+        }
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < kTile; ++e) top = fmaxf(top, s[e]);
+        top *= scale;
+        const bool above = top > m + kSlack;
+        if (__any_sync(kFull, above)) {
+          const float mn = fmaxf(m, top);
+          const float keep = mn == -INFINITY ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= keep;
+          if (t > 0) {
+            // the product before has been added to O: S came after it on the same pipe
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(t_o + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= keep;
+              tmem_st32(t_o + c, reinterpret_cast<uint32_t*>(o));
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint32_t pk[kTile / 2];
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < kTile; e += 2) {
+          const float a = ex2(fmaf(s[e], scale, -mu));
+          const float d = ex2(fmaf(s[e + 1], scale, -mu));
+          sum0 += a;
+          sum1 += d;
+          pk[e / 2] = bf2_pack(a, d);
+        }
+        l += sum0 + sum1;
+        tmem_st32(t_s, pk);
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_bar);
+        if (issuer) {
+          values(k, t == 0);
+          // the next scores overwrite P: they follow the product that reads it on the same pipe
+          if (t + 1 < tiles)
+            scores(k + 1);
+          else
+            mma_commit(o_bar);
+        }
+        __syncwarp();
+      }
+      // ---- output
+      if (tiles > 0 && ok) ok = __all_sync(kFull, wait_bar(o_bar, o_no & 1, abort_v, f.status));
+      tc_after();
+      if (ok) {
+        const bool direct = piece == sg.units;
+        const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = part * kRows + threadIdx.x;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (tiles > 0) {
+            tmem_ld32(t_o + c, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          // channels back in order: the word holds 0, 4, 1, 5, 2, 6, 3, 7
+          if (r < rows && !direct) {
+            float4* dst = reinterpret_cast<float4*>(f.part_o + at * D + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              dst[2 * k] = make_float4(o[8 * k], o[8 * k + 2], o[8 * k + 4], o[8 * k + 6]);
+              dst[2 * k + 1] = make_float4(o[8 * k + 1], o[8 * k + 3], o[8 * k + 5], o[8 * k + 7]);
+            }
+          } else if (r < rows) {
+            uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 v = make_uint4(bf2_pack(o[8 * k] * inv, o[8 * k + 2] * inv),
+                                         bf2_pack(o[8 * k + 4] * inv, o[8 * k + 6] * inv),
+                                         bf2_pack(o[8 * k + 1] * inv, o[8 * k + 3] * inv),
+                                         bf2_pack(o[8 * k + 5] * inv, o[8 * k + 7] * inv));
+              if (f.out_aligned) {
+                *reinterpret_cast<uint4*>(dst + 8 * k) = v;
+              } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  dst[8 * k + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (r < rows) {
+          if (!direct)
+            f.part_ml[at] = make_float2(m, l);
+          else if (p.lse)
+            p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
+                l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+      }
+      tc_before();  // O and Q are read before the next segment's arrive on q_bar
+    } else {
+      // ---------------------------------------------------------------- codes to bf16
+      // lanes 8q .. 8q + 7 take group q (and q + 4, ...) of entries 8w .. 8w + 7 and, 32 further, of
+      // the same again
+      constexpr int GROUPS = D / 32;             // per entry
+      constexpr int PER = 2 * GROUPS / 4;        // pieces of K a thread turns per tile
+      const int w = warp - 4, q4 = lane >> 3, t8 = lane & 7;
+      const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
+      const uint8_t* mask = p.key_mask ? p.key_mask + b * p.mask_stride : nullptr;
+      // piece e of the thread: entry and group
+      auto entry_of = [&](int e) { return GROUPS == 4 ? w * 8 + t8 + 32 * e : w * 8 + t8 + 32 * (q4 >> 1); };
+      auto group_of = [&](int e) { return GROUPS == 4 ? q4 : q4 & 1; };
+      struct Raw {
+        uint4 k[PER], v[PER];
+        uint32_t kp[PER], vp[PER];
+        bool seen[PER];
+      };
+      auto load = [&](Raw& raw, int t) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int j = j0 + t * kTile + entry_of(e);
+          const int pg = t < tiles && j < end ? kv4_page(table, p.table_stride, p.pages, p.page_size, j) : -1;
+          raw.seen[e] = pg >= 0 && (!mask || __ldg(mask + j) != 0);
+          raw.k[e] = raw.v[e] = make_uint4(0u, 0u, 0u, 0u);
+          raw.kp[e] = raw.vp[e] = 0u;
+          if (pg >= 0) {
+            const int64_t row = (static_cast<int64_t>(pg) * p.heads + h) * p.page_size + j % p.page_size;
+            const int g = group_of(e);
+            raw.k[e] = ld_stream_v4(p.k_codes + row * (D / 2) + g * 16);
+            raw.v[e] = ld_stream_v4(p.v_codes + row * (D / 2) + g * 16);
+            raw.kp[e] = __ldg(p.k_params + row * (D / 32) + g);
+            raw.vp[e] = __ldg(p.v_params + row * (D / 32) + g);
+          }
+        }
+      };
+      auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst, int entry, int g) {
+        const Kv4Scale sc = kv4_scale(__byte_perm(param, param, 0x1010));
+        const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
+        const uint32_t row = dst + (g >> 1) * SLAB + entry * 128;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t a = kv4_pair<0>(word[x], sc), c = kv4_pair<1>(word[x], sc),
+                         d = kv4_pair<2>(word[x], sc), z = kv4_pair<3>(word[x], sc);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                           row + ((((g & 1) * 4 + x) ^ (entry & 7)) << 4)),
+                       "r"(a), "r"(c), "r"(d), "r"(z)
+                       : "memory");
+        }
+      };
+      Raw raw;
+      load(raw, 0);
+      bool ok = true;
+      for (int t = 0; t < tiles; ++t) {
+        const int k = step + t, st = k % kStages;
+        Raw cur = raw;
+        load(raw, t + 1);
+        ok = __all_sync(kFull, wait_bar(empty0 + 8 * st, ((k / kStages) & 1) ^ 1, abort_v, f.status));
+        if (!ok) break;
+        const uint32_t sk = sbase + st * M::kStage, sv = sk + M::kTensor;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          turn(cur.k[e], cur.kp[e], sk, entry_of(e), group_of(e));
+          // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
+          turn(cur.v[e], cur.seen[e] ? cur.vp[e] : 0u, sv, entry_of(e), group_of(e));
+        }
+        // entries 8w .. 8w + 7 of each half of the tile
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          unsigned bits;
+          if constexpr (GROUPS == 4)
+            bits = __ballot_sync(kFull, cur.seen[e % PER]) & 0xffu;
+          else
+            bits = __ballot_sync(kFull, cur.seen[0]) >> (16 * e) & 0xffu;
+          if (lane == 0) reinterpret_cast<uint8_t*>(&visible[st][e])[w] = static_cast<uint8_t>(bits);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full0 + 8 * st);
+      }
+    }
+    step += tiles;
+    o_no += tiles > 0;
+    u += piece;
+    if (u < u1) sg.next(p, f);
+  }
+
+  tc_before();
+  __syncthreads();
+  if (warp == 4) {
+    // every product has completed before the tensor memory goes away
+    if (lane == 0 && o_no > 0) drain_bar(o_bar, (o_no - 1) & 1);
+    __syncwarp();
+    tc_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+bool attention_tc_takes(int n, int G, int D) {
+  return (D == 64 || D == 128) && static_cast<int64_t>(n) * G > 32;
+}
+
+size_t attention_tc_ws_bytes(int D, int sm_count) {
+  const size_t parts = static_cast<size_t>(2) * sm_count * kCtasPerSm * kRows;
+  return kWsHeader + parts * D * 4 + parts * 8;
+}
+
+template <int D>
+static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaStream_t stream) {
+  AttnPlan f{};
+  f.unit = kTile;
+  f.row_tiles = (p.n * p.G + kRows - 1) / kRows;
+  f.ctas = sm_count * kCtasPerSm;
+  f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
+  f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
+  f.status = static_cast<int32_t*>(ws);
+  const size_t parts = static_cast<size_t>(2) * f.ctas * kRows;
+  f.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
+  f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + kWsHeader + parts * D * 4);
+  cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(Smem<D>::kBytes));
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(attention_tc_kernel<D>, dim3(f.ctas), dim3(kThreads), Smem<D>::kBytes, stream,
+                       p, f);
+  if (e != cudaSuccess || p.max_len <= f.unit) return e;
+  return launch_join<D, kRows>(p, f, stream);
+}
+
+cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
+                                cudaStream_t stream) {
+  return D == 64 ? launch_tc<64>(p, ws, sm_count, stream) : launch_tc<128>(p, ws, sm_count, stream);
+}
+
+}  // namespace dllm
