@@ -767,7 +767,8 @@ dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, cons
 size_t dllm_attention_kv4_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t n,
                                           int32_t q_heads, int32_t max_len) {
   if (check_attention(cache, B, n, q_heads, max_len) != DLLM_OK) return 0;
-  return dllm::attention_ws_bytes(n, q_heads / cache->heads, cache->head_dim, max_len, sm_count());
+  return dllm::attention_ws_bytes(B, n, q_heads / cache->heads, cache->heads, cache->head_dim,
+                                  max_len, sm_count());
 }
 
 dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
@@ -790,8 +791,8 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
                 static_cast<long long>(mask_stride), max_len);
   if (!aligned(lens, 4) || !aligned(lse, 4))
     return fail(DLLM_ERR_INVALID_ARG, "lens and lse must be 4-byte aligned");
-  const size_t need = dllm::attention_ws_bytes(n, q->heads / cache->heads, cache->head_dim, max_len,
-                                               sm_count());
+  const size_t need = dllm::attention_ws_bytes(B, n, q->heads / cache->heads, cache->heads,
+                                               cache->head_dim, max_len, sm_count());
   if (ws_bytes < need)
     return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed",
                 ws_bytes, need);

@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
     __syncthreads();
     const bool direct = piece == sg.units;
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
+    if (threadIdx.x == 0) note_segment(f, p, line, sg, u, u0, direct);
     for (int e = threadIdx.x; e < ROWS * (D / 2); e += kThreads) {
       const int r = e / (D / 2), ch = e - r * (D / 2);
       if (r0 + r >= rows) break;
@@ -531,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
 struct FewSizes {
   int nt, row_tiles, ctas, unit;
   bool split;  // some segment can have more than one unit
-  size_t off_ml, bytes;
+  size_t off_ml, off_parts, bytes;
 };
 
-FewSizes few_sizes(int n, int G, int D, int max_len, int sm_count) {
+FewSizes few_sizes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
   FewSizes s{};
   const int64_t rows = static_cast<int64_t>(n) * G;
   s.nt = rows > 8 && D <= 128 ? 2 : 1;
@@ -547,7 +548,8 @@ FewSizes few_sizes(int n, int G, int D, int max_len, int sm_count) {
   s.split = max_len > s.unit;
   const size_t parts = static_cast<size_t>(2) * s.ctas * 8 * s.nt;
   s.off_ml = kWsHeader + parts * D * 4;
-  s.bytes = s.off_ml + parts * 8;
+  s.off_parts = s.off_ml + parts * 8;
+  s.bytes = s.off_parts + static_cast<size_t>(B) * s.row_tiles * heads * 8;
   return s;
 }
 
@@ -562,7 +564,7 @@ cudaError_t launch_few(const AttnParams& p, const AttnPlan& f, bool split, cudaS
   e = launch_dependent(attention_few_kernel<D, NT>, dim3(f.ctas), dim3(kThreads), smem,
                                    stream, p, f);
   if (e != cudaSuccess || !split) return e;
-  return launch_join<D, 8 * NT>(p, f, stream);
+  return launch_join<D, 8 * NT, 1>(p, f, stream);
 }
 
 }  // namespace
@@ -572,14 +574,14 @@ bool attention_rows_aligned(const void* x, int64_t sb, int64_t st, int64_t sh) {
           static_cast<uintptr_t>(st * 2) | static_cast<uintptr_t>(sh * 2)) % 16 == 0;
 }
 
-size_t attention_ws_bytes(int n, int G, int D, int max_len, int sm_count) {
-  return attention_tc_takes(n, G, D) ? attention_tc_ws_bytes(D, sm_count)
-                                     : few_sizes(n, G, D, max_len, sm_count).bytes;
+size_t attention_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
+  return attention_tc_takes(n, G, D) ? attention_tc_ws_bytes(B, n, G, heads, D, sm_count)
+                                     : few_sizes(B, n, G, heads, D, max_len, sm_count).bytes;
 }
 
 cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream) {
   if (attention_tc_takes(p.n, p.G, D)) return launch_attention_tc(p, D, ws, sm_count, stream);
-  const FewSizes s = few_sizes(p.n, p.G, D, p.max_len, sm_count);
+  const FewSizes s = few_sizes(p.B, p.n, p.G, p.heads, D, p.max_len, sm_count);
   AttnPlan f{};
   f.row_tiles = s.row_tiles;
   f.ctas = s.ctas;
@@ -587,6 +589,7 @@ cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count,
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + s.off_ml);
+  f.parts = reinterpret_cast<int2*>(static_cast<char*>(ws) + s.off_parts);
   switch (D * 10 + s.nt) {
     case 641: return launch_few<64, 1>(p, f, s.split, stream);
     case 642: return launch_few<64, 2>(p, f, s.split, stream);

@@ -30,13 +30,13 @@ struct AttnParams {
   int B, n;
 };
 
-size_t attention_ws_bytes(int n, int G, int D, int max_len, int sm_count);
+size_t attention_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
 
 cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream);
 
 // Many rows per cache head (attention_tc.cu): head_dim 64 or 128.
 bool attention_tc_takes(int n, int G, int D);
-size_t attention_tc_ws_bytes(int D, int sm_count);
+size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count);
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream);
 

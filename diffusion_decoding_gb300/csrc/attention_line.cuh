@@ -5,7 +5,8 @@
 // cut into units.  All segments form one line of units, and CTA k of a single resident wave takes
 // the k-th equal stretch of it, whatever the lengths.  A segment inside one stretch is written
 // straight to the output; of the others each CTA leaves a partial result (at most two a CTA: the
-// segments its stretch begins and ends in), which attention_join_kernel adds in order.
+// segments its stretch begins and ends in), which attention_join_kernel adds in order; the CTA that
+// starts a segment notes where they are.
 #pragma once
 
 #include "attention.h"
@@ -21,6 +22,7 @@ struct AttnPlan {
   int out_aligned;  // output rows too
   float* part_o;    // [2 * CTAs, rows of a tile, D]
   float2* part_ml;  // [2 * CTAs, rows of a tile]: reference (base 2) and sum of weights
+  int2* parts;      // [segments]: see note_segment
   int ctas;
   int32_t* status;
 };
@@ -119,12 +121,6 @@ struct Line {
       incl = scan(mine);
     }
   }
-  // units before an item
-  __device__ __forceinline__ int64_t before(const AttnParams& p, const AttnPlan& f, int item) const {
-    if (item < 32) return __shfl_sync(kFull, upto - own, item);
-    if (equal) return weight(p, f, 0) * item;
-    return sum_from_32(p, f, item) + __shfl_sync(kFull, upto, 31);
-  }
 };
 
 // Where a CTA is on the line: a segment and the unit in it.
@@ -166,86 +162,131 @@ struct Segment {
 constexpr int kJoinWarps = 4;
 constexpr int kJoinThreads = 32 * kJoinWarps;
 
+// What the CTA that starts a segment leaves for the join: its part, and the last CTA that has one
+// (the CTAs between have theirs first in their stretches); {-1, 0} for a segment that is whole.
+template <int ROWS>
+__device__ __forceinline__ void note_segment(const AttnPlan& f, const AttnParams& p,
+                                             const Line<ROWS>& line, const Segment<ROWS>& sg,
+                                             int64_t u, int64_t u0, bool whole) {
+  if (sg.k0 != 0) return;
+  f.parts[static_cast<int64_t>(sg.item) * p.heads + sg.h] =
+      whole ? make_int2(-1, 0)
+            : make_int2(2 * static_cast<int>(blockIdx.x) + (u == u0 ? 0 : 1),
+                        static_cast<int>(line.holder(u + sg.units - 1)));
+}
+
+__device__ __forceinline__ void store_joined(const AttnParams& p, int b, int h, int r, int ch, float2 a,
+                                             float inv) {
+  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  const uint32_t w = bf2_pack(a.x * inv, a.y * inv);
+  uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + ch;
+  dst[0] = static_cast<uint16_t>(w);
+  dst[1] = static_cast<uint16_t>(w >> 16);
+}
+__device__ __forceinline__ void store_lse(const AttnParams& p, int b, int h, int r, float m, float sum) {
+  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  if (p.lse)
+    p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
+        sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
 // Join the parts of the segments that several CTAs share, in order of their entries:
 //   out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
-// One CTA per row of a segment; each warp takes every fourth part.
-template <int D, int ROWS>
+// RPC = 1: a CTA per row, each warp takes every fourth part (few rows, many parts).  Otherwise a
+// CTA takes RPC rows of a segment, a warp one row at a time (many rows, two or three parts).
+template <int D, int ROWS, int RPC>
 __global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
-  constexpr int V = D / 64;
+  constexpr int V = D / 64, GROUPS = ROWS / RPC;
   __shared__ float2 acc_s[kJoinWarps][D / 2];
   __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = p.n * p.G;
-  const int r = blockIdx.x % rows;
-  const int h = blockIdx.x / rows % p.heads, b = blockIdx.x / rows / p.heads;
   pdl_wait();
   pdl_trigger();
-  const int rt = r / ROWS;
-  const int units = units_of(tile_sees<ROWS>(p, length_of(p, b), rt), f.unit);
-  if (units == 1) return;
-  Line<ROWS> line;
-  line.build(p, f);
-  const int64_t first = line.before(p, f, b * f.row_tiles + rt) + static_cast<int64_t>(h) * units;
-  const int64_t c0 = line.holder(first), c1 = line.holder(first + units - 1);
-  if (c0 == c1) return;  // written by its one CTA
-  // a CTA's part: its first one unless its stretch began in a segment before
-  auto part_of = [&](int64_t c) { return 2 * c + (line.start(c) >= first ? 0 : 1); };
-  float mx = -INFINITY;
-  for (int64_t c = c0 + threadIdx.x; c <= c1; c += kJoinThreads) {
-    mx = fmaxf(mx, f.part_ml[part_of(c) * ROWS + r % ROWS].x);
-  }
+  const int64_t seg = blockIdx.x / GROUPS;
+  const int group = blockIdx.x % GROUPS;
+  const int2 info = f.parts[seg];
+  if (info.x < 0) return;
+  const int h = static_cast<int>(seg % p.heads), item = static_cast<int>(seg / p.heads);
+  const int b = item / f.row_tiles, rt = item - b * f.row_tiles;
+  const int c0 = info.x >> 1, count = info.y - c0 + 1;
+  auto part_of = [&](int k) { return static_cast<int64_t>(k == 0 ? info.x : 2 * (c0 + k)) * ROWS; };
+  const int r_last = min(ROWS, p.n * p.G - rt * ROWS);  // rows of this tile
+  if constexpr (RPC == 1) {
+    const int r = group;
+    if (r >= r_last) return;
+    float mx = -INFINITY;
+    for (int k = threadIdx.x; k < count; k += kJoinThreads) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-  if (lane == 0) max_s[warp] = mx;
-  __syncthreads();
-  mx = max_s[0];
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    if (lane == 0) max_s[warp] = mx;
+    __syncthreads();
+    mx = max_s[0];
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
-  float2 acc[V] = {};
-  float sum = 0.f;
+    for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
+    float2 acc[V] = {};
+    float sum = 0.f;
 #pragma unroll 4
-  for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps) {
-    const int64_t part = part_of(c);
-    const float2 v = f.part_ml[part * ROWS + r % ROWS];
-    const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
-    sum = fmaf(v.y, keep, sum);
-    const float* src = f.part_o + (part * ROWS + r % ROWS) * D;
+    for (int k = warp; k < count; k += kJoinWarps) {
+      const float2 v = f.part_ml[part_of(k) + r];
+      const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
+      sum = fmaf(v.y, keep, sum);
+      const float* src = f.part_o + (part_of(k) + r) * D;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float2 x = *reinterpret_cast<const float2*>(src + 64 * k + 2 * lane);
-      acc[k].x = fmaf(x.x, keep, acc[k].x);
-      acc[k].y = fmaf(x.y, keep, acc[k].y);
+      for (int x = 0; x < V; ++x) {
+        const float2 o = *reinterpret_cast<const float2*>(src + 64 * x + 2 * lane);
+        acc[x].x = fmaf(o.x, keep, acc[x].x);
+        acc[x].y = fmaf(o.y, keep, acc[x].y);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc_s[warp][32 * x + lane] = acc[x];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int e = threadIdx.x; e < D / 2; e += kJoinThreads) {
+      float2 a = acc_s[0][e];
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) {
+        a.x += acc_s[w][e].x;
+        a.y += acc_s[w][e].y;
+      }
+      store_joined(p, b, h, rt * ROWS + r, 2 * e, a, inv);
+    }
+    if (threadIdx.x == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
+  } else {
+    const int r_end = min(r_last, (group + 1) * RPC);
+    for (int r = group * RPC + warp; r < r_end; r += kJoinWarps) {
+      float mx = -INFINITY;
+      for (int k = 0; k < count; ++k) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
+      float2 acc[V] = {};
+      float sum = 0.f;
+      for (int k = 0; k < count; ++k) {
+        const float2 v = f.part_ml[part_of(k) + r];
+        const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
+        sum = fmaf(v.y, keep, sum);
+        const float* src = f.part_o + (part_of(k) + r) * D;
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          const float2 o = *reinterpret_cast<const float2*>(src + 64 * x + 2 * lane);
+          acc[x].x = fmaf(o.x, keep, acc[x].x);
+          acc[x].y = fmaf(o.y, keep, acc[x].y);
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int x = 0; x < V; ++x)
+        store_joined(p, b, h, rt * ROWS + r, 64 * x + 2 * lane, acc[x], inv);
+      if (lane == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
     }
   }
-#pragma unroll
-  for (int k = 0; k < V; ++k) acc_s[warp][32 * k + lane] = acc[k];
-  if (lane == 0) sum_s[warp] = sum;
-  __syncthreads();
-  sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
-  const int i = r / p.G, hq = h * p.G + r - i * p.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int e = threadIdx.x; e < D / 2; e += kJoinThreads) {
-    float2 a = acc_s[0][e];
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
-      a.x += acc_s[w][e].x;
-      a.y += acc_s[w][e].y;
-    }
-    const uint32_t w = bf2_pack(a.x * inv, a.y * inv);
-    uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + 2 * e;
-    dst[0] = static_cast<uint16_t>(w);
-    dst[1] = static_cast<uint16_t>(w >> 16);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
-        sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, int RPC>
 cudaError_t launch_join(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.B) * p.heads * p.n * p.G;
-  return launch_dependent(attention_join_kernel<D, ROWS>, dim3(static_cast<unsigned>(rows)),
+  const int64_t blocks = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (ROWS / RPC);
+  return launch_dependent(attention_join_kernel<D, ROWS, RPC>, dim3(static_cast<unsigned>(blocks)),
                           dim3(kJoinThreads), 0, stream, p, f);
 }
 

@@ -1,20 +1,23 @@
 // Attention over the 4-bit cache for many query rows per cache head (blocks, pieces of prompts), on
 // the 5th-generation tensor cores.
 //
-// A row tile is 128 rows; entries are taken 64 at a time:
-//   S [128 x 64] = Q K^T,   O [128 x D] += P V     (tcgen05.mma, fp32 accumulators in TMEM)
-// Q and P are left operands in TMEM, so shared memory only carries K and V: per 64 entries and
-// D = 128 it is written and read 32 KB each, as many cycles as the two products take.  TMEM columns:
-// Q [0, D/2), S [D/2, D/2 + 64) with P over it, O at 128: 256 columns, so that two CTAs share an SM
-// and one's products run while the other is in its softmax.
+// Entries are taken 64 at a time:
+//   S [128 rows x 64] = Q K^T,   O [128 x D] += P V     (tcgen05.mma, fp32 accumulators in TMEM)
+// Q and P are left operands in TMEM, so shared memory only carries K and V.  Two groups of four
+// warps each hold 128 rows, one row a thread, and run in turn: the products of one fill the tensor
+// cores while the other is in its softmax.  With more than 128 rows in a segment (kShare) the
+// groups are the two halves of a 256-row tile and use every K/V stage both; otherwise they hold
+// the same rows, take the stages in turn, and add up at the end.
 //
-// Warps 0-3, one thread per row: softmax (no shuffles), the rescaling of O when the reference moves
-// (rarely: attention.cu's kSlack), and the output.  Warps 4-7: codes to bf16, into a ring of K/V
-// stages in the 128-byte swizzled layout; a lane turns 32 channels (one group) of one entry, eight
-// lanes of the same group store to eight different bank groups.  Warp 8: one thread issues the
-// products; each stage's release and each score tile's arrival are tcgen05.commit's.
+// Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
+// attention.cu's kSlack), and the output; the first thread of each group issues its products.
+// Warps 8-15: codes to bf16, into a ring of K/V stages in the 128-byte swizzled layout, each half
+// every second stage; a lane turns 32 channels (one group) of an entry, and eight lanes of the same
+// group store to eight different bank groups.
 // The eight channels of a code word come out as pairs (j, j + 4): Q's channels are put in the same
 // order (the scores do not depend on it), and the output's are put back.
+//
+// TMEM columns of group g: Q at 64 g, S with P over it at 128 + 64 g, O at 256 + 128 g.
 #include "attention.h"
 #include "attention_line.cuh"
 #include "common.cuh"
@@ -28,11 +31,9 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kTile = 64;  // entries of a step
-constexpr int kStages = 3;
-constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 2;
-constexpr int kTmemCols = 256;
-constexpr int kOCol = 128;
+constexpr int kStages = 6;
+constexpr int kThreads = 512;
+constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;  // as in attention.cu
 
 // ---- tcgen05, one CTA
@@ -125,31 +126,33 @@ struct Smem {
   static constexpr size_t kBytes = kStages * kStage + 1024;  // and room to align
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int D, bool kShare>
+__global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
   using M = Smem<D>;
+  constexpr int ROWS = kShare ? 2 * kRows : kRows;
   constexpr int SLABS = D / 64;
   constexpr uint32_t SLAB = kTile * 128;
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t bars[2 * kStages + 4];
-  __shared__ uint32_t visible[kStages][2];  // of the stage's 64 entries: bit per entry
+  __shared__ uint64_t bars[2 * kStages + 9];
+  __shared__ uint32_t visible[kStages][2];  // of the stage's 64 entries: a bit per entry
+  __shared__ float2 ml_s[2][kRows];         // groups with the same rows: reference and sum
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
   const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kStages]);
-  const uint32_t q_bar = smem_u32(&bars[2 * kStages]);  // Q is in TMEM, O may be overwritten
-  const uint32_t s_bar = smem_u32(&bars[2 * kStages + 1]);
-  const uint32_t p_bar = smem_u32(&bars[2 * kStages + 2]);
-  const uint32_t o_bar = smem_u32(&bars[2 * kStages + 3]);
+  const uint32_t gbars = smem_u32(&bars[2 * kStages]);  // of group g at + 32 g:
+  constexpr uint32_t kQ = 0, kS = 8, kP = 16, kO = 24;  // Q there and O free; S; P; O complete
+
+  const uint32_t done_bar = gbars + 64;
 
   // nothing of this CTA, its tensor memory included, is taken before the kernels it depends on are
   // done: one of them may be waiting for tensor memory
   pdl_wait();
   pdl_trigger();
-  Line<kRows> line;
+  Line<ROWS> line;
   line.build(p, f);
   const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
   if (u0 >= u1) return;
@@ -157,16 +160,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full0 + 8 * s, 4);
-      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, kShare ? 2 : 1);
     }
-    mbar_init(q_bar, 4);
-    mbar_init(s_bar, 1);
-    mbar_init(p_bar, 4);
-    mbar_init(o_bar, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(gbars + 32 * g + kQ, kShare ? 4 : 8);
+      mbar_init(gbars + 32 * g + kS, 1);
+      mbar_init(gbars + 32 * g + kP, 4);
+      mbar_init(gbars + 32 * g + kO, 1);
+    }
+    mbar_init(done_bar, 2);
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 4) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+  if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   tc_before();
   __syncthreads();
   tc_after();
@@ -174,20 +180,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   volatile int* abort_v = &abort_flag;
   const int rows = p.n * p.G;
 
-  Segment<kRows> sg;
+  Segment<ROWS> sg;
   sg.find(p, f, line, u0);
-  int step = 0;   // K/V tiles so far: stage step % kStages
-  int piece_no = 0, o_no = 0;  // segments so far, and those with tiles
+  int step = 0;      // K/V tiles so far: tile k is in stage k % kStages
+  int piece_no = 0;  // segments so far
+  int mine = 0;      // tiles of this group so far
+  int o_no = 0;      // segments so far with tiles (phases of kO)
   for (int64_t u = u0; u < u1; ++piece_no) {
     const int piece = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), u1 - u));
     const int j0 = sg.k0 * f.unit;
     const int end = min(sg.seen, j0 + piece * f.unit);
     const int tiles = end > j0 ? (end - j0 + kTile - 1) / kTile : 0;
     const int b = sg.b, h = sg.h;
+    constexpr int STRIDE = kShare ? 1 : 2;  // tiles from one of a group to its next
 
-    if (warp < 4) {
+    if (warp < 8) {
       // ---------------------------------------------------------------- softmax, one row a thread
-      const bool issuer = threadIdx.x == 0;
+      const int grp = warp >> 2, row_in = threadIdx.x & (kRows - 1);
+      const bool issuer = row_in == 0;
+      const uint32_t bar = gbars + 32 * grp;
+      const uint32_t c_q = 64 * grp, c_s = 128 + 64 * grp, c_o = 256 + 128 * grp;
+      const int first = kShare ? 0 : (grp ^ step) & 1;  // this group's first tile of the segment
+      const int count = tiles > first ? (tiles - first + STRIDE - 1) / STRIDE : 0;
       // scores of tile k (counted over all segments) once its K is there
       auto scores = [&](int k) {
         const int st = k % kStages;
@@ -196,28 +210,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const uint32_t sk = sbase + st * M::kStage;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
-          mma_ts(tmem + D / 2, tmem + x * 8, sw128(sk + (x >> 2) * SLAB + (x & 3) * 32, 16),
+          mma_ts(tmem + c_s, tmem + c_q + x * 8, sw128(sk + (x >> 2) * SLAB + (x & 3) * 32, 16),
                  idesc(kTile, false), x > 0);
-        mma_commit(s_bar);
+        mma_commit(bar + kS);
       };
-      // the weights of tile k times its V, once all rows' weights are there
-      auto values = [&](int k, bool first) {
+      // the weights of tile k, the group's n-th, times its V, once all rows' weights are there
+      auto values = [&](int k, int n, bool start) {
         const int st = k % kStages;
-        if (!wait_bar(p_bar, k & 1, abort_v, f.status)) return;
+        if (!wait_bar(bar + kP, n & 1, abort_v, f.status)) return;
         tc_after();
         const uint32_t sv = sbase + st * M::kStage + M::kTensor;
 #pragma unroll
         for (int x = 0; x < kTile / 16; ++x)
-          mma_ts(tmem + kOCol, tmem + D / 2 + x * 8, sw128(sv + x * 2048, SLABS > 1 ? SLAB : 16),
-                 idesc(D, true), !first || x > 0);
+          mma_ts(tmem + c_o, tmem + c_s + x * 8, sw128(sv + x * 2048, SLABS > 1 ? SLAB : 16),
+                 idesc(D, true), !start || x > 0);
         mma_commit(empty0 + 8 * st);
       };
-      const int r = sg.rt * kRows + threadIdx.x;
+      const int r = sg.rt * ROWS + (kShare ? grp * kRows : 0) + row_in;
       const int i = r / p.G, hq = h * p.G + r - i * p.G;
-      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      const uint32_t t_s = lanes + D / 2, t_o = lanes + kOCol;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t t_s = lanes + c_s, t_o = lanes + c_o;
       const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+      if (threadIdx.x == 0) note_segment(f, p, line, sg, u, u0, piece == sg.units);
       {
+        // a negative scale turns the sign of Q, one of zero makes Q zero: both exact
         const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const uint32_t q_keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
         const uint16_t* src = p.q + b * p.qb + i * p.qt + hq * p.qh;
@@ -238,7 +254,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                   x[e] = s8[2 * e] | static_cast<uint32_t>(s8[2 * e + 1]) << 16;
               }
             }
-            // a negative scale turns the sign of Q, one of zero makes Q zero: both exact
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = (x[e] ^ q_flip) & q_keep;
             w[4 * k] = __byte_perm(x[0], x[2], 0x5410);
@@ -246,26 +261,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             w[4 * k + 2] = __byte_perm(x[1], x[3], 0x5410);
             w[4 * k + 3] = __byte_perm(x[1], x[3], 0x7632);
           }
-          tmem_st32(lanes + half * 32, w);
+          tmem_st32(lanes + c_q + half * 32, w);
         }
         tmem_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_bar);
-        // every phase of q_bar is waited for, of segments without tiles too
-        if (issuer && wait_bar(q_bar, piece_no & 1, abort_v, f.status) && tiles > 0) scores(step);
+        if (lane == 0) {
+          mbar_arrive(bar + kQ);
+          // both groups read both accumulators of the segment before
+          if (!kShare) mbar_arrive(gbars + 32 * (grp ^ 1) + kQ);
+        }
+        // every phase of kQ is waited for, of segments without tiles too
+        if (issuer && wait_bar(bar + kQ, piece_no & 1, abort_v, f.status) && count > 0)
+          scores(step + first);
+        if (issuer && count == 0 && tiles > 0) mma_commit(bar + kO);  // kO has a phase all the same
         __syncwarp();
       }
-      const int bound = rows_see(p, sg.len, r);                    // entries this row sees
-      const int all_see = rows_see(p, sg.len, sg.rt * kRows);      // what every row of the tile sees
+      const int bound = rows_see(p, sg.len, r);                      // entries this row sees
+      const int all_see = rows_see(p, sg.len, r - row_in);           // what every row of the group sees
       float m = -INFINITY;
-      float l = 0.f;
+      uint64_t l2 = 0;  // two partial sums
       bool ok = true;
-      for (int t = 0; t < tiles; ++t) {
-        const int k = step + t, st = k % kStages;
+      for (int n = 0; n < count; ++n) {
+        const int t = first + n * STRIDE, k = step + t, st = k % kStages;
         // the mask words of the stage, and the scores
         ok = ok && wait_bar(full0 + 8 * st, (k / kStages) & 1, abort_v, f.status);
-        ok = __all_sync(kFull, ok && wait_bar(s_bar, k & 1, abort_v, f.status));
+        ok = __all_sync(kFull, ok && wait_bar(bar + kS, (mine + n) & 1, abort_v, f.status));
         if (!ok) break;
         tc_after();
         float s[kTile];
@@ -282,17 +303,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             s[e] = v ? s[e] : -INFINITY;
           }
         }
-        float top = s[0];
+        float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 1; e < kTile; ++e) top = fmaxf(top, s[e]);
-        top *= scale;
-        const bool above = top > m + kSlack;
-        if (__any_sync(kFull, above)) {
-          const float mn = fmaxf(m, top);
+        for (int e = 4; e < kTile; e += 8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            top[x] = e + 4 + x < kTile ? fmaxf(top[x], fmaxf(s[e + x], s[e + 4 + x]))
+                                       : fmaxf(top[x], s[e + x]);
+        }
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        if (__any_sync(kFull, mx > m + kSlack)) {
+          const float mn = fmaxf(m, mx);
           const float keep = mn == -INFINITY ? 1.f : ex2(m - mn);
           m = mn;
-          l *= keep;
-          if (t > 0) {
+          float la, lb;
+          unpack2(l2, la, lb);
+          l2 = pack2(la * keep, lb * keep);
+          if (n > 0) {
             // the product before has been added to O: S came after it on the same pipe
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -306,49 +333,82 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        uint32_t pk[kTile / 2];
-        float sum0 = 0.f, sum1 = 0.f;
+        const uint64_t scale2 = pack2(scale, scale), mu2 = pack2(-mu, -mu);
+        uint32_t* pk = reinterpret_cast<uint32_t*>(s);  // in place
 #pragma unroll
         for (int e = 0; e < kTile; e += 2) {
-          const float a = ex2(fmaf(s[e], scale, -mu));
-          const float d = ex2(fmaf(s[e + 1], scale, -mu));
-          sum0 += a;
-          sum1 += d;
+          float a, d;
+          unpack2(fma2(pack2(s[e], s[e + 1]), scale2, mu2), a, d);
+          a = ex2(a);
+          d = ex2(d);
+          l2 = add2(l2, pack2(a, d));
           pk[e / 2] = bf2_pack(a, d);
         }
-        l += sum0 + sum1;
         tmem_st32(t_s, pk);
         tmem_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_bar);
+        if (lane == 0) mbar_arrive(bar + kP);
         if (issuer) {
-          values(k, t == 0);
+          values(k, mine + n, n == 0);
           // the next scores overwrite P: they follow the product that reads it on the same pipe
-          if (t + 1 < tiles)
-            scores(k + 1);
+          if (n + 1 < count)
+            scores(k + STRIDE);
           else
-            mma_commit(o_bar);
+            mma_commit(bar + kO);
         }
         __syncwarp();
       }
-      // ---- output
-      if (tiles > 0 && ok) ok = __all_sync(kFull, wait_bar(o_bar, o_no & 1, abort_v, f.status));
+      float l, l_odd;
+      unpack2(l2, l, l_odd);
+      l += l_odd;
+      // ---- output.  Groups with the same rows: each takes half of the channels of both.
+      if constexpr (!kShare) {
+        ml_s[grp][row_in] = make_float2(m, l);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+      if (tiles > 0) {
+        ok = ok && wait_bar(bar + kO, o_no & 1, abort_v, f.status);
+        if (!kShare) ok = ok && wait_bar(gbars + 32 * (grp ^ 1) + kO, o_no & 1, abort_v, f.status);
+      }
+      ok = __all_sync(kFull, ok);
       tc_after();
       if (ok) {
         const bool direct = piece == sg.units;
         const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
+        const int64_t at = part * ROWS + (r - sg.rt * ROWS);
+        float keep0 = count > 0 ? 1.f : 0.f, keep1 = 0.f;  // this group's and the other's
+        if constexpr (!kShare) {
+          const float2 ml = ml_s[grp ^ 1][row_in];
+          const float mn = fmaxf(m, ml.x);
+          keep0 = m == -INFINITY ? 0.f : ex2(m - mn);
+          keep1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+          l = fmaf(l, keep0, ml.y * keep1);
+          m = mn;
+        }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = part * kRows + threadIdx.x;
+        constexpr int SPAN = kShare ? D : D / 2;
+        const int c0 = kShare ? 0 : grp * SPAN;
+        const uint32_t t_other = lanes + 256 + 128 * (grp ^ 1);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = c0; c < c0 + SPAN; c += 32) {
           float o[32];
-          if (tiles > 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          if (count > 0) {
             tmem_ld32(t_o + c, o);
             tmem_wait_ld();
-          } else {
+          }
+          if constexpr (!kShare) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
+            if (tiles > 0) {
+              float x[32];
+              tmem_ld32(t_other + c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
+            }
           }
           // channels back in order: the word holds 0, 4, 1, 5, 2, 6, 3, 7
           if (r < rows && !direct) {
@@ -378,79 +438,109 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
           __syncwarp();
         }
-        if (r < rows) {
+        if (r < rows && (kShare || grp == 0)) {
           if (!direct)
             f.part_ml[at] = make_float2(m, l);
-          else if (p.lse)
-            p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
-                l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          else
+            store_lse(p, b, h, r, m, l);
         }
       }
-      tc_before();  // O and Q are read before the next segment's arrive on q_bar
+      if constexpr (!kShare) asm volatile("bar.sync 1, 256;" ::: "memory");  // ml_s is read
+      tc_before();  // O and Q are read before the next segment's arrival on kQ
+      mine += count;
     } else {
       // ---------------------------------------------------------------- codes to bf16
       // lanes 8q .. 8q + 7 take group q (and q + 4, ...) of entries 8w .. 8w + 7 and, 32 further, of
-      // the same again
+      // the same again; this half of the warps every second tile
       constexpr int GROUPS = D / 32;             // per entry
       constexpr int PER = 2 * GROUPS / 4;        // pieces of K a thread turns per tile
-      const int w = warp - 4, q4 = lane >> 3, t8 = lane & 7;
+      constexpr int AHEAD = 2 * kTile;           // entries from one of its tiles to the next
+      const int half = (warp >> 2) & 1, w = warp & 3, q4 = lane >> 3, t8 = lane & 7;
       const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
       const uint8_t* mask = p.key_mask ? p.key_mask + b * p.mask_stride : nullptr;
       // piece e of the thread: entry and group
-      auto entry_of = [&](int e) { return GROUPS == 4 ? w * 8 + t8 + 32 * e : w * 8 + t8 + 32 * (q4 >> 1); };
-      auto group_of = [&](int e) { return GROUPS == 4 ? q4 : q4 & 1; };
+      const int entry0 = GROUPS == 4 ? w * 8 + t8 : w * 8 + t8 + 32 * (q4 >> 1);
+      const int g = GROUPS == 4 ? q4 : q4 & 1;
       struct Raw {
         uint4 k[PER], v[PER];
         uint32_t kp[PER], vp[PER];
         bool seen[PER];
       };
-      auto load = [&](Raw& raw, int t) {
+      const int t_first = (half ^ step) & 1;
+      // the walk through the pages: word of the table and slot of the entries to look at next
+      int j_at = j0 + t_first * kTile + entry0;
+      int word[PER] = {}, slot[PER] = {}, page[PER];
+      const int step_pages = AHEAD / p.page_size, step_slots = AHEAD % p.page_size;
+      auto look_up = [&](int e) {
+        page[e] = -1;
+        if (j_at + 32 * e < end && word[e] < p.table_stride) {
+          const int pg = __ldg(table + word[e]);
+          if (pg >= 0 && pg < p.pages) page[e] = pg;
+        }
+      };
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        word[e] = (j_at + 32 * e) / p.page_size;
+        slot[e] = j_at + 32 * e - word[e] * p.page_size;
+        look_up(e);
+      }
+      // load the next tile's codes and look the pages of the one after it up
+      auto load = [&](Raw& raw) {
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-          const int j = j0 + t * kTile + entry_of(e);
-          const int pg = t < tiles && j < end ? kv4_page(table, p.table_stride, p.pages, p.page_size, j) : -1;
-          raw.seen[e] = pg >= 0 && (!mask || __ldg(mask + j) != 0);
+          raw.seen[e] = page[e] >= 0 && (!mask || __ldg(mask + j_at + 32 * e) != 0);
           raw.k[e] = raw.v[e] = make_uint4(0u, 0u, 0u, 0u);
           raw.kp[e] = raw.vp[e] = 0u;
-          if (pg >= 0) {
-            const int64_t row = (static_cast<int64_t>(pg) * p.heads + h) * p.page_size + j % p.page_size;
-            const int g = group_of(e);
+          if (page[e] >= 0) {
+            const int64_t row = (static_cast<int64_t>(page[e]) * p.heads + h) * p.page_size + slot[e];
             raw.k[e] = ld_stream_v4(p.k_codes + row * (D / 2) + g * 16);
             raw.v[e] = ld_stream_v4(p.v_codes + row * (D / 2) + g * 16);
             raw.kp[e] = __ldg(p.k_params + row * (D / 32) + g);
             raw.vp[e] = __ldg(p.v_params + row * (D / 32) + g);
           }
         }
+        j_at += AHEAD;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          word[e] += step_pages;
+          slot[e] += step_slots;
+          if (slot[e] >= p.page_size) {
+            slot[e] -= p.page_size;
+            ++word[e];
+          }
+          look_up(e);
+        }
       };
-      auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst, int entry, int g) {
+      const uint32_t to = (g >> 1) * SLAB + entry0 * 128;
+      uint32_t piece_at[4];  // the swizzle depends on the entry modulo 8 alone
+#pragma unroll
+      for (int x = 0; x < 4; ++x) piece_at[x] = to + ((((g & 1) * 4 + x) ^ t8) << 4);
+      auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst) {
         const Kv4Scale sc = kv4_scale(__byte_perm(param, param, 0x1010));
-        const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
-        const uint32_t row = dst + (g >> 1) * SLAB + entry * 128;
+        const uint32_t wd[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const uint32_t a = kv4_pair<0>(word[x], sc), c = kv4_pair<1>(word[x], sc),
-                         d = kv4_pair<2>(word[x], sc), z = kv4_pair<3>(word[x], sc);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           row + ((((g & 1) * 4 + x) ^ (entry & 7)) << 4)),
-                       "r"(a), "r"(c), "r"(d), "r"(z)
+          const uint32_t a = kv4_pair<0>(wd[x], sc), c = kv4_pair<1>(wd[x], sc),
+                         d = kv4_pair<2>(wd[x], sc), z = kv4_pair<3>(wd[x], sc);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + piece_at[x]), "r"(a),
+                       "r"(c), "r"(d), "r"(z)
                        : "memory");
         }
       };
       Raw raw;
-      load(raw, 0);
-      bool ok = true;
-      for (int t = 0; t < tiles; ++t) {
+      load(raw);
+      for (int t = t_first; t < tiles; t += 2) {
         const int k = step + t, st = k % kStages;
         Raw cur = raw;
-        load(raw, t + 1);
-        ok = __all_sync(kFull, wait_bar(empty0 + 8 * st, ((k / kStages) & 1) ^ 1, abort_v, f.status));
-        if (!ok) break;
+        load(raw);
+        if (!__all_sync(kFull, wait_bar(empty0 + 8 * st, ((k / kStages) & 1) ^ 1, abort_v, f.status)))
+          break;
         const uint32_t sk = sbase + st * M::kStage, sv = sk + M::kTensor;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-          turn(cur.k[e], cur.kp[e], sk, entry_of(e), group_of(e));
+          turn(cur.k[e], cur.kp[e], sk + e * 32 * 128);
           // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
-          turn(cur.v[e], cur.seen[e] ? cur.vp[e] : 0u, sv, entry_of(e), group_of(e));
+          turn(cur.v[e], cur.seen[e] ? cur.vp[e] : 0u, sv + e * 32 * 128);
         }
         // entries 8w .. 8w + 7 of each half of the tile
 #pragma unroll
@@ -473,11 +563,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (u < u1) sg.next(p, f);
   }
 
+  if (warp < 8 && (threadIdx.x & (kRows - 1)) == 0) mma_commit(done_bar);
   tc_before();
   __syncthreads();
-  if (warp == 4) {
-    // every product has completed before the tensor memory goes away
-    if (lane == 0 && o_no > 0) drain_bar(o_bar, (o_no - 1) & 1);
+  if (warp == 8) {
+    // every product has completed before the tensor memory goes away (bounded: after a wait that
+    // ran out too)
+    if (lane == 0) drain_bar(done_bar, 0);
     __syncwarp();
     tc_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -490,36 +582,49 @@ bool attention_tc_takes(int n, int G, int D) {
   return (D == 64 || D == 128) && static_cast<int64_t>(n) * G > 32;
 }
 
-size_t attention_tc_ws_bytes(int D, int sm_count) {
-  const size_t parts = static_cast<size_t>(2) * sm_count * kCtasPerSm * kRows;
-  return kWsHeader + parts * D * 4 + parts * 8;
+namespace {
+int tile_rows(int n, int G) { return static_cast<int64_t>(n) * G > kRows ? 2 * kRows : kRows; }
+}  // namespace
+
+size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count) {
+  const int R = tile_rows(n, G);
+  const size_t parts = static_cast<size_t>(2) * sm_count * R;
+  const size_t tiles = (static_cast<size_t>(n) * G + R - 1) / R;
+  return kWsHeader + parts * D * 4 + parts * 8 + B * tiles * heads * 8;
 }
 
-template <int D>
+template <int D, bool kShare>
 static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaStream_t stream) {
+  constexpr int R = kShare ? 2 * kRows : kRows;
   AttnPlan f{};
   f.unit = kTile;
-  f.row_tiles = (p.n * p.G + kRows - 1) / kRows;
-  f.ctas = sm_count * kCtasPerSm;
+  f.row_tiles = (p.n * p.G + R - 1) / R;
+  f.ctas = sm_count;
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
   f.status = static_cast<int32_t*>(ws);
-  const size_t parts = static_cast<size_t>(2) * f.ctas * kRows;
-  f.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
-  f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + kWsHeader + parts * D * 4);
-  cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<D>,
+  const size_t parts = static_cast<size_t>(2) * f.ctas * R;
+  char* at = static_cast<char*>(ws) + kWsHeader;
+  f.part_o = reinterpret_cast<float*>(at);
+  f.part_ml = reinterpret_cast<float2*>(at + parts * D * 4);
+  f.parts = reinterpret_cast<int2*>(at + parts * D * 4 + parts * 8);
+  cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<D, kShare>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Smem<D>::kBytes));
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attention_tc_kernel<D>, dim3(f.ctas), dim3(kThreads), Smem<D>::kBytes, stream,
-                       p, f);
+  e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
+                       Smem<D>::kBytes, stream, p, f);
   if (e != cudaSuccess || p.max_len <= f.unit) return e;
-  return launch_join<D, kRows>(p, f, stream);
+  return launch_join<D, R, 16>(p, f, stream);
 }
 
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream) {
-  return D == 64 ? launch_tc<64>(p, ws, sm_count, stream) : launch_tc<128>(p, ws, sm_count, stream);
+  if (tile_rows(p.n, p.G) == kRows)
+    return D == 64 ? launch_tc<64, false>(p, ws, sm_count, stream)
+                   : launch_tc<128, false>(p, ws, sm_count, stream);
+  return D == 64 ? launch_tc<64, true>(p, ws, sm_count, stream)
+                 : launch_tc<128, true>(p, ws, sm_count, stream);
 }
 
 }  // namespace dllm
