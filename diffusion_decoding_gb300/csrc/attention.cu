@@ -564,7 +564,7 @@ cudaError_t launch_few(const AttnParams& p, const AttnPlan& f, bool split, cudaS
   e = launch_dependent(attention_few_kernel<D, NT>, dim3(f.ctas), dim3(kThreads), smem,
                                    stream, p, f);
   if (e != cudaSuccess || !split) return e;
-  return launch_join<D, 8 * NT, 1>(p, f, stream);
+  return launch_join<D, 8 * NT>(p, f, stream);
 }
 
 }  // namespace

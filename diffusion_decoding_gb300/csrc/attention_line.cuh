@@ -192,101 +192,71 @@ __device__ __forceinline__ void store_lse(const AttnParams& p, int b, int h, int
 
 // Join the parts of the segments that several CTAs share, in order of their entries:
 //   out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
-// RPC = 1: a CTA per row, each warp takes every fourth part (few rows, many parts).  Otherwise a
-// CTA takes RPC rows of a segment, a warp one row at a time (many rows, two or three parts).
-template <int D, int ROWS, int RPC>
+// A CTA per row; each warp takes every fourth part.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
-  constexpr int V = D / 64, GROUPS = ROWS / RPC;
+  constexpr int V = D / 64;
   __shared__ float2 acc_s[kJoinWarps][D / 2];
   __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  const int64_t seg = blockIdx.x / GROUPS;
-  const int group = blockIdx.x % GROUPS;
+  const int64_t seg = blockIdx.x / ROWS;
+  const int r = blockIdx.x % ROWS;
   const int2 info = f.parts[seg];
   if (info.x < 0) return;
   const int h = static_cast<int>(seg % p.heads), item = static_cast<int>(seg / p.heads);
   const int b = item / f.row_tiles, rt = item - b * f.row_tiles;
   const int c0 = info.x >> 1, count = info.y - c0 + 1;
   auto part_of = [&](int k) { return static_cast<int64_t>(k == 0 ? info.x : 2 * (c0 + k)) * ROWS; };
-  const int r_last = min(ROWS, p.n * p.G - rt * ROWS);  // rows of this tile
-  if constexpr (RPC == 1) {
-    const int r = group;
-    if (r >= r_last) return;
-    float mx = -INFINITY;
-    for (int k = threadIdx.x; k < count; k += kJoinThreads) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
+  if (rt * ROWS + r >= p.n * p.G) return;
+  float mx = -INFINITY;
+  for (int k = threadIdx.x; k < count; k += kJoinThreads) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    if (lane == 0) max_s[warp] = mx;
-    __syncthreads();
-    mx = max_s[0];
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+  if (lane == 0) max_s[warp] = mx;
+  __syncthreads();
+  mx = max_s[0];
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
-    float2 acc[V] = {};
-    float sum = 0.f;
+  for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
+  float2 acc[V] = {};
+  float sum = 0.f;
 #pragma unroll 4
-    for (int k = warp; k < count; k += kJoinWarps) {
-      const float2 v = f.part_ml[part_of(k) + r];
-      const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
-      sum = fmaf(v.y, keep, sum);
-      const float* src = f.part_o + (part_of(k) + r) * D;
+  for (int k = warp; k < count; k += kJoinWarps) {
+    const float2 v = f.part_ml[part_of(k) + r];
+    const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
+    sum = fmaf(v.y, keep, sum);
+    const float* src = f.part_o + (part_of(k) + r) * D;
 #pragma unroll
-      for (int x = 0; x < V; ++x) {
-        const float2 o = *reinterpret_cast<const float2*>(src + 64 * x + 2 * lane);
-        acc[x].x = fmaf(o.x, keep, acc[x].x);
-        acc[x].y = fmaf(o.y, keep, acc[x].y);
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < V; ++x) acc_s[warp][32 * x + lane] = acc[x];
-    if (lane == 0) sum_s[warp] = sum;
-    __syncthreads();
-    sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int e = threadIdx.x; e < D / 2; e += kJoinThreads) {
-      float2 a = acc_s[0][e];
-#pragma unroll
-      for (int w = 1; w < kJoinWarps; ++w) {
-        a.x += acc_s[w][e].x;
-        a.y += acc_s[w][e].y;
-      }
-      store_joined(p, b, h, rt * ROWS + r, 2 * e, a, inv);
-    }
-    if (threadIdx.x == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
-  } else {
-    const int r_end = min(r_last, (group + 1) * RPC);
-    for (int r = group * RPC + warp; r < r_end; r += kJoinWarps) {
-      float mx = -INFINITY;
-      for (int k = 0; k < count; ++k) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
-      float2 acc[V] = {};
-      float sum = 0.f;
-      for (int k = 0; k < count; ++k) {
-        const float2 v = f.part_ml[part_of(k) + r];
-        const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
-        sum = fmaf(v.y, keep, sum);
-        const float* src = f.part_o + (part_of(k) + r) * D;
-#pragma unroll
-        for (int x = 0; x < V; ++x) {
-          const float2 o = *reinterpret_cast<const float2*>(src + 64 * x + 2 * lane);
-          acc[x].x = fmaf(o.x, keep, acc[x].x);
-          acc[x].y = fmaf(o.y, keep, acc[x].y);
-        }
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-      for (int x = 0; x < V; ++x)
-        store_joined(p, b, h, rt * ROWS + r, 64 * x + 2 * lane, acc[x], inv);
-      if (lane == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
+    for (int x = 0; x < V; ++x) {
+      const float2 o = *reinterpret_cast<const float2*>(src + 64 * x + 2 * lane);
+      acc[x].x = fmaf(o.x, keep, acc[x].x);
+      acc[x].y = fmaf(o.y, keep, acc[x].y);
     }
   }
+#pragma unroll
+  for (int x = 0; x < V; ++x) acc_s[warp][32 * x + lane] = acc[x];
+  if (lane == 0) sum_s[warp] = sum;
+  __syncthreads();
+  sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int e = threadIdx.x; e < D / 2; e += kJoinThreads) {
+    float2 a = acc_s[0][e];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+      a.x += acc_s[w][e].x;
+      a.y += acc_s[w][e].y;
+    }
+    store_joined(p, b, h, rt * ROWS + r, 2 * e, a, inv);
+  }
+  if (threadIdx.x == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
 }
 
-template <int D, int ROWS, int RPC>
+template <int D, int ROWS>
 cudaError_t launch_join(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
-  const int64_t blocks = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (ROWS / RPC);
-  return launch_dependent(attention_join_kernel<D, ROWS, RPC>, dim3(static_cast<unsigned>(blocks)),
+  const int64_t blocks = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * ROWS;
+  return launch_dependent(attention_join_kernel<D, ROWS>, dim3(static_cast<unsigned>(blocks)),
                           dim3(kJoinThreads), 0, stream, p, f);
 }
 

@@ -3,22 +3,28 @@
 //
 // Entries are taken 64 at a time:
 //   S [128 rows x 64] = Q K^T,   O [128 x D] += P V     (tcgen05.mma, fp32 accumulators in TMEM)
-// Q and P are left operands in TMEM, so shared memory only carries K and V.  Two groups of four
-// warps each hold 128 rows, one row a thread, and run in turn: the products of one fill the tensor
-// cores while the other is in its softmax.  With more than 128 rows in a segment (kShare) the
-// groups are the two halves of a 256-row tile and use every K/V stage both; otherwise they hold
-// the same rows, take the stages in turn, and add up at the end.
+// Two groups of four warps each hold 128 rows, one row a thread.  With more than 128 rows in a
+// segment (kShare) the groups are the two halves of a 256-row tile and use every K/V stage both;
+// otherwise they hold the same rows, take the stages in turn, and add up at the end.
 //
 // Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
-// attention.cu's kSlack), and the output; the first thread of each group issues its products.
-// Warps 8-15: codes to bf16, into a ring of K/V stages in the 128-byte swizzled layout, each half
-// every second stage; a lane turns 32 channels (one group) of an entry, and eight lanes of the same
-// group store to eight different bank groups.
+// attention.cu's kSlack), and the output.  Warps 8-15: codes to bf16, into a ring of K/V stages in
+// the 128-byte swizzled layout, each half every second stage; a lane turns 32 channels (one group)
+// of an entry, and eight lanes of the same group store to eight different bank groups.  Warps 16
+// and 17: one thread each issues the products of a group: the scores of a step as soon as the
+// softmax warps hold those of the step before in registers, so that they are there when the
+// softmax comes back for them.
+//
+// TMEM, 512 columns: O 2 x 128, S 2 x 64, P 2 x 32 and 64 for the queries of group 0 (left operands
+// may lie there).  Group 1's queries are in shared memory.  Per 64 entries and D = 128 shared memory
+// then moves 128 KB (K and V written once and read twice, the queries of group 1 read once), as
+// many cycles as the products of both groups take.
 // The eight channels of a code word come out as pairs (j, j + 4): Q's channels are put in the same
 // order (the scores do not depend on it), and the output's are put back.
-//
-// TMEM columns of group g: Q at 64 g, S with P over it at 128 + 64 g, O at 256 + 128 g.
 #include "attention.h"
+
+#include <algorithm>
+
 #include "attention_line.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -31,8 +37,12 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kTile = 64;  // entries of a step
-constexpr int kStages = 6;
-constexpr int kThreads = 512;
+constexpr int kStages = 5;
+constexpr int kThreads = 640;
+// registers a thread: launched with 96, then shared out anew, 128 threads a figure:
+// 2 x 136 + 2 x 80 + 48 = 5 x 96
+constexpr int kSoftmaxRegs = 136, kTurnRegs = 80, kIssueRegs = 48;
+static_assert(2 * kSoftmaxRegs + 2 * kTurnRegs + kIssueRegs == 5 * 96, "");
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;  // as in attention.cu
 
@@ -61,6 +71,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// the same with A in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread has completed.
@@ -123,7 +142,20 @@ template <int D>
 struct Smem {
   static constexpr uint32_t kTensor = kTile * D * 2;  // K (or V) of a stage
   static constexpr uint32_t kStage = 2 * kTensor;
-  static constexpr size_t kBytes = kStages * kStage + 1024;  // and room to align
+  static constexpr uint32_t kQ = kStages * kStage;  // group 1's queries
+  static constexpr size_t kBytes = kQ + kRows * D * 2 + 1024;  // and room to align
+};
+
+// What a CTA does with one segment.
+template <int ROWS>
+struct Piece {
+  int units, j0, end, tiles;
+  __device__ __forceinline__ Piece(const Segment<ROWS>& sg, const AttnPlan& f, int64_t left) {
+    units = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), left));
+    j0 = sg.k0 * f.unit;
+    end = min(sg.seen, j0 + units * f.unit);
+    tiles = end > j0 ? (end - j0 + kTile - 1) / kTile : 0;
+  }
 };
 
 template <int D, bool kShare>
@@ -131,10 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
   using M = Smem<D>;
   constexpr int ROWS = kShare ? 2 * kRows : kRows;
-  constexpr int SLABS = D / 64;
-  constexpr uint32_t SLAB = kTile * 128;
+  constexpr int STRIDE = kShare ? 1 : 2;  // tiles from one of a group to its next
+  constexpr uint32_t SLAB = kTile * 128, QSLAB = kRows * 128;
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t bars[2 * kStages + 9];
+  __shared__ uint64_t bars[2 * kStages + 11];
   __shared__ uint32_t visible[kStages][2];  // of the stage's 64 entries: a bit per entry
   __shared__ float2 ml_s[2][kRows];         // groups with the same rows: reference and sum
   __shared__ uint32_t tmem_slot;
@@ -143,19 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
   const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kStages]);
-  const uint32_t gbars = smem_u32(&bars[2 * kStages]);  // of group g at + 32 g:
-  constexpr uint32_t kQ = 0, kS = 8, kP = 16, kO = 24;  // Q there and O free; S; P; O complete
-
-  const uint32_t done_bar = gbars + 64;
-
-  // nothing of this CTA, its tensor memory included, is taken before the kernels it depends on are
-  // done: one of them may be waiting for tensor memory
-  pdl_wait();
-  pdl_trigger();
-  Line<ROWS> line;
-  line.build(p, f);
-  const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
-  if (u0 >= u1) return;
+  const uint32_t gbars = smem_u32(&bars[2 * kStages]);  // of group g at + 40 g:
+  // the queries are there and O may be overwritten; S is there; S has been read; P is there; the
+  // product with V has been added
+  constexpr uint32_t kBarQ = 0, kBarS = 8, kBarFree = 16, kBarP = 24, kBarV = 32, kGroupBars = 40;
+  const uint32_t done_bar = gbars + 2 * kGroupBars;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -163,75 +187,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty0 + 8 * s, kShare ? 2 : 1);
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(gbars + 32 * g + kQ, kShare ? 4 : 8);
-      mbar_init(gbars + 32 * g + kS, 1);
-      mbar_init(gbars + 32 * g + kP, 4);
-      mbar_init(gbars + 32 * g + kO, 1);
+      const uint32_t bar = gbars + kGroupBars * g;
+      mbar_init(bar + kBarQ, kShare ? 4 : 8);
+      mbar_init(bar + kBarS, 1);
+      mbar_init(bar + kBarFree, 4);
+      mbar_init(bar + kBarP, 4);
+      mbar_init(bar + kBarV, 1);
     }
     mbar_init(done_bar, 2);
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+  // nothing else of this CTA, its tensor memory included, is taken before the kernels it depends
+  // on are done: one of them may be waiting for tensor memory
+  pdl_wait();
+  pdl_trigger();
+  Line<ROWS> line;
+  line.build(p, f);
+  const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
+  if (u0 >= u1) return;
+  if (warp == 16) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = tmem_slot;
   volatile int* abort_v = &abort_flag;
   const int rows = p.n * p.G;
+  auto col_o = [](int g) { return 128u * g; };
+  auto col_s = [](int g) { return 256u + 64u * g; };
+  auto col_p = [](int g) { return 384u + 32u * g; };
+  constexpr uint32_t col_q = 448;
 
   Segment<ROWS> sg;
   sg.find(p, f, line, u0);
-  int step = 0;      // K/V tiles so far: tile k is in stage k % kStages
-  int piece_no = 0;  // segments so far
-  int mine = 0;      // tiles of this group so far
-  int o_no = 0;      // segments so far with tiles (phases of kO)
-  for (int64_t u = u0; u < u1; ++piece_no) {
-    const int piece = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), u1 - u));
-    const int j0 = sg.k0 * f.unit;
-    const int end = min(sg.seen, j0 + piece * f.unit);
-    const int tiles = end > j0 ? (end - j0 + kTile - 1) / kTile : 0;
-    const int b = sg.b, h = sg.h;
-    constexpr int STRIDE = kShare ? 1 : 2;  // tiles from one of a group to its next
+  int step = 0;  // K/V tiles so far: tile k is in stage k % kStages
+  int mine = 0;  // tiles of this group so far: the phase of its barriers
+  auto stage_of = [](int k) { return k % kStages; };
+  auto parity_of = [](int k) { return static_cast<uint32_t>(k / kStages) & 1u; };
 
-    if (warp < 8) {
-      // ---------------------------------------------------------------- softmax, one row a thread
-      const int grp = warp >> 2, row_in = threadIdx.x & (kRows - 1);
-      const bool issuer = row_in == 0;
-      const uint32_t bar = gbars + 32 * grp;
-      const uint32_t c_q = 64 * grp, c_s = 128 + 64 * grp, c_o = 256 + 128 * grp;
+  if (warp < 8) {
+    // ------------------------------------------------------------------ softmax, one row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int grp = warp >> 2, row_in = threadIdx.x & (kRows - 1);
+    const uint32_t bar = gbars + kGroupBars * grp;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_s = lanes + col_s(grp), t_p = lanes + col_p(grp), t_o = lanes + col_o(grp);
+    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    for (int64_t u = u0; u < u1;) {
+      const Piece<ROWS> pc(sg, f, u1 - u);
+      const int b = sg.b, h = sg.h;
       const int first = kShare ? 0 : (grp ^ step) & 1;  // this group's first tile of the segment
-      const int count = tiles > first ? (tiles - first + STRIDE - 1) / STRIDE : 0;
-      // scores of tile k (counted over all segments) once its K is there
-      auto scores = [&](int k) {
-        const int st = k % kStages;
-        if (!wait_bar(full0 + 8 * st, (k / kStages) & 1, abort_v, f.status)) return;
-        tc_after();
-        const uint32_t sk = sbase + st * M::kStage;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          mma_ts(tmem + c_s, tmem + c_q + x * 8, sw128(sk + (x >> 2) * SLAB + (x & 3) * 32, 16),
-                 idesc(kTile, false), x > 0);
-        mma_commit(bar + kS);
-      };
-      // the weights of tile k, the group's n-th, times its V, once all rows' weights are there
-      auto values = [&](int k, int n, bool start) {
-        const int st = k % kStages;
-        if (!wait_bar(bar + kP, n & 1, abort_v, f.status)) return;
-        tc_after();
-        const uint32_t sv = sbase + st * M::kStage + M::kTensor;
-#pragma unroll
-        for (int x = 0; x < kTile / 16; ++x)
-          mma_ts(tmem + c_o, tmem + c_s + x * 8, sw128(sv + x * 2048, SLABS > 1 ? SLAB : 16),
-                 idesc(D, true), !start || x > 0);
-        mma_commit(empty0 + 8 * st);
-      };
+      const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
       const int r = sg.rt * ROWS + (kShare ? grp * kRows : 0) + row_in;
       const int i = r / p.G, hq = h * p.G + r - i * p.G;
-      const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const uint32_t t_s = lanes + c_s, t_o = lanes + c_o;
-      const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-      if (threadIdx.x == 0) note_segment(f, p, line, sg, u, u0, piece == sg.units);
+      if (threadIdx.x == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
       {
         // a negative scale turns the sign of Q, one of zero makes Q zero: both exact
         const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -261,32 +270,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[4 * k + 2] = __byte_perm(x[1], x[3], 0x5410);
             w[4 * k + 3] = __byte_perm(x[1], x[3], 0x7632);
           }
-          tmem_st32(lanes + c_q + half * 32, w);
+          if (grp == 0) {
+            tmem_st32(lanes + col_q + half * 32, w);
+          } else {
+            const uint32_t dst = sbase + M::kQ + half * QSLAB + row_in * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                               dst + ((k ^ (row_in & 7)) << 4)),
+                           "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                           : "memory");
+          }
         }
-        tmem_wait_st();
+        if (grp == 0)
+          tmem_wait_st();
+        else
+          fence_async_shared();
         tc_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar + kQ);
+          mbar_arrive(bar + kBarQ);
           // both groups read both accumulators of the segment before
-          if (!kShare) mbar_arrive(gbars + 32 * (grp ^ 1) + kQ);
+          if (!kShare) mbar_arrive(gbars + kGroupBars * (grp ^ 1) + kBarQ);
         }
-        // every phase of kQ is waited for, of segments without tiles too
-        if (issuer && wait_bar(bar + kQ, piece_no & 1, abort_v, f.status) && count > 0)
-          scores(step + first);
-        if (issuer && count == 0 && tiles > 0) mma_commit(bar + kO);  // kO has a phase all the same
-        __syncwarp();
       }
-      const int bound = rows_see(p, sg.len, r);                      // entries this row sees
-      const int all_see = rows_see(p, sg.len, r - row_in);           // what every row of the group sees
+      const int bound = rows_see(p, sg.len, r);             // entries this row sees
+      const int all_see = rows_see(p, sg.len, r - row_in);  // what every row of the group sees
       float m = -INFINITY;
       uint64_t l2 = 0;  // two partial sums
       bool ok = true;
       for (int n = 0; n < count; ++n) {
-        const int t = first + n * STRIDE, k = step + t, st = k % kStages;
+        const int t = first + n * STRIDE, k = step + t, st = stage_of(k);
         // the mask words of the stage, and the scores
-        ok = ok && wait_bar(full0 + 8 * st, (k / kStages) & 1, abort_v, f.status);
-        ok = __all_sync(kFull, ok && wait_bar(bar + kS, (mine + n) & 1, abort_v, f.status));
+        ok = ok && wait_bar(full0 + 8 * st, parity_of(k), abort_v, f.status);
+        ok = __all_sync(kFull, ok && wait_bar(bar + kBarS, (mine + n) & 1, abort_v, f.status));
         if (!ok) break;
         tc_after();
         float s[kTile];
@@ -294,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(t_s + 32, s + 32);
         const uint32_t vis0 = visible[st][0], vis1 = visible[st][1];
         tmem_wait_ld();
-        const int j = j0 + t * kTile;
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + kBarFree);
+        const int j = pc.j0 + t * kTile;
         if ((vis0 & vis1) != 0xffffffffu || j + kTile > all_see) {
           const int left = bound - j;  // entries of the tile below the bound
 #pragma unroll
@@ -320,7 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpack2(l2, la, lb);
           l2 = pack2(la * keep, lb * keep);
           if (n > 0) {
-            // the product before has been added to O: S came after it on the same pipe
+            // the products before have been added to O
+            ok = __all_sync(kFull, wait_bar(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status));
+            if (!ok) break;
+            tc_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float o[32];
@@ -344,39 +367,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2 = add2(l2, pack2(a, d));
           pk[e / 2] = bf2_pack(a, d);
         }
-        tmem_st32(t_s, pk);
+        if (n > 0) {  // P of the step before has been read
+          ok = __all_sync(kFull, wait_bar(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status));
+          if (!ok) break;
+          tc_after();
+        }
+        tmem_st32(t_p, pk);
         tmem_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar + kP);
-        if (issuer) {
-          values(k, mine + n, n == 0);
-          // the next scores overwrite P: they follow the product that reads it on the same pipe
-          if (n + 1 < count)
-            scores(k + STRIDE);
-          else
-            mma_commit(bar + kO);
-        }
-        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + kBarP);
       }
       float l, l_odd;
       unpack2(l2, l, l_odd);
       l += l_odd;
       // ---- output.  Groups with the same rows: each takes half of the channels of both.
+      ok = ok && (count == 0 || wait_bar(bar + kBarV, (mine + count - 1) & 1, abort_v, f.status));
+      ok = __all_sync(kFull, ok);
       if constexpr (!kShare) {
         ml_s[grp][row_in] = make_float2(m, l);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // both groups' products are complete
       }
-      if (tiles > 0) {
-        ok = ok && wait_bar(bar + kO, o_no & 1, abort_v, f.status);
-        if (!kShare) ok = ok && wait_bar(gbars + 32 * (grp ^ 1) + kO, o_no & 1, abort_v, f.status);
-      }
-      ok = __all_sync(kFull, ok);
       tc_after();
       if (ok) {
-        const bool direct = piece == sg.units;
+        const bool direct = pc.units == sg.units;
         const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
-        const int64_t at = part * ROWS + (r - sg.rt * ROWS);
+        const int row_tile = r - sg.rt * ROWS;
         float keep0 = count > 0 ? 1.f : 0.f, keep1 = 0.f;  // this group's and the other's
         if constexpr (!kShare) {
           const float2 ml = ml_s[grp ^ 1][row_in];
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         constexpr int SPAN = kShare ? D : D / 2;
         const int c0 = kShare ? 0 : grp * SPAN;
-        const uint32_t t_other = lanes + 256 + 128 * (grp ^ 1);
+        const uint32_t t_other = lanes + col_o(grp ^ 1);
 #pragma unroll 1
         for (int c = c0; c < c0 + SPAN; c += 32) {
           float o[32];
@@ -402,21 +418,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (!kShare) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
-            if (tiles > 0) {
-              float x[32];
-              tmem_ld32(t_other + c, x);
-              tmem_wait_ld();
+            float x[32];
+            tmem_ld32(t_other + c, x);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
           }
           // channels back in order: the word holds 0, 4, 1, 5, 2, 6, 3, 7
           if (r < rows && !direct) {
-            float4* dst = reinterpret_cast<float4*>(f.part_o + at * D + c);
+            // four channels of a row together, rows side by side: the warp's stores are contiguous
+            float4* dst = reinterpret_cast<float4*>(f.part_o) +
+                          (part * (D / 4) + c / 4) * ROWS + row_tile;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              dst[2 * k] = make_float4(o[8 * k], o[8 * k + 2], o[8 * k + 4], o[8 * k + 6]);
-              dst[2 * k + 1] = make_float4(o[8 * k + 1], o[8 * k + 3], o[8 * k + 5], o[8 * k + 7]);
+              dst[(2 * k) * ROWS] = make_float4(o[8 * k], o[8 * k + 2], o[8 * k + 4], o[8 * k + 6]);
+              dst[(2 * k + 1) * ROWS] =
+                  make_float4(o[8 * k + 1], o[8 * k + 3], o[8 * k + 5], o[8 * k + 7]);
             }
           } else if (r < rows) {
             uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + c;
@@ -440,40 +457,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (r < rows && (kShare || grp == 0)) {
           if (!direct)
-            f.part_ml[at] = make_float2(m, l);
+            f.part_ml[part * ROWS + row_tile] = make_float2(m, l);
           else
             store_lse(p, b, h, r, m, l);
         }
       }
       if constexpr (!kShare) asm volatile("bar.sync 1, 256;" ::: "memory");  // ml_s is read
-      tc_before();  // O and Q are read before the next segment's arrival on kQ
+      tc_before();  // O and Q are read before the next segment's arrival on kBarQ
       mine += count;
-    } else {
-      // ---------------------------------------------------------------- codes to bf16
-      // lanes 8q .. 8q + 7 take group q (and q + 4, ...) of entries 8w .. 8w + 7 and, 32 further, of
-      // the same again; this half of the warps every second tile
-      constexpr int GROUPS = D / 32;             // per entry
-      constexpr int PER = 2 * GROUPS / 4;        // pieces of K a thread turns per tile
-      constexpr int AHEAD = 2 * kTile;           // entries from one of its tiles to the next
-      const int half = (warp >> 2) & 1, w = warp & 3, q4 = lane >> 3, t8 = lane & 7;
-      const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
-      const uint8_t* mask = p.key_mask ? p.key_mask + b * p.mask_stride : nullptr;
-      // piece e of the thread: entry and group
-      const int entry0 = GROUPS == 4 ? w * 8 + t8 : w * 8 + t8 + 32 * (q4 >> 1);
-      const int g = GROUPS == 4 ? q4 : q4 & 1;
-      struct Raw {
-        uint4 k[PER], v[PER];
-        uint32_t kp[PER], vp[PER];
-        bool seen[PER];
-      };
+      step += pc.tiles;
+      u += pc.units;
+      if (u < u1) sg.next(p, f);
+    }
+  } else if (warp < 16) {
+    // ------------------------------------------------------------------ codes to bf16
+    // lanes 8q .. 8q + 7 take group q (and q + 4, ...) of entries 8w .. 8w + 7 and, 32 further, of
+    // the same again; this half of the warps every second tile
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTurnRegs));
+    constexpr int GROUPS = D / 32;       // per entry
+    constexpr int PER = 2 * GROUPS / 4;  // pieces of K a thread turns per tile
+    constexpr int AHEAD = 2 * kTile;     // entries from one of its tiles to the next
+    const int half = (warp >> 2) & 1, w = warp & 3, q4 = lane >> 3, t8 = lane & 7;
+    // piece e of the thread: entry entry0 + 32 e, group g
+    const int entry0 = GROUPS == 4 ? w * 8 + t8 : w * 8 + t8 + 32 * (q4 >> 1);
+    const int g = GROUPS == 4 ? q4 : q4 & 1;
+    const int step_pages = AHEAD / p.page_size, step_slots = AHEAD % p.page_size;
+    const uint32_t to = sbase + (g >> 1) * SLAB + entry0 * 128;
+    uint32_t piece_at[4];  // the swizzle depends on the entry modulo 8 alone
+#pragma unroll
+    for (int x = 0; x < 4; ++x) piece_at[x] = to + ((((g & 1) * 4 + x) ^ t8) << 4);
+    auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst) {
+      const Kv4Scale sc = kv4_scale(__byte_perm(param, param, 0x1010));
+      const uint32_t wd[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t a = kv4_pair<0>(wd[x], sc), c = kv4_pair<1>(wd[x], sc),
+                       d = kv4_pair<2>(wd[x], sc), z = kv4_pair<3>(wd[x], sc);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + piece_at[x]), "r"(a),
+                     "r"(c), "r"(d), "r"(z)
+                     : "memory");
+      }
+    };
+    struct Raw {
+      uint4 k[PER], v[PER];
+      uint32_t kp[PER], vp[PER];
+      bool seen[PER];
+    };
+    for (int64_t u = u0; u < u1;) {
+      const Piece<ROWS> pc(sg, f, u1 - u);
+      const int h = sg.h;
+      const int32_t* table = p.table + static_cast<int64_t>(sg.b) * p.table_stride;
+      const uint8_t* mask = p.key_mask ? p.key_mask + sg.b * p.mask_stride : nullptr;
       const int t_first = (half ^ step) & 1;
       // the walk through the pages: word of the table and slot of the entries to look at next
-      int j_at = j0 + t_first * kTile + entry0;
-      int word[PER] = {}, slot[PER] = {}, page[PER];
-      const int step_pages = AHEAD / p.page_size, step_slots = AHEAD % p.page_size;
+      int j_at = pc.j0 + t_first * kTile + entry0;
+      int word[PER] = {}, slot[PER] = {}, page[PER] = {};
       auto look_up = [&](int e) {
         page[e] = -1;
-        if (j_at + 32 * e < end && word[e] < p.table_stride) {
+        if (j_at + 32 * e < pc.end && word[e] < p.table_stride) {
           const int pg = __ldg(table + word[e]);
           if (pg >= 0 && pg < p.pages) page[e] = pg;
         }
@@ -511,31 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           look_up(e);
         }
       };
-      const uint32_t to = (g >> 1) * SLAB + entry0 * 128;
-      uint32_t piece_at[4];  // the swizzle depends on the entry modulo 8 alone
-#pragma unroll
-      for (int x = 0; x < 4; ++x) piece_at[x] = to + ((((g & 1) * 4 + x) ^ t8) << 4);
-      auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst) {
-        const Kv4Scale sc = kv4_scale(__byte_perm(param, param, 0x1010));
-        const uint32_t wd[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t a = kv4_pair<0>(wd[x], sc), c = kv4_pair<1>(wd[x], sc),
-                         d = kv4_pair<2>(wd[x], sc), z = kv4_pair<3>(wd[x], sc);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + piece_at[x]), "r"(a),
-                       "r"(c), "r"(d), "r"(z)
-                       : "memory");
-        }
-      };
       Raw raw;
       load(raw);
-      for (int t = t_first; t < tiles; t += 2) {
-        const int k = step + t, st = k % kStages;
+      for (int t = t_first; t < pc.tiles; t += 2) {
+        const int k = step + t, st = stage_of(k);
         Raw cur = raw;
         load(raw);
-        if (!__all_sync(kFull, wait_bar(empty0 + 8 * st, ((k / kStages) & 1) ^ 1, abort_v, f.status)))
-          break;
-        const uint32_t sk = sbase + st * M::kStage, sv = sk + M::kTensor;
+        if (!__all_sync(kFull, wait_bar(empty0 + 8 * st, parity_of(k) ^ 1, abort_v, f.status))) break;
+        const uint32_t sk = st * M::kStage, sv = sk + M::kTensor;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
           turn(cur.k[e], cur.kp[e], sk + e * 32 * 128);
@@ -556,17 +580,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(full0 + 8 * st);
       }
+      step += pc.tiles;
+      u += pc.units;
+      if (u < u1) sg.next(p, f);
     }
-    step += tiles;
-    o_no += tiles > 0;
-    u += piece;
-    if (u < u1) sg.next(p, f);
+  } else {
+    // ------------------------------------------------------------------ products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    const int grp = warp - 16;
+    if (grp < 2 && lane == 0) {
+      const uint32_t bar = gbars + kGroupBars * grp;
+      const uint32_t t_s = tmem + col_s(grp), t_p = tmem + col_p(grp), t_o = tmem + col_o(grp);
+      bool ok = true;
+      int piece_no = 0;
+      for (int64_t u = u0; u < u1; ++piece_no) {
+        const Piece<ROWS> pc(sg, f, u1 - u);
+        const int first = kShare ? 0 : (grp ^ step) & 1;
+        const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
+        // every phase of kBarQ is waited for, of segments without tiles too
+        ok = ok && wait_bar(bar + kBarQ, piece_no & 1, abort_v, f.status);
+        auto scores = [&](int k) {
+          const uint32_t sk = sbase + stage_of(k) * M::kStage;
+          if (!wait_bar(full0 + 8 * stage_of(k), parity_of(k), abort_v, f.status)) return false;
+          tc_after();
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint64_t kd = sw128(sk + (x >> 2) * SLAB + (x & 3) * 32, 16);
+            if (grp == 0)
+              mma_ts(t_s, tmem + col_q + x * 8, kd, idesc(kTile, false), x > 0);
+            else
+              mma_ss(t_s, sw128(sbase + M::kQ + (x >> 2) * QSLAB + (x & 3) * 32, 16), kd,
+                     idesc(kTile, false), x > 0);
+          }
+          mma_commit(bar + kBarS);
+          return true;
+        };
+        if (count > 0) ok = ok && scores(step + first);
+        for (int n = 0; n < count && ok; ++n) {
+          const int k = step + first + n * STRIDE;
+          if (n + 1 < count) {
+            ok = wait_bar(bar + kBarFree, (mine + n) & 1, abort_v, f.status) && scores(k + STRIDE);
+            if (!ok) break;
+          }
+          ok = wait_bar(bar + kBarP, (mine + n) & 1, abort_v, f.status);
+          if (!ok) break;
+          tc_after();
+          const uint32_t sv = sbase + stage_of(k) * M::kStage + M::kTensor;
+#pragma unroll
+          for (int x = 0; x < kTile / 16; ++x)
+            mma_ts(t_o, t_p + x * 8, sw128(sv + x * 2048, D > 64 ? SLAB : 16), idesc(D, true),
+                   n > 0 || x > 0);
+          mma_commit(bar + kBarV);
+          mma_commit(empty0 + 8 * stage_of(k));
+        }
+        // the last scores' phase of kBarFree is passed over: it is waited for here
+        if (count > 0) ok = ok && wait_bar(bar + kBarFree, (mine + count - 1) & 1, abort_v, f.status);
+        mine += count;
+        step += pc.tiles;
+        u += pc.units;
+        if (u < u1) sg.next(p, f);
+      }
+      mma_commit(done_bar);
+    }
   }
 
-  if (warp < 8 && (threadIdx.x & (kRows - 1)) == 0) mma_commit(done_bar);
   tc_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     // every product has completed before the tensor memory goes away (bounded: after a wait that
     // ran out too)
     if (lane == 0) drain_bar(done_bar, 0);
@@ -574,6 +654,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Join the parts of the segments that several CTAs share, in order of their entries (the sums of
+// attention_line.cuh's join; the parts lie with four channels of a row together and rows side by
+// side).  A CTA takes 32 rows and 64 channels of a segment, a lane one row and 16 channels.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128)
+    attention_tc_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
+  constexpr int GROUPS = ROWS / 32, SPANS = D / 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t seg = blockIdx.x / (GROUPS * SPANS);
+  const int in = blockIdx.x % (GROUPS * SPANS);
+  const int2 info = f.parts[seg];
+  if (info.x < 0) return;
+  const int h = static_cast<int>(seg % p.heads), item = static_cast<int>(seg / p.heads);
+  const int b = item / f.row_tiles, rt = item - b * f.row_tiles;
+  const int c0 = info.x >> 1, count = info.y - c0 + 1;
+  const int row = in % GROUPS * 32 + lane, r = rt * ROWS + row;
+  const int ch = in / GROUPS * 64 + warp * 16;
+  if (r >= p.n * p.G) return;
+  auto part_of = [&](int k) { return static_cast<int64_t>(k == 0 ? info.x : 2 * (c0 + k)); };
+  float mx = -INFINITY;
+#pragma unroll 4
+  for (int k = 0; k < count; ++k) mx = fmaxf(mx, f.part_ml[part_of(k) * ROWS + row].x);
+  float4 acc[4] = {};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < count; ++k) {
+    const float2 v = f.part_ml[part_of(k) * ROWS + row];
+    const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
+    sum = fmaf(v.y, keep, sum);
+    const float4* src = reinterpret_cast<const float4*>(f.part_o) +
+                        (part_of(k) * (D / 4) + ch / 4) * ROWS + row;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float4 o = src[x * ROWS];
+      acc[x].x = fmaf(o.x, keep, acc[x].x);
+      acc[x].y = fmaf(o.y, keep, acc[x].y);
+      acc[x].z = fmaf(o.z, keep, acc[x].z);
+      acc[x].w = fmaf(o.w, keep, acc[x].w);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + ch;
+#pragma unroll
+  for (int x = 0; x < 4; x += 2) {
+    const uint4 v = make_uint4(bf2_pack(acc[x].x * inv, acc[x].y * inv),
+                               bf2_pack(acc[x].z * inv, acc[x].w * inv),
+                               bf2_pack(acc[x + 1].x * inv, acc[x + 1].y * inv),
+                               bf2_pack(acc[x + 1].z * inv, acc[x + 1].w * inv));
+    if (f.out_aligned) {
+      *reinterpret_cast<uint4*>(dst + 4 * x) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dst[4 * x + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+  if (ch == 0) store_lse(p, b, h, r, mx, sum);
 }
 
 }  // namespace
@@ -599,11 +741,15 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   AttnPlan f{};
   f.unit = kTile;
   f.row_tiles = (p.n * p.G + R - 1) / R;
-  f.ctas = sm_count;
+  // a stretch is kLeast units at least: parts have to be joined again
+  constexpr int kLeast = 4;
+  const int64_t units = static_cast<int64_t>(p.B) * f.row_tiles * p.heads *
+                        std::max<int64_t>(1, (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile);
+  f.ctas = static_cast<int>(std::min<int64_t>(sm_count, (units + kLeast - 1) / kLeast));
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
   f.status = static_cast<int32_t*>(ws);
-  const size_t parts = static_cast<size_t>(2) * f.ctas * R;
+  const size_t parts = static_cast<size_t>(2) * sm_count * R;
   char* at = static_cast<char*>(ws) + kWsHeader;
   f.part_o = reinterpret_cast<float*>(at);
   f.part_ml = reinterpret_cast<float2*>(at + parts * D * 4);
@@ -615,7 +761,9 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
                        Smem<D>::kBytes, stream, p, f);
   if (e != cudaSuccess || p.max_len <= f.unit) return e;
-  return launch_join<D, R, 16>(p, f, stream);
+  const int64_t joins = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (R / 32) * (D / 64);
+  return launch_dependent(attention_tc_join_kernel<D, R>, dim3(static_cast<unsigned>(joins)),
+                          dim3(128), 0, stream, p, f);
 }
 
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
