@@ -64,28 +64,41 @@ __device__ __forceinline__ void tc_before() {
 __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// D [128 x N] (+)= A [128 x 16] B [16 x N], A in TMEM, B in shared memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+// The products are issued by whole warps with uniform operands, one elected lane (`lead`) executing:
+// in a branch of one lane the compiler has to move every operand to the uniform registers anew, and
+// issuing the twelve products of a step took longer than computing them.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
+}
+// D [128 x N] (+)= A [128 x 16] B [16 x N], A in TMEM, B in shared memory
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 // the same with A in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread has completed.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -112,6 +125,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
       "r"(r[30]), "r"(r[31]), "r"(t)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -123,10 +144,15 @@ __device__ __forceinline__ void tmem_wait_st() {
 // 16-byte piece c of row i at i * 128 + ((c ^ (i & 7)) * 16), 8-row groups 1024 bytes apart, 64
 // channels further 64 rows on.  K is K-major (the product runs over the channels of a row); V is
 // MN-major (it runs over the rows): its leading offset steps to the next 64 channels.
-__device__ __forceinline__ uint64_t sw128(uint32_t saddr, uint32_t leading) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(leading >> 4) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
-         static_cast<uint64_t>(2) << 61;
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) {
+  return ((saddr & 0x3FFFFu) >> 4) | (leading >> 4) << 16;
+}
+// the descriptor `bytes` further on
+__device__ __forceinline__ uint64_t desc_at(uint32_t low, uint32_t bytes) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low + (bytes >> 4)), "r"(kDescHigh));
+  return d;
 }
 // D fp32, A and B bf16, M = 128; b_mn: B is MN-major
 __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
@@ -143,7 +169,8 @@ struct Smem {
   static constexpr uint32_t kTensor = kTile * D * 2;  // K (or V) of a stage
   static constexpr uint32_t kStage = 2 * kTensor;
   static constexpr uint32_t kQ = kStages * kStage;  // group 1's queries
-  static constexpr size_t kBytes = kQ + kRows * D * 2 + 1024;  // and room to align
+  static constexpr uint32_t kScratch = kQ + kRows * D * 2;  // 2 KB for each softmax warp
+  static constexpr size_t kBytes = kScratch + 8 * 2048 + 1024;  // and room to align
 };
 
 // What a CTA does with one segment.
@@ -232,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar = gbars + kGroupBars * grp;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + col_s(grp), t_p = lanes + col_p(grp), t_o = lanes + col_o(grp);
+    const uint32_t scratch = sbase + M::kScratch + warp * 2048;
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     for (int64_t u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
@@ -239,47 +267,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = kShare ? 0 : (grp ^ step) & 1;  // this group's first tile of the segment
       const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
       const int r = sg.rt * ROWS + (kShare ? grp * kRows : 0) + row_in;
-      const int i = r / p.G, hq = h * p.G + r - i * p.G;
       if (threadIdx.x == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
       {
         // a negative scale turns the sign of Q, one of zero makes Q zero: both exact
         const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const uint32_t q_keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
-        const uint16_t* src = p.q + b * p.qb + i * p.qt + hq * p.qh;
+        // The warp loads its 32 rows, four lanes 64 bytes (32 channels) of a row, and puts them where
+        // they belong: group 1's at once, group 0's 32 channels at a time by way of the warp's
+        // scratch, from where each thread takes those of its own row to TMEM.
+        const int lr = lane >> 2, lp = lane & 3;
+        uint4 v[D / 32][4];
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          uint32_t w[32];
+        for (int e = 0; e < 4; ++e) {
+          const int rr = r - lane + e * 8 + lr;
+          const int ri = rr / p.G;
+          const uint16_t* src =
+              p.q + b * p.qb + ri * p.qt + (h * p.G + rr - ri * p.G) * p.qh + lp * 8;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t x[4] = {0u, 0u, 0u, 0u};
-            if (r < rows) {
-              const uint16_t* s8 = src + half * 64 + k * 8;
+          for (int c = 0; c < D / 32; ++c) {
+            v[c][e] = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < rows) {
               if (f.q_aligned) {
-                const uint4 v = *reinterpret_cast<const uint4*>(s8);
-                x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                v[c][e] = *reinterpret_cast<const uint4*>(src + c * 32);
               } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  x[e] = s8[2 * e] | static_cast<uint32_t>(s8[2 * e + 1]) << 16;
+                const uint16_t* s8 = src + c * 32;
+                v[c][e].x = s8[0] | static_cast<uint32_t>(s8[1]) << 16;
+                v[c][e].y = s8[2] | static_cast<uint32_t>(s8[3]) << 16;
+                v[c][e].z = s8[4] | static_cast<uint32_t>(s8[5]) << 16;
+                v[c][e].w = s8[6] | static_cast<uint32_t>(s8[7]) << 16;
               }
             }
+          }
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (x[e] ^ q_flip) & q_keep;
-            w[4 * k] = __byte_perm(x[0], x[2], 0x5410);
-            w[4 * k + 1] = __byte_perm(x[0], x[2], 0x7632);
-            w[4 * k + 2] = __byte_perm(x[1], x[3], 0x5410);
-            w[4 * k + 3] = __byte_perm(x[1], x[3], 0x7632);
+        for (int c = 0; c < D / 32; ++c) {
+          if (grp == 0) __syncwarp();  // what was in the scratch has been taken
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x[4] = {v[c][e].x, v[c][e].y, v[c][e].z, v[c][e].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = (x[k] ^ q_flip) & q_keep;
+            const int rw = e * 8 + lr, rg = (warp & 3) * 32 + rw;  // row of the warp, of the group
+            const uint32_t dst =
+                grp == 0 ? scratch + rw * 64 + ((lp ^ (rw >> 1 & 3)) << 4)
+                         : sbase + M::kQ + (c >> 1) * QSLAB + rg * 128 +
+                               ((((c & 1) * 4 + lp) ^ (rg & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst),
+                         "r"(__byte_perm(x[0], x[2], 0x5410)), "r"(__byte_perm(x[0], x[2], 0x7632)),
+                         "r"(__byte_perm(x[1], x[3], 0x5410)), "r"(__byte_perm(x[1], x[3], 0x7632))
+                         : "memory");
           }
           if (grp == 0) {
-            tmem_st32(lanes + col_q + half * 32, w);
-          } else {
-            const uint32_t dst = sbase + M::kQ + half * QSLAB + row_in * 128;
+            __syncwarp();
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                               dst + ((k ^ (row_in & 7)) << 4)),
-                           "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
-                           : "memory");
+            for (int k = 0; k < 4; ++k) {
+              const uint4 y = ld_shared_v4(scratch + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4));
+              w[4 * k] = y.x, w[4 * k + 1] = y.y, w[4 * k + 2] = y.z, w[4 * k + 3] = y.w;
+            }
+            tmem_st16(lanes + col_q + c * 16, w);
           }
         }
         if (grp == 0)
@@ -435,21 +481,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[(2 * k + 1) * ROWS] =
                   make_float4(o[8 * k + 1], o[8 * k + 3], o[8 * k + 5], o[8 * k + 7]);
             }
-          } else if (r < rows) {
-            uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + c;
+          } else if (direct) {
+            // by way of the scratch, so that four lanes store 64 contiguous bytes of a row
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 v = make_uint4(bf2_pack(o[8 * k] * inv, o[8 * k + 2] * inv),
-                                         bf2_pack(o[8 * k + 4] * inv, o[8 * k + 6] * inv),
-                                         bf2_pack(o[8 * k + 1] * inv, o[8 * k + 3] * inv),
-                                         bf2_pack(o[8 * k + 5] * inv, o[8 * k + 7] * inv));
-              if (f.out_aligned) {
-                *reinterpret_cast<uint4*>(dst + 8 * k) = v;
-              } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int k = 0; k < 4; ++k)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                               scratch + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)),
+                           "r"(bf2_pack(o[8 * k] * inv, o[8 * k + 2] * inv)),
+                           "r"(bf2_pack(o[8 * k + 4] * inv, o[8 * k + 6] * inv)),
+                           "r"(bf2_pack(o[8 * k + 1] * inv, o[8 * k + 3] * inv)),
+                           "r"(bf2_pack(o[8 * k + 5] * inv, o[8 * k + 7] * inv))
+                           : "memory");
+            __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  dst[8 * k + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+            for (int e = 0; e < 4; ++e) {
+              const int lr = e * 8 + (lane >> 2), lp = lane & 3, rr = r - lane + lr;
+              const uint4 v = ld_shared_v4(scratch + lr * 64 + ((lp ^ (lr >> 1 & 3)) << 4));
+              if (rr < rows) {
+                const int ri = rr / p.G;
+                uint16_t* dst =
+                    p.out + b * p.ob + ri * p.ot + (h * p.G + rr - ri * p.G) * p.oh + c + lp * 8;
+                if (f.out_aligned) {
+                  *reinterpret_cast<uint4*>(dst) = v;
+                } else {
+                  const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) dst[x] = static_cast<uint16_t>(y[x >> 1] >> (16 * (x & 1)));
+                }
               }
             }
           }
@@ -587,60 +645,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    const int grp = warp - 16;
-    if (grp < 2 && lane == 0) {
+    const int grp = __shfl_sync(kFull, warp, 0) - 16;
+    if (grp < 2) {
+      const uint32_t lead = elect_lane();
       const uint32_t bar = gbars + kGroupBars * grp;
-      const uint32_t t_s = tmem + col_s(grp), t_p = tmem + col_p(grp), t_o = tmem + col_o(grp);
+      const uint32_t base = __shfl_sync(kFull, tmem, 0);
+      const uint32_t t_s = base + col_s(grp), t_p = base + col_p(grp), t_o = base + col_o(grp);
+      const uint32_t q_low = desc_low(sbase + M::kQ, 16);
       bool ok = true;
       int piece_no = 0;
       for (int64_t u = u0; u < u1; ++piece_no) {
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int first = kShare ? 0 : (grp ^ step) & 1;
         const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
+        auto wait = [&](uint32_t at, uint32_t parity) {
+          return __all_sync(kFull, wait_bar(at, parity, abort_v, f.status)) != 0;
+        };
         // every phase of kBarQ is waited for, of segments without tiles too
-        ok = ok && wait_bar(bar + kBarQ, piece_no & 1, abort_v, f.status);
+        ok = ok && wait(bar + kBarQ, piece_no & 1);
         auto scores = [&](int k) {
-          const uint32_t sk = sbase + stage_of(k) * M::kStage;
-          if (!wait_bar(full0 + 8 * stage_of(k), parity_of(k), abort_v, f.status)) return false;
+          const int st = __shfl_sync(kFull, stage_of(k), 0);
+          if (!wait(full0 + 8 * st, parity_of(k))) return false;
           tc_after();
+          const uint32_t low = desc_low(sbase + st * M::kStage, 16);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            const uint64_t kd = sw128(sk + (x >> 2) * SLAB + (x & 3) * 32, 16);
+            const uint64_t kd = desc_at(low, (x >> 2) * SLAB + (x & 3) * 32);
             if (grp == 0)
-              mma_ts(t_s, tmem + col_q + x * 8, kd, idesc(kTile, false), x > 0);
+              mma_ts(lead, t_s, base + col_q + x * 8, kd, idesc(kTile, false), x > 0);
             else
-              mma_ss(t_s, sw128(sbase + M::kQ + (x >> 2) * QSLAB + (x & 3) * 32, 16), kd,
+              mma_ss(lead, t_s, desc_at(q_low, (x >> 2) * QSLAB + (x & 3) * 32), kd,
                      idesc(kTile, false), x > 0);
           }
-          mma_commit(bar + kBarS);
+          mma_commit(lead, bar + kBarS);
           return true;
         };
         if (count > 0) ok = ok && scores(step + first);
         for (int n = 0; n < count && ok; ++n) {
           const int k = step + first + n * STRIDE;
           if (n + 1 < count) {
-            ok = wait_bar(bar + kBarFree, (mine + n) & 1, abort_v, f.status) && scores(k + STRIDE);
+            ok = wait(bar + kBarFree, (mine + n) & 1) && scores(k + STRIDE);
             if (!ok) break;
           }
-          ok = wait_bar(bar + kBarP, (mine + n) & 1, abort_v, f.status);
+          ok = wait(bar + kBarP, (mine + n) & 1);
           if (!ok) break;
           tc_after();
-          const uint32_t sv = sbase + stage_of(k) * M::kStage + M::kTensor;
+          const int st = __shfl_sync(kFull, stage_of(k), 0);
+          const uint32_t low = desc_low(sbase + st * M::kStage + M::kTensor, D > 64 ? SLAB : 16);
 #pragma unroll
           for (int x = 0; x < kTile / 16; ++x)
-            mma_ts(t_o, t_p + x * 8, sw128(sv + x * 2048, D > 64 ? SLAB : 16), idesc(D, true),
-                   n > 0 || x > 0);
-          mma_commit(bar + kBarV);
-          mma_commit(empty0 + 8 * stage_of(k));
+            mma_ts(lead, t_o, t_p + x * 8, desc_at(low, x * 2048), idesc(D, true), n > 0 || x > 0);
+          mma_commit(lead, bar + kBarV);
+          mma_commit(lead, empty0 + 8 * st);
         }
         // the last scores' phase of kBarFree is passed over: it is waited for here
-        if (count > 0) ok = ok && wait_bar(bar + kBarFree, (mine + count - 1) & 1, abort_v, f.status);
+        if (count > 0) ok = ok && wait(bar + kBarFree, (mine + count - 1) & 1);
         mine += count;
         step += pc.tiles;
         u += pc.units;
         if (u < u1) sg.next(p, f);
       }
-      mma_commit(done_bar);
+      mma_commit(lead, done_bar);
     }
   }
 
