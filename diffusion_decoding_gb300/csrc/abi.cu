@@ -810,6 +810,9 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
   p.page_size = cache->page_size;
   p.heads = cache->heads;
   p.G = q->heads / cache->heads;
+  p.g_magic = p.G > 1 && static_cast<int64_t>(n) * p.G * p.G < (int64_t{1} << 32)
+                  ? static_cast<uint32_t>((uint64_t{1} << 32) / p.G + 1)
+                  : 0u;
   p.lens = lens;
   p.max_len = max_len;
   p.key_mask = key_mask;

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
   pdl_trigger();
   Line<ROWS> line;
   line.build(p, f);
-  const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
+  const int u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
   if (u0 >= u1) return;
   Segment<ROWS> sg;
   sg.find(p, f, line, u0);
@@ -225,18 +225,18 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
   const uint8_t* v_of_lane = p.v_codes + lane * 16;
   const typename R::Lane at_lane(ring, c, g);
 
-  for (int64_t u = u0; u < u1;) {
-    const int piece = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), u1 - u));
+  for (int u = u0; u < u1;) {
+    const int piece = min(sg.units - sg.k0, u1 - u);
     const int b = sg.b, h = sg.h, len = sg.len, r0 = sg.rt * ROWS, k0 = sg.k0;
     const int seen_first = rows_see(p, len, r0);  // what the tile's first row sees
-    const int end = min(sg.seen, (k0 + piece) * f.unit);
+    const int end = min(sg.seen, (k0 + piece) << f.unit_log2);
 
     // queries: channel pairs (j, j + 4) of the lane's words, as the K fragments hold them
     uint32_t q[NT][2 * KW][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = r0 + t * 8 + g;
-      const int i = r / p.G;
+      const int i = token_of(p, r);
       const uint16_t* src =
           p.q + b * p.qb + i * p.qt + (static_cast<int64_t>(h) * p.G + r - i * p.G) * p.qh;
 #pragma unroll
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
     const uint8_t* mask = p.key_mask ? p.key_mask + b * p.mask_stride : nullptr;
     // the walk through the pages, ahead of the computation: word of the table and slot of the
     // next tile to copy
-    const int j0 = k0 * f.unit + warp * 16;
+    const int j0 = (k0 << f.unit_log2) + warp * 16;
     int j_ahead = j0;
     int t_ahead = j_ahead / p.page_size, slot_ahead = j_ahead - t_ahead * p.page_size;
     auto page_ahead = [&]() {
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
         *reinterpret_cast<float2*>(f.part_o + (part * ROWS + r) * D + 2 * ch) = acc;
         if (ch == 0) f.part_ml[part * ROWS + r] = make_float2(mx, sum);
       } else {
-        const int i = (r0 + r) / p.G, hq = h * p.G + (r0 + r) - i * p.G;
+        const int i = token_of(p, r0 + r), hq = h * p.G + (r0 + r) - i * p.G;
         uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + 2 * ch;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const uint32_t w = bf2_pack(acc.x * inv, acc.y * inv);
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
 }
 
 struct FewSizes {
-  int nt, row_tiles, ctas, unit;
+  int nt, row_tiles, ctas, unit_log2;
   bool split;  // some segment can have more than one unit
   size_t off_ml, off_parts, bytes;
 };
@@ -543,9 +543,12 @@ FewSizes few_sizes(int B, int n, int G, int heads, int D, int max_len, int sm_co
   s.ctas = sm_count * few_ctas_per_sm(D, s.nt);
   // Up to kShort entries a segment is one unit: four warps take it in a few tiles each, sooner than
   // a second kernel could join its parts.
-  constexpr int kShort = 512;
-  s.unit = max_len <= kShort ? kShort : kStep;
-  s.split = max_len > s.unit;
+  constexpr int kShort = 9;  // log2
+  static_assert(1 << 6 == kStep, "");
+  s.unit_log2 = max_len <= 1 << kShort
+                    ? kShort
+                    : unit_log2_of(static_cast<int64_t>(B) * s.row_tiles * heads, max_len, 6);
+  s.split = max_len > 1 << s.unit_log2;
   const size_t parts = static_cast<size_t>(2) * s.ctas * 8 * s.nt;
   s.off_ml = kWsHeader + parts * D * 4;
   s.off_parts = s.off_ml + parts * 8;
@@ -585,7 +588,7 @@ cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count,
   AttnPlan f{};
   f.row_tiles = s.row_tiles;
   f.ctas = s.ctas;
-  f.unit = s.unit;
+  f.unit_log2 = s.unit_log2;
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + s.off_ml);

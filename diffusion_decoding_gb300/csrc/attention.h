@@ -21,6 +21,7 @@ struct AttnParams {
   int table_stride, pages, page_size;
   int heads;  // of the cache
   int G;      // query heads per cache head
+  uint32_t g_magic;  // floor(2^32 / G) + 1: r / G = umulhi(r, g_magic) while r * G < 2^32 (0: divide)
   const int32_t* lens;
   int max_len;
   const uint8_t* key_mask;

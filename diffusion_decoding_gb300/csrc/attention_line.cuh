@@ -16,7 +16,7 @@
 namespace dllm {
 
 struct AttnPlan {
-  int unit;         // entries of a unit
+  int unit_log2;    // entries of a unit, a power of two; the line has fewer than 2^31 units
   int row_tiles;
   int q_aligned;    // query rows on 16-byte boundaries
   int out_aligned;  // output rows too
@@ -27,17 +27,29 @@ struct AttnPlan {
   int32_t* status;
 };
 
+// log2 of the entries of a unit: at least `least`, and so many that no line reaches 2^31 units.
+inline int unit_log2_of(int64_t segments, int max_len, int least) {
+  int lg = least;
+  while (segments * ((static_cast<int64_t>(max_len) >> lg) + 1) >= (int64_t{1} << 31)) ++lg;
+  return lg;
+}
+
 namespace {
 
 __device__ __forceinline__ int length_of(const AttnParams& p, int b) {
   return p.lens ? max(0, min(__ldg(p.lens + b), p.max_len)) : p.max_len;
 }
-__device__ __forceinline__ int units_of(int entries, int unit) {
-  return max(1, (entries + unit - 1) / unit);
+__device__ __forceinline__ int units_of(int entries, const AttnPlan& f) {
+  return max(1, (entries + (1 << f.unit_log2) - 1) >> f.unit_log2);
+}
+// Token of row r.
+__device__ __forceinline__ int token_of(const AttnParams& p, int r) {
+  return p.g_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.g_magic))
+                   : p.G == 1 ? r : r / p.G;
 }
 // Row r sees the entries below this (if its mask and the pages let it).
 __device__ __forceinline__ int rows_see(const AttnParams& p, int len, int r) {
-  return p.causal ? min(len, len - p.n + r / p.G + 1) : len;
+  return p.causal ? min(len, len - p.n + token_of(p, r) + 1) : len;
 }
 // The last row of a tile sees the most.
 template <int ROWS>
@@ -49,32 +61,24 @@ __device__ __forceinline__ int tile_sees(const AttnParams& p, int len, int rt) {
 // cut into f.ctas stretches that differ by one unit at most.  Built and asked by whole warps.
 template <int ROWS>
 struct Line {
-  int64_t total, each, longer;  // units; units of a stretch; stretches with one unit more
-  int64_t own, upto;            // this lane's item (of the first 32): its units, and all up to it
+  int total, each, longer;  // units; units of a stretch; stretches with one unit more
+  int own, upto;            // this lane's item (of the first 32): its units, and all up to it
   int items;
   bool equal;
 
-  __device__ __forceinline__ int64_t weight(const AttnParams& p, const AttnPlan& f, int item) const {
+  __device__ __forceinline__ int weight(const AttnParams& p, const AttnPlan& f, int item) const {
     if (item >= items) return 0;
-    const int b = item / f.row_tiles, rt = item - b * f.row_tiles;
-    return static_cast<int64_t>(p.heads) * units_of(tile_sees<ROWS>(p, length_of(p, b), rt), f.unit);
+    const int b = f.row_tiles == 1 ? item : item / f.row_tiles, rt = item - b * f.row_tiles;
+    return p.heads * units_of(tile_sees<ROWS>(p, length_of(p, b), rt), f);
   }
-  static __device__ __forceinline__ int64_t scan(int64_t v) {
+  static __device__ __forceinline__ int scan(int v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(kFull, v, o);
+      const int x = __shfl_up_sync(kFull, v, o);
       if (lane >= o) v += x;
     }
     return v;
-  }
-  // sum of the weights of items [32, upto)
-  __device__ __forceinline__ int64_t sum_from_32(const AttnParams& p, const AttnPlan& f, int to) const {
-    int64_t sum = 0;
-    for (int k = 32 + (threadIdx.x & 31); k < to; k += 32) sum += weight(p, f, k);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    return sum;
   }
   __device__ __forceinline__ void build(const AttnParams& p, const AttnPlan& f) {
     items = p.B * f.row_tiles;
@@ -82,32 +86,37 @@ struct Line {
     own = weight(p, f, threadIdx.x & 31);
     upto = scan(own);
     total = __shfl_sync(kFull, upto, 31);
-    if (items > 32) total = equal ? weight(p, f, 0) * items : total + sum_from_32(p, f, items);
-    if (total >> 32)
-      each = total / f.ctas;
-    else
-      each = static_cast<uint32_t>(total) / static_cast<uint32_t>(f.ctas);
+    if (items > 32) {
+      if (equal) {
+        total = weight(p, f, 0) * items;
+      } else {
+        int sum = 0;
+        for (int k = 32 + (threadIdx.x & 31); k < items; k += 32) sum += weight(p, f, k);
+        total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(sum)));
+      }
+    }
+    each = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(f.ctas));
     longer = total - each * f.ctas;
   }
   // first unit of CTA c's stretch
-  __device__ __forceinline__ int64_t start(int64_t c) const {
-    return each * c + (c < longer ? c : longer);
-  }
+  __device__ __forceinline__ int start(int c) const { return each * c + min(c, longer); }
   // CTA whose stretch holds unit u
-  __device__ __forceinline__ int64_t holder(int64_t u) const {
-    const int64_t head = longer * (each + 1);
-    return u < head ? u / (each + 1) : longer + (u - head) / each;
+  __device__ __forceinline__ int holder(int u) const {
+    const int head = longer * (each + 1);
+    return u < head ? static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(each + 1))
+                    : longer + static_cast<int>(static_cast<unsigned>(u - head) /
+                                                static_cast<unsigned>(each));
   }
   // item that holds unit `at` (< total), and the units before that item
-  __device__ __forceinline__ int find(const AttnParams& p, const AttnPlan& f, int64_t at,
-                                      int64_t* before) const {
+  __device__ __forceinline__ int find(const AttnParams& p, const AttnPlan& f, int at,
+                                      int* before) const {
     const int lane = threadIdx.x & 31;
     if (items > 32 && equal) {
-      const int64_t per = weight(p, f, 0);
-      *before = at / per * per;
-      return static_cast<int>(at / per);
+      const int per = weight(p, f, 0), item = at / per;
+      *before = item * per;
+      return item;
     }
-    int64_t base = 0, mine = own, incl = upto;
+    int base = 0, mine = own, incl = upto;
     for (int i0 = 0;;) {
       const unsigned hit = __ballot_sync(kFull, base + incl > at);
       if (hit != 0u || i0 + 32 >= items) {
@@ -133,21 +142,20 @@ struct Segment {
   int k0;     // first unit to do
 
   __device__ __forceinline__ void at_item(const AttnParams& p, const AttnPlan& f) {
-    b = item / f.row_tiles;
+    b = f.row_tiles == 1 ? item : item / f.row_tiles;
     rt = item - b * f.row_tiles;
     len = length_of(p, b);
     seen = tile_sees<ROWS>(p, len, rt);
-    units = units_of(seen, f.unit);
+    units = units_of(seen, f);
   }
   __device__ __forceinline__ void find(const AttnParams& p, const AttnPlan& f, const Line<ROWS>& line,
-                                       int64_t u) {
-    int64_t before;
+                                       int u) {
+    int before;
     item = line.find(p, f, u, &before);
     at_item(p, f);
-    const int64_t in = u - before;
-    h = static_cast<int>(in >> 32 ? in / units
-                                  : static_cast<uint32_t>(in) / static_cast<uint32_t>(units));
-    k0 = static_cast<int>(in - static_cast<int64_t>(h) * units);
+    const int in = u - before;
+    h = static_cast<int>(static_cast<unsigned>(in) / static_cast<unsigned>(units));
+    k0 = in - h * units;
   }
   __device__ __forceinline__ void next(const AttnParams& p, const AttnPlan& f) {
     k0 = 0;
@@ -167,24 +175,24 @@ constexpr int kJoinThreads = 32 * kJoinWarps;
 template <int ROWS>
 __device__ __forceinline__ void note_segment(const AttnPlan& f, const AttnParams& p,
                                              const Line<ROWS>& line, const Segment<ROWS>& sg,
-                                             int64_t u, int64_t u0, bool whole) {
+                                             int u, int u0, bool whole) {
   if (sg.k0 != 0) return;
   f.parts[static_cast<int64_t>(sg.item) * p.heads + sg.h] =
       whole ? make_int2(-1, 0)
             : make_int2(2 * static_cast<int>(blockIdx.x) + (u == u0 ? 0 : 1),
-                        static_cast<int>(line.holder(u + sg.units - 1)));
+                        line.holder(u + sg.units - 1));
 }
 
 __device__ __forceinline__ void store_joined(const AttnParams& p, int b, int h, int r, int ch, float2 a,
                                              float inv) {
-  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  const int i = token_of(p, r), hq = h * p.G + r - i * p.G;
   const uint32_t w = bf2_pack(a.x * inv, a.y * inv);
   uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + ch;
   dst[0] = static_cast<uint16_t>(w);
   dst[1] = static_cast<uint16_t>(w >> 16);
 }
 __device__ __forceinline__ void store_lse(const AttnParams& p, int b, int h, int r, float m, float sum) {
-  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  const int i = token_of(p, r), hq = h * p.G + r - i * p.G;
   if (p.lse)
     p.lse[(static_cast<int64_t>(b) * p.heads * p.G + hq) * p.n + i] =
         sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;

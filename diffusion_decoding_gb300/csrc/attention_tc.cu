@@ -177,10 +177,10 @@ struct Smem {
 template <int ROWS>
 struct Piece {
   int units, j0, end, tiles;
-  __device__ __forceinline__ Piece(const Segment<ROWS>& sg, const AttnPlan& f, int64_t left) {
-    units = static_cast<int>(min(static_cast<int64_t>(sg.units - sg.k0), left));
-    j0 = sg.k0 * f.unit;
-    end = min(sg.seen, j0 + units * f.unit);
+  __device__ __forceinline__ Piece(const Segment<ROWS>& sg, const AttnPlan& f, int left) {
+    units = min(sg.units - sg.k0, left);
+    j0 = sg.k0 << f.unit_log2;
+    end = min(sg.seen, (sg.k0 + units) << f.unit_log2);
     tiles = end > j0 ? (end - j0 + kTile - 1) / kTile : 0;
   }
 };
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   Line<ROWS> line;
   line.build(p, f);
-  const int64_t u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
+  const int u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
   if (u0 >= u1) return;
   if (warp == 16) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   tc_before();
@@ -261,13 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = lanes + col_s(grp), t_p = lanes + col_p(grp), t_o = lanes + col_o(grp);
     const uint32_t scratch = sbase + M::kScratch + warp * 2048;
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-    for (int64_t u = u0; u < u1;) {
+    for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       const int b = sg.b, h = sg.h;
       const int first = kShare ? 0 : (grp ^ step) & 1;  // this group's first tile of the segment
       const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
       const int r = sg.rt * ROWS + (kShare ? grp * kRows : 0) + row_in;
-      if (threadIdx.x == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
       {
         // a negative scale turns the sign of Q, one of zero makes Q zero: both exact
         const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int rr = r - lane + e * 8 + lr;
-          const int ri = rr / p.G;
+          const int ri = token_of(p, rr);
           const uint16_t* src =
               p.q + b * p.qb + ri * p.qt + (h * p.G + rr - ri * p.G) * p.qh + lp * 8;
 #pragma unroll
@@ -452,6 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int SPAN = kShare ? D : D / 2;
         const int c0 = kShare ? 0 : grp * SPAN;
         const uint32_t t_other = lanes + col_o(grp ^ 1);
+        int64_t out_row[4];  // element of p.out where the lane's piece of row 8 e + lane / 4 starts
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int rr = r - lane + e * 8 + (lane >> 2), ri = token_of(p, rr);
+          out_row[e] = rr < rows ? b * p.ob + ri * p.ot + (h * p.G + rr - ri * p.G) * p.oh +
+                                       (lane & 3) * 8
+                                 : INT64_MIN;
+        }
 #pragma unroll 1
         for (int c = c0; c < c0 + SPAN; c += 32) {
           float o[32];
@@ -493,21 +500,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                            "r"(bf2_pack(o[8 * k + 5] * inv, o[8 * k + 7] * inv))
                            : "memory");
             __syncwarp();
+            uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int lr = e * 8 + (lane >> 2), lp = lane & 3, rr = r - lane + lr;
-              const uint4 v = ld_shared_v4(scratch + lr * 64 + ((lp ^ (lr >> 1 & 3)) << 4));
-              if (rr < rows) {
-                const int ri = rr / p.G;
-                uint16_t* dst =
-                    p.out + b * p.ob + ri * p.ot + (h * p.G + rr - ri * p.G) * p.oh + c + lp * 8;
-                if (f.out_aligned) {
-                  *reinterpret_cast<uint4*>(dst) = v;
-                } else {
-                  const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+              const int lr = e * 8 + (lane >> 2);
+              v[e] = ld_shared_v4(scratch + lr * 64 + (((lane & 3) ^ (lr >> 1 & 3)) << 4));
+            }
 #pragma unroll
-                  for (int x = 0; x < 8; ++x) dst[x] = static_cast<uint16_t>(y[x >> 1] >> (16 * (x & 1)));
-                }
+            for (int e = 0; e < 4; ++e) {
+              if (out_row[e] == INT64_MIN) continue;
+              uint16_t* dst = p.out + out_row[e] + c;
+              if (f.out_aligned) {
+                *reinterpret_cast<uint4*>(dst) = v[e];
+              } else {
+                const uint32_t y[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+                for (int x = 0; x < 8; ++x) dst[x] = static_cast<uint16_t>(y[x >> 1] >> (16 * (x & 1)));
               }
             }
           }
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kp[PER], vp[PER];
       bool seen[PER];
     };
-    for (int64_t u = u0; u < u1;) {
+    for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       const int h = sg.h;
       const int32_t* table = p.table + static_cast<int64_t>(sg.b) * p.table_stride;
@@ -654,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_low = desc_low(sbase + M::kQ, 16);
       bool ok = true;
       int piece_no = 0;
-      for (int64_t u = u0; u < u1; ++piece_no) {
+      for (int u = u0; u < u1; ++piece_no) {
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int first = kShare ? 0 : (grp ^ step) & 1;
         const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
@@ -706,6 +714,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < u1) sg.next(p, f);
       }
       mma_commit(lead, done_bar);
+    } else if (grp == 2) {
+      // notes for the join, and the next segment's queries on their way to L2
+      for (int u = u0; u < u1;) {
+        const Piece<ROWS> pc(sg, f, u1 - u);
+        if (lane == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
+        u += pc.units;
+        if (u >= u1) break;
+        sg.next(p, f);
+        const int r1 = min((sg.rt + 1) * ROWS, rows);
+        for (int r = sg.rt * ROWS + lane; r < r1; r += 32) {
+          const int i = token_of(p, r);
+          const uint16_t* src = p.q + sg.b * p.qb + i * p.qt + (sg.h * p.G + r - i * p.G) * p.qh;
+#pragma unroll
+          for (int c = 0; c < D; c += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
+        }
+      }
     }
   }
 
@@ -764,7 +789,7 @@ __global__ void __launch_bounds__(128)
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = r / p.G, hq = h * p.G + r - i * p.G;
+  const int i = token_of(p, r), hq = h * p.G + r - i * p.G;
   uint16_t* dst = p.out + b * p.ob + i * p.ot + hq * p.oh + ch;
 #pragma unroll
   for (int x = 0; x < 4; x += 2) {
@@ -804,12 +829,14 @@ template <int D, bool kShare>
 static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaStream_t stream) {
   constexpr int R = kShare ? 2 * kRows : kRows;
   AttnPlan f{};
-  f.unit = kTile;
+  static_assert(1 << 6 == kTile, "");
+  f.unit_log2 = unit_log2_of(static_cast<int64_t>(p.B) * ((p.n * p.G + R - 1) / R) * p.heads,
+                             p.max_len, 6);
   f.row_tiles = (p.n * p.G + R - 1) / R;
   // a stretch is kLeast units at least: parts have to be joined again
   constexpr int kLeast = 4;
   const int64_t units = static_cast<int64_t>(p.B) * f.row_tiles * p.heads *
-                        std::max<int64_t>(1, (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile);
+                        ((static_cast<int64_t>(p.max_len) >> f.unit_log2) + 1);
   f.ctas = static_cast<int>(std::min<int64_t>(sm_count, (units + kLeast - 1) / kLeast));
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
@@ -825,7 +852,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   if (e != cudaSuccess) return e;
   e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
                        Smem<D>::kBytes, stream, p, f);
-  if (e != cudaSuccess || p.max_len <= f.unit) return e;
+  if (e != cudaSuccess || p.max_len <= 1 << f.unit_log2) return e;
   const int64_t joins = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (R / 32) * (D / 64);
   return launch_dependent(attention_tc_join_kernel<D, R>, dim3(static_cast<unsigned>(joins)),
                           dim3(128), 0, stream, p, f);
