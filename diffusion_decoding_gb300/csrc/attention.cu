@@ -275,16 +275,15 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
     const int j0 = (k0 << f.unit_log2) + warp * 16;
     int j_ahead = j0;
     int t_ahead = j_ahead / p.page_size, slot_ahead = j_ahead - t_ahead * p.page_size;
+    // (the word is looked at only when its tile is copied: a test here would wait for the load)
     auto page_ahead = [&]() {
-      if (j_ahead >= end || t_ahead >= p.table_stride) return -1;
-      const int pg = __ldg(table + t_ahead);
-      return pg >= 0 && pg < p.pages ? pg : -1;
+      return j_ahead < end && t_ahead < p.table_stride ? __ldg(table + t_ahead) : -1;
     };
     int page = page_ahead();
     // copy the next tile into the stage at byte `at` of the ring and look the page after it up;
     // whether the tile was there
     auto copy = [&](uint32_t at) {
-      const bool there = page >= 0;
+      const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
       if (there) {
         const int64_t row = (static_cast<int64_t>(page) * p.heads + h) * p.page_size + slot_ahead;
         const uint8_t* ks = k_of_lane + row * (D / 2);

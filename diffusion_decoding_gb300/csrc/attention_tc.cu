@@ -164,6 +164,13 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A whole warp's wait: one vote when the phase is complete already; the same bounded wait otherwise.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* status) {
+  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status)) != 0;
+}
+
 template <int D>
 struct Smem {
   static constexpr uint32_t kTensor = kTile * D * 2;  // K (or V) of a stage
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int g = 0; g < 2; ++g) {
       const uint32_t bar = gbars + kGroupBars * g;
       mbar_init(bar + kBarQ, kShare ? 4 : 8);
-      mbar_init(bar + kBarS, 1);
+      mbar_init(bar + kBarS, 2);  // the scores' completion, and the issuer's word that their mask is there
       mbar_init(bar + kBarFree, 4);
       mbar_init(bar + kBarP, 4);
       mbar_init(bar + kBarV, 1);
@@ -346,9 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int n = 0; n < count; ++n) {
         const int t = first + n * STRIDE, k = step + t, st = stage_of(k);
-        // the mask words of the stage, and the scores
-        ok = ok && wait_bar(full0 + 8 * st, parity_of(k), abort_v, f.status);
-        ok = __all_sync(kFull, ok && wait_bar(bar + kBarS, (mine + n) & 1, abort_v, f.status));
+        // the scores and the mask words of their stage
+        ok = wait_warp(bar + kBarS, (mine + n) & 1, abort_v, f.status);
         if (!ok) break;
         tc_after();
         float s[kTile];
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2 = pack2(la * keep, lb * keep);
           if (n > 0) {
             // the products before have been added to O
-            ok = __all_sync(kFull, wait_bar(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status));
+            ok = wait_warp(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status);
             if (!ok) break;
             tc_after();
 #pragma unroll 1
@@ -413,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[e / 2] = bf2_pack(a, d);
         }
         if (n > 0) {  // P of the step before has been read
-          ok = __all_sync(kFull, wait_bar(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status));
+          ok = wait_warp(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status);
           if (!ok) break;
           tc_after();
         }
@@ -427,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unpack2(l2, l, l_odd);
       l += l_odd;
       // ---- output.  Groups with the same rows: each takes half of the channels of both.
-      ok = ok && (count == 0 || wait_bar(bar + kBarV, (mine + count - 1) & 1, abort_v, f.status));
-      ok = __all_sync(kFull, ok);
+      if (count > 0 && ok) ok = wait_warp(bar + kBarV, (mine + count - 1) & 1, abort_v, f.status);
       if constexpr (!kShare) {
         ml_s[grp][row_in] = make_float2(m, l);
         asm volatile("bar.sync 1, 256;" ::: "memory");  // both groups' products are complete
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_other = lanes + col_o(grp ^ 1);
         int64_t out_row[4];  // element of p.out where the lane's piece of row 8 e + lane / 4 starts
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4 && direct; ++e) {
           const int rr = r - lane + e * 8 + (lane >> 2), ri = token_of(p, rr);
           out_row[e] = rr < rows ? b * p.ob + ri * p.ot + (h * p.G + rr - ri * p.G) * p.oh +
                                        (lane & 3) * 8
@@ -564,11 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
       }
     };
-    struct Raw {
-      uint4 k[PER], v[PER];
-      uint32_t kp[PER], vp[PER];
-      bool seen[PER];
-    };
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       const int h = sg.h;
@@ -579,11 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j_at = pc.j0 + t_first * kTile + entry0;
       int word[PER] = {}, slot[PER] = {}, page[PER] = {};
       auto look_up = [&](int e) {
+        // (looked at only when its codes are loaded: a test here would wait for the load)
         page[e] = -1;
-        if (j_at + 32 * e < pc.end && word[e] < p.table_stride) {
-          const int pg = __ldg(table + word[e]);
-          if (pg >= 0 && pg < p.pages) page[e] = pg;
-        }
+        if (j_at + 32 * e < pc.end && word[e] < p.table_stride) page[e] = __ldg(table + word[e]);
       };
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
@@ -591,21 +589,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot[e] = j_at + 32 * e - word[e] * p.page_size;
         look_up(e);
       }
-      // load the next tile's codes and look the pages of the one after it up
-      auto load = [&](Raw& raw) {
+      // Codes of one tile in registers.  As soon as a piece has been turned, that of the thread's
+      // next tile is loaded in its place.
+      uint4 kc[PER], vc[PER];
+      uint32_t kp[PER], vp[PER], seen[PER];
+      int64_t row[PER];  // of the cache, -1: absent
+      auto next_rows = [&]() {
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          raw.seen[e] = page[e] >= 0 && (!mask || __ldg(mask + j_at + 32 * e) != 0);
-          raw.k[e] = raw.v[e] = make_uint4(0u, 0u, 0u, 0u);
-          raw.kp[e] = raw.vp[e] = 0u;
-          if (page[e] >= 0) {
-            const int64_t row = (static_cast<int64_t>(page[e]) * p.heads + h) * p.page_size + slot[e];
-            raw.k[e] = ld_stream_v4(p.k_codes + row * (D / 2) + g * 16);
-            raw.v[e] = ld_stream_v4(p.v_codes + row * (D / 2) + g * 16);
-            raw.kp[e] = __ldg(p.k_params + row * (D / 32) + g);
-            raw.vp[e] = __ldg(p.v_params + row * (D / 32) + g);
-          }
+        for (int e = 0; e < PER; ++e)
+          row[e] = static_cast<unsigned>(page[e]) < static_cast<unsigned>(p.pages)
+                       ? (static_cast<int64_t>(page[e]) * p.heads + h) * p.page_size + slot[e]
+                       : -1;
+      };
+      auto load_k = [&](int e) {
+        kc[e] = make_uint4(0u, 0u, 0u, 0u);
+        kp[e] = seen[e] = 0u;
+        if (row[e] >= 0) {
+          kc[e] = ld_stream_v4(p.k_codes + row[e] * (D / 2) + g * 16);
+          kp[e] = __ldg(p.k_params + row[e] * (D / 32) + g);
+          seen[e] = mask ? __ldg(mask + j_at + 32 * e) : 1u;
         }
+      };
+      auto load_v = [&](int e) {
+        vc[e] = make_uint4(0u, 0u, 0u, 0u);
+        vp[e] = 0u;
+        if (row[e] >= 0) {
+          vc[e] = ld_stream_v4(p.v_codes + row[e] * (D / 2) + g * 16);
+          vp[e] = __ldg(p.v_params + row[e] * (D / 32) + g);
+        }
+      };
+      auto advance = [&]() {
         j_at += AHEAD;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
@@ -618,33 +631,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           look_up(e);
         }
       };
-      Raw raw;
-      load(raw);
+      next_rows();
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        load_k(e);
+        load_v(e);
+      }
+      advance();
       for (int t = t_first; t < pc.tiles; t += 2) {
         const int k = step + t, st = stage_of(k);
-        Raw cur = raw;
-        load(raw);
-        if (!__all_sync(kFull, wait_bar(empty0 + 8 * st, parity_of(k) ^ 1, abort_v, f.status))) break;
-        const uint32_t sk = st * M::kStage, sv = sk + M::kTensor;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          turn(cur.k[e], cur.kp[e], sk + e * 32 * 128);
-          // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
-          turn(cur.v[e], cur.seen[e] ? cur.vp[e] : 0u, sv + e * 32 * 128);
-        }
+        if (!wait_warp(empty0 + 8 * st, parity_of(k) ^ 1, abort_v, f.status)) break;
         // entries 8w .. 8w + 7 of each half of the tile
+        uint32_t see_v[PER];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           unsigned bits;
           if constexpr (GROUPS == 4)
-            bits = __ballot_sync(kFull, cur.seen[e % PER]) & 0xffu;
+            bits = __ballot_sync(kFull, seen[e % PER] != 0u) & 0xffu;
           else
-            bits = __ballot_sync(kFull, cur.seen[0]) >> (16 * e) & 0xffu;
+            bits = __ballot_sync(kFull, seen[0] != 0u) >> (16 * e) & 0xffu;
           if (lane == 0) reinterpret_cast<uint8_t*>(&visible[st][e])[w] = static_cast<uint8_t>(bits);
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) see_v[e] = seen[e];
+        next_rows();
+        const uint32_t sk = st * M::kStage, sv = sk + M::kTensor;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          turn(kc[e], kp[e], sk + e * 32 * 128);
+          load_k(e);
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
+          turn(vc[e], see_v[e] != 0u ? vp[e] : 0u, sv + e * 32 * 128);
+          load_v(e);
         }
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(full0 + 8 * st);
+        advance();
       }
       step += pc.tiles;
       u += pc.units;
@@ -667,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first = kShare ? 0 : (grp ^ step) & 1;
         const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
         auto wait = [&](uint32_t at, uint32_t parity) {
-          return __all_sync(kFull, wait_bar(at, parity, abort_v, f.status)) != 0;
+          return wait_warp(at, parity, abort_v, f.status);
         };
         // every phase of kBarQ is waited for, of segments without tiles too
         ok = ok && wait(bar + kBarQ, piece_no & 1);
@@ -686,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      idesc(kTile, false), x > 0);
           }
           mma_commit(lead, bar + kBarS);
+          if (lead) mbar_arrive(bar + kBarS);
           return true;
         };
         if (count > 0) ok = ok && scores(step + first);
