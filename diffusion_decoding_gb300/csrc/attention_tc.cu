@@ -351,8 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;
       uint64_t l2 = 0;  // two partial sums
       bool ok = true;
+      int st = stage_of(step + first);
       for (int n = 0; n < count; ++n) {
-        const int t = first + n * STRIDE, k = step + t, st = stage_of(k);
+        const int t = first + n * STRIDE;
         // the scores and the mask words of their stage
         ok = wait_warp(bar + kBarS, (mine + n) & 1, abort_v, f.status);
         if (!ok) break;
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(t_s, s);
         tmem_ld32(t_s + 32, s + 32);
         const uint32_t vis0 = visible[st][0], vis1 = visible[st][1];
+        st = st + STRIDE >= kStages ? st + STRIDE - kStages : st + STRIDE;
         tmem_wait_ld();
         tc_before();
         __syncwarp();
@@ -409,29 +411,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mu = m == -INFINITY ? 0.f : m;
         const uint64_t scale2 = pack2(scale, scale), mu2 = pack2(-mu, -mu);
         uint32_t* pk = reinterpret_cast<uint32_t*>(s);  // in place
+        // P of the step before has been read, as a rule: asked now, needed after the exponentials
+        const bool p_free = n == 0 || mbar_try_wait(bar + kBarV, (mine + n - 1) & 1);
+        uint64_t l_odd = 0;
 #pragma unroll
-        for (int e = 0; e < kTile; e += 2) {
-          float a, d;
-          unpack2(fma2(pack2(s[e], s[e + 1]), scale2, mu2), a, d);
-          a = ex2(a);
-          d = ex2(d);
-          l2 = add2(l2, pack2(a, d));
-          pk[e / 2] = bf2_pack(a, d);
+        for (int e = 0; e < kTile; e += 4) {
+          float a0, a1, a2, a3;
+          unpack2(fma2(pack2(s[e], s[e + 1]), scale2, mu2), a0, a1);
+          unpack2(fma2(pack2(s[e + 2], s[e + 3]), scale2, mu2), a2, a3);
+          a0 = ex2(a0), a1 = ex2(a1), a2 = ex2(a2), a3 = ex2(a3);
+          l2 = add2(l2, pack2(a0, a1));
+          l_odd = add2(l_odd, pack2(a2, a3));
+          pk[e / 2] = bf2_pack(a0, a1);
+          pk[e / 2 + 1] = bf2_pack(a2, a3);
         }
-        if (n > 0) {  // P of the step before has been read
+        l2 = add2(l2, l_odd);
+        if (!__all_sync(kFull, p_free)) {
           ok = wait_warp(bar + kBarV, (mine + n - 1) & 1, abort_v, f.status);
           if (!ok) break;
-          tc_after();
         }
+        tc_after();
         tmem_st32(t_p, pk);
         tmem_wait_st();
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + kBarP);
       }
-      float l, l_odd;
-      unpack2(l2, l, l_odd);
-      l += l_odd;
+      float l, l_hi;
+      unpack2(l2, l, l_hi);
+      l += l_hi;
       // ---- output.  Groups with the same rows: each takes half of the channels of both.
       if (count > 0 && ok) ok = wait_warp(bar + kBarV, (mine + count - 1) & 1, abort_v, f.status);
       if constexpr (!kShare) {
@@ -607,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row[e] >= 0) {
           kc[e] = ld_stream_v4(p.k_codes + row[e] * (D / 2) + g * 16);
           kp[e] = __ldg(p.k_params + row[e] * (D / 32) + g);
-          seen[e] = mask ? __ldg(mask + j_at + 32 * e) : 1u;
+          seen[e] = mask ? __ldg(mask + j_at - AHEAD + 32 * e) : 1u;
         }
       };
       auto load_v = [&](int e) {
@@ -632,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       next_rows();
+      advance();
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
         load_k(e);
         load_v(e);
       }
-      advance();
       for (int t = t_first; t < pc.tiles; t += 2) {
         const int k = step + t, st = stage_of(k);
         if (!wait_warp(empty0 + 8 * st, parity_of(k) ^ 1, abort_v, f.status)) break;
@@ -655,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < PER; ++e) see_v[e] = seen[e];
         next_rows();
+        advance();  // the pages of the tile after the next have a whole round to arrive
         const uint32_t sk = st * M::kStage, sv = sk + M::kTensor;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
@@ -670,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(full0 + 8 * st);
-        advance();
       }
       step += pc.tiles;
       u += pc.units;
