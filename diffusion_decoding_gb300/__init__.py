@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -67,7 +68,9 @@ class dllm_kv4_cache(ctypes.Structure):
                 ("page_size", _c_i32), ("head_dim", _c_i32), ("table_stride", _c_i32)]
 
 
-_P_HEADS, _P_CACHE = ctypes.POINTER(dllm_heads), ctypes.POINTER(dllm_kv4_cache)
+_byref = ctypes.byref
+_P_HEADS = _c_vp  # const dllm_heads*: byref of the structure, or its bytes
+_P_CACHE = ctypes.POINTER(dllm_kv4_cache)
 
 _SIGS = {
     "dllm_last_error": (ctypes.c_char_p, []),
@@ -171,8 +174,16 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch._C._cuda_getDevice())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
+
+
+# The current stream's handle without a Stream object around it (a quarter of the time).
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               if hasattr(torch._C, "_cuda_getDevice") else None)
 
 
 def _check(status: int, name: str) -> None:
@@ -278,25 +289,40 @@ class Kv4Cache:
         self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
         self._c = dllm_kv4_cache(_ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params),
                                  _ptr(table), pages, heads, page_size, 2 * half, table.shape[1])
+        self.B, self.ref = table.shape[0], _byref(self._c)
 
     def c(self) -> dllm_kv4_cache:
         return self._c
+
+
+_DTYPES = {torch.float32: DLLM_F32, torch.bfloat16: DLLM_BF16}
+_pack_heads = struct.Struct("Pii3q").pack  # dllm_heads
+assert struct.calcsize("Pii3q") == ctypes.sizeof(dllm_heads)
 
 
 def heads_of(t: torch.Tensor) -> dllm_heads:
     """Descriptor of a [B, n, heads, head_dim] bf16 or fp32 tensor with contiguous channels."""
     if t.dim() != 4:
         raise ValueError("need a [B, n, heads, head_dim] tensor")
-    sb, st, sh, sc = t.stride()
-    if sc != 1 and t.shape[3] != 1:
-        raise ValueError("channels must be contiguous")
-    if t.dtype == torch.bfloat16:
-        dt = DLLM_BF16
-    elif t.dtype == torch.float32:
-        dt = DLLM_F32
-    else:
+    return dllm_heads.from_buffer_copy(_rows(t, t.shape[0], t.shape[1], t.shape[3]))
+
+
+def _rows(t: torch.Tensor, B: int, n: int, D: int) -> bytes:
+    """The bytes of heads_of a tensor that has to be [B, n, any, D] (a ctypes structure takes longer
+    to make than they do, and a small call takes as long as the host needs to make it)."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError("need bfloat16 or float32")
-    return dllm_heads(t.data_ptr(), t.shape[2], dt, sb, st, sh)
+    stride = t.stride()
+    if len(stride) != 4:
+        raise ValueError("need [B, n, heads, head_dim] tensors")
+    b, m, h, d = t.shape
+    sb, st, sh, sc = stride
+    if b != B or m != n or d != D:
+        raise ValueError("the tensors differ in B, n or head_dim")
+    if sc != 1 and d != 1:
+        raise ValueError("channels must be contiguous")
+    return _pack_heads(t.data_ptr(), h, dt, sb, st, sh)
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -468,10 +494,13 @@ def dllm_rope_phases(rotary_dim: int, phases: torch.Tensor, base: float = 10000.
 def _pos_stride(pos, B: int, n: int) -> int:
     if pos is None:
         return 0
-    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[0] != B or pos.shape[1] < n \
-            or (pos.stride(1) != 1 and pos.shape[1] != 1):
+    if pos.dtype is not torch.int32 or pos.dim() != 2:
+        raise ValueError("pos must be [B, >= n] int32")
+    b, m = pos.shape
+    stride, unit = pos.stride()
+    if b != B or m < n or (unit != 1 and m != 1):
         raise ValueError("pos must be [B, >= n] int32 with contiguous rows")
-    return pos.stride(0)
+    return stride
 
 
 def dllm_qk_norm_rope(q, k, q_out, k_out, pos, phases, q_weight=None, k_weight=None,
@@ -482,46 +511,52 @@ def dllm_qk_norm_rope(q, k, q_out, k_out, pos, phases, q_weight=None, k_weight=N
     dllm_rope_phases table, two channels per entry are rotated (None: no rotation)."""
     x = q if q is not None else k
     B, n, _, D = x.shape
-    for t in (q, k, q_out, k_out):
-        if t is not None and (t.shape[0] != B or t.shape[1] != n or t.shape[3] != D):
-            raise ValueError("the tensors differ in B, n or head_dim")
+    dtype = x.dtype
     for w in (q_weight, k_weight):
-        if w is not None and (w.numel() != D or w.dtype != x.dtype or not w.is_contiguous()):
+        if w is not None and (w.dtype is not dtype or w.numel() != D or not w.is_contiguous()):
             raise ValueError("weights must be contiguous, [head_dim], of the tensors' dtype")
-    hs = [None if t is None else ctypes.byref(heads_of(t)) for t in (q, q_out, k, k_out)]
-    rotary = 0 if phases is None else 2 * phases.numel()
-    _check(lib().dllm_qk_norm_rope(*hs, B, n, D, _ptr(pos), _pos_stride(pos, B, n), _ptr(phases),
-                                   rotary, int(interleaved), magnitude, int(norm), _ptr(q_weight),
-                                   _ptr(k_weight), eps, _stream(stream)), "dllm_qk_norm_rope")
+    hq = hqo = hk = hko = None
+    if q is not None:
+        hq = _rows(q, B, n, D)
+    if q_out is not None:
+        hqo = _rows(q_out, B, n, D)
+    if k is not None:
+        hk = _rows(k, B, n, D)
+    if k_out is not None:
+        hko = _rows(k_out, B, n, D)
+    status = lib().dllm_qk_norm_rope(
+        hq, hqo, hk, hko, B, n, D, _ptr(pos), _pos_stride(pos, B, n), _ptr(phases),
+        0 if phases is None else 2 * phases.numel(), interleaved, magnitude, norm, _ptr(q_weight),
+        _ptr(k_weight), eps, _stream(stream))
+    if status:
+        _check(status, "dllm_qk_norm_rope")
 
 
-def _check_rows(cache: Kv4Cache, k, v) -> None:
-    if k.shape != v.shape or k.shape[3] != cache.head_dim or k.shape[0] != cache.table.shape[0]:
+def _cache_rows(cache: Kv4Cache, k, v, pos):
+    B, n, _, D = k.shape
+    if D != cache.head_dim or B != cache.B:
         raise ValueError("k and v must be [B, n, heads, head_dim] of the cache")
+    return (cache.ref, _rows(k, B, n, D), _rows(v, B, n, D), B, n, _ptr(pos),
+            _pos_stride(pos, B, n))
 
 
 def dllm_kv4_write(cache: Kv4Cache, k, v, pos, stream=None) -> None:
     """Quantise k, v ([B, n, heads, head_dim]) into the entries pos ([B, >= n] int32, < 0: skip)."""
-    _check_rows(cache, k, v)
-    _check(lib().dllm_kv4_write(ctypes.byref(cache.c()), ctypes.byref(heads_of(k)),
-                                ctypes.byref(heads_of(v)), k.shape[0], k.shape[1], _ptr(pos),
-                                _pos_stride(pos, k.shape[0], k.shape[1]), _stream(stream)),
-           "dllm_kv4_write")
+    status = lib().dllm_kv4_write(*_cache_rows(cache, k, v, pos), _stream(stream))
+    if status:
+        _check(status, "dllm_kv4_write")
 
 
 def dllm_kv4_read(cache: Kv4Cache, k, v, pos=None, stream=None) -> None:
     """Read the entries pos (None: 0 .. n-1) back into k, v ([B, n, heads, head_dim])."""
-    _check_rows(cache, k, v)
-    _check(lib().dllm_kv4_read(ctypes.byref(cache.c()), ctypes.byref(heads_of(k)),
-                               ctypes.byref(heads_of(v)), k.shape[0], k.shape[1], _ptr(pos),
-                               _pos_stride(pos, k.shape[0], k.shape[1]), _stream(stream)),
-           "dllm_kv4_read")
+    status = lib().dllm_kv4_read(*_cache_rows(cache, k, v, pos), _stream(stream))
+    if status:
+        _check(status, "dllm_kv4_read")
 
 
 def dllm_attention_kv4_workspace_bytes(cache: Kv4Cache, B: int, n: int, q_heads: int,
                                        max_len: int) -> int:
-    return int(lib().dllm_attention_kv4_workspace_bytes(ctypes.byref(cache.c()), B, n, q_heads,
-                                                        max_len))
+    return int(lib().dllm_attention_kv4_workspace_bytes(cache.ref, B, n, q_heads, max_len))
 
 
 def dllm_attention_kv4(q, cache: Kv4Cache, lens, max_len: int, out, ws, lse=None, key_mask=None,
@@ -530,25 +565,26 @@ def dllm_attention_kv4(q, cache: Kv4Cache, lens, max_len: int, out, ws, lse=None
     [B, heads, n] fp32 or None; key_mask: [B, >= max_len] uint8 or bool, 0 = hidden; scale: None
     for head_dim ** -0.5."""
     B, n, H, D = q.shape
-    if out.shape != q.shape or D != cache.head_dim or B != cache.table.shape[0]:
+    if D != cache.head_dim or B != cache.B:
         raise ValueError("q and out must be [B, n, heads, head_dim] of the cache")
-    if lens is not None and (lens.dtype != torch.int32 or lens.numel() != B
+    if lens is not None and (lens.dtype is not torch.int32 or lens.numel() != B
                              or not lens.is_contiguous()):
         raise ValueError("lens must be [B] int32, contiguous")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, n)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, H, n)
                             or not lse.is_contiguous()):
         raise ValueError("lse must be [B, heads, n] float32, contiguous")
-    if key_mask is not None and (key_mask.element_size() != 1 or key_mask.dim() != 2
-                                 or key_mask.shape[0] != B or key_mask.shape[1] < max_len
-                                 or key_mask.stride(1) != 1):
-        raise ValueError("key_mask must be [B, >= max_len] uint8 or bool with contiguous rows")
-    _check(lib().dllm_attention_kv4(ctypes.byref(heads_of(q)), ctypes.byref(cache.c()),
-                                    _ptr(lens), max_len, _ptr(key_mask),
-                                    0 if key_mask is None else key_mask.stride(0),
-                                    D ** -0.5 if scale is None else scale, int(causal),
-                                    ctypes.byref(heads_of(out)), _ptr(lse), B, n, _ptr(ws),
-                                    ws.numel(), _stream(stream)),
-           "dllm_attention_kv4")
+    mask_stride = 0
+    if key_mask is not None:
+        if key_mask.element_size() != 1 or key_mask.dim() != 2 or key_mask.shape[0] != B \
+                or key_mask.shape[1] < max_len or key_mask.stride(1) != 1:
+            raise ValueError("key_mask must be [B, >= max_len] uint8 or bool with contiguous rows")
+        mask_stride = key_mask.stride(0)
+    status = lib().dllm_attention_kv4(
+        _rows(q, B, n, D), cache.ref, _ptr(lens), max_len, _ptr(key_mask), mask_stride,
+        D ** -0.5 if scale is None else scale, causal, _rows(out, B, n, D), _ptr(lse), B, n,
+        _ptr(ws), ws.numel(), _stream(stream))
+    if status:
+        _check(status, "dllm_attention_kv4")
 
 
 def dllm_capture_condition(default_value: int = 0, stream=None) -> int:

@@ -182,7 +182,7 @@ dllm_status check_cache(const dllm_kv4_cache* c) {
   if (c->head_dim < 32 || c->head_dim > 512 || c->head_dim % 32 != 0)
     return fail(DLLM_ERR_UNSUPPORTED, "head_dim=%d is not a multiple of 32 in [32, 512]",
                 c->head_dim);
-  if (c->heads > 65536) return fail(DLLM_ERR_UNSUPPORTED, "heads=%d exceeds 65536", c->heads);
+  if (c->heads > 4096) return fail(DLLM_ERR_UNSUPPORTED, "heads=%d exceeds 4096", c->heads);
   if (static_cast<int64_t>(c->table_stride) * c->page_size >= (int64_t{1} << 31))
     return fail(DLLM_ERR_UNSUPPORTED, "table_stride * page_size exceeds 2^31 - 1");
   if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_params, 16) ||

@@ -559,9 +559,7 @@ template <int D, int NT>
 cudaError_t launch_few(const AttnParams& p, const AttnPlan& f, bool split, cudaStream_t stream) {
   constexpr size_t smem = few_smem<D, NT>();
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(attention_few_kernel<D, NT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (smem > 48 * 1024) e = allow_smem<attention_few_kernel<D, NT>>(smem);
   if (e != cudaSuccess) return e;
   e = launch_dependent(attention_few_kernel<D, NT>, dim3(f.ctas), dim3(kThreads), smem,
                                    stream, p, f);

@@ -881,9 +881,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   f.part_o = reinterpret_cast<float*>(at);
   f.part_ml = reinterpret_cast<float2*>(at + parts * D * 4);
   f.parts = reinterpret_cast<int2*>(at + parts * D * 4 + parts * 8);
-  cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<D, kShare>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(Smem<D>::kBytes));
+  cudaError_t e = allow_smem<attention_tc_kernel<D, kShare>>(Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
   e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
                        Smem<D>::kBytes, stream, p, f);

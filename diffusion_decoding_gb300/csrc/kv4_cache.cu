@@ -26,30 +26,44 @@ struct Kv4Params {
   const int32_t* pos;
   int64_t pos_stride;
   int n;
-  int64_t tokens;
-  int segs;  // warps per token and tensor
+  unsigned tokens;
+  uint32_t head_magic;
 };
 
 // One warp's work: a token, keys or values, and pieces [first, first + 32 * ITEMS) of its heads.
+// The grid is (warps over the tokens, segments of 32 * ITEMS pieces, keys and values).
 struct Unit {
-  int b, i, side, first;
+  int b, i, first;
   int entry;  // cache entry, -1: none
+  int page, slot;
   bool valid;
 };
 
 __device__ __forceinline__ Unit unit_of(const Kv4Params& p, int items) {
-  const int64_t warp = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
-  const int64_t row = warp / p.segs;  // token * 2 + side
+  const unsigned token = blockIdx.x * (kThreads / 32u) + (threadIdx.x >> 5);
   Unit u;
-  u.first = static_cast<int>(warp - row * p.segs) * 32 * items;
-  u.side = static_cast<int>(row & 1);
-  const int64_t token = row >> 1;
+  u.first = static_cast<int>(blockIdx.y) * 32 * items;
   u.valid = token < p.tokens;
-  u.b = static_cast<int>(token / p.n);
-  u.i = static_cast<int>(token - static_cast<int64_t>(u.b) * p.n);
-  u.entry = -1;
+  u.b = static_cast<int>(token / static_cast<unsigned>(p.n));
+  u.i = static_cast<int>(token) - u.b * p.n;
+  u.entry = u.page = -1;
+  u.slot = 0;
   if (u.valid) u.entry = p.pos ? p.pos[u.b * p.pos_stride + u.i] : u.i;
+  if (u.entry >= 0) {
+    const int t = static_cast<int>(static_cast<unsigned>(u.entry) / static_cast<unsigned>(p.page_size));
+    u.slot = u.entry - t * p.page_size;
+    if (t < p.table_stride) {
+      const int pg = __ldg(p.table + static_cast<int64_t>(u.b) * p.table_stride + t);
+      if (pg >= 0 && pg < p.pages) u.page = pg;
+    }
+  }
   return u;
+}
+
+// Head of piece c (head_dim / 8 pieces a head): a product with floor(2^32 / (D / 8)) + 1, exact
+// while c * D / 8 < 2^32.
+__device__ __forceinline__ int head_of(const Kv4Params& p, int c) {
+  return static_cast<int>(__umulhi(static_cast<uint32_t>(c), p.head_magic));
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -88,16 +102,14 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
   pdl_wait();
   pdl_trigger();
   const Unit u = unit_of(p, ITEMS);
-  if (!u.valid || u.entry < 0) return;
-  const int page = kv4_page(p.table + static_cast<int64_t>(u.b) * p.table_stride, p.table_stride,
-                            p.pages, p.page_size, u.entry);
-  if (page < 0) return;
-  const int slot = u.entry % p.page_size;
+  if (u.page < 0) return;
+  const int side = blockIdx.z;
   const int cpr = p.D / 8, pieces = p.heads * cpr;
-  const char* x = p.x[u.side] + u.b * p.xb[u.side] + u.i * p.xt[u.side];
-  const int64_t xh = p.xh[u.side];
-  uint8_t* codes = p.codes[u.side];
-  uint16_t* params = p.params[u.side];
+  const char* x = p.x[side] + u.b * p.xb[side] + u.i * p.xt[side];
+  const int64_t xh = p.xh[side];
+  const int64_t row0 = static_cast<int64_t>(u.page) * p.heads * p.page_size + u.slot;
+  uint8_t* codes = p.codes[side] + row0 * (p.D / 2);
+  uint16_t* params = p.params[side] + row0 * (p.D / kKv4Group);
 
   uint32_t raw[ITEMS][DT == DLLM_BF16 ? 4 : 8];
 #pragma unroll
@@ -106,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < (DT == DLLM_BF16 ? 4 : 8); ++e) raw[t][e] = 0u;
     if (c >= pieces) continue;
-    const int h = c / cpr;
+    const int h = head_of(p, c);
     const char* src = x + h * xh + (c - h * cpr) * (DT == DLLM_BF16 ? 16 : 32);
     if constexpr (kAligned) {
       const uint4 a = ld_stream_v4(src);
@@ -174,9 +186,9 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
 #pragma unroll
       for (int e = 7; e >= 0; --e) {
         const float v = e & 1 ? bf16hi(raw[t][e >> 1]) : bf16lo(raw[t][e >> 1]);
-        const uint32_t n = min(__float_as_uint(fmaf(v, inv, base)), 0x4B40000Fu);
-        w = w * 16u + (n - 0x4B400000u);
+        w = w * 16u + min(__float_as_uint(fmaf(v, inv, base)), 0x4B40000Fu);
       }
+      w -= 0x4B400000u * 0x11111111u;  // what the eight words' upper bits have added up to
     } else {
       const float d = hi - lo;
       s = __fdiv_rn(d, 15.f);
@@ -196,8 +208,8 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
     }
     if (c >= pieces) continue;
     if (s != s) z = 0u;
-    const int h = c / cpr, cc = c - h * cpr;
-    const int64_t row = (static_cast<int64_t>(page) * p.heads + h) * p.page_size + slot;
+    const int h = head_of(p, c), cc = c - h * cpr;
+    const int64_t row = static_cast<int64_t>(h) * p.page_size;
     *reinterpret_cast<uint32_t*>(codes + row * (p.D / 2) + cc * 4) = w;
     if ((cc & 3) == 0)
       params[row * (p.D / kKv4Group) + (cc >> 2)] =
@@ -212,29 +224,29 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
   pdl_trigger();
   const Unit u = unit_of(p, ITEMS);
   if (!u.valid) return;
-  const int page = u.entry < 0 ? -1
-                               : kv4_page(p.table + static_cast<int64_t>(u.b) * p.table_stride,
-                                          p.table_stride, p.pages, p.page_size, u.entry);
-  const int slot = u.entry % p.page_size;
+  const int side = blockIdx.z;
   const int cpr = p.D / 8, pieces = p.heads * cpr;
-  char* x = p.x[u.side] + u.b * p.xb[u.side] + u.i * p.xt[u.side];
-  const int64_t xh = p.xh[u.side];
+  char* x = p.x[side] + u.b * p.xb[side] + u.i * p.xt[side];
+  const int64_t xh = p.xh[side];
+  const int64_t row0 = static_cast<int64_t>(max(u.page, 0)) * p.heads * p.page_size + u.slot;
+  const uint8_t* codes = p.codes[side] + row0 * (p.D / 2);
+  const uint16_t* params = p.params[side] + row0 * (p.D / kKv4Group);
   uint32_t w[ITEMS], pp[ITEMS];
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
     const int c = u.first + t * 32 + lane;
     w[t] = pp[t] = 0u;
-    if (page < 0 || c >= pieces) continue;
-    const int h = c / cpr, cc = c - h * cpr;
-    const int64_t row = (static_cast<int64_t>(page) * p.heads + h) * p.page_size + slot;
-    w[t] = __ldg(reinterpret_cast<const uint32_t*>(p.codes[u.side] + row * (p.D / 2) + cc * 4));
-    pp[t] = __ldg(p.params[u.side] + row * (p.D / kKv4Group) + (cc >> 2));
+    if (u.page < 0 || c >= pieces) continue;
+    const int h = head_of(p, c), cc = c - h * cpr;
+    const int64_t row = static_cast<int64_t>(h) * p.page_size;
+    w[t] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (p.D / 2) + cc * 4));
+    pp[t] = __ldg(params + row * (p.D / kKv4Group) + (cc >> 2));
   }
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
     const int c = u.first + t * 32 + lane;
     if (c >= pieces) continue;
-    const int h = c / cpr, cc = c - h * cpr;
+    const int h = head_of(p, c), cc = c - h * cpr;
     const Kv4Scale sc = kv4_scale(__byte_perm(pp[t], pp[t], 0x1010));
     // pairs of channels (j, j + 4), put back side by side
     const uint32_t a = kv4_pair<0>(w[t], sc), b = kv4_pair<1>(w[t], sc), d = kv4_pair<2>(w[t], sc),
@@ -279,14 +291,13 @@ template <bool kWrite, int DT, bool kAligned>
 cudaError_t launch_items(Kv4Params& p, int sm_count, cudaStream_t stream) {
   const int pieces = p.heads * (p.D / 8);
   auto run = [&](auto kern, int items) {
-    p.segs = (pieces + 32 * items - 1) / (32 * items);
-    const int64_t warps = p.tokens * 2 * p.segs;
-    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    return launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+    const dim3 grid((p.tokens + kThreads / 32 - 1) / (kThreads / 32),
+                    static_cast<unsigned>((pieces + 32 * items - 1) / (32 * items)), 2);
+    return launch_dependent(kern, grid, dim3(kThreads), 0, stream, p);
   };
   // Four pieces a warp hide more of the load latency and share the page lookup; one piece a warp
   // when the call has too few warps to fill the SMs.
-  const bool few = p.tokens * 2 * ((pieces + 127) / 128) < static_cast<int64_t>(sm_count) * 16;
+  const bool few = static_cast<int64_t>(p.tokens) * 2 * ((pieces + 127) / 128) < static_cast<int64_t>(sm_count) * 16;
   if constexpr (kWrite)
     return few ? run(kv4_write_kernel<DT, kAligned, 1>, 1)
                : run(kv4_write_kernel<DT, kAligned, kItems>, kItems);
@@ -319,7 +330,8 @@ cudaError_t launch(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_
   p.pos = pos;
   p.pos_stride = pos_stride;
   p.n = n;
-  p.tokens = static_cast<int64_t>(B) * n;
+  p.tokens = static_cast<unsigned>(B) * static_cast<unsigned>(n);
+  p.head_magic = static_cast<uint32_t>((uint64_t{1} << 32) / (cache.head_dim / 8) + 1);
   const bool al = aligned16(k) && aligned16(v);
   if (k.dtype == DLLM_BF16)
     return al ? launch_items<kWrite, DLLM_BF16, true>(p, sm_count, stream)

@@ -8,19 +8,24 @@
 // radians at position 131072.  The hardware sine and cosine then see |angle| <= pi, where their
 // error is at most 2^-21.
 //
-// HBM-bound: 2 * heads * head_dim values move per token and ~8 instructions are spent per value.
-// A group of head_dim / 16 lanes (padded to a power of two) owns a head, each lane 16 channels as
-// two 16-byte pieces that hold whole pairs, so the mean is a shuffle sum over the group and the
-// rotation stays in the lane.  A lane keeps the same channels for every head of its token: the
-// eight sines and cosines are computed once per warp and used for all the heads it loops over.
+// HBM-bound: 2 * heads * head_dim values move per token.  A group of head_dim / 16 lanes (padded to a
+// power of two) owns a head, each lane 16 channels as two 16-byte pieces that hold whole pairs, so
+// the mean is a shuffle sum over the group and the rotation stays in the lane.  A warp takes up to
+// kUnits such sets of heads of one token, queries or keys, and has all their loads on the way
+// before it uses the first; a lane keeps the same channels for all of them, so that sines,
+// cosines and weights become 32 factors once:
+//   out_a = r (a * w_a cos - c * w_c sin),  out_c = r (c * w_c cos + a * w_a sin),
+// two packed fp32 operations for two channels.
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
+#include "vec_math.cuh"
 
 namespace dllm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnits = 4;
 
 struct Side {  // one tensor pair; strides in bytes
   const char* x;
@@ -39,8 +44,8 @@ struct NormRopeParams {
   int64_t tokens;  // B * n
   int D, R, interleaved, norm;
   float magnitude, eps;
-  int chunks;  // warps per token
-  int units;   // head groups per warp
+  int units;       // sets of heads a warp takes, <= kUnits
+  int chunks[2];   // warps per token for the queries and for the keys
 };
 
 // cos and sin of p * u turns-in-2^-64, times m
@@ -92,127 +97,144 @@ __device__ __forceinline__ void store_piece(char* p, const float (&x)[8]) {
   }
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return pack2(hi, lo);
+}
+
 // GL lanes per head (a power of two >= D / 16); D % 16 == 0, R % 16 == 0, 16-byte aligned rows.
-template <int DT, int GL>
+template <int DT, int GL, bool kInter>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int ES = DT == DLLM_BF16 ? 2 : 4;
   constexpr int HPW = 32 / GL;  // heads a warp holds at once
-  const int64_t warp = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  const unsigned warp = blockIdx.x * (kThreads / 32u) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const int64_t token = warp / p.chunks;
+  const unsigned per_token = p.chunks[0] + p.chunks[1];
+  const unsigned token = warp / per_token;
   if (token >= p.tokens) return;
-  const int chunk = static_cast<int>(warp - token * p.chunks);
-  const int b = static_cast<int>(token / p.n), i = static_cast<int>(token - static_cast<int64_t>(b) * p.n);
+  int chunk = static_cast<int>(warp - token * per_token);
+  const int b = static_cast<int>(token / static_cast<unsigned>(p.n));
+  const int i = static_cast<int>(token) - b * p.n;
   const int pos = p.pos ? p.pos[b * p.pos_stride + i] : 0;
   if (pos < 0) return;
+  const int side = chunk >= p.chunks[0];
+  if (side) chunk -= p.chunks[0];
+  const Side& s = p.s[side];
 
   const int sub = lane % GL, slot = lane / GL;
   const bool active = sub < p.D / 16;
   const bool turns = sub < p.R / 16;
-  int o0, o1;
-  if (!turns) {
-    o0 = 16 * sub;  // = R + 16 * (sub - R / 16)
-    o1 = o0 + 8;
-  } else if (p.interleaved) {
-    o0 = 16 * sub;
-    o1 = o0 + 8;
-  } else {
-    o0 = 8 * sub;
-    o1 = p.R / 2 + 8 * sub;
-  }
-  float cs[8], sn[8];
-  if (turns) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      phase_sincos(pos, __ldg(p.phases + 8 * sub + e), p.magnitude, cs[e], sn[e]);
-  }
-  const int nq = p.s[0].heads, total = nq + p.s[1].heads;
-  Piece<DT> wq0{}, wq1{}, wk0{}, wk1{};
-  if (active) {
-    if (p.s[0].w) {
-      wq0 = load_piece<DT>(p.s[0].w + o0 * ES);
-      wq1 = load_piece<DT>(p.s[0].w + o1 * ES);
-    }
-    if (p.s[1].w) {
-      wk0 = load_piece<DT>(p.s[1].w + o0 * ES);
-      wk1 = load_piece<DT>(p.s[1].w + o1 * ES);
-    }
-  }
-  const char* xq = p.s[0].x + b * p.s[0].xb + i * p.s[0].xt;
-  const char* xk = p.s[1].x + b * p.s[1].xb + i * p.s[1].xt;
-  char* yq = p.s[0].y + b * p.s[0].yb + i * p.s[0].yt;
-  char* yk = p.s[1].y + b * p.s[1].yb + i * p.s[1].yt;
-  const float inv_d = 1.f / static_cast<float>(p.D);
-
-  auto src = [&](int h) {
-    return h < nq ? xq + h * p.s[0].xh : xk + (h - nq) * p.s[1].xh;
-  };
+  // the lane's two pieces of eight channels: both halves of its pairs, or side by side
+  const int o0 = !turns || kInter ? 16 * sub : 8 * sub;
+  const int o1 = !turns || kInter ? o0 + 8 : p.R / 2 + o0;
+  const char* x = s.x + b * s.xb + i * s.xt;
+  char* y = s.y + b * s.yb + i * s.yt;
   const int h0 = chunk * p.units * HPW + slot;
-  Piece<DT> a0{}, a1{};
-  if (active && h0 < total) {
-    a0 = load_piece<DT>(src(h0) + o0 * ES);
-    a1 = load_piece<DT>(src(h0) + o1 * ES);
-  }
-  for (int u = 0; u < p.units; ++u) {
+  Piece<DT> a0[kUnits], a1[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    a0[u] = Piece<DT>{};
+    a1[u] = Piece<DT>{};
     const int h = h0 + u * HPW;
-    const bool mine = active && h < total;
-    float v0[8], v1[8];
-    unpack<DT>(a0, v0);
-    unpack<DT>(a1, v1);
-    if (u + 1 < p.units && active && h + HPW < total) {  // the next heads are on their way
-      a0 = load_piece<DT>(src(h + HPW) + o0 * ES);
-      a1 = load_piece<DT>(src(h + HPW) + o1 * ES);
+    if (u < p.units && active && h < s.heads) {
+      a0[u] = load_piece<DT>(x + h * s.xh + o0 * ES);
+      a1[u] = load_piece<DT>(x + h * s.xh + o1 * ES);
     }
-    if (p.norm) {
-      float ss = 0.f;
+  }
+  // factors of a piece's own channels and of their partners' (two channels a word)
+  uint64_t own[2][4], other[2][4];
+  {
+    float w0[8], w1[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v0[e], v0[e], fmaf(v1[e], v1[e], ss));
-      if (!active) ss = 0.f;
-#pragma unroll
-      for (int o = GL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-      const float r = rsqrtf(ss * inv_d + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v0[e] *= r;
-        v1[e] *= r;
-      }
-      if (h < nq ? p.s[0].w != nullptr : p.s[1].w != nullptr) {
-        float w0[8], w1[8];
-        unpack<DT>(h < nq ? wq0 : wk0, w0);
-        unpack<DT>(h < nq ? wq1 : wk1, w1);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v0[e] *= w0[e];
-          v1[e] *= w1[e];
-        }
-      }
+    for (int e = 0; e < 8; ++e) w0[e] = w1[e] = 1.f;
+    if (s.w && active) {
+      unpack<DT>(load_piece<DT>(s.w + o0 * ES), w0);
+      unpack<DT>(load_piece<DT>(s.w + o1 * ES), w1);
     }
     if (turns) {
-      if (p.interleaved) {
+      float cs[8], sn[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a = v0[2 * e], c = v0[2 * e + 1];
-          v0[2 * e] = a * cs[e] - c * sn[e];
-          v0[2 * e + 1] = c * cs[e] + a * sn[e];
-          a = v1[2 * e], c = v1[2 * e + 1];
-          v1[2 * e] = a * cs[4 + e] - c * sn[4 + e];
-          v1[2 * e + 1] = c * cs[4 + e] + a * sn[4 + e];
-        }
-      } else {
+      for (int e = 0; e < 8; ++e)
+        phase_sincos(pos, __ldg(p.phases + 8 * sub + e), p.magnitude, cs[e], sn[e]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = v0[e], c = v1[e];
-          v0[e] = a * cs[e] - c * sn[e];
-          v1[e] = c * cs[e] + a * sn[e];
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (kInter) {  // a piece is four pairs
+          own[0][j] = pack2(w0[2 * j] * cs[j], w0[2 * j + 1] * cs[j]);
+          other[0][j] = pack2(-w0[2 * j + 1] * sn[j], w0[2 * j] * sn[j]);
+          own[1][j] = pack2(w1[2 * j] * cs[4 + j], w1[2 * j + 1] * cs[4 + j]);
+          other[1][j] = pack2(-w1[2 * j + 1] * sn[4 + j], w1[2 * j] * sn[4 + j]);
+        } else {
+          own[0][j] = pack2(w0[2 * j] * cs[2 * j], w0[2 * j + 1] * cs[2 * j + 1]);
+          other[0][j] = pack2(-w1[2 * j] * sn[2 * j], -w1[2 * j + 1] * sn[2 * j + 1]);
+          own[1][j] = pack2(w1[2 * j] * cs[2 * j], w1[2 * j + 1] * cs[2 * j + 1]);
+          other[1][j] = pack2(w0[2 * j] * sn[2 * j], w0[2 * j + 1] * sn[2 * j + 1]);
         }
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        own[0][j] = pack2(w0[2 * j], w0[2 * j + 1]);
+        own[1][j] = pack2(w1[2 * j], w1[2 * j + 1]);
+        other[0][j] = other[1][j] = 0;
+      }
     }
-    if (mine) {
-      char* y = h < nq ? yq + h * p.s[0].yh : yk + (h - nq) * p.s[1].yh;
-      store_piece<DT>(y + o0 * ES, v0);
-      store_piece<DT>(y + o1 * ES, v1);
+  }
+  const float inv_d = 1.f / static_cast<float>(p.D);
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    if (u >= p.units) break;
+    const int h = h0 + u * HPW;
+    uint64_t v[2][4];
+    {
+      float f0[8], f1[8];
+      unpack<DT>(a0[u], f0);
+      unpack<DT>(a1[u], f1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[0][j] = pack2(f0[2 * j], f0[2 * j + 1]);
+        v[1][j] = pack2(f1[2 * j], f1[2 * j + 1]);
+      }
+    }
+    float r = 1.f;
+    if (p.norm) {
+      uint64_t q0 = 0, q1 = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q0 = fma2(v[0][j], v[0][j], q0);
+        q1 = fma2(v[1][j], v[1][j], q1);
+      }
+      float lo, hi;
+      unpack2(add2(q0, q1), lo, hi);
+      float ss = lo + hi;
+#pragma unroll
+      for (int o = GL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      r = rsqrtf(ss * inv_d + p.eps);
+    }
+    const uint64_t r2 = pack2(r, r);
+    float out[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint64_t t;
+        if (turns)
+          t = fma2(v[k][j], own[k][j], mul2(kInter ? swap2(v[k][j]) : v[k ^ 1][j], other[k][j]));
+        else
+          t = mul2(v[k][j], own[k][j]);
+        unpack2(mul2(t, r2), out[k][2 * j], out[k][2 * j + 1]);
+      }
+    }
+    if (active && h < s.heads) {
+      store_piece<DT>(y + h * s.yh + o0 * ES, out[0]);
+      store_piece<DT>(y + h * s.yh + o1 * ES, out[1]);
     }
   }
 }
@@ -298,22 +320,24 @@ bool rows_aligned(const Side& s) {
 
 template <int DT, int GL>
 cudaError_t launch_vec(NormRopeParams& p, int sm_count, cudaStream_t stream) {
-  const int groups = (p.s[0].heads + p.s[1].heads + 32 / GL - 1) / (32 / GL);
-  // A warp takes as many of its token's head groups as still leave 32 warps per SM: the sines and
-  // cosines and the weights are then used for more heads; fewer tokens spread over more warps.
-  const int64_t spare = p.tokens * groups / (static_cast<int64_t>(sm_count) * 32);
-  p.units = static_cast<int>(spare < 1 ? 1 : spare > groups ? groups : spare);
-  p.chunks = (groups + p.units - 1) / p.units;
-  const int64_t warps = p.tokens * p.chunks;
-  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  return launch_dependent(norm_rope_kernel<DT, GL>, dim3(static_cast<unsigned>(blocks)),
-                          dim3(kThreads), 0, stream, p);
+  constexpr int HPW = 32 / GL;
+  // As many sets of heads a warp (more loads on the way, sines and cosines used more often) as
+  // leave 16 warps an SM; a call with fewer tokens spreads each over more warps.
+  int64_t warps = 0;
+  for (p.units = kUnits;; p.units /= 2) {
+    for (int j = 0; j < 2; ++j) p.chunks[j] = (p.s[j].heads + HPW * p.units - 1) / (HPW * p.units);
+    warps = p.tokens * (p.chunks[0] + p.chunks[1]);
+    if (p.units == 1 || warps >= static_cast<int64_t>(sm_count) * 16) break;
+  }
+  const dim3 grid(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
+  return p.interleaved
+             ? launch_dependent(norm_rope_kernel<DT, GL, true>, grid, dim3(kThreads), 0, stream, p)
+             : launch_dependent(norm_rope_kernel<DT, GL, false>, grid, dim3(kThreads), 0, stream, p);
 }
 
 template <int DT>
 cudaError_t launch_vec_dt(NormRopeParams& p, int sm_count, cudaStream_t stream) {
   const int lanes = p.D / 16;
-  if (lanes <= 1) return launch_vec<DT, 1>(p, sm_count, stream);
   if (lanes <= 2) return launch_vec<DT, 2>(p, sm_count, stream);
   if (lanes <= 4) return launch_vec<DT, 4>(p, sm_count, stream);
   if (lanes <= 8) return launch_vec<DT, 8>(p, sm_count, stream);
