@@ -2,10 +2,12 @@
 // explainer, KV-cache manager: refreshed entries replace the stale ones in the cache).  The format
 // is described in kv4.cuh and include/dllm.h.
 //
-// Both kernels are HBM-bound (bf16: 2 bytes of values and 9/16 bytes of cache per value).  A lane
-// handles eight channels, so a warp reads or writes 512 contiguous bytes of bf16 values per access
-// and 128 of codes; the four lanes of a group find its extremes with two shuffles.  A warp takes
-// up to kItems such pieces of one token and issues all their loads before it uses the first.
+// Both kernels are HBM-bound (bf16: 2 bytes of values and 9/16 bytes of cache per value), with
+// little to spare: the write has about a dozen instructions a value.  A lane handles 16 channels
+// (32 bytes of bf16 in one access, 8 bytes of codes), so the two lanes of a group find its extremes
+// with one shuffle and work out its step together with 16 values each.  A warp takes up to kItems
+// such pieces of one token and issues all their loads before it uses the first, the values' before
+// it even knows their place in the cache.
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -14,7 +16,7 @@ namespace dllm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;
+constexpr int kItems = 2;
 
 struct Kv4Params {
   char* x[2];  // keys, values; strides in bytes
@@ -49,6 +51,11 @@ __device__ __forceinline__ Unit unit_of(const Kv4Params& p, int items) {
   u.entry = u.page = -1;
   u.slot = 0;
   if (u.valid) u.entry = p.pos ? p.pos[u.b * p.pos_stride + u.i] : u.i;
+  return u;
+}
+
+// Page and slot of the unit's entry.
+__device__ __forceinline__ void find_page(const Kv4Params& p, Unit& u) {
   if (u.entry >= 0) {
     const int t = static_cast<int>(static_cast<unsigned>(u.entry) / static_cast<unsigned>(p.page_size));
     u.slot = u.entry - t * p.page_size;
@@ -57,11 +64,10 @@ __device__ __forceinline__ Unit unit_of(const Kv4Params& p, int items) {
       if (pg >= 0 && pg < p.pages) u.page = pg;
     }
   }
-  return u;
 }
 
-// Head of piece c (head_dim / 8 pieces a head): a product with floor(2^32 / (D / 8)) + 1, exact
-// while c * D / 8 < 2^32.
+// Head of piece c (head_dim / 16 pieces a head): a product with floor(2^32 / (D / 16)) + 1, exact
+// while c * D / 16 < 2^32.
 __device__ __forceinline__ int head_of(const Kv4Params& p, int c) {
   return static_cast<int>(__umulhi(static_cast<uint32_t>(c), p.head_magic));
 }
@@ -95,48 +101,60 @@ __device__ __forceinline__ float kv4_step(float lo, float hi) {
   return d != d ? __uint_as_float(kKv4NaNParam << 16) : s;
 }
 
-// kAligned: rows on 16-byte boundaries; otherwise values are read one by one.
+__device__ __forceinline__ void load32(const char* p, uint32_t* w) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+                 "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(char* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// kAligned: rows on 32-byte boundaries; otherwise values are read one by one.
 template <int DT, bool kAligned, int ITEMS>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_constant__ Kv4Params p) {
+  constexpr int NW = DT == DLLM_BF16 ? 8 : 16;  // words of a piece
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const Unit u = unit_of(p, ITEMS);
-  if (u.page < 0) return;
+  Unit u = unit_of(p, ITEMS);
+  if (!u.valid) return;
   const int side = blockIdx.z;
-  const int cpr = p.D / 8, pieces = p.heads * cpr;
+  const int cpr = p.D / 16, pieces = p.heads * cpr;
   const char* x = p.x[side] + u.b * p.xb[side] + u.i * p.xt[side];
   const int64_t xh = p.xh[side];
-  const int64_t row0 = static_cast<int64_t>(u.page) * p.heads * p.page_size + u.slot;
-  uint8_t* codes = p.codes[side] + row0 * (p.D / 2);
-  uint16_t* params = p.params[side] + row0 * (p.D / kKv4Group);
 
-  uint32_t raw[ITEMS][DT == DLLM_BF16 ? 4 : 8];
+  // the values are on their way while the entry and its page are looked up
+  uint32_t raw[ITEMS][NW];
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
     const int c = u.first + t * 32 + lane;
 #pragma unroll
-    for (int e = 0; e < (DT == DLLM_BF16 ? 4 : 8); ++e) raw[t][e] = 0u;
+    for (int e = 0; e < NW; ++e) raw[t][e] = 0u;
     if (c >= pieces) continue;
     const int h = head_of(p, c);
-    const char* src = x + h * xh + (c - h * cpr) * (DT == DLLM_BF16 ? 16 : 32);
+    const char* src = x + h * xh + (c - h * cpr) * (NW * 4);
     if constexpr (kAligned) {
-      const uint4 a = ld_stream_v4(src);
-      raw[t][0] = a.x, raw[t][1] = a.y, raw[t][2] = a.z, raw[t][3] = a.w;
-      if constexpr (DT == DLLM_F32) {
-        const uint4 d = ld_stream_v4(src + 16);
-        raw[t][4] = d.x, raw[t][5] = d.y, raw[t][6] = d.z, raw[t][7] = d.w;
-      }
+#pragma unroll
+      for (int e = 0; e < NW; e += 8) load32(src + 4 * e, raw[t] + e);
     } else if constexpr (DT == DLLM_BF16) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < NW; ++e)
         raw[t][e] = reinterpret_cast<const uint16_t*>(src)[2 * e] |
                     static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[2 * e + 1]) << 16;
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) raw[t][e] = reinterpret_cast<const uint32_t*>(src)[e];
+      for (int e = 0; e < NW; ++e) raw[t][e] = reinterpret_cast<const uint32_t*>(src)[e];
     }
   }
+  find_page(p, u);
+  if (u.page < 0) return;
+  const int64_t row0 = static_cast<int64_t>(u.page) * p.heads * p.page_size + u.slot;
+  uint8_t* codes = p.codes[side] + row0 * (p.D / 2);
+  uint16_t* params = p.params[side] + row0 * (p.D / kKv4Group);
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
     const int c = u.first + t * 32 + lane;
@@ -145,33 +163,28 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
       // extremes in packed bf16; the maximum and the negated minimum share a word
       uint32_t mx = raw[t][0], mn = raw[t][0];
 #pragma unroll
-      for (int e = 1; e < 4; ++e) {
+      for (int e = 1; e < NW; ++e) {
         mx = bf2_max_nan(mx, raw[t][e]);
         mn = bf2_min_nan(mn, raw[t][e]);
       }
       mn ^= 0x80008000u;
       uint32_t both = bf2_max_nan(__byte_perm(mx, mn, 0x5410), __byte_perm(mx, mn, 0x7632));
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) both = bf2_max_nan(both, __shfl_xor_sync(kFull, both, o));
+      both = bf2_max_nan(both, __shfl_xor_sync(kFull, both, 1));
       both = bf2_max_nan(both, 0u);
       hi = bf16lo(both);
       lo = -bf16hi(both);
     } else {
       hi = 0.f, lo = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < NW; ++e) {
         hi = max_nan(hi, __uint_as_float(raw[t][e]));
         lo = max_nan(lo, -__uint_as_float(raw[t][e]));
       }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
-        lo = max_nan(lo, __shfl_xor_sync(kFull, lo, o));
-      }
-      lo = -lo;
+      hi = max_nan(hi, __shfl_xor_sync(kFull, hi, 1));
+      lo = -max_nan(lo, __shfl_xor_sync(kFull, lo, 1));
     }
     float s;
-    uint32_t z, w = 0u;
+    uint32_t z, w[2] = {0u, 0u};
     if constexpr (DT == DLLM_BF16) {
       s = kv4_step(lo, hi);
       // x / s has at most eight and three significant bits: apart from exact ties it is no nearer
@@ -181,14 +194,16 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
       float inv;
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
       inv = s > 0.f ? inv * 1.0000152587890625f : 0.f;
-      z = __float_as_uint(fmaf(-lo, inv, 12582912.f)) & 15u;
-      const float base = 12582912.f + static_cast<float>(z);
+      const float zf = fmaf(-lo, inv, 12582912.f);  // z in the low bits
+      z = __float_as_uint(zf) & 15u;
 #pragma unroll
-      for (int e = 7; e >= 0; --e) {
+      for (int e = 15; e >= 0; --e) {
         const float v = e & 1 ? bf16hi(raw[t][e >> 1]) : bf16lo(raw[t][e >> 1]);
-        w = w * 16u + min(__float_as_uint(fmaf(v, inv, base)), 0x4B40000Fu);
+        w[e >> 3] = w[e >> 3] * 16u + min(__float_as_uint(fmaf(v, inv, zf)), 0x4B40000Fu);
       }
-      w -= 0x4B400000u * 0x11111111u;  // what the eight words' upper bits have added up to
+      // what the eight words' upper bits have added up to
+#pragma unroll
+      for (int e = 0; e < 2; ++e) w[e] -= 0x4B400000u * 0x11111111u;
     } else {
       const float d = hi - lo;
       s = __fdiv_rn(d, 15.f);
@@ -199,20 +214,20 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
       const float den = s > 0.f ? s : 1.f;
       z = static_cast<uint32_t>(fminf(floorf(__fadd_rn(__fdiv_rn(-lo, den), 0.5f)), 15.f));
 #pragma unroll
-      for (int e = 7; e >= 0; --e) {
+      for (int e = 15; e >= 0; --e) {
         const float r = __fdiv_rn(__uint_as_float(raw[t][e]), den);
         const float k = s > 0.f ? copysignf(floorf(__fadd_rn(fabsf(r), 0.5f)), r) : 0.f;
         const float nf = fminf(fmaxf(k + static_cast<float>(z), 0.f), 15.f);
-        w = w * 16u + static_cast<uint32_t>(nf);
+        w[e >> 3] = w[e >> 3] * 16u + static_cast<uint32_t>(nf);
       }
     }
     if (c >= pieces) continue;
     if (s != s) z = 0u;
     const int h = head_of(p, c), cc = c - h * cpr;
     const int64_t row = static_cast<int64_t>(h) * p.page_size;
-    *reinterpret_cast<uint32_t*>(codes + row * (p.D / 2) + cc * 4) = w;
-    if ((cc & 3) == 0)
-      params[row * (p.D / kKv4Group) + (cc >> 2)] =
+    *reinterpret_cast<uint2*>(codes + row * (p.D / 2) + cc * 8) = make_uint2(w[0], w[1]);
+    if ((cc & 1) == 0)
+      params[row * (p.D / kKv4Group) + (cc >> 1)] =
           static_cast<uint16_t>((__float_as_uint(s) >> 16) | z);
   }
 }
@@ -222,25 +237,28 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const Unit u = unit_of(p, ITEMS);
+  Unit u = unit_of(p, ITEMS);
   if (!u.valid) return;
+  find_page(p, u);
   const int side = blockIdx.z;
-  const int cpr = p.D / 8, pieces = p.heads * cpr;
+  const int cpr = p.D / 16, pieces = p.heads * cpr;
   char* x = p.x[side] + u.b * p.xb[side] + u.i * p.xt[side];
   const int64_t xh = p.xh[side];
   const int64_t row0 = static_cast<int64_t>(max(u.page, 0)) * p.heads * p.page_size + u.slot;
   const uint8_t* codes = p.codes[side] + row0 * (p.D / 2);
   const uint16_t* params = p.params[side] + row0 * (p.D / kKv4Group);
-  uint32_t w[ITEMS], pp[ITEMS];
+  uint2 w[ITEMS];
+  uint32_t pp[ITEMS];
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
     const int c = u.first + t * 32 + lane;
-    w[t] = pp[t] = 0u;
+    w[t] = make_uint2(0u, 0u);
+    pp[t] = 0u;
     if (u.page < 0 || c >= pieces) continue;
     const int h = head_of(p, c), cc = c - h * cpr;
     const int64_t row = static_cast<int64_t>(h) * p.page_size;
-    w[t] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (p.D / 2) + cc * 4));
-    pp[t] = __ldg(params + row * (p.D / kKv4Group) + (cc >> 2));
+    w[t] = __ldg(reinterpret_cast<const uint2*>(codes + row * (p.D / 2) + cc * 8));
+    pp[t] = __ldg(params + row * (p.D / kKv4Group) + (cc >> 1));
   }
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
@@ -248,56 +266,63 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
     if (c >= pieces) continue;
     const int h = head_of(p, c), cc = c - h * cpr;
     const Kv4Scale sc = kv4_scale(__byte_perm(pp[t], pp[t], 0x1010));
-    // pairs of channels (j, j + 4), put back side by side
-    const uint32_t a = kv4_pair<0>(w[t], sc), b = kv4_pair<1>(w[t], sc), d = kv4_pair<2>(w[t], sc),
-                   e = kv4_pair<3>(w[t], sc);
-    const uint32_t v[4] = {__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410),
-                           __byte_perm(a, b, 0x7632), __byte_perm(d, e, 0x7632)};
-    char* dst = x + h * xh + cc * (DT == DLLM_BF16 ? 16 : 32);
+    uint32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // pairs of channels (j, j + 4), put back side by side
+      const uint32_t word = k ? w[t].y : w[t].x;
+      const uint32_t a = kv4_pair<0>(word, sc), b = kv4_pair<1>(word, sc),
+                     d = kv4_pair<2>(word, sc), e = kv4_pair<3>(word, sc);
+      v[4 * k] = __byte_perm(a, b, 0x5410);
+      v[4 * k + 1] = __byte_perm(d, e, 0x5410);
+      v[4 * k + 2] = __byte_perm(a, b, 0x7632);
+      v[4 * k + 3] = __byte_perm(d, e, 0x7632);
+    }
+    char* dst = x + h * xh + cc * (DT == DLLM_BF16 ? 32 : 64);
     if constexpr (DT == DLLM_BF16) {
       if constexpr (kAligned) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+        store32(dst, v);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 16; ++k)
           reinterpret_cast<uint16_t*>(dst)[k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
       }
     } else {
-      float f[8];
+      uint32_t f[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[2 * k] = bf16lo(v[k]);
-        f[2 * k + 1] = bf16hi(v[k]);
+      for (int k = 0; k < 8; ++k) {
+        f[2 * k] = v[k] << 16;
+        f[2 * k + 1] = v[k] & 0xffff0000u;
       }
       if constexpr (kAligned) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        store32(dst, f);
+        store32(dst + 32, f + 8);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) reinterpret_cast<float*>(dst)[k] = f[k];
+        for (int k = 0; k < 16; ++k) reinterpret_cast<uint32_t*>(dst)[k] = f[k];
       }
     }
   }
 }
 
-bool aligned16(const dllm_heads& h) {
+bool aligned32(const dllm_heads& h) {
   const int es = h.dtype == DLLM_BF16 ? 2 : 4;
   return (reinterpret_cast<uintptr_t>(h.data) | static_cast<uintptr_t>(h.batch_stride * es) |
           static_cast<uintptr_t>(h.token_stride * es) | static_cast<uintptr_t>(h.head_stride * es)) %
-             16 == 0;
+             32 == 0;
 }
 
 template <bool kWrite, int DT, bool kAligned>
 cudaError_t launch_items(Kv4Params& p, int sm_count, cudaStream_t stream) {
-  const int pieces = p.heads * (p.D / 8);
+  const int pieces = p.heads * (p.D / 16);
   auto run = [&](auto kern, int items) {
     const dim3 grid((p.tokens + kThreads / 32 - 1) / (kThreads / 32),
                     static_cast<unsigned>((pieces + 32 * items - 1) / (32 * items)), 2);
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, p);
   };
-  // Four pieces a warp hide more of the load latency and share the page lookup; one piece a warp
+  // Two pieces a lane hide more of the load latency and share the page lookup; one piece a lane
   // when the call has too few warps to fill the SMs.
-  const bool few = static_cast<int64_t>(p.tokens) * 2 * ((pieces + 127) / 128) < static_cast<int64_t>(sm_count) * 16;
+  const bool few = static_cast<int64_t>(p.tokens) * 2 * ((pieces + 63) / 64) < static_cast<int64_t>(sm_count) * 16;
   if constexpr (kWrite)
     return few ? run(kv4_write_kernel<DT, kAligned, 1>, 1)
                : run(kv4_write_kernel<DT, kAligned, kItems>, kItems);
@@ -331,8 +356,8 @@ cudaError_t launch(const dllm_kv4_cache& cache, const dllm_heads& k, const dllm_
   p.pos_stride = pos_stride;
   p.n = n;
   p.tokens = static_cast<unsigned>(B) * static_cast<unsigned>(n);
-  p.head_magic = static_cast<uint32_t>((uint64_t{1} << 32) / (cache.head_dim / 8) + 1);
-  const bool al = aligned16(k) && aligned16(v);
+  p.head_magic = static_cast<uint32_t>((uint64_t{1} << 32) / (cache.head_dim / 16) + 1);
+  const bool al = aligned32(k) && aligned32(v);
   if (k.dtype == DLLM_BF16)
     return al ? launch_items<kWrite, DLLM_BF16, true>(p, sm_count, stream)
               : launch_items<kWrite, DLLM_BF16, false>(p, sm_count, stream);

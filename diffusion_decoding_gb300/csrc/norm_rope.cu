@@ -24,7 +24,7 @@
 namespace dllm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnits = 4;
 
 struct Side {  // one tensor pair; strides in bytes
@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   int chunk = static_cast<int>(warp - token * per_token);
   const int b = static_cast<int>(token / static_cast<unsigned>(p.n));
   const int i = static_cast<int>(token) - b * p.n;
-  const int pos = p.pos ? p.pos[b * p.pos_stride + i] : 0;
-  if (pos < 0) return;
+  const int pos = p.pos ? p.pos[b * p.pos_stride + i] : 0;  // looked at when the loads are under way
   const int side = chunk >= p.chunks[0];
   if (side) chunk -= p.chunks[0];
   const Side& s = p.s[side];
@@ -149,6 +148,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       a1[u] = load_piece<DT>(x + h * s.xh + o1 * ES);
     }
   }
+  if (pos < 0) return;
   // factors of a piece's own channels and of their partners' (two channels a word)
   uint64_t own[2][4], other[2][4];
   {

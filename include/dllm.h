@@ -390,7 +390,8 @@ dllm_status dllm_loop_continue(const dllm_block_state* state, int32_t B, int32_t
  *   data[b*batch_stride + i*token_stride + h*head_stride + c]
  * (strides in elements, so queries, keys and values may be slices of one projection's output).
  * Any strides and any pointer aligned to the element size are accepted; rows that all start on
- * 16-byte boundaries are read and written with 16-byte accesses, others element by element.
+ * 32-byte boundaries are read and written with wide accesses (16-byte boundaries do for
+ * dllm_qk_norm_rope and dllm_attention_kv4), others element by element.
  */
 typedef struct {
   void* data;
