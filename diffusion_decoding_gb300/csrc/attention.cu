@@ -57,12 +57,6 @@ __device__ __forceinline__ void lds_words(uint32_t p, uint32_t* w) {
   else
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t p) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
-  return v;
-}
-
 // A tile of 16 entries in shared memory: K codes, V codes (rows in the order of the fragments'
 // rows), K params, V params (in entry order).
 //
@@ -136,15 +130,15 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < KW; ++i) lds_words<1>(l.k + row + 16 * i, &k[e][i]);
 #pragma unroll
-        for (int i = 0; i < 6; ++i) kp[e][i] = lds_u16(par + 2 * i);
+        for (int i = 0; i < 6; ++i) kp[e][i] = ld_shared_u16(par + 2 * i);
       } else if constexpr (D == 256) {
         lds_words<4>(l.k + row, &k[e][0]);
         lds_words<4>(l.k2 + row, &k[e][4]);
-        kp[e][0] = lds_u16(par);
-        kp[e][1] = lds_u16(par + 2);
+        kp[e][0] = ld_shared_u16(par);
+        kp[e][1] = ld_shared_u16(par + 2);
       } else {
         lds_words<KW>(l.k + row, &k[e][0]);
-        kp[e][0] = lds_u16(par);
+        kp[e][0] = ld_shared_u16(par);
       }
     }
   }
@@ -157,10 +151,10 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < VW; ++i) lds_words<1>(row + 32 * i, &v[e][i]);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) vp[e][i] = lds_u16(par + 4 * i);
+        for (int i = 0; i < 3; ++i) vp[e][i] = ld_shared_u16(par + 4 * i);
       } else {
         lds_words<VW>(row, &v[e][0]);
-        vp[e][0] = lds_u16(par);
+        vp[e][0] = ld_shared_u16(par);
       }
     }
   }

@@ -8,12 +8,13 @@
 // otherwise they hold the same rows, take the stages in turn, and add up at the end.
 //
 // Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
-// attention.cu's kSlack), and the output.  Warps 8-15: codes to bf16, into a ring of K/V stages in
-// the 128-byte swizzled layout, each half every second stage; a lane turns 32 channels (one group)
-// of an entry, and eight lanes of the same group store to eight different bank groups.  Warps 16
-// and 17: one thread each issues the products of a group: the scores of a step as soon as the
-// softmax warps hold those of the step before in registers, so that they are there when the
-// softmax comes back for them.
+// attention.cu's kSlack), and the output.  Warp 19 looks the pages up and has the tiles' codes and
+// params copied into a ring (bulk copies of 16 entries).  Warps 8-15 turn codes to bf16, into a ring
+// of K/V stages in the 128-byte swizzled layout, each half of them every second tile; a lane turns
+// 32 channels (one group) of an entry, in an order in which no two lanes meet in a bank.  Warps 16
+// and 17 issue the products of a group each: the scores of a step as soon as the softmax warps
+// hold those of the step before in registers, so that they are there when the softmax comes back
+// for them.  Warp 18 leaves the notes for the join and fetches the next queries to L2.
 //
 // TMEM, 512 columns: O 2 x 128, S 2 x 64, P 2 x 32 and 64 for the queries of group 0 (left operands
 // may lie there).  Group 1's queries are in shared memory.  Per 64 entries and D = 128 shared memory
@@ -37,7 +38,8 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kTile = 64;  // entries of a step
-constexpr int kStages = 5;
+constexpr int kStages = 4;
+constexpr int kRawTiles = 4;
 constexpr int kThreads = 640;
 // registers a thread: launched with 96, then shared out anew, 128 threads a figure:
 // 2 x 136 + 2 x 80 + 48 = 5 x 96
@@ -164,6 +166,12 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // A whole warp's wait: one vote when the phase is complete already; the same bounded wait otherwise.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int32_t* status) {
@@ -177,7 +185,11 @@ struct Smem {
   static constexpr uint32_t kStage = 2 * kTensor;
   static constexpr uint32_t kQ = kStages * kStage;  // group 1's queries
   static constexpr uint32_t kScratch = kQ + kRows * D * 2;  // 2 KB for each softmax warp
-  static constexpr size_t kBytes = kScratch + 8 * 2048 + 1024;  // and room to align
+  // codes and params as they come from the cache, kRawTiles tiles: K codes, V codes, K and V params
+  static constexpr uint32_t kRaw = kScratch + 8 * 2048;
+  static constexpr uint32_t kRawCodes = kTile * D / 2, kRawPar = kTile * D / 16;
+  static constexpr uint32_t kRawTile = 2 * (kRawCodes + kRawPar);
+  static constexpr size_t kBytes = kRaw + kRawTiles * kRawTile + 1024;  // and room to align
 };
 
 // What a CTA does with one segment.
@@ -200,8 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int STRIDE = kShare ? 1 : 2;  // tiles from one of a group to its next
   constexpr uint32_t SLAB = kTile * 128, QSLAB = kRows * 128;
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t bars[2 * kStages + 11];
+  __shared__ uint64_t bars[2 * kStages + 2 * kRawTiles + 11];
   __shared__ uint32_t visible[kStages][2];  // of the stage's 64 entries: a bit per entry
+  __shared__ uint32_t raw_visible[kRawTiles][2];
   __shared__ float2 ml_s[2][kRows];         // groups with the same rows: reference and sum
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -214,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // product with V has been added
   constexpr uint32_t kBarQ = 0, kBarS = 8, kBarFree = 16, kBarP = 24, kBarV = 32, kGroupBars = 40;
   const uint32_t done_bar = gbars + 2 * kGroupBars;
+  const uint32_t raw_full0 = done_bar + 8, raw_empty0 = raw_full0 + 8 * kRawTiles;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -229,6 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar + kBarV, 1);
     }
     mbar_init(done_bar, 2);
+    for (int s = 0; s < kRawTiles; ++s) {
+      mbar_init(raw_full0 + 8 * s, 4);   // the four lanes that copy 16 entries each
+      mbar_init(raw_empty0 + 8 * s, 4);  // the four warps that turn them
+    }
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -381,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 4; e < kTile; e += 8) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            top[x] = e + 4 + x < kTile ? fmaxf(top[x], fmaxf(s[e + x], s[e + 4 + x]))
+            top[x] = e + 4 + x < kTile ? max3(top[x], s[e + x], s[e + 4 + x])
                                        : fmaxf(top[x], s[e + x]);
         }
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
@@ -550,24 +568,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------------ codes to bf16
-    // lanes 8q .. 8q + 7 take group q (and q + 4, ...) of entries 8w .. 8w + 7 and, 32 further, of
-    // the same again; this half of the warps every second tile
+    // this half of the warps every second tile
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTurnRegs));
-    constexpr int GROUPS = D / 32;       // per entry
-    constexpr int PER = 2 * GROUPS / 4;  // pieces of K a thread turns per tile
-    constexpr int AHEAD = 2 * kTile;     // entries from one of its tiles to the next
-    const int half = (warp >> 2) & 1, w = warp & 3, q4 = lane >> 3, t8 = lane & 7;
+    constexpr int GROUPS = D / 32;  // per entry
+    constexpr int PER = GROUPS / 2;  // pieces of K (and of V) a thread turns per tile
+    const int half = (warp >> 2) & 1, w = warp & 3;
     // piece e of the thread: entry entry0 + 32 e, group g
-    const int entry0 = GROUPS == 4 ? w * 8 + t8 : w * 8 + t8 + 32 * (q4 >> 1);
-    const int g = GROUPS == 4 ? q4 : q4 & 1;
-    const int step_pages = AHEAD / p.page_size, step_slots = AHEAD % p.page_size;
-    const uint32_t to = sbase + (g >> 1) * SLAB + entry0 * 128;
-    uint32_t piece_at[4];  // the swizzle depends on the entry modulo 8 alone
+    const int entry0 = (w * 32 + lane) / GROUPS, g = lane % GROUPS;
+    const uint32_t raw0 = sbase + M::kRaw + (w * 32 + lane) * 16;
+    const uint32_t par0 = sbase + M::kRaw + 2 * M::kRawCodes + (w * 32 + lane) * 2;
+    // Word x goes to 16-byte piece (4 (g % 2) + x) ^ (entry % 8) of the entry's row in slab g / 2.
+    // Lanes of slab 1 store words in the order 2, 3, 0, 1: with eight lanes (two entries, four
+    // groups) at a time, all eight pieces of a 128-byte row are then hit once.
+    const int turn_x = D > 64 && g >= 2 ? 2 : 0;
+    uint32_t piece_at[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) piece_at[x] = to + ((((g & 1) * 4 + x) ^ t8) << 4);
+    for (int x = 0; x < 4; ++x)
+      piece_at[x] = sbase + (g >> 1) * SLAB + entry0 * 128 +
+                    ((((g & 1) * 4 + (x ^ turn_x)) ^ (entry0 & 7)) << 4);
     auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst) {
       const Kv4Scale sc = kv4_scale(__byte_perm(param, param, 0x1010));
-      const uint32_t wd[4] = {codes.x, codes.y, codes.z, codes.w};
+      const uint32_t wd[4] = {turn_x ? codes.z : codes.x, turn_x ? codes.w : codes.y,
+                              turn_x ? codes.x : codes.z, turn_x ? codes.y : codes.w};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const uint32_t a = kv4_pair<0>(wd[x], sc), c = kv4_pair<1>(wd[x], sc),
@@ -579,102 +601,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
-      const int h = sg.h;
-      const int32_t* table = p.table + static_cast<int64_t>(sg.b) * p.table_stride;
-      const uint8_t* mask = p.key_mask ? p.key_mask + sg.b * p.mask_stride : nullptr;
-      const int t_first = (half ^ step) & 1;
-      // the walk through the pages: word of the table and slot of the entries to look at next
-      int j_at = pc.j0 + t_first * kTile + entry0;
-      int word[PER] = {}, slot[PER] = {}, page[PER] = {};
-      auto look_up = [&](int e) {
-        // (looked at only when its codes are loaded: a test here would wait for the load)
-        page[e] = -1;
-        if (j_at + 32 * e < pc.end && word[e] < p.table_stride) page[e] = __ldg(table + word[e]);
-      };
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        word[e] = (j_at + 32 * e) / p.page_size;
-        slot[e] = j_at + 32 * e - word[e] * p.page_size;
-        look_up(e);
-      }
-      // Codes of one tile in registers.  As soon as a piece has been turned, that of the thread's
-      // next tile is loaded in its place.
-      uint4 kc[PER], vc[PER];
-      uint32_t kp[PER], vp[PER], seen[PER];
-      int64_t row[PER];  // of the cache, -1: absent
-      auto next_rows = [&]() {
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-          row[e] = static_cast<unsigned>(page[e]) < static_cast<unsigned>(p.pages)
-                       ? (static_cast<int64_t>(page[e]) * p.heads + h) * p.page_size + slot[e]
-                       : -1;
-      };
-      auto load_k = [&](int e) {
-        kc[e] = make_uint4(0u, 0u, 0u, 0u);
-        kp[e] = seen[e] = 0u;
-        if (row[e] >= 0) {
-          kc[e] = ld_stream_v4(p.k_codes + row[e] * (D / 2) + g * 16);
-          kp[e] = __ldg(p.k_params + row[e] * (D / 32) + g);
-          seen[e] = mask ? __ldg(mask + j_at - AHEAD + 32 * e) : 1u;
-        }
-      };
-      auto load_v = [&](int e) {
-        vc[e] = make_uint4(0u, 0u, 0u, 0u);
-        vp[e] = 0u;
-        if (row[e] >= 0) {
-          vc[e] = ld_stream_v4(p.v_codes + row[e] * (D / 2) + g * 16);
-          vp[e] = __ldg(p.v_params + row[e] * (D / 32) + g);
-        }
-      };
-      auto advance = [&]() {
-        j_at += AHEAD;
+      for (int t = (half ^ step) & 1; t < pc.tiles; t += 2) {
+        const int k = step + t, st = stage_of(k), rs = k % kRawTiles;
+        if (!wait_warp(raw_full0 + 8 * rs, (k / kRawTiles) & 1, abort_v, f.status)) break;
+        const uint32_t at = raw0 + rs * M::kRawTile, par = par0 + rs * M::kRawTile;
+        uint4 kc[PER], vc[PER];
+        uint32_t kp[PER], vp[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-          word[e] += step_pages;
-          slot[e] += step_slots;
-          if (slot[e] >= p.page_size) {
-            slot[e] -= p.page_size;
-            ++word[e];
-          }
-          look_up(e);
+          kc[e] = ld_shared_v4(at + e * 2048);
+          vc[e] = ld_shared_v4(at + M::kRawCodes + e * 2048);
+          kp[e] = ld_shared_u16(par + e * 256);
+          vp[e] = ld_shared_u16(par + M::kRawPar + e * 256);
         }
-      };
-      next_rows();
-      advance();
+        const uint32_t vis[2] = {raw_visible[rs][0], raw_visible[rs][1]};
 #pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        load_k(e);
-        load_v(e);
-      }
-      for (int t = t_first; t < pc.tiles; t += 2) {
-        const int k = step + t, st = stage_of(k);
+        for (int e = 0; e < PER; ++e) {
+          // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
+          const int entry = entry0 + 32 * e;
+          const uint32_t word = PER == 2 ? vis[e] : entry < 32 ? vis[0] : vis[1];
+          if (!(word >> (entry & 31) & 1u)) vp[e] = 0u;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(raw_empty0 + 8 * rs);
         if (!wait_warp(empty0 + 8 * st, parity_of(k) ^ 1, abort_v, f.status)) break;
-        // entries 8w .. 8w + 7 of each half of the tile
-        uint32_t see_v[PER];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          unsigned bits;
-          if constexpr (GROUPS == 4)
-            bits = __ballot_sync(kFull, seen[e % PER] != 0u) & 0xffu;
-          else
-            bits = __ballot_sync(kFull, seen[0] != 0u) >> (16 * e) & 0xffu;
-          if (lane == 0) reinterpret_cast<uint8_t*>(&visible[st][e])[w] = static_cast<uint8_t>(bits);
-        }
-#pragma unroll
-        for (int e = 0; e < PER; ++e) see_v[e] = seen[e];
-        next_rows();
-        advance();  // the pages of the tile after the next have a whole round to arrive
+        if (w == 0 && lane < 2) visible[st][lane] = lane ? vis[1] : vis[0];
         const uint32_t sk = st * M::kStage, sv = sk + M::kTensor;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
           turn(kc[e], kp[e], sk + e * 32 * 128);
-          load_k(e);
-        }
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
-          turn(vc[e], see_v[e] != 0u ? vp[e] : 0u, sv + e * 32 * 128);
-          load_v(e);
+          turn(vc[e], vp[e], sv + e * 32 * 128);
         }
         fence_async_shared();
         __syncwarp();
@@ -765,6 +721,75 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < D; c += 64)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
         }
+      }
+    } else {
+      // copies: lane l of the first four takes entries 16 l .. 16 l + 15 of a tile
+      const int step_pages = kTile / p.page_size, step_slots = kTile % p.page_size;
+      int sent = 0;
+      for (int u = u0; u < u1;) {
+        const Piece<ROWS> pc(sg, f, u1 - u);
+        const int32_t* table = p.table + static_cast<int64_t>(sg.b) * p.table_stride;
+        const uint8_t* mask = p.key_mask ? p.key_mask + sg.b * p.mask_stride : nullptr;
+        int j = pc.j0, word = (j + 16 * (lane & 3)) / p.page_size;
+        int slot = j + 16 * (lane & 3) - word * p.page_size;
+        // page word and mask bytes of the next tile (looked at one round after they are asked for)
+        int page = -1;
+        uint32_t m0 = 1u, m1 = 1u;
+        auto ask = [&]() {
+          page = j + 16 * (lane & 3) < pc.end && word < p.table_stride ? __ldg(table + word) : -1;
+          if (mask) {
+            m0 = j + lane < pc.end ? __ldg(mask + j + lane) : 0u;
+            m1 = j + 32 + lane < pc.end ? __ldg(mask + j + 32 + lane) : 0u;
+          }
+        };
+        ask();
+        for (int t = 0; t < pc.tiles; ++t) {
+          const int k = step + t, rs = k % kRawTiles;
+          const int pg = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages) ? page : -1;
+          const int64_t row = (static_cast<int64_t>(pg) * p.heads + sg.h) * p.page_size + slot;
+          const bool there0 = __shfl_sync(kFull, pg, lane >> 4) >= 0;
+          const bool there1 = __shfl_sync(kFull, pg, 2 + (lane >> 4)) >= 0;
+          const uint32_t v0 = __ballot_sync(kFull, there0 && m0 != 0u && j + lane < pc.end);
+          const uint32_t v1 = __ballot_sync(kFull, there1 && m1 != 0u && j + 32 + lane < pc.end);
+          j += kTile;
+          word += step_pages;
+          slot += step_slots;
+          if (slot >= p.page_size) {
+            slot -= p.page_size;
+            ++word;
+          }
+          ask();
+          if (!wait_warp(raw_empty0 + 8 * rs, ((k / kRawTiles) & 1) ^ 1, abort_v, f.status)) break;
+          sent = k + 1;
+          if (lane < 4) {
+            const uint32_t bar = raw_full0 + 8 * rs;
+            if (lane == 0) {
+              raw_visible[rs][0] = v0;
+              raw_visible[rs][1] = v1;
+            }
+            if (pg < 0) {
+              mbar_arrive(bar);
+            } else {
+              constexpr uint32_t kC = 16 * D / 2, kP = 16 * D / 16;  // bytes of 16 entries
+              const uint32_t at = sbase + M::kRaw + rs * M::kRawTile;
+              mbar_expect_tx(bar, 2 * (kC + kP));
+              bulk_g2s(at + lane * kC, p.k_codes + row * (D / 2), kC, bar);
+              bulk_g2s(at + M::kRawCodes + lane * kC, p.v_codes + row * (D / 2), kC, bar);
+              bulk_g2s(at + 2 * M::kRawCodes + lane * kP, p.k_params + row * (D / 32), kP, bar);
+              bulk_g2s(at + 2 * M::kRawCodes + M::kRawPar + lane * kP, p.v_params + row * (D / 32),
+                       kP, bar);
+            }
+          }
+          __syncwarp();
+        }
+        step += pc.tiles;
+        u += pc.units;
+        if (u < u1) sg.next(p, f);
+      }
+      // after a wait that ran out, the last copies into each place may still be under way
+      if (*abort_v && lane < kRawTiles && sent > lane) {
+        const int last = (sent - 1 - lane) / kRawTiles;  // rounds of this place before its last
+        drain_bar(raw_full0 + 8 * lane, last & 1);
       }
     }
   }
