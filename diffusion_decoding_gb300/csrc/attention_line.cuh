@@ -20,6 +20,7 @@ struct AttnPlan {
   int row_tiles;
   int q_aligned;    // query rows on 16-byte boundaries
   int out_aligned;  // output rows too
+  int copy_span;    // entries that surely lie in one page: 16, 32 or 64
   float* part_o;    // [2 * CTAs, rows of a tile, D]
   float2* part_ml;  // [2 * CTAs, rows of a tile]: reference (base 2) and sum of weights
   int2* parts;      // [segments]: see note_segment

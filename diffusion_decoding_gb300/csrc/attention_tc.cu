@@ -40,6 +40,10 @@ constexpr int kRows = 128;
 constexpr int kTile = 64;  // entries of a step
 constexpr int kStages = 4;
 constexpr int kRawTiles = 4;
+// A parity wait tells a phase from the one before it only.  The halves of the turning warps (and, with
+// the same rows, the groups) take every second tile: with even rings they take every use of their
+// own places and so wait for every phase of those barriers.
+static_assert(kStages % 2 == 0 && kRawTiles % 2 == 0, "");
 constexpr int kThreads = 640;
 // registers a thread: launched with 96, then shared out anew, 128 threads a figure:
 // 2 x 136 + 2 x 80 + 48 = 5 x 96
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(done_bar, 2);
     for (int s = 0; s < kRawTiles; ++s) {
-      mbar_init(raw_full0 + 8 * s, 4);   // the four lanes that copy 16 entries each
+      mbar_init(raw_full0 + 8 * s, kTile / f.copy_span);  // the lanes that copy
       mbar_init(raw_empty0 + 8 * s, 4);  // the four warps that turn them
     }
     abort_flag = 0;
@@ -723,20 +727,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // copies: lane l of the first four takes entries 16 l .. 16 l + 15 of a tile
+      // Copies, in as few pieces as the pages allow (each costs the issuing lane about a hundred
+      // cycles): a tile lies in one page when 64 divides the page size, in two or four otherwise.
+      // Lane l takes entries span * l .. of the tile.
+      const int span = f.copy_span, mine_from = span * lane;
+      const bool copier = mine_from < kTile;
       const int step_pages = kTile / p.page_size, step_slots = kTile % p.page_size;
+      const uint32_t codes_bytes = span * D / 2, par_bytes = span * D / 16;
+      const uint32_t to_c = sbase + M::kRaw + lane * codes_bytes;
+      const uint32_t to_p = sbase + M::kRaw + 2 * M::kRawCodes + lane * par_bytes;
       int sent = 0;
       for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int32_t* table = p.table + static_cast<int64_t>(sg.b) * p.table_stride;
         const uint8_t* mask = p.key_mask ? p.key_mask + sg.b * p.mask_stride : nullptr;
-        int j = pc.j0, word = (j + 16 * (lane & 3)) / p.page_size;
-        int slot = j + 16 * (lane & 3) - word * p.page_size;
+        int j = pc.j0, word = (j + mine_from) / p.page_size;
+        int slot = j + mine_from - word * p.page_size;
         // page word and mask bytes of the next tile (looked at one round after they are asked for)
         int page = -1;
         uint32_t m0 = 1u, m1 = 1u;
         auto ask = [&]() {
-          page = j + 16 * (lane & 3) < pc.end && word < p.table_stride ? __ldg(table + word) : -1;
+          page = copier && j + mine_from < pc.end && word < p.table_stride ? __ldg(table + word) : -1;
           if (mask) {
             m0 = j + lane < pc.end ? __ldg(mask + j + lane) : 0u;
             m1 = j + 32 + lane < pc.end ? __ldg(mask + j + 32 + lane) : 0u;
@@ -745,12 +756,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ask();
         for (int t = 0; t < pc.tiles; ++t) {
           const int k = step + t, rs = k % kRawTiles;
-          const int pg = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages) ? page : -1;
-          const int64_t row = (static_cast<int64_t>(pg) * p.heads + sg.h) * p.page_size + slot;
-          const bool there0 = __shfl_sync(kFull, pg, lane >> 4) >= 0;
-          const bool there1 = __shfl_sync(kFull, pg, 2 + (lane >> 4)) >= 0;
-          const uint32_t v0 = __ballot_sync(kFull, there0 && m0 != 0u && j + lane < pc.end);
-          const uint32_t v1 = __ballot_sync(kFull, there1 && m1 != 0u && j + 32 + lane < pc.end);
+          const bool here = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
+          const unsigned there = __ballot_sync(kFull, here);  // by piece of `span` entries
+          const int64_t row = (static_cast<int64_t>(page) * p.heads + sg.h) * p.page_size + slot;
+          const uint32_t v0 = __ballot_sync(kFull, (there >> (lane / span) & 1u) && m0 != 0u &&
+                                                       j + lane < pc.end);
+          const uint32_t v1 = __ballot_sync(kFull, (there >> ((lane + 32) / span) & 1u) && m1 != 0u &&
+                                                       j + 32 + lane < pc.end);
           j += kTile;
           word += step_pages;
           slot += step_slots;
@@ -761,23 +773,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           ask();
           if (!wait_warp(raw_empty0 + 8 * rs, ((k / kRawTiles) & 1) ^ 1, abort_v, f.status)) break;
           sent = k + 1;
-          if (lane < 4) {
+          if (copier) {
             const uint32_t bar = raw_full0 + 8 * rs;
             if (lane == 0) {
               raw_visible[rs][0] = v0;
               raw_visible[rs][1] = v1;
             }
-            if (pg < 0) {
+            if (!here) {
               mbar_arrive(bar);
             } else {
-              constexpr uint32_t kC = 16 * D / 2, kP = 16 * D / 16;  // bytes of 16 entries
-              const uint32_t at = sbase + M::kRaw + rs * M::kRawTile;
-              mbar_expect_tx(bar, 2 * (kC + kP));
-              bulk_g2s(at + lane * kC, p.k_codes + row * (D / 2), kC, bar);
-              bulk_g2s(at + M::kRawCodes + lane * kC, p.v_codes + row * (D / 2), kC, bar);
-              bulk_g2s(at + 2 * M::kRawCodes + lane * kP, p.k_params + row * (D / 32), kP, bar);
-              bulk_g2s(at + 2 * M::kRawCodes + M::kRawPar + lane * kP, p.v_params + row * (D / 32),
-                       kP, bar);
+              const uint32_t at = rs * M::kRawTile;
+              mbar_expect_tx(bar, 2 * (codes_bytes + par_bytes));
+              bulk_g2s(to_c + at, p.k_codes + row * (D / 2), codes_bytes, bar);
+              bulk_g2s(to_c + at + M::kRawCodes, p.v_codes + row * (D / 2), codes_bytes, bar);
+              bulk_g2s(to_p + at, p.k_params + row * (D / 32), par_bytes, bar);
+              bulk_g2s(to_p + at + M::kRawPar, p.v_params + row * (D / 32), par_bytes, bar);
             }
           }
           __syncwarp();
@@ -893,6 +903,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   f.unit_log2 = unit_log2_of(static_cast<int64_t>(p.B) * ((p.n * p.G + R - 1) / R) * p.heads,
                              p.max_len, 6);
   f.row_tiles = (p.n * p.G + R - 1) / R;
+  f.copy_span = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
   // a stretch is kLeast units at least: parts have to be joined again
   constexpr int kLeast = 4;
   const int64_t units = static_cast<int64_t>(p.B) * f.row_tiles * p.heads *
