@@ -4,22 +4,23 @@
 // Entries are taken 64 at a time:
 //   S [128 rows x 64] = Q K^T,   O [128 x D] += P V     (tcgen05.mma, fp32 accumulators in TMEM)
 // Two groups of four warps each hold 128 rows, one row a thread.  With more than 128 rows in a
-// segment (kShare) the groups are the two halves of a 256-row tile and use every K/V stage both;
-// otherwise they hold the same rows, take the stages in turn, and add up at the end.
+// segment (kShare) the groups are the two halves of a 256-row tile and both use every K and V tile;
+// otherwise they hold the same rows, take the tiles in turn, and add up at the end.
 //
 // Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
-// attention.cu's kSlack), and the output.  Warp 19 looks the pages up and has the tiles' codes and
-// params copied into a ring (bulk copies of 16 entries).  Warps 8-15 turn codes to bf16, into a ring
-// of K/V stages in the 128-byte swizzled layout, each half of them every second tile; a lane turns
-// 32 channels (one group) of an entry, in an order in which no two lanes meet in a bank.  Warps 16
-// and 17 issue the products of a group each: the scores of a step as soon as the softmax warps
-// hold those of the step before in registers, so that they are there when the softmax comes back
-// for them.  Warp 18 leaves the notes for the join and fetches the next queries to L2.
+// attention.cu's kSlack), and the output.  Warps 18 and 19 look the pages up and have the tiles' codes
+// and params copied into a ring (bulk copies, V's and K's); they also fetch the next queries to L2 and
+// leave the notes for the join.  Warps 8-15 turn codes to bf16, into rings of K and V tiles in the
+// 128-byte swizzled layout, each half of them every second tile; a lane turns 32 channels (one group)
+// of an entry, in an order in which no two lanes meet in a bank.  Warps 16 and 17 issue the products
+// of a group each: the scores of a step as soon as the softmax warps hold those of the step before
+// in registers, so that they are there when the softmax comes back for them.
 //
-// TMEM, 512 columns: O 2 x 128, S 2 x 64, P 2 x 32 and 64 for the queries of group 0 (left operands
-// may lie there).  Group 1's queries are in shared memory.  Per 64 entries and D = 128 shared memory
-// then moves 128 KB (K and V written once and read twice, the queries of group 1 read once), as
-// many cycles as the products of both groups take.
+// TMEM, 512 columns: O 2 x 128, S 2 x 64, P 2 x 32 and 64 for the queries (left operands may lie
+// there): those of group 0, or of both groups where the rows are the same.  Otherwise group 1's are
+// in shared memory.  Per 64 entries, 256 rows and D = 128 shared memory then moves 128 KB (K and V
+// written once and read twice, the queries of group 1 read once), as many cycles as the products of
+// both groups take.
 // The eight channels of a code word come out as pairs (j, j + 4): Q's channels are put in the same
 // order (the scores do not depend on it), and the output's are put back.
 #include "attention.h"
@@ -38,12 +39,17 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kTile = 64;  // entries of a step
-constexpr int kStages = 4;
+// K tiles and V tiles have a ring each: a K tile is free again as soon as its scores are there, a V
+// tile only when its weights have been taken off them and multiplied.
+constexpr int kKTiles = 4;
+__host__ __device__ constexpr int v_tiles(bool share) { return share ? 4 : 6; }
 constexpr int kRawTiles = 4;
+constexpr int kVisible = 2 * kKTiles;  // scores 4 tiles on are not begun before those here are read
 // A parity wait tells a phase from the one before it only.  The halves of the turning warps (and, with
 // the same rows, the groups) take every second tile: with even rings they take every use of their
 // own places and so wait for every phase of those barriers.
-static_assert(kStages % 2 == 0 && kRawTiles % 2 == 0, "");
+static_assert(kKTiles % 2 == 0 && v_tiles(false) % 2 == 0 && v_tiles(true) % 2 == 0, "");
+static_assert(kRawTiles % 2 == 0, "");
 constexpr int kThreads = 640;
 // registers a thread: launched with 96, then shared out anew, 128 threads a figure:
 // 2 x 136 + 2 x 80 + 48 = 5 x 96
@@ -183,12 +189,12 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
   return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status)) != 0;
 }
 
-template <int D>
+template <int D, bool kShare>
 struct Smem {
-  static constexpr uint32_t kTensor = kTile * D * 2;  // K (or V) of a stage
-  static constexpr uint32_t kStage = 2 * kTensor;
-  static constexpr uint32_t kQ = kStages * kStage;  // group 1's queries
-  static constexpr uint32_t kScratch = kQ + kRows * D * 2;  // 2 KB for each softmax warp
+  static constexpr uint32_t kTensor = kTile * D * 2;  // a K (or V) tile
+  static constexpr uint32_t kV = kKTiles * kTensor;
+  static constexpr uint32_t kQ = kV + v_tiles(kShare) * kTensor;  // group 1's own queries
+  static constexpr uint32_t kScratch = kQ + (kShare ? kRows * D * 2 : 0);  // 2 KB a softmax warp
   // codes and params as they come from the cache, kRawTiles tiles: K codes, V codes, K and V params
   static constexpr uint32_t kRaw = kScratch + 8 * 2048;
   static constexpr uint32_t kRawCodes = kTile * D / 2, kRawPar = kTile * D / 16;
@@ -211,13 +217,14 @@ struct Piece {
 template <int D, bool kShare>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
-  using M = Smem<D>;
+  using M = Smem<D, kShare>;
+  constexpr int kVTiles = v_tiles(kShare);
   constexpr int ROWS = kShare ? 2 * kRows : kRows;
   constexpr int STRIDE = kShare ? 1 : 2;  // tiles from one of a group to its next
   constexpr uint32_t SLAB = kTile * 128, QSLAB = kRows * 128;
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t bars[2 * kStages + 2 * kRawTiles + 11];
-  __shared__ uint32_t visible[kStages][2];  // of the stage's 64 entries: a bit per entry
+  __shared__ uint64_t bars[2 * kKTiles + 2 * kVTiles + 2 * kRawTiles + 11];
+  __shared__ uint32_t visible[kVisible][2];  // of a tile's 64 entries: a bit per entry
   __shared__ uint32_t raw_visible[kRawTiles][2];
   __shared__ float2 ml_s[2][kRows];         // groups with the same rows: reference and sum
   __shared__ uint32_t tmem_slot;
@@ -225,8 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
-  const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kStages]);
-  const uint32_t gbars = smem_u32(&bars[2 * kStages]);  // of group g at + 40 g:
+  const uint32_t k_full0 = smem_u32(&bars[0]), k_empty0 = k_full0 + 8 * kKTiles;
+  const uint32_t v_full0 = k_empty0 + 8 * kKTiles, v_empty0 = v_full0 + 8 * kVTiles;
+  const uint32_t gbars = v_empty0 + 8 * kVTiles;  // of group g at + 40 g:
   // the queries are there and O may be overwritten; S is there; S has been read; P is there; the
   // product with V has been added
   constexpr uint32_t kBarQ = 0, kBarS = 8, kBarFree = 16, kBarP = 24, kBarV = 32, kGroupBars = 40;
@@ -234,9 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw_full0 = done_bar + 8, raw_empty0 = raw_full0 + 8 * kRawTiles;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 4);
-      mbar_init(empty0 + 8 * s, kShare ? 2 : 1);
+    for (int s = 0; s < kKTiles; ++s) {
+      mbar_init(k_full0 + 8 * s, 4);
+      mbar_init(k_empty0 + 8 * s, kShare ? 2 : 1);
+    }
+    for (int s = 0; s < kVTiles; ++s) {
+      mbar_init(v_full0 + 8 * s, 4);
+      mbar_init(v_empty0 + 8 * s, kShare ? 2 : 1);
     }
     for (int g = 0; g < 2; ++g) {
       const uint32_t bar = gbars + kGroupBars * g;
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(done_bar, 2);
     for (int s = 0; s < kRawTiles; ++s) {
-      mbar_init(raw_full0 + 8 * s, kTile / f.copy_span);  // the lanes that copy
+      mbar_init(raw_full0 + 8 * s, 2 * (kTile / f.copy_span));  // the lanes that copy
       mbar_init(raw_empty0 + 8 * s, 4);  // the four warps that turn them
     }
     abort_flag = 0;
@@ -276,10 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Segment<ROWS> sg;
   sg.find(p, f, line, u0);
-  int step = 0;  // K/V tiles so far: tile k is in stage k % kStages
+  int step = 0;  // tiles so far
   int mine = 0;  // tiles of this group so far: the phase of its barriers
-  auto stage_of = [](int k) { return k % kStages; };
-  auto parity_of = [](int k) { return static_cast<uint32_t>(k / kStages) & 1u; };
+  // tile k's place in a ring of `of` places, and the parity of its use of it
+  auto place = [](int k, unsigned of) { return static_cast<int>(static_cast<unsigned>(k) % of); };
+  auto parity = [](int k, unsigned of) { return static_cast<unsigned>(k) / of & 1u; };
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax, one row a thread
@@ -301,18 +314,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const uint32_t q_keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
         // The warp loads its 32 rows, four lanes 64 bytes (32 channels) of a row, and puts them where
-        // they belong: group 1's at once, group 0's 32 channels at a time by way of the warp's
-        // scratch, from where each thread takes those of its own row to TMEM.
+        // they belong: group 1's own at once, the others 32 channels at a time by way of the warp's
+        // scratch, from where each thread takes those of its own row to TMEM.  Groups with the same
+        // rows share the queries there, and each brings half of the channels.
         const int lr = lane >> 2, lp = lane & 3;
-        uint4 v[D / 32][4];
+        constexpr int CHUNKS = kShare ? D / 32 : D / 64;
+        const bool to_tmem = !kShare || grp == 0;
+        const int chunk0 = kShare ? 0 : grp * CHUNKS;
+        uint4 v[CHUNKS][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int rr = r - lane + e * 8 + lr;
           const int ri = token_of(p, rr);
           const uint16_t* src =
-              p.q + b * p.qb + ri * p.qt + (h * p.G + rr - ri * p.G) * p.qh + lp * 8;
+              p.q + b * p.qb + ri * p.qt + (h * p.G + rr - ri * p.G) * p.qh + chunk0 * 32 + lp * 8;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < CHUNKS; ++c) {
             v[c][e] = make_uint4(0u, 0u, 0u, 0u);
             if (rr < rows) {
               if (f.q_aligned) {
@@ -328,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          if (grp == 0) __syncwarp();  // what was in the scratch has been taken
+        for (int c = 0; c < CHUNKS; ++c) {
+          if (to_tmem) __syncwarp();  // what was in the scratch has been taken
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t x[4] = {v[c][e].x, v[c][e].y, v[c][e].z, v[c][e].w};
@@ -337,15 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) x[k] = (x[k] ^ q_flip) & q_keep;
             const int rw = e * 8 + lr, rg = (warp & 3) * 32 + rw;  // row of the warp, of the group
             const uint32_t dst =
-                grp == 0 ? scratch + rw * 64 + ((lp ^ (rw >> 1 & 3)) << 4)
-                         : sbase + M::kQ + (c >> 1) * QSLAB + rg * 128 +
-                               ((((c & 1) * 4 + lp) ^ (rg & 7)) << 4);
+                to_tmem ? scratch + rw * 64 + ((lp ^ (rw >> 1 & 3)) << 4)
+                        : sbase + M::kQ + (c >> 1) * QSLAB + rg * 128 +
+                              ((((c & 1) * 4 + lp) ^ (rg & 7)) << 4);
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst),
                          "r"(__byte_perm(x[0], x[2], 0x5410)), "r"(__byte_perm(x[0], x[2], 0x7632)),
                          "r"(__byte_perm(x[1], x[3], 0x5410)), "r"(__byte_perm(x[1], x[3], 0x7632))
                          : "memory");
           }
-          if (grp == 0) {
+          if (to_tmem) {
             __syncwarp();
             uint32_t w[16];
 #pragma unroll
@@ -353,10 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint4 y = ld_shared_v4(scratch + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4));
               w[4 * k] = y.x, w[4 * k + 1] = y.y, w[4 * k + 2] = y.z, w[4 * k + 3] = y.w;
             }
-            tmem_st16(lanes + col_q + c * 16, w);
+            tmem_st16(lanes + col_q + (chunk0 + c) * 16, w);
           }
         }
-        if (grp == 0)
+        if (to_tmem)
           tmem_wait_st();
         else
           fence_async_shared();
@@ -364,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar + kBarQ);
-          // both groups read both accumulators of the segment before
+          // both groups read both accumulators of the segment before, and the queries are shared
           if (!kShare) mbar_arrive(gbars + kGroupBars * (grp ^ 1) + kBarQ);
         }
       }
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;
       uint64_t l2 = 0;  // two partial sums
       bool ok = true;
-      int st = stage_of(step + first);
+      int vis_at = place(step + first, kVisible);
       for (int n = 0; n < count; ++n) {
         const int t = first + n * STRIDE;
         // the scores and the mask words of their stage
@@ -383,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s[kTile];
         tmem_ld32(t_s, s);
         tmem_ld32(t_s + 32, s + 32);
-        const uint32_t vis0 = visible[st][0], vis1 = visible[st][1];
-        st = st + STRIDE >= kStages ? st + STRIDE - kStages : st + STRIDE;
+        const uint32_t vis0 = visible[vis_at][0], vis1 = visible[vis_at][1];
+        vis_at = place(vis_at + STRIDE, kVisible);
         tmem_wait_ld();
         tc_before();
         __syncwarp();
@@ -462,6 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l, l_hi;
       unpack2(l2, l, l_hi);
       l += l_hi;
+      const bool direct = pc.units == sg.units;
+      int64_t out_row[4];  // element of p.out where the lane's piece of row 8 e + lane / 4 starts
+#pragma unroll
+      for (int e = 0; e < 4 && direct; ++e) {
+        const int rr = r - lane + e * 8 + (lane >> 2), ri = token_of(p, rr);
+        out_row[e] = rr < rows ? b * p.ob + ri * p.ot + (h * p.G + rr - ri * p.G) * p.oh +
+                                     (lane & 3) * 8
+                               : INT64_MIN;
+      }
       // ---- output.  Groups with the same rows: each takes half of the channels of both.
       if (count > 0 && ok) ok = wait_warp(bar + kBarV, (mine + count - 1) & 1, abort_v, f.status);
       if constexpr (!kShare) {
@@ -470,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_after();
       if (ok) {
-        const bool direct = pc.units == sg.units;
         const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
         const int row_tile = r - sg.rt * ROWS;
         float keep0 = count > 0 ? 1.f : 0.f, keep1 = 0.f;  // this group's and the other's
@@ -486,29 +511,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int SPAN = kShare ? D : D / 2;
         const int c0 = kShare ? 0 : grp * SPAN;
         const uint32_t t_other = lanes + col_o(grp ^ 1);
-        int64_t out_row[4];  // element of p.out where the lane's piece of row 8 e + lane / 4 starts
-#pragma unroll
-        for (int e = 0; e < 4 && direct; ++e) {
-          const int rr = r - lane + e * 8 + (lane >> 2), ri = token_of(p, rr);
-          out_row[e] = rr < rows ? b * p.ob + ri * p.ot + (h * p.G + rr - ri * p.G) * p.oh +
-                                       (lane & 3) * 8
-                                 : INT64_MIN;
-        }
 #pragma unroll 1
         for (int c = c0; c < c0 + SPAN; c += 32) {
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          if (count > 0) {
-            tmem_ld32(t_o + c, o);
-            tmem_wait_ld();
-          }
-          if constexpr (!kShare) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
+          if constexpr (kShare) {
+            if (count > 0) {
+              tmem_ld32(t_o + c, o);
+              tmem_wait_ld();
+            }
+          } else {
             float x[32];
+            if (count > 0) tmem_ld32(t_o + c, o);
             tmem_ld32(t_other + c, x);
             tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
           }
@@ -606,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       for (int t = (half ^ step) & 1; t < pc.tiles; t += 2) {
-        const int k = step + t, st = stage_of(k), rs = k % kRawTiles;
-        if (!wait_warp(raw_full0 + 8 * rs, (k / kRawTiles) & 1, abort_v, f.status)) break;
+        const int k = step + t, rs = place(k, kRawTiles);
+        if (!wait_warp(raw_full0 + 8 * rs, parity(k, kRawTiles), abort_v, f.status)) break;
         const uint32_t at = raw0 + rs * M::kRawTile, par = par0 + rs * M::kRawTile;
         uint4 kc[PER], vc[PER];
         uint32_t kp[PER], vp[PER];
@@ -628,17 +647,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(raw_empty0 + 8 * rs);
-        if (!wait_warp(empty0 + 8 * st, parity_of(k) ^ 1, abort_v, f.status)) break;
-        if (w == 0 && lane < 2) visible[st][lane] = lane ? vis[1] : vis[0];
-        const uint32_t sk = st * M::kStage, sv = sk + M::kTensor;
+        const int ks = place(k, kKTiles), vs = place(k, kVTiles);
+        if (!wait_warp(k_empty0 + 8 * ks, parity(k, kKTiles) ^ 1, abort_v, f.status)) break;
+        if (w == 0 && lane < 2) visible[place(k, kVisible)][lane] = lane ? vis[1] : vis[0];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          turn(kc[e], kp[e], sk + e * 32 * 128);
-          turn(vc[e], vp[e], sv + e * 32 * 128);
-        }
+        for (int e = 0; e < PER; ++e) turn(kc[e], kp[e], ks * M::kTensor + e * 32 * 128);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full0 + 8 * st);
+        if (lane == 0) mbar_arrive(k_full0 + 8 * ks);
+        if (!wait_warp(v_empty0 + 8 * vs, parity(k, kVTiles) ^ 1, abort_v, f.status)) break;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) turn(vc[e], vp[e], M::kV + vs * M::kTensor + e * 32 * 128);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full0 + 8 * vs);
       }
       step += pc.tiles;
       u += pc.units;
@@ -660,26 +682,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int first = kShare ? 0 : (grp ^ step) & 1;
         const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
-        auto wait = [&](uint32_t at, uint32_t parity) {
-          return wait_warp(at, parity, abort_v, f.status);
+        auto wait = [&](uint32_t at, uint32_t phase) {
+          return wait_warp(at, phase, abort_v, f.status);
         };
         // every phase of kBarQ is waited for, of segments without tiles too
         ok = ok && wait(bar + kBarQ, piece_no & 1);
         auto scores = [&](int k) {
-          const int st = __shfl_sync(kFull, stage_of(k), 0);
-          if (!wait(full0 + 8 * st, parity_of(k))) return false;
+          const int ks = __shfl_sync(kFull, place(k, kKTiles), 0);
+          if (!wait(k_full0 + 8 * ks, parity(k, kKTiles))) return false;
           tc_after();
-          const uint32_t low = desc_low(sbase + st * M::kStage, 16);
+          const uint32_t low = desc_low(sbase + ks * M::kTensor, 16);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             const uint64_t kd = desc_at(low, (x >> 2) * SLAB + (x & 3) * 32);
-            if (grp == 0)
+            if (!kShare || grp == 0)
               mma_ts(lead, t_s, base + col_q + x * 8, kd, idesc(kTile, false), x > 0);
             else
               mma_ss(lead, t_s, desc_at(q_low, (x >> 2) * QSLAB + (x & 3) * 32), kd,
                      idesc(kTile, false), x > 0);
           }
           mma_commit(lead, bar + kBarS);
+          mma_commit(lead, k_empty0 + 8 * ks);
           if (lead) mbar_arrive(bar + kBarS);
           return true;
         };
@@ -692,14 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = wait(bar + kBarP, (mine + n) & 1);
           if (!ok) break;
+          const int vs = __shfl_sync(kFull, place(k, kVTiles), 0);
+          ok = wait(v_full0 + 8 * vs, parity(k, kVTiles));
+          if (!ok) break;
           tc_after();
-          const int st = __shfl_sync(kFull, stage_of(k), 0);
-          const uint32_t low = desc_low(sbase + st * M::kStage + M::kTensor, D > 64 ? SLAB : 16);
+          const uint32_t low = desc_low(sbase + M::kV + vs * M::kTensor, D > 64 ? SLAB : 16);
 #pragma unroll
           for (int x = 0; x < kTile / 16; ++x)
             mma_ts(lead, t_o, t_p + x * 8, desc_at(low, x * 2048), idesc(D, true), n > 0 || x > 0);
           mma_commit(lead, bar + kBarV);
-          mma_commit(lead, empty0 + 8 * st);
+          mma_commit(lead, v_empty0 + 8 * vs);
         }
         // the last scores' phase of kBarFree is passed over: it is waited for here
         if (count > 0) ok = ok && wait(bar + kBarFree, (mine + count - 1) & 1);
@@ -709,33 +734,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < u1) sg.next(p, f);
       }
       mma_commit(lead, done_bar);
-    } else if (grp == 2) {
-      // notes for the join, and the next segment's queries on their way to L2
-      for (int u = u0; u < u1;) {
-        const Piece<ROWS> pc(sg, f, u1 - u);
-        if (lane == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
-        u += pc.units;
-        if (u >= u1) break;
-        sg.next(p, f);
-        const int r1 = min((sg.rt + 1) * ROWS, rows);
-        for (int r = sg.rt * ROWS + lane; r < r1; r += 32) {
-          const int i = token_of(p, r);
-          const uint16_t* src = p.q + sg.b * p.qb + i * p.qt + (sg.h * p.G + r - i * p.G) * p.qh;
-#pragma unroll
-          for (int c = 0; c < D; c += 64)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
-        }
-      }
     } else {
       // Copies, in as few pieces as the pages allow (each costs the issuing lane about a hundred
       // cycles): a tile lies in one page when 64 divides the page size, in two or four otherwise.
-      // Lane l takes entries span * l .. of the tile.
+      // Lane l takes entries span * l .. of the tile; one warp K, the other V.
+      const bool is_k = grp == 3;
+      const uint8_t* codes = is_k ? p.k_codes : p.v_codes;
+      const uint16_t* params = is_k ? p.k_params : p.v_params;
       const int span = f.copy_span, mine_from = span * lane;
       const bool copier = mine_from < kTile;
       const int step_pages = kTile / p.page_size, step_slots = kTile % p.page_size;
       const uint32_t codes_bytes = span * D / 2, par_bytes = span * D / 16;
-      const uint32_t to_c = sbase + M::kRaw + lane * codes_bytes;
-      const uint32_t to_p = sbase + M::kRaw + 2 * M::kRawCodes + lane * par_bytes;
+      const uint32_t to_c = sbase + M::kRaw + (is_k ? 0 : M::kRawCodes) + lane * codes_bytes;
+      const uint32_t to_p =
+          sbase + M::kRaw + 2 * M::kRawCodes + (is_k ? 0 : M::kRawPar) + lane * par_bytes;
       int sent = 0;
       for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
@@ -755,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         ask();
         for (int t = 0; t < pc.tiles; ++t) {
-          const int k = step + t, rs = k % kRawTiles;
+          const int k = step + t, rs = place(k, kRawTiles);
           const bool here = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
           const unsigned there = __ballot_sync(kFull, here);  // by piece of `span` entries
           const int64_t row = (static_cast<int64_t>(page) * p.heads + sg.h) * p.page_size + slot;
@@ -771,11 +783,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++word;
           }
           ask();
-          if (!wait_warp(raw_empty0 + 8 * rs, ((k / kRawTiles) & 1) ^ 1, abort_v, f.status)) break;
+          if (!wait_warp(raw_empty0 + 8 * rs, parity(k, kRawTiles) ^ 1, abort_v, f.status)) break;
           sent = k + 1;
           if (copier) {
             const uint32_t bar = raw_full0 + 8 * rs;
-            if (lane == 0) {
+            if (is_k && lane == 0) {
               raw_visible[rs][0] = v0;
               raw_visible[rs][1] = v1;
             }
@@ -783,18 +795,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(bar);
             } else {
               const uint32_t at = rs * M::kRawTile;
-              mbar_expect_tx(bar, 2 * (codes_bytes + par_bytes));
-              bulk_g2s(to_c + at, p.k_codes + row * (D / 2), codes_bytes, bar);
-              bulk_g2s(to_c + at + M::kRawCodes, p.v_codes + row * (D / 2), codes_bytes, bar);
-              bulk_g2s(to_p + at, p.k_params + row * (D / 32), par_bytes, bar);
-              bulk_g2s(to_p + at + M::kRawPar, p.v_params + row * (D / 32), par_bytes, bar);
+              mbar_expect_tx(bar, codes_bytes + par_bytes);
+              bulk_g2s(to_c + at, codes + row * (D / 2), codes_bytes, bar);
+              bulk_g2s(to_p + at, params + row * (D / 32), par_bytes, bar);
             }
           }
           __syncwarp();
         }
         step += pc.tiles;
+        if (is_k && lane == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
         u += pc.units;
-        if (u < u1) sg.next(p, f);
+        if (u >= u1) break;
+        sg.next(p, f);
+        if (is_k) continue;
+        // the next segment's queries on their way to L2
+        const int r1 = min((sg.rt + 1) * ROWS, rows);
+        for (int r = sg.rt * ROWS + lane; r < r1; r += 32) {
+          const int i = token_of(p, r);
+          const uint16_t* src = p.q + sg.b * p.qb + i * p.qt + (sg.h * p.G + r - i * p.G) * p.qh;
+#pragma unroll
+          for (int c = 0; c < D; c += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
+        }
       }
       // after a wait that ran out, the last copies into each place may still be under way
       if (*abort_v && lane < kRawTiles && sent > lane) {
@@ -900,15 +922,27 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   constexpr int R = kShare ? 2 * kRows : kRows;
   AttnPlan f{};
   static_assert(1 << 6 == kTile, "");
-  f.unit_log2 = unit_log2_of(static_cast<int64_t>(p.B) * ((p.n * p.G + R - 1) / R) * p.heads,
-                             p.max_len, 6);
   f.row_tiles = (p.n * p.G + R - 1) / R;
   f.copy_span = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
-  // a stretch is kLeast units at least: parts have to be joined again
-  constexpr int kLeast = 4;
-  const int64_t units = static_cast<int64_t>(p.B) * f.row_tiles * p.heads *
-                        ((static_cast<int64_t>(p.max_len) >> f.unit_log2) + 1);
-  f.ctas = static_cast<int>(std::min<int64_t>(sm_count, (units + kLeast - 1) / kLeast));
+  const int64_t segments = static_cast<int64_t>(p.B) * f.row_tiles * p.heads;
+  const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile;
+  // Whole segments, or equal stretches that are joined again (of kLeast tiles at least).  A split costs
+  // a second start and end for most CTAs and the join: measured as much as 12 to 18 tiles.  With 128
+  // segments of 17 tiles of 128 rows whole segments take 20.2 us and stretches 30.7; with 64 of 256
+  // rows, 24.6 against 30.2 at 17 tiles and 68.8 against 48.7 at 65.  Where the lengths may differ
+  // the mean is taken for three quarters of the longest.
+  constexpr int kLeast = 4, kSplit = 13;
+  const int64_t rounds = (segments + sm_count - 1) / sm_count;
+  const int64_t mean = segments * tiles / sm_count * (p.lens || p.causal ? 3 : 4) / 4;
+  if (rounds * tiles <= std::max<int64_t>(mean, kLeast) + kSplit) {
+    f.unit_log2 = 6;
+    while (p.max_len > 1 << f.unit_log2) ++f.unit_log2;
+    f.ctas = static_cast<int>(std::min<int64_t>(sm_count, segments));
+  } else {
+    f.unit_log2 = unit_log2_of(segments, p.max_len, 6);
+    const int64_t units = segments * ((static_cast<int64_t>(p.max_len) >> f.unit_log2) + 1);
+    f.ctas = static_cast<int>(std::min<int64_t>(sm_count, (units + kLeast - 1) / kLeast));
+  }
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
   f.status = static_cast<int32_t*>(ws);
@@ -917,10 +951,10 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   f.part_o = reinterpret_cast<float*>(at);
   f.part_ml = reinterpret_cast<float2*>(at + parts * D * 4);
   f.parts = reinterpret_cast<int2*>(at + parts * D * 4 + parts * 8);
-  cudaError_t e = allow_smem<attention_tc_kernel<D, kShare>>(Smem<D>::kBytes);
+  cudaError_t e = allow_smem<attention_tc_kernel<D, kShare>>(Smem<D, kShare>::kBytes);
   if (e != cudaSuccess) return e;
   e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
-                       Smem<D>::kBytes, stream, p, f);
+                       Smem<D, kShare>::kBytes, stream, p, f);
   if (e != cudaSuccess || p.max_len <= 1 << f.unit_log2) return e;
   const int64_t joins = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (R / 32) * (D / 64);
   return launch_dependent(attention_tc_join_kernel<D, R>, dim3(static_cast<unsigned>(joins)),
