@@ -26,9 +26,9 @@
 namespace dllm {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16 * kWarps;  // entries that the warps take together
+// Warps of a CTA: four, so that many CTAs share an SM's registers; eight where segments are few and
+// short, so that each is done in half the steps.
+constexpr int kWarps = 4, kWideWarps = 8;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -175,21 +175,22 @@ constexpr int few_ctas_per_sm(int D, int NT) {
   return D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? 4 : 3) : 2;
 }
 constexpr int kStages = 4;
-template <int D, int NT>
+template <int D, int NT, int WARPS>
 constexpr size_t few_smem() {
-  const size_t ring = static_cast<size_t>(kWarps) * kStages * Tile<D>::kBytes;
-  const size_t join = static_cast<size_t>(kWarps) * 8 * NT * D * 4;
+  const size_t ring = static_cast<size_t>(WARPS) * kStages * Tile<D>::kBytes;
+  const size_t join = static_cast<size_t>(WARPS) * 8 * NT * D * 4;
   return ring > join ? ring : join;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
+template <int D, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / WARPS)
     attention_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
   using R = Tile<D>;
-  constexpr int KW = R::KW, VW = R::VW, MT = D / 16, ROWS = 8 * NT;
+  constexpr int KW = R::KW, VW = R::VW, MT = D / 16, ROWS = 8 * NT, kThreads = 32 * WARPS;
+  constexpr int kStep = 16 * WARPS;  // entries that the warps take together
   extern __shared__ float4 smem_raw[];
-  float* so = reinterpret_cast<float*>(smem_raw);  // [kWarps][ROWS][D]
-  __shared__ float sm[kWarps][ROWS], sl[kWarps][ROWS];
+  float* so = reinterpret_cast<float*>(smem_raw);  // [WARPS][ROWS][D]
+  __shared__ float sm[WARPS][ROWS], sl[WARPS][ROWS];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
         const int r = t * 8 + 2 * c + x;
         float mx = sm[0][r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm[w][r]);
+        for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm[w][r]);
         const float keep = m[t][x] == -INFINITY ? 0.f : ex2(m[t][x] - mx);
         float* dst = so + (warp * ROWS + r) * D;
 #pragma unroll
@@ -487,17 +488,17 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
       if (r0 + r >= rows) break;
       float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         const float2 v = *reinterpret_cast<const float2*>(so + (w * ROWS + r) * D + 2 * ch);
         acc.x += v.x;
         acc.y += v.y;
       }
       float mx = sm[0][r];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm[w][r]);
+      for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm[w][r]);
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
+      for (int w = 0; w < WARPS; ++w)
         sum += sm[w][r] == -INFINITY ? 0.f : sl[w][r] * ex2(sm[w][r] - mx);
       if (!direct) {
         *reinterpret_cast<float2*>(f.part_o + (part * ROWS + r) * D + 2 * ch) = acc;
@@ -524,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas_per_sm(D, NT))
 
 struct FewSizes {
   int nt, row_tiles, ctas, unit_log2;
+  bool wide;   // eight warps a CTA
   bool split;  // some segment can have more than one unit
   size_t off_ml, off_parts, bytes;
 };
@@ -533,14 +535,15 @@ FewSizes few_sizes(int B, int n, int G, int heads, int D, int max_len, int sm_co
   const int64_t rows = static_cast<int64_t>(n) * G;
   s.nt = rows > 8 && D <= 128 ? 2 : 1;
   s.row_tiles = static_cast<int>((rows + 8 * s.nt - 1) / (8 * s.nt));
-  s.ctas = sm_count * few_ctas_per_sm(D, s.nt);
-  // Up to kShort entries a segment is one unit: four warps take it in a few tiles each, sooner than
-  // a second kernel could join its parts.
-  constexpr int kShort = 9;  // log2
-  static_assert(1 << 6 == kStep, "");
-  s.unit_log2 = max_len <= 1 << kShort
-                    ? kShort
-                    : unit_log2_of(static_cast<int64_t>(B) * s.row_tiles * heads, max_len, 6);
+  const int64_t segments = static_cast<int64_t>(B) * s.row_tiles * heads;
+  // Up to 2^kShort entries a segment is one unit: its warps take it in a few tiles each, sooner than a
+  // second kernel could join its parts; in eight warps' steps where that leaves no SM without a CTA.
+  // Four segments of 512 entries take 7.5 us whole with eight warps, 8.6 with four, 7.4 to 7.6 split;
+  // 64 segments 7.9, 9.0 and 9 to 10; four of 1024 entries 10.8 whole and 7.5 split.
+  constexpr int kShort = 9;
+  s.wide = segments <= sm_count && max_len <= 1 << kShort;
+  s.ctas = s.wide ? sm_count : sm_count * few_ctas_per_sm(D, s.nt);
+  s.unit_log2 = max_len <= 1 << kShort ? kShort : unit_log2_of(segments, max_len, 6);
   s.split = max_len > 1 << s.unit_log2;
   const size_t parts = static_cast<size_t>(2) * s.ctas * 8 * s.nt;
   s.off_ml = kWsHeader + parts * D * 4;
@@ -549,15 +552,22 @@ FewSizes few_sizes(int B, int n, int G, int heads, int D, int max_len, int sm_co
   return s;
 }
 
-template <int D, int NT>
-cudaError_t launch_few(const AttnParams& p, const AttnPlan& f, bool split, cudaStream_t stream) {
-  constexpr size_t smem = few_smem<D, NT>();
+template <int D, int NT, int WARPS>
+cudaError_t launch_few_warps(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
+  constexpr size_t smem = few_smem<D, NT, WARPS>();
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = allow_smem<attention_few_kernel<D, NT>>(smem);
+  if (smem > 48 * 1024) e = allow_smem<attention_few_kernel<D, NT, WARPS>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attention_few_kernel<D, NT>, dim3(f.ctas), dim3(kThreads), smem,
-                                   stream, p, f);
-  if (e != cudaSuccess || !split) return e;
+  return launch_dependent(attention_few_kernel<D, NT, WARPS>, dim3(f.ctas), dim3(32 * WARPS), smem,
+                          stream, p, f);
+}
+
+template <int D, int NT>
+cudaError_t launch_few(const AttnParams& p, const AttnPlan& f, const FewSizes& s,
+                       cudaStream_t stream) {
+  if (s.wide) return launch_few_warps<D, NT, kWideWarps>(p, f, stream);
+  const cudaError_t e = launch_few_warps<D, NT, kWarps>(p, f, stream);
+  if (e != cudaSuccess || !s.split) return e;
   return launch_join<D, 8 * NT>(p, f, stream);
 }
 
@@ -585,12 +595,12 @@ cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count,
   f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + s.off_ml);
   f.parts = reinterpret_cast<int2*>(static_cast<char*>(ws) + s.off_parts);
   switch (D * 10 + s.nt) {
-    case 641: return launch_few<64, 1>(p, f, s.split, stream);
-    case 642: return launch_few<64, 2>(p, f, s.split, stream);
-    case 1281: return launch_few<128, 1>(p, f, s.split, stream);
-    case 1282: return launch_few<128, 2>(p, f, s.split, stream);
-    case 1921: return launch_few<192, 1>(p, f, s.split, stream);
-    default: return launch_few<256, 1>(p, f, s.split, stream);
+    case 641: return launch_few<64, 1>(p, f, s, stream);
+    case 642: return launch_few<64, 2>(p, f, s, stream);
+    case 1281: return launch_few<128, 1>(p, f, s, stream);
+    case 1282: return launch_few<128, 2>(p, f, s, stream);
+    case 1921: return launch_few<192, 1>(p, f, s, stream);
+    default: return launch_few<256, 1>(p, f, s, stream);
   }
 }
 

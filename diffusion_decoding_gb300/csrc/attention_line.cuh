@@ -168,9 +168,6 @@ struct Segment {
   }
 };
 
-constexpr int kJoinWarps = 4;
-constexpr int kJoinThreads = 32 * kJoinWarps;
-
 // What the CTA that starts a segment leaves for the join: its part, and the last CTA that has one
 // (the CTAs between have theirs first in their stretches); {-1, 0} for a segment that is whole.
 template <int ROWS>
@@ -201,13 +198,13 @@ __device__ __forceinline__ void store_lse(const AttnParams& p, int b, int h, int
 
 // Join the parts of the segments that several CTAs share, in order of their entries:
 //   out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
-// A CTA per row; each warp takes every fourth part.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads)
+// A CTA per row; each of its WARPS warps takes every WARPS-th part.
+template <int D, int ROWS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
     attention_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
-  constexpr int V = D / 64;
-  __shared__ float2 acc_s[kJoinWarps][D / 2];
-  __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
+  constexpr int V = D / 64, kThreadsJ = 32 * WARPS;
+  __shared__ float2 acc_s[WARPS][D / 2];
+  __shared__ float sum_s[WARPS], max_s[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
@@ -221,18 +218,18 @@ __global__ void __launch_bounds__(kJoinThreads)
   auto part_of = [&](int k) { return static_cast<int64_t>(k == 0 ? info.x : 2 * (c0 + k)) * ROWS; };
   if (rt * ROWS + r >= p.n * p.G) return;
   float mx = -INFINITY;
-  for (int k = threadIdx.x; k < count; k += kJoinThreads) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
+  for (int k = threadIdx.x; k < count; k += kThreadsJ) mx = fmaxf(mx, f.part_ml[part_of(k) + r].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
   if (lane == 0) max_s[warp] = mx;
   __syncthreads();
   mx = max_s[0];
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
+  for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, max_s[w]);
   float2 acc[V] = {};
   float sum = 0.f;
-#pragma unroll 4
-  for (int k = warp; k < count; k += kJoinWarps) {
+#pragma unroll 8
+  for (int k = warp; k < count; k += WARPS) {
     const float2 v = f.part_ml[part_of(k) + r];
     const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
     sum = fmaf(v.y, keep, sum);
@@ -248,12 +245,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int x = 0; x < V; ++x) acc_s[warp][32 * x + lane] = acc[x];
   if (lane == 0) sum_s[warp] = sum;
   __syncthreads();
-  sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+  sum = sum_s[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) sum += sum_s[w];
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int e = threadIdx.x; e < D / 2; e += kJoinThreads) {
+  for (int e = threadIdx.x; e < D / 2; e += kThreadsJ) {
     float2 a = acc_s[0][e];
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
+    for (int w = 1; w < WARPS; ++w) {
       a.x += acc_s[w][e].x;
       a.y += acc_s[w][e].y;
     }
@@ -262,11 +261,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (threadIdx.x == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
 }
 
+// Sixteen warps where a segment is cut into more than 16 parts, else four.
 template <int D, int ROWS>
 cudaError_t launch_join(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
-  const int64_t blocks = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * ROWS;
-  return launch_dependent(attention_join_kernel<D, ROWS>, dim3(static_cast<unsigned>(blocks)),
-                          dim3(kJoinThreads), 0, stream, p, f);
+  const int64_t segments = static_cast<int64_t>(p.B) * f.row_tiles * p.heads;
+  const dim3 blocks(static_cast<unsigned>(segments * ROWS));
+  if (f.ctas > 16 * segments)
+    return launch_dependent(attention_join_kernel<D, ROWS, 16>, blocks, dim3(512), 0, stream, p, f);
+  return launch_dependent(attention_join_kernel<D, ROWS, 4>, blocks, dim3(128), 0, stream, p, f);
 }
 
 }  // namespace
