@@ -52,8 +52,8 @@ static_assert(kKTiles % 2 == 0 && v_tiles(false) % 2 == 0 && v_tiles(true) % 2 =
 static_assert(kRawTiles % 2 == 0, "");
 constexpr int kThreads = 640;
 // registers a thread: launched with 96, then shared out anew, 128 threads a figure:
-// 2 x 136 + 2 x 80 + 48 = 5 x 96
-constexpr int kSoftmaxRegs = 136, kTurnRegs = 80, kIssueRegs = 48;
+// 2 x 152 + 2 x 64 + 48 = 5 x 96
+constexpr int kSoftmaxRegs = 152, kTurnRegs = 64, kIssueRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kTurnRegs + kIssueRegs == 5 * 96, "");
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;  // as in attention.cu
@@ -379,11 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_shared();
         tc_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar + kBarQ);
-          // both groups read both accumulators of the segment before, and the queries are shared
-          if (!kShare) mbar_arrive(gbars + kGroupBars * (grp ^ 1) + kBarQ);
-        }
+        // only of a group with tiles here: it is held up at the end until its issuer has passed
+        if (lane == 0 && count > 0) mbar_arrive(bar + kBarQ);
+        // both groups read both accumulators of the segment before, and the queries are shared
+        if (!kShare && lane == 0 && pc.tiles > 1 - first)
+          mbar_arrive(gbars + kGroupBars * (grp ^ 1) + kBarQ);
       }
       const int bound = rows_see(p, sg.len, r);             // entries this row sees
       const int all_see = rows_see(p, sg.len, r - row_in);  // what every row of the group sees
@@ -677,16 +677,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t_s = base + col_s(grp), t_p = base + col_p(grp), t_o = base + col_o(grp);
       const uint32_t q_low = desc_low(sbase + M::kQ, 16);
       bool ok = true;
-      int piece_no = 0;
-      for (int u = u0; u < u1; ++piece_no) {
+      int piece_no = 0;  // segments with tiles of this group
+      for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int first = kShare ? 0 : (grp ^ step) & 1;
         const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
         auto wait = [&](uint32_t at, uint32_t phase) {
           return wait_warp(at, phase, abort_v, f.status);
         };
-        // every phase of kBarQ is waited for, of segments without tiles too
-        ok = ok && wait(bar + kBarQ, piece_no & 1);
+        if (count > 0) ok = ok && wait(bar + kBarQ, piece_no++ & 1);
         auto scores = [&](int k) {
           const int ks = __shfl_sync(kFull, place(k, kKTiles), 0);
           if (!wait(k_full0 + 8 * ks, parity(k, kKTiles))) return false;
