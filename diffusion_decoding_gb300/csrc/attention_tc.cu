@@ -41,20 +41,20 @@ constexpr int kRows = 128;
 constexpr int kTile = 64;  // entries of a step
 // K tiles and V tiles have a ring each: a K tile is free again as soon as its scores are there, a V
 // tile only when its weights have been taken off them and multiplied.
-constexpr int kKTiles = 4;
-__host__ __device__ constexpr int v_tiles(bool share) { return share ? 4 : 6; }
+// Sizes of the rings, by what fits beside the rest.  A parity wait tells a phase from the one before
+// it only.  The halves of the turning warps (and, with the same rows, the groups) take every second
+// tile: with even rings they take every use of their own places and so wait for every phase of those
+// barriers.
+__host__ __device__ constexpr int k_tiles(int D) { return D > 128 ? 2 : 4; }
+__host__ __device__ constexpr int v_tiles(int D, bool share) { return D > 128 ? 2 : share ? 4 : 6; }
 constexpr int kRawTiles = 4;
-constexpr int kVisible = 2 * kKTiles;  // scores 4 tiles on are not begun before those here are read
-// A parity wait tells a phase from the one before it only.  The halves of the turning warps (and, with
-// the same rows, the groups) take every second tile: with even rings they take every use of their
-// own places and so wait for every phase of those barriers.
-static_assert(kKTiles % 2 == 0 && v_tiles(false) % 2 == 0 && v_tiles(true) % 2 == 0, "");
-static_assert(kRawTiles % 2 == 0, "");
 constexpr int kThreads = 640;
-// registers a thread: launched with 96, then shared out anew, 128 threads a figure:
-// 2 x 152 + 2 x 64 + 48 = 5 x 96
-constexpr int kSoftmaxRegs = 152, kTurnRegs = 64, kIssueRegs = 48;
-static_assert(2 * kSoftmaxRegs + 2 * kTurnRegs + kIssueRegs == 5 * 96, "");
+// registers a thread: launched with 96, then shared out anew, 128 threads a figure (two groups:
+// 2 x 152 + 2 x 64 + 48; one group: 152 + 24 + 2 x 128 + 48; both at most 5 x 96)
+constexpr int kSoftmaxRegs = 152, kIssueRegs = 48, kIdleRegs = 24;
+__host__ __device__ constexpr int turn_regs(int D) { return D > 128 ? 128 : 64; }
+static_assert(2 * kSoftmaxRegs + 2 * turn_regs(128) + kIssueRegs <= 5 * 96, "");
+static_assert(kSoftmaxRegs + kIdleRegs + 2 * turn_regs(256) + kIssueRegs <= 5 * 96, "");
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;  // as in attention.cu
 
@@ -192,11 +192,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 template <int D, bool kShare>
 struct Smem {
   static constexpr uint32_t kTensor = kTile * D * 2;  // a K (or V) tile
-  static constexpr uint32_t kV = kKTiles * kTensor;
-  static constexpr uint32_t kQ = kV + v_tiles(kShare) * kTensor;  // group 1's own queries
+  static constexpr uint32_t kV = k_tiles(D) * kTensor;
+  static constexpr uint32_t kQ = kV + v_tiles(D, kShare) * kTensor;  // group 1's own queries
   static constexpr uint32_t kScratch = kQ + (kShare ? kRows * D * 2 : 0);  // 2 KB a softmax warp
   // codes and params as they come from the cache, kRawTiles tiles: K codes, V codes, K and V params
-  static constexpr uint32_t kRaw = kScratch + 8 * 2048;
+  static constexpr uint32_t kRaw = kScratch + (D > 128 ? 4 : 8) * 2048;
   static constexpr uint32_t kRawCodes = kTile * D / 2, kRawPar = kTile * D / 16;
   static constexpr uint32_t kRawTile = 2 * (kRawCodes + kRawPar);
   static constexpr size_t kBytes = kRaw + kRawTiles * kRawTile + 1024;  // and room to align
@@ -218,9 +218,13 @@ template <int D, bool kShare>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
   using M = Smem<D, kShare>;
-  constexpr int kVTiles = v_tiles(kShare);
+  constexpr bool kTwo = D <= 128;            // two groups: O of one is all that fits beyond
+  constexpr bool kSame = kTwo && !kShare;    // of the same rows
+  constexpr int kKTiles = k_tiles(D), kVTiles = v_tiles(D, kShare);
+  static_assert(kKTiles % 2 == 0 && kVTiles % 2 == 0 && kRawTiles % 2 == 0, "");
+  constexpr int kVisible = 2 * kKTiles;  // scores kKTiles on are not begun before those here are read
   constexpr int ROWS = kShare ? 2 * kRows : kRows;
-  constexpr int STRIDE = kShare ? 1 : 2;  // tiles from one of a group to its next
+  constexpr int STRIDE = kSame ? 2 : 1;  // tiles from one of a group to its next
   constexpr uint32_t SLAB = kTile * 128, QSLAB = kRows * 128;
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t bars[2 * kKTiles + 2 * kVTiles + 2 * kRawTiles + 11];
@@ -252,13 +256,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       const uint32_t bar = gbars + kGroupBars * g;
-      mbar_init(bar + kBarQ, kShare ? 4 : 8);
+      mbar_init(bar + kBarQ, kSame ? 8 : 4);
       mbar_init(bar + kBarS, 2);  // the scores' completion, and the issuer's word that their mask is there
       mbar_init(bar + kBarFree, 4);
       mbar_init(bar + kBarP, 4);
       mbar_init(bar + kBarV, 1);
     }
-    mbar_init(done_bar, 2);
+    mbar_init(done_bar, kTwo ? 2 : 1);
     for (int s = 0; s < kRawTiles; ++s) {
       mbar_init(raw_full0 + 8 * s, 2 * (kTile / f.copy_span));  // the lanes that copy
       mbar_init(raw_empty0 + 8 * s, 4);  // the four warps that turn them
@@ -283,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rows = p.n * p.G;
   auto col_o = [](int g) { return 128u * g; };
   auto col_s = [](int g) { return 256u + 64u * g; };
-  auto col_p = [](int g) { return 384u + 32u * g; };
-  constexpr uint32_t col_q = 448;
+  auto col_p = [](int g) { return kTwo ? 384u + 32u * g : 320u; };
+  constexpr uint32_t col_q = kTwo ? 448 : 384;
 
   Segment<ROWS> sg;
   sg.find(p, f, line, u0);
@@ -294,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto place = [](int k, unsigned of) { return static_cast<int>(static_cast<unsigned>(k) % of); };
   auto parity = [](int k, unsigned of) { return static_cast<unsigned>(k) / of & 1u; };
 
-  if (warp < 8) {
+  if (!kTwo && warp >= 4 && warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIdleRegs));
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax, one row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int grp = warp >> 2, row_in = threadIdx.x & (kRows - 1);
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       const int b = sg.b, h = sg.h;
-      const int first = kShare ? 0 : (grp ^ step) & 1;  // this group's first tile of the segment
+      const int first = kSame ? (grp ^ step) & 1 : 0;  // this group's first tile of the segment
       const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
       const int r = sg.rt * ROWS + (kShare ? grp * kRows : 0) + row_in;
       {
@@ -318,59 +324,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scratch, from where each thread takes those of its own row to TMEM.  Groups with the same
         // rows share the queries there, and each brings half of the channels.
         const int lr = lane >> 2, lp = lane & 3;
-        constexpr int CHUNKS = kShare ? D / 32 : D / 64;
+        constexpr int CHUNKS = kSame ? D / 64 : D / 32, BLOCK = CHUNKS < 4 ? CHUNKS : 4;
         const bool to_tmem = !kShare || grp == 0;
-        const int chunk0 = kShare ? 0 : grp * CHUNKS;
-        uint4 v[CHUNKS][4];
+#pragma unroll 1
+        for (int c0 = 0; c0 < CHUNKS; c0 += BLOCK) {
+          const int chunk0 = (kSame ? grp * CHUNKS : 0) + c0;
+          uint4 v[BLOCK][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int rr = r - lane + e * 8 + lr;
-          const int ri = token_of(p, rr);
-          const uint16_t* src =
-              p.q + b * p.qb + ri * p.qt + (h * p.G + rr - ri * p.G) * p.qh + chunk0 * 32 + lp * 8;
+          for (int e = 0; e < 4; ++e) {
+            const int rr = r - lane + e * 8 + lr;
+            const int ri = token_of(p, rr);
+            const uint16_t* src =
+                p.q + b * p.qb + ri * p.qt + (h * p.G + rr - ri * p.G) * p.qh + chunk0 * 32 + lp * 8;
 #pragma unroll
-          for (int c = 0; c < CHUNKS; ++c) {
-            v[c][e] = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < rows) {
-              if (f.q_aligned) {
-                v[c][e] = *reinterpret_cast<const uint4*>(src + c * 32);
-              } else {
-                const uint16_t* s8 = src + c * 32;
-                v[c][e].x = s8[0] | static_cast<uint32_t>(s8[1]) << 16;
-                v[c][e].y = s8[2] | static_cast<uint32_t>(s8[3]) << 16;
-                v[c][e].z = s8[4] | static_cast<uint32_t>(s8[5]) << 16;
-                v[c][e].w = s8[6] | static_cast<uint32_t>(s8[7]) << 16;
+            for (int c = 0; c < BLOCK; ++c) {
+              v[c][e] = make_uint4(0u, 0u, 0u, 0u);
+              if (rr < rows) {
+                if (f.q_aligned) {
+                  v[c][e] = *reinterpret_cast<const uint4*>(src + c * 32);
+                } else {
+                  const uint16_t* s8 = src + c * 32;
+                  v[c][e].x = s8[0] | static_cast<uint32_t>(s8[1]) << 16;
+                  v[c][e].y = s8[2] | static_cast<uint32_t>(s8[3]) << 16;
+                  v[c][e].z = s8[4] | static_cast<uint32_t>(s8[5]) << 16;
+                  v[c][e].w = s8[6] | static_cast<uint32_t>(s8[7]) << 16;
+                }
               }
             }
           }
-        }
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          if (to_tmem) __syncwarp();  // what was in the scratch has been taken
+          for (int c = 0; c < BLOCK; ++c) {
+            if (to_tmem) __syncwarp();  // what was in the scratch has been taken
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t x[4] = {v[c][e].x, v[c][e].y, v[c][e].z, v[c][e].w};
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4] = {v[c][e].x, v[c][e].y, v[c][e].z, v[c][e].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = (x[k] ^ q_flip) & q_keep;
-            const int rw = e * 8 + lr, rg = (warp & 3) * 32 + rw;  // row of the warp, of the group
-            const uint32_t dst =
-                to_tmem ? scratch + rw * 64 + ((lp ^ (rw >> 1 & 3)) << 4)
-                        : sbase + M::kQ + (c >> 1) * QSLAB + rg * 128 +
-                              ((((c & 1) * 4 + lp) ^ (rg & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst),
-                         "r"(__byte_perm(x[0], x[2], 0x5410)), "r"(__byte_perm(x[0], x[2], 0x7632)),
-                         "r"(__byte_perm(x[1], x[3], 0x5410)), "r"(__byte_perm(x[1], x[3], 0x7632))
-                         : "memory");
-          }
-          if (to_tmem) {
-            __syncwarp();
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 y = ld_shared_v4(scratch + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4));
-              w[4 * k] = y.x, w[4 * k + 1] = y.y, w[4 * k + 2] = y.z, w[4 * k + 3] = y.w;
+              for (int k = 0; k < 4; ++k) x[k] = (x[k] ^ q_flip) & q_keep;
+              const int rw = e * 8 + lr, rg = (warp & 3) * 32 + rw;  // row of the warp, of the group
+              const uint32_t dst =
+                  to_tmem ? scratch + rw * 64 + ((lp ^ (rw >> 1 & 3)) << 4)
+                          : sbase + M::kQ + (c >> 1) * QSLAB + rg * 128 +
+                                ((((c & 1) * 4 + lp) ^ (rg & 7)) << 4);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst),
+                           "r"(__byte_perm(x[0], x[2], 0x5410)), "r"(__byte_perm(x[0], x[2], 0x7632)),
+                           "r"(__byte_perm(x[1], x[3], 0x5410)), "r"(__byte_perm(x[1], x[3], 0x7632))
+                           : "memory");
             }
-            tmem_st16(lanes + col_q + (chunk0 + c) * 16, w);
+            if (to_tmem) {
+              __syncwarp();
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 y = ld_shared_v4(scratch + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4));
+                w[4 * k] = y.x, w[4 * k + 1] = y.y, w[4 * k + 2] = y.z, w[4 * k + 3] = y.w;
+              }
+              tmem_st16(lanes + col_q + (chunk0 + c) * 16, w);
+            }
           }
         }
         if (to_tmem)
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // only of a group with tiles here: it is held up at the end until its issuer has passed
         if (lane == 0 && count > 0) mbar_arrive(bar + kBarQ);
         // both groups read both accumulators of the segment before, and the queries are shared
-        if (!kShare && lane == 0 && pc.tiles > 1 - first)
+        if (kSame && lane == 0 && pc.tiles > 1 - first)
           mbar_arrive(gbars + kGroupBars * (grp ^ 1) + kBarQ);
       }
       const int bound = rows_see(p, sg.len, r);             // entries this row sees
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- output.  Groups with the same rows: each takes half of the channels of both.
       if (count > 0 && ok) ok = wait_warp(bar + kBarV, (mine + count - 1) & 1, abort_v, f.status);
-      if constexpr (!kShare) {
+      if constexpr (kSame) {
         ml_s[grp][row_in] = make_float2(m, l);
         asm volatile("bar.sync 1, 256;" ::: "memory");  // both groups' products are complete
       }
@@ -499,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
         const int row_tile = r - sg.rt * ROWS;
         float keep0 = count > 0 ? 1.f : 0.f, keep1 = 0.f;  // this group's and the other's
-        if constexpr (!kShare) {
+        if constexpr (kSame) {
           const float2 ml = ml_s[grp ^ 1][row_in];
           const float mn = fmaxf(m, ml.x);
           keep0 = m == -INFINITY ? 0.f : ex2(m - mn);
@@ -508,15 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mn;
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        constexpr int SPAN = kShare ? D : D / 2;
-        const int c0 = kShare ? 0 : grp * SPAN;
+        constexpr int SPAN = kSame ? D / 2 : D;
+        const int c0 = kSame ? grp * SPAN : 0;
         const uint32_t t_other = lanes + col_o(grp ^ 1);
 #pragma unroll 1
         for (int c = c0; c < c0 + SPAN; c += 32) {
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          if constexpr (kShare) {
+          if constexpr (!kSame) {
             if (count > 0) {
               tmem_ld32(t_o + c, o);
               tmem_wait_ld();
@@ -575,14 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (r < rows && (kShare || grp == 0)) {
+        if (r < rows && (!kSame || grp == 0)) {
           if (!direct)
             f.part_ml[part * ROWS + row_tile] = make_float2(m, l);
           else
             store_lse(p, b, h, r, m, l);
         }
       }
-      if constexpr (!kShare) asm volatile("bar.sync 1, 256;" ::: "memory");  // ml_s is read
+      if constexpr (kSame) asm volatile("bar.sync 1, 256;" ::: "memory");  // ml_s is read
       tc_before();  // O and Q are read before the next segment's arrival on kBarQ
       mine += count;
       step += pc.tiles;
@@ -592,18 +601,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 16) {
     // ------------------------------------------------------------------ codes to bf16
     // this half of the warps every second tile
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTurnRegs));
+    if constexpr (turn_regs(D) < 96)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(turn_regs(D)));
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(turn_regs(D)));
     constexpr int GROUPS = D / 32;  // per entry
     constexpr int PER = GROUPS / 2;  // pieces of K (and of V) a thread turns per tile
+    constexpr int APART = 128 / GROUPS;  // entries from one to the next
     const int half = (warp >> 2) & 1, w = warp & 3;
-    // piece e of the thread: entry entry0 + 32 e, group g
+    // piece e of the thread: entry entry0 + APART * e, group g
     const int entry0 = (w * 32 + lane) / GROUPS, g = lane % GROUPS;
     const uint32_t raw0 = sbase + M::kRaw + (w * 32 + lane) * 16;
     const uint32_t par0 = sbase + M::kRaw + 2 * M::kRawCodes + (w * 32 + lane) * 2;
     // Word x goes to 16-byte piece (4 (g % 2) + x) ^ (entry % 8) of the entry's row in slab g / 2.
-    // Lanes of slab 1 store words in the order 2, 3, 0, 1: with eight lanes (two entries, four
-    // groups) at a time, all eight pieces of a 128-byte row are then hit once.
-    const int turn_x = D > 64 && g >= 2 ? 2 : 0;
+    // Lanes of slab 1 store words in the order 2, 3, 0, 1 (D = 128), those of slab s word x ^ s in
+    // place of word x (D = 256): with eight lanes at a time (two entries of four groups, or one of
+    // eight), all eight pieces of a 128-byte row are then hit once.
+    const int turn_x = D > 128 ? g >> 1 : D > 64 && g >= 2 ? 2 : 0;
     uint32_t piece_at[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x)
@@ -611,8 +625,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ((((g & 1) * 4 + (x ^ turn_x)) ^ (entry0 & 7)) << 4);
     auto turn = [&](const uint4& codes, uint32_t param, uint32_t dst) {
       const Kv4Scale sc = kv4_scale(__byte_perm(param, param, 0x1010));
-      const uint32_t wd[4] = {turn_x ? codes.z : codes.x, turn_x ? codes.w : codes.y,
-                              turn_x ? codes.x : codes.z, turn_x ? codes.y : codes.w};
+      uint32_t wd[4] = {codes.x, codes.y, codes.z, codes.w};
+      if (turn_x & 2) {
+        wd[0] = codes.z, wd[1] = codes.w, wd[2] = codes.x, wd[3] = codes.y;
+      }
+      if (D > 128 && (turn_x & 1)) {
+        const uint32_t w0 = wd[0], w2 = wd[2];
+        wd[0] = wd[1], wd[1] = w0, wd[2] = wd[3], wd[3] = w2;
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const uint32_t a = kv4_pair<0>(wd[x], sc), c = kv4_pair<1>(wd[x], sc),
@@ -641,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
           // values of hidden entries are 0, whatever they hold: their weight of 0 must not meet a NaN
-          const int entry = entry0 + 32 * e;
-          const uint32_t word = PER == 2 ? vis[e] : entry < 32 ? vis[0] : vis[1];
+          const int entry = entry0 + APART * e;
+          const uint32_t word = entry < 32 ? vis[0] : vis[1];
           if (!(word >> (entry & 31) & 1u)) vp[e] = 0u;
         }
         __syncwarp();
@@ -651,13 +671,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(k_empty0 + 8 * ks, parity(k, kKTiles) ^ 1, abort_v, f.status)) break;
         if (w == 0 && lane < 2) visible[place(k, kVisible)][lane] = lane ? vis[1] : vis[0];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) turn(kc[e], kp[e], ks * M::kTensor + e * 32 * 128);
+        for (int e = 0; e < PER; ++e) turn(kc[e], kp[e], ks * M::kTensor + e * APART * 128);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full0 + 8 * ks);
         if (!wait_warp(v_empty0 + 8 * vs, parity(k, kVTiles) ^ 1, abort_v, f.status)) break;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) turn(vc[e], vp[e], M::kV + vs * M::kTensor + e * 32 * 128);
+        for (int e = 0; e < PER; ++e) turn(vc[e], vp[e], M::kV + vs * M::kTensor + e * APART * 128);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full0 + 8 * vs);
@@ -670,7 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     const int grp = __shfl_sync(kFull, warp, 0) - 16;
-    if (grp < 2) {
+    if (!kTwo && grp == 1) {
+      // no second group
+    } else if (grp < 2) {
       const uint32_t lead = elect_lane();
       const uint32_t bar = gbars + kGroupBars * grp;
       const uint32_t base = __shfl_sync(kFull, tmem, 0);
@@ -680,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int piece_no = 0;  // segments with tiles of this group
       for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
-        const int first = kShare ? 0 : (grp ^ step) & 1;
+        const int first = kSame ? (grp ^ step) & 1 : 0;
         const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
         auto wait = [&](uint32_t at, uint32_t phase) {
           return wait_warp(at, phase, abort_v, f.status);
@@ -902,15 +924,17 @@ __global__ void __launch_bounds__(128)
 }  // namespace
 
 bool attention_tc_takes(int n, int G, int D) {
-  return (D == 64 || D == 128) && static_cast<int64_t>(n) * G > 32;
+  return (D == 64 || D == 128 || D == 256) && static_cast<int64_t>(n) * G > 32;
 }
 
 namespace {
-int tile_rows(int n, int G) { return static_cast<int64_t>(n) * G > kRows ? 2 * kRows : kRows; }
+int tile_rows(int n, int G, int D) {
+  return D <= 128 && static_cast<int64_t>(n) * G > kRows ? 2 * kRows : kRows;
+}
 }  // namespace
 
 size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count) {
-  const int R = tile_rows(n, G);
+  const int R = tile_rows(n, G, D);
   const size_t parts = static_cast<size_t>(2) * sm_count * R;
   const size_t tiles = (static_cast<size_t>(n) * G + R - 1) / R;
   return kWsHeader + parts * D * 4 + parts * 8 + B * tiles * heads * 8;
@@ -926,7 +950,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   const int64_t segments = static_cast<int64_t>(p.B) * f.row_tiles * p.heads;
   const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile;
   // Whole segments, or equal stretches that are joined again (of kLeast tiles at least).  A split costs
-  // a second start and end for most CTAs and the join: measured as much as 12 to 18 tiles.  With 128
+  // a second start and end for most CTAs and the join: measured as much as 9 to 18 tiles.  With 128
   // segments of 17 tiles of 128 rows whole segments take 20.2 us and stretches 30.7; with 64 of 256
   // rows, 24.6 against 30.2 at 17 tiles and 68.8 against 48.7 at 65.  Where the lengths may differ
   // the mean is taken for three quarters of the longest.
@@ -962,7 +986,8 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
 
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream) {
-  if (tile_rows(p.n, p.G) == kRows)
+  if (D == 256) return launch_tc<256, false>(p, ws, sm_count, stream);
+  if (tile_rows(p.n, p.G, D) == kRows)
     return D == 64 ? launch_tc<64, false>(p, ws, sm_count, stream)
                    : launch_tc<128, false>(p, ws, sm_count, stream);
   return D == 64 ? launch_tc<64, true>(p, ws, sm_count, stream)

@@ -1,0 +1,31 @@
+"""Attention over the 4-bit cache for heads of 256 channels and many rows: sizes around the row and
+entry tiles, against the 64-bit statement (tolerances as for the other head sizes: weights and the
+result rounded to bf16)."""
+import pytest
+import torch
+
+import refresh_ref as ref
+from test_gpu_refresh_ops import DEV, check_attention, entries, fill, gen, make_cache, randn, run, seen_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,n,H,G,ps,T,lens", [
+    (1, 33, 1, 1, 16, 1, None), (2, 64, 1, 2, 64, 64, [64, 63]), (1, 43, 2, 3, 48, 65, None),
+    (3, 17, 1, 8, 16, 300, [300, 0, 129]), (2, 128, 2, 1, 256, 1000, [1000, 700]),
+    (1, 200, 1, 3, 32, 777, None), (2, 40, 5, 4, 64, 2500, [2500, 100]), (40, 36, 4, 1, 16, 40, None)])
+def test_attention_of_wide_heads(B, n, H, G, ps, T, lens, causal, masked):
+    D = 256
+    g = gen(n + T)
+    c = make_cache(g, B, T, H, D, ps)
+    k, v = fill(g, c, T)
+    q = randn(g, B, n, H * G, D).to(torch.bfloat16)
+    mask = None
+    if masked:
+        mask = (torch.rand(B, T, generator=g, device=DEV) < 0.7).to(torch.uint8)
+        mask[0, :min(T, 40)] = 0
+    out, lse = run(c, q, lens, T, causal=causal, mask=mask)
+    check_attention(out, lse, q, k, v, seen_of(B, n, T, lens or [T] * B, mask, causal, c),
+                    D ** -0.5)
