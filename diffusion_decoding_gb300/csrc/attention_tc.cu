@@ -417,12 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar + kBarFree);
         const int j = pc.j0 + t * kTile;
         if ((vis0 & vis1) != 0xffffffffu || j + kTile > all_see) {
-          const int left = bound - j;  // entries of the tile below the bound
+          // what this row sees of the tile, a bit per entry
+          auto below = [](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
+          const uint32_t see[2] = {vis0 & below(bound - j), vis1 & below(bound - j - 32)};
 #pragma unroll
-          for (int e = 0; e < kTile; ++e) {
-            const bool v = ((e < 32 ? vis0 : vis1) >> (e & 31) & 1u) && e < left;
-            s[e] = v ? s[e] : -INFINITY;
-          }
+          for (int e = 0; e < kTile; ++e) s[e] = see[e >> 5] & (1u << (e & 31)) ? s[e] : -INFINITY;
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
