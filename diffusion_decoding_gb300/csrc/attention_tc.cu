@@ -939,6 +939,49 @@ size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count
   return kWsHeader + parts * D * 4 + parts * 8 + B * tiles * heads * 8;
 }
 
+// How the line of units is cut, by the tiles that the busiest CTA has to do and what it costs besides,
+// as tiles (times: 128 rows a segment and 128 channels unless said otherwise).
+//  - Whole segments, nothing to join.
+//  - Parts, a CTA each: at least as many CTAs as there are parts.  A part more costs the join half a
+//    tile.  8 segments of 65 tiles: 17.7 us in parts of 8 tiles, 18.0 of 4, 21.6 of 16; whole 49.7; in
+//    equal stretches 22.4.
+//  - Equal stretches: every CTA busy, but most start and end two segments, and the parts are many:
+//    taken for 26 tiles.  64 segments of 256 rows and 65 tiles: 48 us, whole 68.8; 128 segments of 47
+//    tiles: 46.8 us, whole 39.8; 128 of 65 tiles and 256 channels: 83 us, whole 72.
+// Where the lengths may differ the mean is taken for three quarters of the longest.
+template <int D>
+static void plan_line(const AttnParams& p, int sm_count, AttnPlan* f) {
+  constexpr int kLeast = 4;  // tiles of a stretch
+  constexpr int kSplit = 26;
+  const int64_t segments = static_cast<int64_t>(p.B) * f->row_tiles * p.heads;
+  const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile;
+  const int64_t whole = (segments + sm_count - 1) / sm_count * tiles;
+  const int64_t mean = segments * tiles / sm_count * (p.lens || p.causal ? 3 : 4) / 4;
+  const int64_t split = std::max<int64_t>(mean, kLeast) + kSplit;
+  int parts_log2 = 0;
+  int64_t parts = INT64_MAX;  // twice their cost
+  for (int lg = 6; segments <= sm_count; ++lg) {
+    const int64_t per = int64_t{1} << (lg - 6), count = (tiles + per - 1) / per;
+    if (segments * count <= sm_count && (parts == INT64_MAX || 2 * per + count <= parts + 1)) {
+      parts = 2 * per + count;
+      parts_log2 = lg;
+    }
+    if (count <= 1) break;
+  }
+  if (whole <= split && whole <= parts / 2 + 3) {
+    f->unit_log2 = 6;
+    while (p.max_len > 1 << f->unit_log2) ++f->unit_log2;
+    f->ctas = static_cast<int>(std::min<int64_t>(sm_count, segments));
+  } else if (parts / 2 + 1 <= split) {
+    f->unit_log2 = parts_log2;
+    f->ctas = static_cast<int>(segments * ((p.max_len + (int64_t{1} << parts_log2) - 1) >> parts_log2));
+  } else {
+    f->unit_log2 = unit_log2_of(segments, p.max_len, 6);
+    const int64_t units = segments * ((static_cast<int64_t>(p.max_len) >> f->unit_log2) + 1);
+    f->ctas = static_cast<int>(std::min<int64_t>(sm_count, (units + kLeast - 1) / kLeast));
+  }
+}
+
 template <int D, bool kShare>
 static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaStream_t stream) {
   constexpr int R = kShare ? 2 * kRows : kRows;
@@ -946,25 +989,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   static_assert(1 << 6 == kTile, "");
   f.row_tiles = (p.n * p.G + R - 1) / R;
   f.copy_span = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
-  const int64_t segments = static_cast<int64_t>(p.B) * f.row_tiles * p.heads;
-  const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile;
-  // Whole segments, or equal stretches that are joined again (of kLeast tiles at least).  A split costs
-  // a second start and end for most CTAs and the join: measured as much as 9 to 18 tiles.  With 128
-  // segments of 17 tiles of 128 rows whole segments take 20.2 us and stretches 30.7; with 64 of 256
-  // rows, 24.6 against 30.2 at 17 tiles and 68.8 against 48.7 at 65.  Where the lengths may differ
-  // the mean is taken for three quarters of the longest.
-  constexpr int kLeast = 4, kSplit = 13;
-  const int64_t rounds = (segments + sm_count - 1) / sm_count;
-  const int64_t mean = segments * tiles / sm_count * (p.lens || p.causal ? 3 : 4) / 4;
-  if (rounds * tiles <= std::max<int64_t>(mean, kLeast) + kSplit) {
-    f.unit_log2 = 6;
-    while (p.max_len > 1 << f.unit_log2) ++f.unit_log2;
-    f.ctas = static_cast<int>(std::min<int64_t>(sm_count, segments));
-  } else {
-    f.unit_log2 = unit_log2_of(segments, p.max_len, 6);
-    const int64_t units = segments * ((static_cast<int64_t>(p.max_len) >> f.unit_log2) + 1);
-    f.ctas = static_cast<int>(std::min<int64_t>(sm_count, (units + kLeast - 1) / kLeast));
-  }
+  plan_line<D>(p, sm_count, &f);
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
   f.status = static_cast<int32_t*>(ws);
