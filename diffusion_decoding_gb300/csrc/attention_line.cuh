@@ -228,17 +228,29 @@ __global__ void __launch_bounds__(32 * WARPS)
   for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, max_s[w]);
   float2 acc[V] = {};
   float sum = 0.f;
-#pragma unroll 8
-  for (int k = warp; k < count; k += WARPS) {
-    const float2 v = f.part_ml[part_of(k) + r];
-    const float keep = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
-    sum = fmaf(v.y, keep, sum);
-    const float* src = f.part_o + (part_of(k) + r) * D;
+  // kAhead parts of the warp at a time, all their loads before the first use
+  constexpr int kAhead = 4;
+  for (int k0 = warp; k0 < count; k0 += kAhead * WARPS) {
+    float2 v[kAhead], o[kAhead][V];
 #pragma unroll
-    for (int x = 0; x < V; ++x) {
-      const float2 o = *reinterpret_cast<const float2*>(src + 64 * x + 2 * lane);
-      acc[x].x = fmaf(o.x, keep, acc[x].x);
-      acc[x].y = fmaf(o.y, keep, acc[x].y);
+    for (int y = 0; y < kAhead; ++y) {
+      const int k = k0 + y * WARPS;
+      const int64_t part = part_of(k < count ? k : 0) + r;
+      v[y] = k < count ? f.part_ml[part] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < V; ++x)
+        o[y][x] = k < count ? *reinterpret_cast<const float2*>(f.part_o + part * D + 64 * x + 2 * lane)
+                            : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const float keep = v[y].x == -INFINITY ? 0.f : ex2(v[y].x - mx);
+      sum = fmaf(v[y].y, keep, sum);
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        acc[x].x = fmaf(o[y][x].x, keep, acc[x].x);
+        acc[x].y = fmaf(o[y][x].y, keep, acc[x].y);
+      }
     }
   }
 #pragma unroll
