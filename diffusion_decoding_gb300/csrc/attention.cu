@@ -16,8 +16,10 @@
 // their way into a ring of its own in shared memory (16-byte asynchronous copies, no block
 // barrier), and page ids one tile further ahead.
 #include "attention.h"
-#include "attention_line.cuh"
 
+#include <algorithm>
+
+#include "attention_line.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -579,12 +581,15 @@ bool attention_rows_aligned(const void* x, int64_t sb, int64_t st, int64_t sh) {
 }
 
 size_t attention_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
-  return attention_tc_takes(n, G, D) ? attention_tc_ws_bytes(B, n, G, heads, D, sm_count)
-                                     : few_sizes(B, n, G, heads, D, max_len, sm_count).bytes;
+  // which kernel runs depends on the lengths too: enough for both
+  const size_t few = few_sizes(B, n, G, heads, D, max_len, sm_count).bytes;
+  return attention_tc_can(n, G, D)
+             ? std::max(few, attention_tc_ws_bytes(B, n, G, heads, D, sm_count))
+             : few;
 }
 
 cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream) {
-  if (attention_tc_takes(p.n, p.G, D)) return launch_attention_tc(p, D, ws, sm_count, stream);
+  if (attention_tc_takes(p, D, sm_count)) return launch_attention_tc(p, D, ws, sm_count, stream);
   const FewSizes s = few_sizes(p.B, p.n, p.G, p.heads, D, p.max_len, sm_count);
   AttnPlan f{};
   f.row_tiles = s.row_tiles;

@@ -35,8 +35,9 @@ size_t attention_ws_bytes(int B, int n, int G, int heads, int D, int max_len, in
 
 cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count, cudaStream_t stream);
 
-// Many rows per cache head (attention_tc.cu): head_dim 64 or 128.
-bool attention_tc_takes(int n, int G, int D);
+// Many rows per cache head (attention_tc.cu): whether it can have these rows, and has this call.
+bool attention_tc_can(int n, int G, int D);
+bool attention_tc_takes(const AttnParams& p, int D, int sm_count);
 size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count);
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream);

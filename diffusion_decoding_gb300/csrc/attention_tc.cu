@@ -922,8 +922,20 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace
 
-bool attention_tc_takes(int n, int G, int D) {
-  return (D == 64 || D == 128 || D == 256) && static_cast<int64_t>(n) * G > 32;
+bool attention_tc_can(int n, int G, int D) {
+  const int64_t least = D == 64 ? 32 : D == 128 ? 16 : D == 256 ? 8 : INT64_MAX;
+  return static_cast<int64_t>(n) * G > least;
+}
+
+// Up to 32 rows only with enough to do: 24 rows of 128 channels take 50 us here and 62 in the other
+// kernel (128 heads of 4000 entries), 10.8 and 14.6 (128 of 300), but 22.6 and 17.7 (8 of 8000) and
+// 9.8 and 8.8 (8 of 300); 16 rows of 256 channels 69 and 78, 14.0 and 14.9, 26.6 and 23.5, 12.6 and 11.2.
+// 48 rows of 64 channels 46 and 61, 9.5 and 12.6, 21.3 and 16.8, 8.7 and 7.3.
+bool attention_tc_takes(const AttnParams& p, int D, int sm_count) {
+  if (!attention_tc_can(p.n, p.G, D)) return false;
+  const int64_t segments = static_cast<int64_t>(p.B) * p.heads;
+  return static_cast<int64_t>(p.n) * p.G > 32 || segments >= 64 ||
+         segments * p.max_len >= int64_t{16} * kTile * sm_count;
 }
 
 namespace {

@@ -1,6 +1,6 @@
-"""Attention over the 4-bit cache for heads of 256 channels and many rows: sizes around the row and
-entry tiles, against the 64-bit statement (tolerances as for the other head sizes: weights and the
-result rounded to bf16)."""
+"""Attention over the 4-bit cache for heads of 256 channels and many rows, and for some rows of many
+heads: sizes around the row and entry tiles, against the 64-bit statement (tolerances as for the
+other sizes: weights and the result rounded to bf16)."""
 import pytest
 import torch
 
@@ -29,3 +29,19 @@ def test_attention_of_wide_heads(B, n, H, G, ps, T, lens, causal, masked):
     out, lse = run(c, q, lens, T, causal=causal, mask=mask)
     check_attention(out, lse, q, k, v, seen_of(B, n, T, lens or [T] * B, mask, causal, c),
                     D ** -0.5)
+
+
+@pytest.mark.parametrize("B,n,H,G,D,ps,T,lens", [
+    (16, 5, 4, 4, 128, 16, 200, None), (9, 9, 8, 1, 256, 48, 70, None), (33, 8, 2, 3, 128, 64, 65, None),
+    (2, 8, 3, 4, 128, 64, 30000, [30000, 17]), (1, 3, 2, 7, 256, 256, 80000, None),
+    (1, 3, 2, 7, 256, 16, 500, None), (3, 11, 4, 2, 128, 32, 900, [900, 0, 31])])
+def test_attention_of_some_rows(B, n, H, G, D, ps, T, lens):
+    """9 to 32 rows: either kernel, by how much there is to do."""
+    g = gen(n + T)
+    c = make_cache(g, B, T, H, D, ps)
+    k, v = fill(g, c, T)
+    q = randn(g, B, n, H * G, D).to(torch.bfloat16)
+    for causal in (False, True):
+        out, lse = run(c, q, lens, T, causal=causal)
+        check_attention(out, lse, q, k, v, seen_of(B, n, T, lens or [T] * B, None, causal, c),
+                        D ** -0.5)
