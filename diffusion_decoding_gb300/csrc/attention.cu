@@ -12,9 +12,15 @@
 //
 // The grid is one wave of resident CTAs that share the work evenly (attention_line.cuh).
 //
-// HBM-bound: an entry of one head costs 9/8 * head_dim bytes.  Each warp keeps kStages - 1 tiles on
+// An entry of one head costs 9/8 * head_dim bytes of HBM traffic.  Each warp keeps kStages - 1 tiles on
 // their way into a ring of its own in shared memory (16-byte asynchronous copies, no block
 // barrier), and page ids one tile further ahead.
+//
+// Measured: one token of each of 32 sequences of up to 8192 entries, 4 query heads to each of 8 cache
+// heads of 128 channels: 66.8 us, 3.4 TB/s of cache.  The rate is set by the integer work that turns
+// codes into values: about 490 instructions a warp and tile of 16 entries, 66 % of the issue slots and
+// 63 % of the integer pipe busy, at four warps a scheduler (123 registers; five CTAs an SM spill and
+// take 72.7 us).  One sequence of 65536 entries: 21 us, of which the join takes a third.
 #include "attention.h"
 
 #include <algorithm>
@@ -534,18 +540,21 @@ struct FewSizes {
 
 FewSizes few_sizes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
   FewSizes s{};
-  const int64_t rows = static_cast<int64_t>(n) * G;
-  s.nt = rows > 8 && D <= 128 ? 2 : 1;
+  const int64_t rows = static_cast<int64_t>(n) * G, per_tile = static_cast<int64_t>(B) * heads;
+  constexpr int kShort = 9;
+  const bool brief = max_len <= 1 << kShort;
+  // Sixteen rows a tile read the cache half as often (16 rows over 32 x 8192 entries: 94 us, 141 with
+  // eight); eight where short segments leave SMs free anyway (1 x 331 entries: 7.3 us, 8.9 with 16).
+  s.nt = rows > 8 && D <= 128 && !(brief && per_tile * ((rows + 7) / 8) <= sm_count) ? 2 : 1;
   s.row_tiles = static_cast<int>((rows + 8 * s.nt - 1) / (8 * s.nt));
-  const int64_t segments = static_cast<int64_t>(B) * s.row_tiles * heads;
+  const int64_t segments = per_tile * s.row_tiles;
   // Up to 2^kShort entries a segment is one unit: its warps take it in a few tiles each, sooner than a
   // second kernel could join its parts; in eight warps' steps where that leaves no SM without a CTA.
   // Four segments of 512 entries take 7.5 us whole with eight warps, 8.6 with four, 7.4 to 7.6 split;
   // 64 segments 7.9, 9.0 and 9 to 10; four of 1024 entries 10.8 whole and 7.5 split.
-  constexpr int kShort = 9;
-  s.wide = segments <= sm_count && max_len <= 1 << kShort;
+  s.wide = brief && segments <= sm_count;
   s.ctas = s.wide ? sm_count : sm_count * few_ctas_per_sm(D, s.nt);
-  s.unit_log2 = max_len <= 1 << kShort ? kShort : unit_log2_of(segments, max_len, 6);
+  s.unit_log2 = brief ? kShort : unit_log2_of(segments, max_len, 6);
   s.split = max_len > 1 << s.unit_log2;
   const size_t parts = static_cast<size_t>(2) * s.ctas * 8 * s.nt;
   s.off_ml = kWsHeader + parts * D * 4;

@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(32 * WARPS)
   if (threadIdx.x == 0) store_lse(p, b, h, rt * ROWS + r, mx, sum);
 }
 
-// Sixteen warps where a segment is cut into more than 16 parts, else four.
+// Sixteen warps where a segment is cut into more than 16 parts (152 parts a row: attention and join
+// 21 us, 29 with four warps), else four (fewer than 16 parts would leave warps idle).
 template <int D, int ROWS>
 cudaError_t launch_join(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
   const int64_t segments = static_cast<int64_t>(p.B) * f.row_tiles * p.heads;

@@ -5,7 +5,9 @@
 //   S [128 rows x 64] = Q K^T,   O [128 x D] += P V     (tcgen05.mma, fp32 accumulators in TMEM)
 // Two groups of four warps each hold 128 rows, one row a thread.  With more than 128 rows in a
 // segment (kShare) the groups are the two halves of a 256-row tile and both use every K and V tile;
-// otherwise they hold the same rows, take the tiles in turn, and add up at the end.
+// otherwise they hold the same rows, take the tiles in turn, and add up at the end.  (1024 tokens of
+// 4 heads over 16384 entries: 393 us; with the same rows in both groups 549.)  With 256 channels the
+// accumulator of one group fills half of the tensor memory, and there is no second group.
 //
 // Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
 // attention.cu's kSlack), and the output.  Warps 18 and 19 look the pages up and have the tiles' codes
@@ -18,9 +20,16 @@
 //
 // TMEM, 512 columns: O 2 x 128, S 2 x 64, P 2 x 32 and 64 for the queries (left operands may lie
 // there): those of group 0, or of both groups where the rows are the same.  Otherwise group 1's are
-// in shared memory.  Per 64 entries, 256 rows and D = 128 shared memory then moves 128 KB (K and V
-// written once and read twice, the queries of group 1 read once), as many cycles as the products of
-// both groups take.
+// in shared memory.  Per 64 entries, 256 rows and D = 128 shared memory then moves 146 KB (K and V
+// written once and read twice, the queries of group 1 read once, the codes in and out), 1150
+// cycles, about as many as the products of both groups take (1152).
+//
+// Measured: a step of 256 rows takes 1750 to 1900 cycles, so 0.62 to 0.66 of the tensor cores' time
+// (1.27 PFLOP/s on the piece above, 0.66 of the card's burst rate); what is left is the chain scores ->
+// softmax -> weights -> product, each hand-over 120 cycles, with 61 % of the issue slots busy.  One
+// segment by itself costs about 9 us (launch, queries, one tile, output).  Measured slower: two places
+// for each group's scores with all queries in shared memory (444 us: its reads bind), two threads a
+// row (478), other orders of the warps (402, 432), a poll with a sleep hint (418).
 // The eight channels of a code word come out as pairs (j, j + 4): Q's channels are put in the same
 // order (the scores do not depend on it), and the output's are put back.
 #include "attention.h"

@@ -8,6 +8,10 @@
 // with one shuffle and work out its step together with 16 values each.  A warp takes up to kItems
 // such pieces of one token and issues all their loads before it uses the first, the values' before
 // it even knows their place in the cache.
+//
+// Measured, 32768 entries of 8 heads of 128 channels, keys and values in bf16 (153 MB each way): write
+// 33.6 us, 80 % of the issue slots busy; read 29.3 us, 66 %; one after the other 59 us, 5.2 TB/s, 0.77
+// of the card's copy rate.  One piece a lane: 74 us; four: 69.5 (registers).
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -321,8 +325,9 @@ cudaError_t launch_items(Kv4Params& p, int sm_count, cudaStream_t stream) {
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, p);
   };
   // Two pieces a lane hide more of the load latency and share the page lookup; one piece a lane
-  // when the call has too few warps to fill the SMs.
-  const bool few = static_cast<int64_t>(p.tokens) * 2 * ((pieces + 63) / 64) < static_cast<int64_t>(sm_count) * 16;
+  // when the call has too few warps to fill the SMs (1152 entries of 4 heads: 4.7 us, 5.1 with two).
+  const bool few = static_cast<int64_t>(p.tokens) * 2 * ((pieces + 63) / 64) <
+                   static_cast<int64_t>(sm_count) * 16;
   if constexpr (kWrite)
     return few ? run(kv4_write_kernel<DT, kAligned, 1>, 1)
                : run(kv4_write_kernel<DT, kAligned, kItems>, kItems);

@@ -16,6 +16,11 @@
 // cosines and weights become 32 factors once:
 //   out_a = r (a * w_a cos - c * w_c sin),  out_c = r (c * w_c cos + a * w_a sin),
 // two packed fp32 operations for two channels.
+//
+// Measured: 16384 tokens of 32 + 8 heads of 128 channels, bf16 (336 MB): 56.5 us, 5.9 TB/s, 0.88 of the
+// card's copy rate, with 64 % of the issue slots and 48 % of the integer pipe busy; with one set of
+// heads a warp in place of four 84 us, with two 61.  Small calls take a launch and the chain position ->
+// factors -> store: 2.2 us for one token.
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -322,12 +327,14 @@ template <int DT, int GL>
 cudaError_t launch_vec(NormRopeParams& p, int sm_count, cudaStream_t stream) {
   constexpr int HPW = 32 / GL;
   // As many sets of heads a warp (more loads on the way, sines and cosines used more often) as
-  // leave 16 warps an SM; a call with fewer tokens spreads each over more warps.
+  // leave 12 warps an SM; a call with fewer tokens spreads each over more warps.  512 tokens of 32 + 8
+  // heads take 3.9 us in 17 warps an SM of one set, 4.4 in 8 of two; 999 tokens of 7 + 7 heads of 80
+  // fp32 channels 4.6 us in 13 warps of two, 5.4 in 26 of one.
   int64_t warps = 0;
   for (p.units = kUnits;; p.units /= 2) {
     for (int j = 0; j < 2; ++j) p.chunks[j] = (p.s[j].heads + HPW * p.units - 1) / (HPW * p.units);
     warps = p.tokens * (p.chunks[0] + p.chunks[1]);
-    if (p.units == 1 || warps >= static_cast<int64_t>(sm_count) * 16) break;
+    if (p.units == 1 || warps >= static_cast<int64_t>(sm_count) * 12) break;
   }
   const dim3 grid(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
   return p.interleaved

@@ -1,6 +1,7 @@
 """Run one kernel family of the decode step a fixed number of times, for external profilers.
 
     python -m diffusion_decoding_gb300.kernel_driver {stats|probs|gemm|step|fused} [n [B L]]
+    python -m diffusion_decoding_gb300.kernel_driver {rope|cache|token|block|piece} [n]
 
 The inputs have the smoothing-step sizes (B=16, L=64, V=126464 bf16 logits, d=2048 embedding
 table; about 0.8 GB on the device), so every launch reads more than the L2 holds; `stats`
@@ -9,6 +10,11 @@ iteration).  Nothing is timed here: a profiler (ncu) attaches to the launches.  
 the fused statistics + threshold commit; `probs` the probability rows; `gemm` the smoothing
 GEMM (after one probability pass); `step` the whole step (commit, probabilities, GEMM, KV
 refresh) through the separate calls; `fused` the whole step through the single-read call.
+
+The second line runs the operators of the KV refresh (below 0.5 GB on the device): `rope` norm and
+rotation of 16384 tokens, `cache` write and read of 32768 entries, `token` attention of single tokens
+over 32 sequences of 8192 entries, `block` of 64-token blocks over 16 of 4160, `piece` of 1024 tokens of
+a prompt over 2 of 16384.
 """
 import sys
 
@@ -20,9 +26,54 @@ B_, L_, V, D = 16, 64, 126464, 2048
 PREFIX, WINDOW, TAU = 1024, 4, 0.9
 
 
+def refresh_operator(what: str, n: int) -> None:
+    dev, bf16 = torch.device("cuda"), torch.bfloat16
+    D, page = 128, 64
+    if what == "rope":
+        qkv = torch.randn(4, 4096, 40, D, device=dev).to(bf16)
+        q, k = qkv[:, :, :32], qkv[:, :, 32:]
+        qo, ko = torch.empty_like(q, memory_format=torch.contiguous_format), \
+            torch.empty_like(k, memory_format=torch.contiguous_format)
+        pos = torch.arange(4096, dtype=torch.int32, device=dev).repeat(4, 1)
+        phases = torch.empty(D // 2, dtype=torch.int64, device=dev)
+        dd.dllm_rope_phases(D, phases)
+        for _ in range(n):
+            dd.dllm_qk_norm_rope(q, k, qo, ko, pos, phases)
+        torch.cuda.synchronize()
+        return
+    B, m, heads, group, T, causal = {"cache": (8, 4096, 8, 1, 4096, False),
+                                     "token": (32, 1, 8, 4, 8192, False),
+                                     "block": (16, 64, 2, 8, 4160, False),
+                                     "piece": (2, 1024, 8, 4, 16384, True)}[what]
+    cache = dd.Kv4Cache(B * (T // page), heads, page, D, B, T // page, dev)
+    cache.table.copy_(torch.randperm(B * (T // page), device=dev).view(B, -1).to(torch.int32))
+    for b in range(0, T, 1024):  # fill it, a stretch of entries at a time
+        k = torch.randn(B, min(1024, T - b), heads, D, device=dev).to(bf16)
+        pos = torch.arange(b, b + k.shape[1], dtype=torch.int32, device=dev).repeat(B, 1)
+        dd.dllm_kv4_write(cache, k, k, pos)
+    if what == "cache":
+        k, v = (torch.randn(B, m, heads, D, device=dev).to(bf16) for _ in range(2))
+        pos = torch.arange(m, dtype=torch.int32, device=dev).repeat(B, 1)
+        for _ in range(n):
+            dd.dllm_kv4_write(cache, k, v, pos)
+            dd.dllm_kv4_read(cache, k, v, pos)
+        torch.cuda.synchronize()
+        return
+    q = torch.randn(B, m, heads * group, D, device=dev).to(bf16)
+    out = torch.empty_like(q)
+    ws = dd.workspace(dd.dllm_attention_kv4_workspace_bytes(cache, B, m, heads * group, T), dev)
+    for _ in range(n):
+        dd.dllm_attention_kv4(q, cache, None, T, out, ws, causal=causal)
+    if dd.dllm_get_status(ws) != dd.DLLM_OK:
+        raise SystemExit("attention reported a fault")
+
+
 def main(argv) -> None:
     what = argv[0] if argv else "step"
     n = int(argv[1]) if len(argv) > 1 else 4
+    if what in ("rope", "cache", "token", "block", "piece"):
+        refresh_operator(what, n)
+        return
     if what not in ("stats", "probs", "gemm", "step", "fused"):
         raise SystemExit(f"unknown kernel family {what!r}")
     B, L = (int(argv[2]), int(argv[3])) if what == "stats" and len(argv) > 3 else (B_, L_)

@@ -457,8 +457,8 @@ dllm_status dllm_qk_norm_rope(const dllm_heads* q, const dllm_heads* q_out, cons
  * for s * (n - z), which bf16 holds exactly.  codes: [pages, heads, page_size, head_dim / 2]
  * bytes, channel 2c in the low nibble of byte c.  params: [pages, heads, page_size, head_dim / 32]
  * 16-bit words, the bf16 bits of s with z in the low four.  4.5 bits a value.
- * heads <= 4096; page_size a multiple of 16 in [16, 65536]; head_dim a multiple of 32 in [32, 512]; codes and params
- * 16-byte aligned.  The caller owns all arrays; nothing has to be initialised.
+ * heads <= 4096; page_size a multiple of 16 in [16, 65536]; head_dim a multiple of 32 in [32, 512];
+ * codes and params 16-byte aligned.  The caller owns all arrays; nothing has to be initialised.
  */
 typedef struct {
   uint8_t* k_codes;
