@@ -604,6 +604,7 @@ cudaError_t launch_attention(const AttnParams& p, int D, void* ws, int sm_count,
   f.row_tiles = s.row_tiles;
   f.ctas = s.ctas;
   f.unit_log2 = s.unit_log2;
+  f.whole = !s.split;
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   f.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + s.off_ml);

@@ -17,6 +17,7 @@ namespace dllm {
 
 struct AttnPlan {
   int unit_log2;    // entries of a unit, a power of two; the line has fewer than 2^31 units
+  int whole;        // a segment is one unit whatever its length: the line needs no lengths
   int row_tiles;
   int q_aligned;    // query rows on 16-byte boundaries
   int out_aligned;  // output rows too
@@ -69,6 +70,7 @@ struct Line {
 
   __device__ __forceinline__ int weight(const AttnParams& p, const AttnPlan& f, int item) const {
     if (item >= items) return 0;
+    if (f.whole) return p.heads;
     const int b = f.row_tiles == 1 ? item : item / f.row_tiles, rt = item - b * f.row_tiles;
     return p.heads * units_of(tile_sees<ROWS>(p, length_of(p, b), rt), f);
   }
@@ -83,18 +85,16 @@ struct Line {
   }
   __device__ __forceinline__ void build(const AttnParams& p, const AttnPlan& f) {
     items = p.B * f.row_tiles;
-    equal = !p.lens && !p.causal;
-    own = weight(p, f, threadIdx.x & 31);
-    upto = scan(own);
-    total = __shfl_sync(kFull, upto, 31);
-    if (items > 32) {
-      if (equal) {
-        total = weight(p, f, 0) * items;
-      } else {
-        int sum = 0;
-        for (int k = 32 + (threadIdx.x & 31); k < items; k += 32) sum += weight(p, f, k);
-        total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(sum)));
-      }
+    equal = f.whole || (!p.lens && !p.causal);
+    if (equal) {
+      total = weight(p, f, 0) * items;
+    } else {
+      own = weight(p, f, threadIdx.x & 31);
+      upto = scan(own);
+      total = __shfl_sync(kFull, upto, 31);
+      int sum = 0;
+      for (int k = 32 + (threadIdx.x & 31); k < items; k += 32) sum += weight(p, f, k);
+      if (items > 32) total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(sum)));
     }
     each = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(f.ctas));
     longer = total - each * f.ctas;
@@ -112,7 +112,7 @@ struct Line {
   __device__ __forceinline__ int find(const AttnParams& p, const AttnPlan& f, int at,
                                       int* before) const {
     const int lane = threadIdx.x & 31;
-    if (items > 32 && equal) {
+    if (equal) {
       const int per = weight(p, f, 0), item = at / per;
       *before = item * per;
       return item;

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t visible[kVisible][2];  // of a tile's 64 entries: a bit per entry
   __shared__ uint32_t raw_visible[kRawTiles][2];
   __shared__ float2 ml_s[2][kRows];         // groups with the same rows: reference and sum
+  __shared__ int start_s[12];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -283,10 +284,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // on are done: one of them may be waiting for tensor memory
   pdl_wait();
   pdl_trigger();
-  Line<ROWS> line;
-  line.build(p, f);
-  const int u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
-  if (u0 >= u1) return;
+  {
+    Line<ROWS> line;
+    line.build(p, f);
+    const int u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
+    if (u0 >= u1) return;
+    if (warp == 0) {
+      Segment<ROWS> sg;
+      sg.find(p, f, line, u0);
+      if (lane == 0) {
+        const int v[12] = {sg.item,  sg.b,  sg.rt, sg.h, sg.len,    sg.seen,
+                           sg.units, sg.k0, u0,    u1,   line.each, line.longer};
+#pragma unroll
+        for (int i = 0; i < 12; ++i) start_s[i] = v[i];
+      }
+    }
+  }
   if (warp == 16) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   tc_before();
   __syncthreads();
@@ -299,8 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto col_p = [](int g) { return kTwo ? 384u + 32u * g : 320u; };
   constexpr uint32_t col_q = kTwo ? 448 : 384;
 
+  // Where the CTA begins.  Each role reads it for itself once it has its own share of the registers:
+  // taken across the split it was spilled, and read back in every step (128 segments of 65 tiles and 256
+  // channels: 72 us in place of 65).
   Segment<ROWS> sg;
-  sg.find(p, f, line, u0);
+  int u0, u1;
+  auto begin = [&]() {
+    volatile int* v = start_s;
+    sg.item = v[0], sg.b = v[1], sg.rt = v[2], sg.h = v[3], sg.len = v[4], sg.seen = v[5];
+    sg.units = v[6], sg.k0 = v[7], u0 = v[8], u1 = v[9];
+  };
   int step = 0;  // tiles so far
   int mine = 0;  // tiles of this group so far: the phase of its barriers
   // tile k's place in a ring of `of` places, and the parity of its use of it
@@ -318,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = lanes + col_s(grp), t_p = lanes + col_p(grp), t_o = lanes + col_o(grp);
     const uint32_t scratch = sbase + M::kScratch + warp * 2048;
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    begin();
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       const int b = sg.b, h = sg.h;
@@ -543,10 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (count > 0) tmem_ld32(t_o + c, o);
             tmem_ld32(t_other + c, x);
             tmem_wait_ld();
+            {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
+              for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
+              for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
+            }
           }
           // channels back in order: the word holds 0, 4, 1, 5, 2, 6, 3, 7
           if (r < rows && !direct) {
@@ -650,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
       }
     };
+    begin();
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
       for (int t = (half ^ step) & 1; t < pc.tiles; t += 2) {
@@ -708,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_low = desc_low(sbase + M::kQ, 16);
       bool ok = true;
       int piece_no = 0;  // segments with tiles of this group
+      begin();
       for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int first = kSame ? (grp ^ step) & 1 : 0;
@@ -778,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t to_p =
           sbase + M::kRaw + 2 * M::kRawCodes + (is_k ? 0 : M::kRawPar) + lane * par_bytes;
       int sent = 0;
+      begin();
       for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
         const int32_t* table = p.table + static_cast<int64_t>(sg.b) * p.table_stride;
@@ -832,7 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         step += pc.tiles;
-        if (is_k && lane == 0) note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
+        if (is_k && lane == 0) {
+          Line<ROWS> line;
+          line.each = start_s[10], line.longer = start_s[11];
+          note_segment(f, p, line, sg, u, u0, pc.units == sg.units);
+        }
         u += pc.units;
         if (u >= u1) break;
         sg.next(p, f);
@@ -1011,6 +1042,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   f.row_tiles = (p.n * p.G + R - 1) / R;
   f.copy_span = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
   plan_line<D>(p, sm_count, &f);
+  f.whole = p.max_len <= 1 << f.unit_log2;
   f.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
   f.out_aligned = attention_rows_aligned(p.out, p.ob, p.ot, p.oh);
   f.status = static_cast<int32_t*>(ws);
@@ -1023,7 +1055,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   if (e != cudaSuccess) return e;
   e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
                        Smem<D, kShare>::kBytes, stream, p, f);
-  if (e != cudaSuccess || p.max_len <= 1 << f.unit_log2) return e;
+  if (e != cudaSuccess || f.whole) return e;
   const int64_t joins = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (R / 32) * (D / 64);
   return launch_dependent(attention_tc_join_kernel<D, R>, dim3(static_cast<unsigned>(joins)),
                           dim3(128), 0, stream, p, f);
