@@ -95,6 +95,10 @@ __device__ __forceinline__ uint32_t elect_lane() {
       : "=r"(e));
   return e;
 }
+// A value that all lanes hold, in a uniform register (a reduction's result is): what is computed from
+// it stays there.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(kFull, x); }
+__device__ __forceinline__ int uniform(int x) { return static_cast<int>(uniform(static_cast<uint32_t>(x))); }
 // D [128 x N] (+)= A [128 x 16] B [16 x N], A in TMEM, B in shared memory
 __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -195,6 +199,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int32_t* status) {
   if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status)) != 0;
+}
+
+// The same for waits that may end a little late (the copies, and the codes they bring): the warp
+// sleeps between its looks and leaves the issue slots to the others (prompt piece 387 us, 391 without;
+// 420 if the turning warps' waits for free places sleep too).
+template <unsigned NS>
+__device__ __forceinline__ bool wait_warp_lazy(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               int32_t* status) {
+  for (int i = 0; i < 64; ++i) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    __nanosleep(NS);
+  }
   return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status)) != 0;
 }
 
@@ -679,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece<ROWS> pc(sg, f, u1 - u);
       for (int t = (half ^ step) & 1; t < pc.tiles; t += 2) {
         const int k = step + t, rs = place(k, kRawTiles);
-        if (!wait_warp(raw_full0 + 8 * rs, parity(k, kRawTiles), abort_v, f.status)) break;
+        if (!wait_warp_lazy<50>(raw_full0 + 8 * rs, parity(k, kRawTiles), abort_v, f.status)) break;
         const uint32_t at = raw0 + rs * M::kRawTile, par = par0 + rs * M::kRawTile;
         uint4 kc[PER], vc[PER];
         uint32_t kp[PER], vp[PER];
@@ -722,31 +739,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    const int grp = __shfl_sync(kFull, warp, 0) - 16;
+    const int grp = uniform(warp) - 16;
     if (!kTwo && grp == 1) {
       // no second group
     } else if (grp < 2) {
       const uint32_t lead = elect_lane();
       const uint32_t bar = gbars + kGroupBars * grp;
-      const uint32_t base = __shfl_sync(kFull, tmem, 0);
+      const uint32_t base = uniform(tmem);
       const uint32_t t_s = base + col_s(grp), t_p = base + col_p(grp), t_o = base + col_o(grp);
-      const uint32_t q_low = desc_low(sbase + M::kQ, 16);
+      const uint32_t smem0 = uniform(sbase), q_low = desc_low(smem0 + M::kQ, 16);
       bool ok = true;
       int piece_no = 0;  // segments with tiles of this group
       begin();
       for (int u = u0; u < u1;) {
         const Piece<ROWS> pc(sg, f, u1 - u);
+        const int tiles = uniform(pc.tiles);
         const int first = kSame ? (grp ^ step) & 1 : 0;
-        const int count = pc.tiles > first ? (pc.tiles - first + STRIDE - 1) / STRIDE : 0;
+        const int count = tiles > first ? (tiles - first + STRIDE - 1) / STRIDE : 0;
         auto wait = [&](uint32_t at, uint32_t phase) {
           return wait_warp(at, phase, abort_v, f.status);
         };
         if (count > 0) ok = ok && wait(bar + kBarQ, piece_no++ & 1);
         auto scores = [&](int k) {
-          const int ks = __shfl_sync(kFull, place(k, kKTiles), 0);
+          const int ks = place(k, kKTiles);
           if (!wait(k_full0 + 8 * ks, parity(k, kKTiles))) return false;
           tc_after();
-          const uint32_t low = desc_low(sbase + ks * M::kTensor, 16);
+          const uint32_t low = desc_low(smem0 + ks * M::kTensor, 16);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             const uint64_t kd = desc_at(low, (x >> 2) * SLAB + (x & 3) * 32);
@@ -770,11 +788,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = wait(bar + kBarP, (mine + n) & 1);
           if (!ok) break;
-          const int vs = __shfl_sync(kFull, place(k, kVTiles), 0);
+          const int vs = place(k, kVTiles);
           ok = wait(v_full0 + 8 * vs, parity(k, kVTiles));
           if (!ok) break;
           tc_after();
-          const uint32_t low = desc_low(sbase + M::kV + vs * M::kTensor, D > 64 ? SLAB : 16);
+          const uint32_t low = desc_low(smem0 + M::kV + vs * M::kTensor, D > 64 ? SLAB : 16);
 #pragma unroll
           for (int x = 0; x < kTile / 16; ++x)
             mma_ts(lead, t_o, t_p + x * 8, desc_at(low, x * 2048), idesc(D, true), n > 0 || x > 0);
@@ -784,8 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last scores' phase of kBarFree is passed over: it is waited for here
         if (count > 0) ok = ok && wait(bar + kBarFree, (mine + count - 1) & 1);
         mine += count;
-        step += pc.tiles;
-        u += pc.units;
+        step += tiles;
+        u += uniform(pc.units);
         if (u < u1) sg.next(p, f);
       }
       mma_commit(lead, done_bar);
@@ -839,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++word;
           }
           ask();
-          if (!wait_warp(raw_empty0 + 8 * rs, parity(k, kRawTiles) ^ 1, abort_v, f.status)) break;
+          if (!wait_warp_lazy<200>(raw_empty0 + 8 * rs, parity(k, kRawTiles) ^ 1, abort_v, f.status)) break;
           sent = k + 1;
           if (copier) {
             const uint32_t bar = raw_full0 + 8 * rs;
