@@ -18,9 +18,10 @@
 //
 // Measured: one token of each of 32 sequences of up to 8192 entries, 4 query heads to each of 8 cache
 // heads of 128 channels: 66.8 us, 3.4 TB/s of cache.  The rate is set by the integer work that turns
-// codes into values: about 490 instructions a warp and tile of 16 entries, 66 % of the issue slots and
+// codes into values: about 450 instructions a warp and tile of 16 entries, 66 % of the issue slots and
 // 63 % of the integer pipe busy, at four warps a scheduler (123 registers; five CTAs an SM spill and
-// take 72.7 us).  One sequence of 65536 entries: 21 us, of which the join takes a third.
+// take 72.7 us; shifts done by the multiplier 69.5 to 76.5).  One sequence of 65536 entries: 21 us, of
+// which the join takes a third.
 #include "attention.h"
 
 #include <algorithm>

@@ -6,7 +6,7 @@
 // Two groups of four warps each hold 128 rows, one row a thread.  With more than 128 rows in a
 // segment (kShare) the groups are the two halves of a 256-row tile and both use every K and V tile;
 // otherwise they hold the same rows, take the tiles in turn, and add up at the end.  (1024 tokens of
-// 4 heads over 16384 entries: 393 us; with the same rows in both groups 549.)  With 256 channels the
+// 4 heads over 16384 entries: 387 us; with the same rows in both groups 549.)  With 256 channels the
 // accumulator of one group fills half of the tensor memory, and there is no second group.
 //
 // Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
@@ -24,12 +24,14 @@
 // written once and read twice, the queries of group 1 read once, the codes in and out), 1150
 // cycles, about as many as the products of both groups take (1152).
 //
-// Measured: a step of 256 rows takes 1750 to 1900 cycles, so 0.62 to 0.66 of the tensor cores' time
-// (1.27 PFLOP/s on the piece above, 0.66 of the card's burst rate); what is left is the chain scores ->
-// softmax -> weights -> product, each hand-over 120 cycles, with 61 % of the issue slots busy.  One
-// segment by itself costs about 9 us (launch, queries, one tile, output).  Measured slower: two places
-// for each group's scores with all queries in shared memory (444 us: its reads bind), two threads a
-// row (478), other orders of the warps (402, 432), a poll with a sleep hint (418).
+// Measured: a step of 256 rows takes 1750 to 1850 cycles, so 0.62 to 0.66 of the tensor cores' time
+// (1.29 PFLOP/s on the piece above, 0.66 of the card's burst rate; 1.07 with 256 channels, 128 segments
+// of 65 tiles in 65 us).  What is left is the chain scores -> softmax -> weights -> product, each
+// hand-over 120 cycles, with 60 % of the issue slots busy.  One segment by itself costs about 8 us
+// (launch, queries, one tile, output).  Measured slower, on the piece: two places for each group's
+// scores with all queries in shared memory (444 us: its reads bind), two threads a row (478), other
+// orders of the warps (402, 432), a poll with a sleep hint everywhere (418), scores unpacked for
+// single multiplications (395).
 // The eight channels of a code word come out as pairs (j, j + 4): Q's channels are put in the same
 // order (the scores do not depend on it), and the output's are put back.
 #include "attention.h"
