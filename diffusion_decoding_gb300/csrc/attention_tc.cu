@@ -6,8 +6,9 @@
 // Two groups of four warps each hold 128 rows, one row a thread.  With more than 128 rows in a
 // segment (kShare) the groups are the two halves of a 256-row tile and both use every K and V tile;
 // otherwise they hold the same rows, take the tiles in turn, and add up at the end.  (1024 tokens of
-// 4 heads over 16384 entries: 387 us; with the same rows in both groups 549.)  With 256 channels the
-// accumulator of one group fills half of the tensor memory, and there is no second group.
+// 4 heads over 16384 entries: 387 us; with the same rows in both groups 549.)  With 192 or 256
+// channels the accumulator of one group fills most of half of the tensor memory, and there is no
+// second group.
 //
 // Warps 0-7: softmax (no shuffles), the rescaling of O when the reference moves (rarely:
 // attention.cu's kSlack), and the output.  Warps 18 and 19 look the pages up and have the tiles' codes
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scratch, from where each thread takes those of its own row to TMEM.  Groups with the same
         // rows share the queries there, and each brings half of the channels.
         const int lr = lane >> 2, lp = lane & 3;
-        constexpr int CHUNKS = kSame ? D / 64 : D / 32, BLOCK = CHUNKS < 4 ? CHUNKS : 4;
+        constexpr int CHUNKS = kSame ? D / 64 : D / 32, BLOCK = CHUNKS % 4 == 0 ? 4 : CHUNKS % 3 == 0 ? 3 : CHUNKS;
         const bool to_tmem = !kShare || grp == 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < CHUNKS; c0 += BLOCK) {
@@ -658,16 +659,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(turn_regs(D)));
     constexpr int GROUPS = D / 32;  // per entry
     constexpr int PER = GROUPS / 2;  // pieces of K (and of V) a thread turns per tile
-    constexpr int APART = 128 / GROUPS;  // entries from one to the next
+    // Piece e of the thread: entry entry0 + APART * e, group g; with 192 channels, whose six groups do
+    // not divide the threads, entry entry0 and group g + 2 e.
+    constexpr bool kByEntry = D == 192;
+    constexpr int APART = kByEntry ? 0 : 128 / GROUPS;
+    constexpr uint32_t RAW_STEP = kByEntry ? 32 : 2048, PAR_STEP = kByEntry ? 4 : 256;
+    constexpr uint32_t DST_STEP = kByEntry ? SLAB : APART * 128;
     const int half = (warp >> 2) & 1, w = warp & 3;
-    // piece e of the thread: entry entry0 + APART * e, group g
-    const int entry0 = (w * 32 + lane) / GROUPS, g = lane % GROUPS;
-    const uint32_t raw0 = sbase + M::kRaw + (w * 32 + lane) * 16;
-    const uint32_t par0 = sbase + M::kRaw + 2 * M::kRawCodes + (w * 32 + lane) * 2;
+    const int entry0 = kByEntry ? w * 16 + (lane & 15) : (w * 32 + lane) / GROUPS;
+    const int g = kByEntry ? lane >> 4 : lane % GROUPS;
+    const uint32_t raw0 = sbase + M::kRaw + entry0 * (D / 2) + g * 16;
+    const uint32_t par0 = sbase + M::kRaw + 2 * M::kRawCodes + entry0 * (D / 16) + g * 2;
     // Word x goes to 16-byte piece (4 (g % 2) + x) ^ (entry % 8) of the entry's row in slab g / 2.
     // Lanes of slab 1 store words in the order 2, 3, 0, 1 (D = 128), those of slab s word x ^ s in
     // place of word x (D = 256): with eight lanes at a time (two entries of four groups, or one of
-    // eight), all eight pieces of a 128-byte row are then hit once.
+    // eight), all eight pieces of a 128-byte row are then hit once; eight entries of one group (D = 192)
+    // do that by themselves.
     const int turn_x = D > 128 ? g >> 1 : D > 64 && g >= 2 ? 2 : 0;
     uint32_t piece_at[4];
 #pragma unroll
@@ -704,10 +711,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t kp[PER], vp[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-          kc[e] = ld_shared_v4(at + e * 2048);
-          vc[e] = ld_shared_v4(at + M::kRawCodes + e * 2048);
-          kp[e] = ld_shared_u16(par + e * 256);
-          vp[e] = ld_shared_u16(par + M::kRawPar + e * 256);
+          kc[e] = ld_shared_v4(at + e * RAW_STEP);
+          vc[e] = ld_shared_v4(at + M::kRawCodes + e * RAW_STEP);
+          kp[e] = ld_shared_u16(par + e * PAR_STEP);
+          vp[e] = ld_shared_u16(par + M::kRawPar + e * PAR_STEP);
         }
         const uint32_t vis[2] = {raw_visible[rs][0], raw_visible[rs][1]};
 #pragma unroll
@@ -723,13 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(k_empty0 + 8 * ks, parity(k, kKTiles) ^ 1, abort_v, f.status)) break;
         if (w == 0 && lane < 2) visible[place(k, kVisible)][lane] = lane ? vis[1] : vis[0];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) turn(kc[e], kp[e], ks * M::kTensor + e * APART * 128);
+        for (int e = 0; e < PER; ++e) turn(kc[e], kp[e], ks * M::kTensor + e * DST_STEP);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full0 + 8 * ks);
         if (!wait_warp(v_empty0 + 8 * vs, parity(k, kVTiles) ^ 1, abort_v, f.status)) break;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) turn(vc[e], vp[e], M::kV + vs * M::kTensor + e * APART * 128);
+        for (int e = 0; e < PER; ++e) turn(vc[e], vp[e], M::kV + vs * M::kTensor + e * DST_STEP);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full0 + 8 * vs);
@@ -983,13 +990,14 @@ __global__ void __launch_bounds__(128)
 }  // namespace
 
 bool attention_tc_can(int n, int G, int D) {
-  const int64_t least = D == 64 ? 32 : D == 128 ? 16 : D == 256 ? 8 : INT64_MAX;
+  const int64_t least = D == 64 ? 32 : D == 128 ? 16 : 8;
   return static_cast<int64_t>(n) * G > least;
 }
 
 // Up to 32 rows only with enough to do: 24 rows of 128 channels take 50 us here and 62 in the other
 // kernel (128 heads of 4000 entries), 10.8 and 14.6 (128 of 300), but 22.6 and 17.7 (8 of 8000) and
-// 9.8 and 8.8 (8 of 300); 16 rows of 256 channels 69 and 78, 14.0 and 14.9, 26.6 and 23.5, 12.6 and 11.2.
+// 9.8 and 8.8 (8 of 300); 16 rows of 256 channels 69 and 78, 14.0 and 14.9, 26.6 and 23.5, 12.6 and 11.2;
+// 16 rows of 192 channels 61 and 70, 12.0 and 11.7.
 // 48 rows of 64 channels 46 and 61, 9.5 and 12.6, 21.3 and 16.8, 8.7 and 7.3.
 bool attention_tc_takes(const AttnParams& p, int D, int sm_count) {
   if (!attention_tc_can(p.n, p.G, D)) return false;
@@ -1084,6 +1092,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream) {
   if (D == 256) return launch_tc<256, false>(p, ws, sm_count, stream);
+  if (D == 192) return launch_tc<192, false>(p, ws, sm_count, stream);
   if (tile_rows(p.n, p.G, D) == kRows)
     return D == 64 ? launch_tc<64, false>(p, ws, sm_count, stream)
                    : launch_tc<128, false>(p, ws, sm_count, stream);

@@ -45,3 +45,24 @@ def test_attention_of_some_rows(B, n, H, G, D, ps, T, lens):
         out, lse = run(c, q, lens, T, causal=causal)
         check_attention(out, lse, q, k, v, seen_of(B, n, T, lens or [T] * B, None, causal, c),
                         D ** -0.5)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,n,H,G,ps,T,lens", [
+    (1, 33, 1, 1, 16, 1, None), (2, 64, 1, 2, 64, 64, [64, 63]), (1, 43, 2, 3, 48, 65, None),
+    (3, 17, 1, 8, 16, 300, [300, 0, 129]), (2, 128, 2, 1, 256, 1000, [1000, 700]),
+    (1, 200, 1, 3, 32, 777, None), (20, 5, 5, 4, 64, 500, None)])
+def test_attention_of_six_groups(B, n, H, G, ps, T, lens, causal, masked):
+    """192 channels: six groups of an entry, three slabs of a tile."""
+    D = 192
+    g = gen(n + T)
+    c = make_cache(g, B, T, H, D, ps)
+    k, v = fill(g, c, T)
+    q = randn(g, B, n, H * G, D).to(torch.bfloat16)
+    mask = None
+    if masked:
+        mask = (torch.rand(B, T, generator=g, device=DEV) < 0.7).to(torch.uint8)
+        mask[0, :min(T, 40)] = 0
+    out, lse = run(c, q, lens, T, causal=causal, mask=mask)
+    check_attention(out, lse, q, k, v, seen_of(B, n, T, lens or [T] * B, mask, causal, c), D ** -0.5)
