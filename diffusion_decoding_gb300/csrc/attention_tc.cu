@@ -101,7 +101,9 @@ __device__ __forceinline__ uint32_t elect_lane() {
 // A value that all lanes hold, in a uniform register (a reduction's result is): what is computed from
 // it stays there.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(kFull, x); }
-__device__ __forceinline__ int uniform(int x) { return static_cast<int>(uniform(static_cast<uint32_t>(x))); }
+__device__ __forceinline__ int uniform(int x) {
+  return static_cast<int>(uniform(static_cast<uint32_t>(x)));
+}
 // D [128 x N] (+)= A [128 x 16] B [16 x N], A in TMEM, B in shared memory
 __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -375,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scratch, from where each thread takes those of its own row to TMEM.  Groups with the same
         // rows share the queries there, and each brings half of the channels.
         const int lr = lane >> 2, lp = lane & 3;
-        constexpr int CHUNKS = kSame ? D / 64 : D / 32, BLOCK = CHUNKS % 4 == 0 ? 4 : CHUNKS % 3 == 0 ? 3 : CHUNKS;
+        constexpr int CHUNKS = kSame ? D / 64 : D / 32;
+        constexpr int BLOCK = CHUNKS % 4 == 0 ? 4 : CHUNKS % 3 == 0 ? 3 : CHUNKS;
         const bool to_tmem = !kShare || grp == 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < CHUNKS; c0 += BLOCK) {
