@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / 
         for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm[w][r]);
         const float keep = m[t][x] == -INFINITY ? 0.f : ex2(m[t][x] - mx);
         float* dst = so + (warp * ROWS + r) * D;
+        if (r0 + r >= rows) continue;
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           // the lane's word holds channels 0..7; tile k of the word has channels 2k and 2k + 1
@@ -552,7 +553,8 @@ FewSizes few_sizes(int B, int n, int G, int heads, int D, int max_len, int sm_co
   // Up to 2^kShort entries a segment is one unit: its warps take it in a few tiles each, sooner than a
   // second kernel could join its parts; in eight warps' steps where that leaves no SM without a CTA.
   // Four segments of 512 entries take 7.5 us whole with eight warps, 8.6 with four, 7.4 to 7.6 split;
-  // 64 segments 7.9, 9.0 and 9 to 10; four of 1024 entries 10.8 whole and 7.5 split.
+  // 64 segments 7.9, 9.0 and 9 to 10; four of 1024 entries 10.8 whole and 7.5 split.  (Sixteen warps
+  // lose more in adding up their rows than they gain: 331 entries 7.7 us, 6.5 with eight.)
   s.wide = brief && segments <= sm_count;
   s.ctas = s.wide ? sm_count : sm_count * few_ctas_per_sm(D, s.nt);
   s.unit_log2 = brief ? kShort : unit_log2_of(segments, max_len, 6);
