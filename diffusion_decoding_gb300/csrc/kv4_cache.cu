@@ -34,6 +34,7 @@ struct Kv4Params {
   int n;
   unsigned tokens;
   uint32_t head_magic;
+  int lanes_log2;  // lanes of a token: 32, or fewer where its pieces are few
 };
 
 // One warp's work: a token, keys or values, and pieces [first, first + 32 * ITEMS) of its heads.
@@ -42,14 +43,18 @@ struct Unit {
   int b, i, first;
   int entry;  // cache entry, -1: none
   int page, slot;
+  int lane;  // of the token's
   bool valid;
 };
 
-__device__ __forceinline__ Unit unit_of(const Kv4Params& p, int items) {
-  const unsigned token = blockIdx.x * (kThreads / 32u) + (threadIdx.x >> 5);
+template <int ITEMS>
+__device__ __forceinline__ Unit unit_of(const Kv4Params& p) {
+  const int lanes_log2 = ITEMS == 1 ? p.lanes_log2 : 5;  // with more, a token has a warp at least
+  const unsigned token = (blockIdx.x * static_cast<unsigned>(kThreads) + threadIdx.x) >> lanes_log2;
   Unit u;
-  u.first = static_cast<int>(blockIdx.y) * 32 * items;
+  u.first = static_cast<int>(blockIdx.y) * 32 * ITEMS;
   u.valid = token < p.tokens;
+  u.lane = static_cast<int>(threadIdx.x) & ((1 << lanes_log2) - 1);
   u.b = static_cast<int>(token / static_cast<unsigned>(p.n));
   u.i = static_cast<int>(token) - u.b * p.n;
   u.entry = u.page = -1;
@@ -121,11 +126,10 @@ __device__ __forceinline__ void store32(char* p, const uint32_t* w) {
 template <int DT, bool kAligned, int ITEMS>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_constant__ Kv4Params p) {
   constexpr int NW = DT == DLLM_BF16 ? 8 : 16;  // words of a piece
-  const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  Unit u = unit_of(p, ITEMS);
-  if (!u.valid) return;
+  Unit u = unit_of<ITEMS>(p);
+  if (ITEMS > 1 && !u.valid) return;
   const int side = blockIdx.z;
   const int cpr = p.D / 16, pieces = p.heads * cpr;
   const char* x = p.x[side] + u.b * p.xb[side] + u.i * p.xt[side];
@@ -135,10 +139,10 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
   uint32_t raw[ITEMS][NW];
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
-    const int c = u.first + t * 32 + lane;
+    const int c = u.first + t * 32 + u.lane;
 #pragma unroll
     for (int e = 0; e < NW; ++e) raw[t][e] = 0u;
-    if (c >= pieces) continue;
+    if (c >= pieces || (ITEMS == 1 && !u.valid)) continue;
     const int h = head_of(p, c);
     const char* src = x + h * xh + (c - h * cpr) * (NW * 4);
     if constexpr (kAligned) {
@@ -155,13 +159,13 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
     }
   }
   find_page(p, u);
-  if (u.page < 0) return;
+  if (ITEMS > 1 ? u.page < 0 : !__any_sync(kFull, u.page >= 0)) return;
   const int64_t row0 = static_cast<int64_t>(u.page) * p.heads * p.page_size + u.slot;
   uint8_t* codes = p.codes[side] + row0 * (p.D / 2);
   uint16_t* params = p.params[side] + row0 * (p.D / kKv4Group);
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
-    const int c = u.first + t * 32 + lane;
+    const int c = u.first + t * 32 + u.lane;
     float hi, lo;
     if constexpr (DT == DLLM_BF16) {
       // extremes in packed bf16; the maximum and the negated minimum share a word
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
         w[e >> 3] = w[e >> 3] * 16u + static_cast<uint32_t>(nf);
       }
     }
-    if (c >= pieces) continue;
+    if (c >= pieces || (ITEMS == 1 && u.page < 0)) continue;
     if (s != s) z = 0u;
     const int h = head_of(p, c), cc = c - h * cpr;
     const int64_t row = static_cast<int64_t>(h) * p.page_size;
@@ -238,10 +242,9 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
 
 template <int DT, bool kAligned, int ITEMS>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ Kv4Params p) {
-  const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  Unit u = unit_of(p, ITEMS);
+  Unit u = unit_of<ITEMS>(p);
   if (!u.valid) return;
   find_page(p, u);
   const int side = blockIdx.z;
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
   uint32_t pp[ITEMS];
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
-    const int c = u.first + t * 32 + lane;
+    const int c = u.first + t * 32 + u.lane;
     w[t] = make_uint2(0u, 0u);
     pp[t] = 0u;
     if (u.page < 0 || c >= pieces) continue;
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
   }
 #pragma unroll
   for (int t = 0; t < ITEMS; ++t) {
-    const int c = u.first + t * 32 + lane;
+    const int c = u.first + t * 32 + u.lane;
     if (c >= pieces) continue;
     const int h = head_of(p, c), cc = c - h * cpr;
     const Kv4Scale sc = kv4_scale(__byte_perm(pp[t], pp[t], 0x1010));
@@ -319,14 +322,19 @@ bool aligned32(const dllm_heads& h) {
 template <bool kWrite, int DT, bool kAligned>
 cudaError_t launch_items(Kv4Params& p, int sm_count, cudaStream_t stream) {
   const int pieces = p.heads * (p.D / 16);
+  // Tokens of up to 16 pieces share a warp (32768 entries of one head: 11.8 us written and read, 39.3
+  // with a token a warp; of two 20.7, 39.7).
+  p.lanes_log2 = 5;
+  while (p.lanes_log2 > 1 && pieces <= 1 << (p.lanes_log2 - 1)) --p.lanes_log2;
+  const unsigned per_block = kThreads >> p.lanes_log2;
   auto run = [&](auto kern, int items) {
-    const dim3 grid((p.tokens + kThreads / 32 - 1) / (kThreads / 32),
+    const dim3 grid((p.tokens + per_block - 1) / per_block,
                     static_cast<unsigned>((pieces + 32 * items - 1) / (32 * items)), 2);
     return launch_dependent(kern, grid, dim3(kThreads), 0, stream, p);
   };
   // Two pieces a lane hide more of the load latency and share the page lookup; one piece a lane
   // when the call has too few warps to fill the SMs (1152 entries of 4 heads: 4.7 us, 5.1 with two).
-  const bool few = static_cast<int64_t>(p.tokens) * 2 * ((pieces + 63) / 64) <
+  const bool few = pieces <= 32 || static_cast<int64_t>(p.tokens) * 2 * ((pieces + 63) / 64) <
                    static_cast<int64_t>(sm_count) * 16;
   if constexpr (kWrite)
     return few ? run(kv4_write_kernel<DT, kAligned, 1>, 1)

@@ -50,7 +50,8 @@ struct NormRopeParams {
   int D, R, interleaved, norm;
   float magnitude, eps;
   int units;       // sets of heads a warp takes, <= kUnits
-  int chunks[2];   // warps per token for the queries and for the keys
+  int pack_log2;   // tokens that share a warp (few heads)
+  int chunks[2];   // warps per token (or tokens that share one) for the queries and for the keys
 };
 
 // cos and sin of p * u turns-in-2^-64, times m
@@ -114,26 +115,34 @@ __device__ __forceinline__ uint64_t swap2(uint64_t v) {
 }
 
 // GL lanes per head (a power of two >= D / 16); D % 16 == 0, R % 16 == 0, 16-byte aligned rows.
-template <int DT, int GL, bool kInter>
+// kPack: tokens share a warp (a form of its own: asking costs the others 4 %).
+template <int DT, int GL, bool kInter, bool kPack>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int ES = DT == DLLM_BF16 ? 2 : 4;
   constexpr int HPW = 32 / GL;  // heads a warp holds at once
+  constexpr int kHpwLog2 = HPW == 1 ? 0 : HPW == 2 ? 1 : HPW == 4 ? 2 : HPW == 8 ? 3 : HPW == 16 ? 4 : 5;
   const unsigned warp = blockIdx.x * (kThreads / 32u) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   const unsigned per_token = p.chunks[0] + p.chunks[1];
-  const unsigned token = warp / per_token;
-  if (token >= p.tokens) return;
-  int chunk = static_cast<int>(warp - token * per_token);
+  const unsigned group = warp / per_token;  // of the tokens that share a warp
+  int chunk = static_cast<int>(warp - group * per_token);
+  const int sub = lane % GL;
+  const int pack_log2 = kPack ? p.pack_log2 : 0;
+  const int heads_log2 = kHpwLog2 - pack_log2;  // of a token at once
+  const int slot = (lane / GL) & ((1 << heads_log2) - 1);
+  const unsigned token = (group << pack_log2) + (lane / GL >> heads_log2);
+  const bool valid = token < p.tokens;
+  if (!kPack && !valid) return;
   const int b = static_cast<int>(token / static_cast<unsigned>(p.n));
   const int i = static_cast<int>(token) - b * p.n;
-  const int pos = p.pos ? p.pos[b * p.pos_stride + i] : 0;  // looked at when the loads are under way
+  // looked at when the loads are under way
+  const int pos = kPack && !valid ? -1 : p.pos ? p.pos[b * p.pos_stride + i] : 0;
   const int side = chunk >= p.chunks[0];
   if (side) chunk -= p.chunks[0];
   const Side& s = p.s[side];
 
-  const int sub = lane % GL, slot = lane / GL;
   const bool active = sub < p.D / 16;
   const bool turns = sub < p.R / 16;
   // the lane's two pieces of eight channels: both halves of its pairs, or side by side
@@ -141,19 +150,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   const int o1 = !turns || kInter ? o0 + 8 : p.R / 2 + o0;
   const char* x = s.x + b * s.xb + i * s.xt;
   char* y = s.y + b * s.yb + i * s.yt;
-  const int h0 = chunk * p.units * HPW + slot;
+  const int at_once = 1 << heads_log2;
+  const int h0 = chunk * p.units * at_once + slot;
   Piece<DT> a0[kUnits], a1[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
     a0[u] = Piece<DT>{};
     a1[u] = Piece<DT>{};
-    const int h = h0 + u * HPW;
-    if (u < p.units && active && h < s.heads) {
+    const int h = h0 + u * at_once;
+    if (u < p.units && active && (!kPack || valid) && h < s.heads) {
       a0[u] = load_piece<DT>(x + h * s.xh + o0 * ES);
       a1[u] = load_piece<DT>(x + h * s.xh + o1 * ES);
     }
   }
-  if (pos < 0) return;
+  if (kPack ? !__any_sync(kFull, pos >= 0) : pos < 0) return;
   // factors of a piece's own channels and of their partners' (two channels a word)
   uint64_t own[2][4], other[2][4];
   {
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
     if (u >= p.units) break;
-    const int h = h0 + u * HPW;
+    const int h = h0 + u * at_once;
     uint64_t v[2][4];
     {
       float f0[8], f1[8];
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         unpack2(mul2(t, r2), out[k][2 * j], out[k][2 * j + 1]);
       }
     }
-    if (active && h < s.heads) {
+    if (active && (!kPack || pos >= 0) && h < s.heads) {
       store_piece<DT>(y + h * s.yh + o0 * ES, out[0]);
       store_piece<DT>(y + h * s.yh + o1 * ES, out[1]);
     }
@@ -326,20 +336,30 @@ bool rows_aligned(const Side& s) {
 template <int DT, int GL>
 cudaError_t launch_vec(NormRopeParams& p, int sm_count, cudaStream_t stream) {
   constexpr int HPW = 32 / GL;
-  // As many sets of heads a warp (more loads on the way, sines and cosines used more often) as
-  // leave 12 warps an SM; a call with fewer tokens spreads each over more warps.  512 tokens of 32 + 8
-  // heads take 3.9 us in 17 warps an SM of one set, 4.4 in 8 of two; 999 tokens of 7 + 7 heads of 80
-  // fp32 channels 4.6 us in 13 warps of two, 5.4 in 26 of one.
+  // With at most half a warp's heads, tokens share a warp (9944 tokens of 1 + 1 heads of 80 channels:
+  // 5.6 us, 19.1 with a token a warp; 16384 of 2 + 1 heads of 128: 12.2, 29.2).  Otherwise as many sets of heads a warp (more loads on the way,
+  // sines and cosines used more often) as leave 12 warps an SM; a call with fewer tokens spreads each
+  // over more warps.  512 tokens of 32 + 8 heads take 3.9 us in 17 warps an SM of one set, 4.4 in 8 of
+  // two; 999 tokens of 7 + 7 heads of 80 fp32 channels 4.6 us in 13 warps of two, 5.4 in 26 of one.
+  const int most = p.s[0].heads > p.s[1].heads ? p.s[0].heads : p.s[1].heads;
+  p.pack_log2 = 0;
+  while ((most << (p.pack_log2 + 1)) <= HPW) ++p.pack_log2;
   int64_t warps = 0;
-  for (p.units = kUnits;; p.units /= 2) {
-    for (int j = 0; j < 2; ++j) p.chunks[j] = (p.s[j].heads + HPW * p.units - 1) / (HPW * p.units);
-    warps = p.tokens * (p.chunks[0] + p.chunks[1]);
+  for (p.units = p.pack_log2 > 0 ? 1 : kUnits;; p.units /= 2) {
+    const int heads = p.units * HPW >> p.pack_log2;
+    for (int j = 0; j < 2; ++j) p.chunks[j] = (p.s[j].heads + heads - 1) / heads;
+    warps = ((p.tokens + (1 << p.pack_log2) - 1) >> p.pack_log2) * (p.chunks[0] + p.chunks[1]);
     if (p.units == 1 || warps >= static_cast<int64_t>(sm_count) * 12) break;
   }
   const dim3 grid(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
-  return p.interleaved
-             ? launch_dependent(norm_rope_kernel<DT, GL, true>, grid, dim3(kThreads), 0, stream, p)
-             : launch_dependent(norm_rope_kernel<DT, GL, false>, grid, dim3(kThreads), 0, stream, p);
+  auto run = [&](auto kern) { return launch_dependent(kern, grid, dim3(kThreads), 0, stream, p); };
+  if constexpr (HPW > 1) {
+    if (p.pack_log2 > 0)
+      return p.interleaved ? run(norm_rope_kernel<DT, GL, true, true>)
+                           : run(norm_rope_kernel<DT, GL, false, true>);
+  }
+  return p.interleaved ? run(norm_rope_kernel<DT, GL, true, false>)
+                       : run(norm_rope_kernel<DT, GL, false, false>);
 }
 
 template <int DT>

@@ -72,3 +72,48 @@ def test_decode_loop_keeps_the_cache_current():
     dd.dllm_kv4_read(layer2.cache, k2, v2)
     changed = (v0 != v2).flatten(2).any(-1)
     assert torch.equal(changed, tokens != tokens2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,n,Hq,Hk,D", [(1, 1, 1, 1, 64), (2, 7, 1, 1, 128), (3, 5, 2, 1, 64),
+                                         (1, 13, 1, 1, 32), (2, 9, 3, 2, 32), (1, 6, 1, 1, 256)])
+def test_few_heads_share_a_warp(dtype, B, n, Hq, Hk, D):
+    """Tokens share a warp where heads are few: skipped tokens, and ends that do not fill one."""
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev)
+    g.manual_seed(n + D)
+    q, k, v = (torch.randn(B, n, h, D, device=dev, generator=g).to(dtype) for h in (Hq, Hk, Hk))
+    pos = torch.stack([torch.randperm(60, device=dev, generator=g)[:n] for _ in range(B)])
+    pos = pos.to(torch.int32)
+    pos[0, n // 2] = -1
+    live = pos >= 0
+    phases = torch.empty(D // 2, dtype=torch.int64, device=dev)
+    dd.dllm_rope_phases(D, phases)
+    qo, ko = (torch.full_like(x, 3.0) for x in (q, k))
+    dd.dllm_qk_norm_rope(q, k, qo, ko, pos, phases)
+    for x, y in ((q, qo), (k, ko)):
+        o, size = ref.norm_rope(x, pos, ref.frequencies(D, 10000.0), None, 1e-6, False)
+        tol = 4e-6 * size + (2.0 ** -8 * o.abs() if dtype == torch.bfloat16 else 0) + 1e-30
+        assert ((y.double() - o).abs() <= tol)[live].all()
+        assert (y[~live] == 3.0).all()
+    cache = dd.Kv4Cache(4 * B, Hk, 16, D, B, 4)
+    cache.table.copy_(torch.arange(4 * B, dtype=torch.int32, device=dev).view(B, 4))
+    for t in (cache.k_codes, cache.v_codes, cache.k_params, cache.v_params):
+        t.zero_()
+    dd.dllm_kv4_write(cache, k, v, pos)
+    kr, vr = (torch.full_like(k, 5.0) for _ in range(2))
+    dd.dllm_kv4_read(cache, kr, vr, pos)
+    for x, y in ((k, kr), (v, vr)):
+        if dtype == torch.bfloat16:
+            assert torch.equal(y[live].double(), ref.quantised(x)[live])
+        else:  # a quotient next to a tie may round either way: within half a step, a step in all
+            s, _ = ref.steps(x)
+            half = s.repeat_interleave(32, -1).view_as(x)
+            assert ((y.double() - x.double()).abs() <= 0.5001 * half + 1e-30)[live].all()
+        assert (y[~live] == 0).all()
+    everything = torch.empty(B, 64, Hk, D, dtype=dtype, device=dev)
+    dd.dllm_kv4_read(cache, everything, torch.empty_like(everything))
+    untouched = torch.ones(B, 64, dtype=torch.bool, device=dev)
+    for b in range(B):
+        untouched[b, pos[b, live[b]].long()] = False
+    assert (everything[untouched] == 0).all()
