@@ -506,10 +506,11 @@ __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / 
       float mx = sm[0][r];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm[w][r]);
+      // A warp whose reference is -inf saw nothing (a sum of 0) or scores that are NaN (a sum of NaN).
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w)
-        sum += sm[w][r] == -INFINITY ? 0.f : sl[w][r] * ex2(sm[w][r] - mx);
+        sum += sm[w][r] == -INFINITY ? sl[w][r] : sl[w][r] * ex2(sm[w][r] - mx);
       if (!direct) {
         *reinterpret_cast<float2*>(f.part_o + (part * ROWS + r) * D + 2 * ch) = acc;
         if (ch == 0) f.part_ml[part * ROWS + r] = make_float2(mx, sum);

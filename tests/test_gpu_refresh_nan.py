@@ -1,0 +1,94 @@
+"""Attention over the 4-bit cache where a query, a key or a value is NaN (a group of the cache that held
+a NaN or an infinity reads back as NaN): by the formulas a row is NaN where a score that it sees is,
+an output channel where a value that the row sees is, and nothing else is touched.  Everything that
+is not NaN is held to the tolerances of the other sizes (test_gpu_refresh_ops.py)."""
+import math
+
+import pytest
+import torch
+
+import refresh_ref as ref
+from test_gpu_refresh_ops import DEV, entries, gen, make_cache, randn, run, seen_of
+
+pytestmark = pytest.mark.gpu
+
+
+def check(out, lse, q, k, v, seen, scale):
+    """Against the 64-bit statement of the finite parts; q, k, v may hold NaN."""
+    B, n, H, D = q.shape
+    G = H // k.shape[2]
+    kn, vn = k.isnan().any(-1), v.isnan()  # [B, T, Hkv], [B, T, Hkv, D]
+    zero = lambda x: torch.where(x.isnan(), torch.zeros_like(x), x)  # noqa: E731
+    o, l, mag, top = ref.attention(zero(q), zero(k), zero(v), seen, scale)
+    s = seen.double()
+    bad_score = torch.einsum("bnt,bth->bnh", s, kn.double()).repeat_interleave(G, 2) > 0
+    bad_score |= q.isnan().any(-1) & seen.any(-1)[:, :, None]
+    bad = torch.einsum("bnt,bthd->bnhd", s, vn.double()).repeat_interleave(G, 2) > 0
+    bad |= bad_score[..., None]
+    assert torch.equal(out.isnan(), bad)
+    err, tol = (out.double() - o).abs(), 2.0 ** -8 * 1.03 * (mag + o.abs())
+    assert (err <= tol + 1e-30)[~bad].all()
+    nan_l = bad_score.permute(0, 2, 1)
+    assert torch.equal(lse.isnan(), nan_l)
+    none = ~seen.any(-1)[:, None].expand_as(lse)
+    assert (lse[none] == -math.inf).all() and (out.permute(0, 2, 1, 3)[none] == 0).all()
+    rest = ~none & ~nan_l
+    d = (lse.double() - l).abs()[rest]
+    assert (d <= 1e-5 * l.abs().clamp(min=1)[rest] + 2.0 ** -20 * top[rest]).all()
+
+
+def store(g, c, T, nan_k=(), nan_v=()):
+    """Random keys and values of T entries, with NaN in one channel of the listed (sequence, entry,
+    head, channel); what the cache then holds."""
+    B = c.table.shape[0]
+    k, v = (randn(g, B, T, c.heads, c.head_dim).to(torch.bfloat16) for _ in range(2))
+    for x, where in ((k, nan_k), (v, nan_v)):
+        for at in where:
+            x[at] = math.nan
+    import diffusion_decoding_gb300 as dd
+    dd.dllm_kv4_write(c, k, v, torch.arange(T, dtype=torch.int32, device=DEV).repeat(B, 1))
+    return entries(c, c.k_codes, c.k_params, T), entries(c, c.v_codes, c.v_params, T)
+
+
+# few rows in tiles of 8 and 16, whole and split; many rows: the same in two groups, 256 in two groups,
+# one group of 128 rows
+ROWS = [(1, 2, 128, 16), (3, 4, 128, 64), (1, 5, 64, 16), (1, 3, 192, 32), (2, 3, 256, 16), (48, 2, 128, 16),
+        (100, 3, 64, 64), (48, 1, 192, 16), (40, 1, 256, 64)]
+
+
+@pytest.mark.parametrize("n,G,D,ps", ROWS)
+@pytest.mark.parametrize("T", [1, 17, 331, 5000])
+def test_nan_queries(n, G, D, ps, T):
+    g = gen(T + n)
+    B, H = 2, 2
+    c = make_cache(g, B, T, H, D, ps)
+    k, v = store(g, c, T)
+    q = (1.5 * randn(g, B, n, H * G, D)).to(torch.bfloat16)
+    q[0, 0, 0, 3] = math.nan
+    q[1, n - 1, H * G - 1, D - 1] = math.nan
+    mask = (torch.rand(B, T, generator=g, device=DEV) < 0.7).to(torch.uint8)
+    for m in (None, mask):
+        out, lse = run(c, q, None, T, mask=m)
+        check(out, lse, q, k, v, seen_of(B, n, T, [T] * B, m, False, c), D ** -0.5)
+
+
+@pytest.mark.parametrize("n,G,D,ps", ROWS)
+@pytest.mark.parametrize("T,at", [(1, 0), (17, 16), (331, 330), (331, 200), (5000, 4999), (5000, 0)])
+def test_nan_keys(n, G, D, ps, T, at):
+    g = gen(T + n + at)
+    B, H = 2, 2
+    c = make_cache(g, B, T, H, D, ps)
+    k, v = store(g, c, T, nan_k=[(1, at, 1, 40)])
+    q = (1.5 * randn(g, B, n, H * G, D)).to(torch.bfloat16)
+    out, lse = run(c, q, None, T)
+    check(out, lse, q, k, v, seen_of(B, n, T, [T] * B, None, False, c), D ** -0.5)
+    # hidden by the mask it is not used; alone in a stretch it is the only thing seen there
+    mask = torch.ones(B, T, dtype=torch.uint8, device=DEV)
+    mask[1, at] = 0
+    out, lse = run(c, q, None, T, mask=mask)
+    check(out, lse, q, k, v, seen_of(B, n, T, [T] * B, mask, False, c), D ** -0.5)
+    lone = torch.ones(B, T, dtype=torch.uint8, device=DEV)
+    lone[1, max(0, at - 300):at] = 0
+    lone[1, at + 1:at + 300] = 0
+    out, lse = run(c, q, None, T, mask=lone)
+    check(out, lse, q, k, v, seen_of(B, n, T, [T] * B, lone, False, c), D ** -0.5)
