@@ -178,6 +178,7 @@ struct Tile {
 // A weight may reach 2^kSlack before the reference moves: sums of 2^30 of them stay far inside fp32,
 // and bf16 keeps the same relative precision at every magnitude.
 constexpr float kSlack = 8.f;
+constexpr uint32_t kDiagonal = 1u << 16;  // beside a tile's 16 entries: not all rows see the same of them
 
 // CTAs of the one resident wave per SM: what the registers allow (checked with -Xptxas -v).
 constexpr int few_ctas_per_sm(int D, int NT) {
@@ -191,15 +192,23 @@ constexpr size_t few_smem() {
   return ring > join ? ring : join;
 }
 
+// A function of its own: inlined it costs single tokens over a masked cache 2 %.
+template <int D, int ROWS>
+__device__ __noinline__ void put_nans_few(const AttnParams& p, const AttnPlan& f, Segment<ROWS> sg, int u0,
+                                          int u1) {
+  put_nans<D, ROWS, 16, false>(p, f, sg, u0, u1);
+}
+
 template <int D, int NT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / WARPS)
     attention_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPlan f) {
   using R = Tile<D>;
   constexpr int KW = R::KW, VW = R::VW, MT = D / 16, ROWS = 8 * NT, kThreads = 32 * WARPS;
   constexpr int kStep = 16 * WARPS;  // entries that the warps take together
-  extern __shared__ float4 smem_raw[];
+  extern __shared__ __align__(128) float4 smem_raw[];  // (the rings' bank pattern counts on it)
   float* so = reinterpret_cast<float*>(smem_raw);  // [WARPS][ROWS][D]
   __shared__ float sm[WARPS][ROWS], sl[WARPS][ROWS];
+  __shared__ uint32_t nan_s[WARPS];  // the warp met a NaN of V on the diagonal
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / 
   const uint8_t* v_of_lane = p.v_codes + lane * 16;
   const typename R::Lane at_lane(ring, c, g);
 
+  if (lane == 0) nan_s[warp] = 0u;
   for (int u = u0; u < u1;) {
     const int piece = min(sg.units - sg.k0, u1 - u);
     const int b = sg.b, h = sg.h, len = sg.len, r0 = sg.rt * ROWS, k0 = sg.k0;
@@ -320,6 +330,7 @@ __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / 
         const int e = j + (lane & 15);
         vis = __ballot_sync(kFull, e < end && (!mask || __ldg(mask + e) != 0)) & 0xffffu;
         if (vis == 0u) return;
+        if (p.causal && !whole) vis |= kDiagonal;
       }
       cur.read_k(at_lane, at);
       float s[NT][4];
@@ -407,6 +418,14 @@ __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / 
           if (!(vis >> (c + 4 * e) & 1u)) {
 #pragma unroll
             for (int k = 0; k < (R::kSpread ? 3 : 1); ++k) cur.vp[e][k] = 0u;
+          }
+        }
+        if (vis & kDiagonal) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int k = 0; k < (R::kSpread ? 3 : 1); ++k)
+              if (kv4_nan(cur.vp[e][k])) cur.vp[e][k] = 0u, nan_s[warp] = 1u;
           }
         }
       }
@@ -531,6 +550,15 @@ __global__ void __launch_bounds__(32 * WARPS, few_ctas_per_sm(D, NT) * kWarps / 
       __syncthreads();  // the buffers are reused
       sg.next(p, f);
     }
+  }
+  if (!p.causal) return;
+  __syncthreads();
+  uint32_t nan_met = nan_s[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) nan_met |= nan_s[w];
+  if (nan_met) {
+    sg.find(p, f, line, u0);
+    put_nans_few<D, ROWS>(p, f, sg, u0, u1);
   }
 }
 

@@ -181,6 +181,55 @@ __device__ __forceinline__ void note_segment(const AttnPlan& f, const AttnParams
                         line.holder(u + sg.units - 1));
 }
 
+// On the diagonal of a causal call a weight of 0 must not meet a NaN of V that only later rows of the tile
+// see.  Entries in tiles of `TILE` that not all rows see alike therefore count as 0 in the products where
+// their group of V is NaN; a CTA that met one runs this when it is done (all its threads, its stores made
+// visible to each other): the rows that do see such an entry get their NaN.  It stands at the end,
+// out of the way: the same look-up in a segment's own end cost every call 1 to 9 %, as it is single tokens
+// over a masked cache take 62.5 us (61.4 without), pieces of 256 channels 44.4 (43.7), others the same.
+template <int D, int ROWS, int TILE, bool kRowsTogether>
+__device__ __forceinline__ void put_nans(const AttnParams& p, const AttnPlan& f, Segment<ROWS> sg, int u0,
+                                         int u1) {
+  constexpr int GROUPS = D / 32;
+#pragma unroll 1
+  for (int u = u0; u < u1;) {
+    const int piece = min(sg.units - sg.k0, u1 - u), r0 = sg.rt * ROWS;
+    const int from = max(sg.k0 << f.unit_log2, max(rows_see(p, sg.len, r0), 0) & ~(TILE - 1));
+    const int end = min(sg.seen, (sg.k0 + piece) << f.unit_log2);
+    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
+#pragma unroll 1
+    for (int x = threadIdx.x; x < ROWS * GROUPS; x += blockDim.x) {
+      const int row = x / GROUPS, g = x - row * GROUPS, r = r0 + row;
+      if (r >= p.n * p.G) break;
+      const int to = min(end, rows_see(p, sg.len, r));
+      bool nan = false;
+#pragma unroll 1
+      for (int e = from; e < to && !nan; ++e) {
+        if (p.key_mask && __ldg(p.key_mask + sg.b * p.mask_stride + e) == 0) continue;
+        const int word = e / p.page_size;
+        const int page = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_stride + word);
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) continue;
+        const int64_t at = (static_cast<int64_t>(page) * p.heads + sg.h) * p.page_size + e - word * p.page_size;
+        nan = kv4_nan(__ldg(p.v_params + at * GROUPS + g));
+      }
+      if (!nan) continue;
+      const int i = token_of(p, r), hq = sg.h * p.G + r - i * p.G;
+      uint16_t* out = p.out + sg.b * p.ob + i * p.ot + hq * p.oh + g * 32;
+#pragma unroll 1
+      for (int c = g * 32; c < g * 32 + 32; ++c) {
+        if (piece == sg.units)
+          *out++ = 0x7FFFu;
+        else if (kRowsTogether)  // the layout of attention_tc.cu
+          f.part_o[((part * (D / 4) + c / 4) * ROWS + row) * 4 + c % 4] = NAN;
+        else
+          f.part_o[(part * ROWS + row) * D + c] = NAN;
+      }
+    }
+    u += piece;
+    if (u < u1) sg.next(p, f);
+  }
+}
+
 __device__ __forceinline__ void store_joined(const AttnParams& p, int b, int h, int r, int ch, float2 a,
                                              float inv) {
   const int i = token_of(p, r), hq = h * p.G + r - i * p.G;

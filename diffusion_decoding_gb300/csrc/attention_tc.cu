@@ -37,6 +37,8 @@
 // order (the scores do not depend on it), and the output's are put back.
 #include "attention.h"
 
+#include <limits.h>
+
 #include <algorithm>
 
 #include "attention_line.cuh"
@@ -265,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int start_s[12];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int nan_met;  // a NaN of V on a diagonal
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(raw_full0 + 8 * s, 2 * (kTile / f.copy_span));  // the lanes that copy
       mbar_init(raw_empty0 + 8 * s, 4);  // the four warps that turn them
     }
-    abort_flag = 0;
+    abort_flag = nan_met = 0;
     fence_mbar_init();
   }
   // nothing else of this CTA, its tensor memory included, is taken before the kernels it depends
@@ -706,6 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin();
     for (int u = u0; u < u1;) {
       const Piece<ROWS> pc(sg, f, u1 - u);
+      // first tile that not every row sees whole
+      const int t_diagonal = p.causal ? (rows_see(p, sg.len, sg.rt * ROWS) - pc.j0) >> 6 : INT_MAX;
       for (int t = (half ^ step) & 1; t < pc.tiles; t += 2) {
         const int k = step + t, rs = place(k, kRawTiles);
         if (!wait_warp_lazy<50>(raw_full0 + 8 * rs, parity(k, kRawTiles), abort_v, f.status)) break;
@@ -737,6 +742,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full0 + 8 * ks);
+        if (t >= t_diagonal) {  // (attention_line.cuh: put_nans; K's values come first, its scores wait)
+          bool nan = false;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            nan |= kv4_nan(vp[e]);
+            vp[e] = kv4_nan(vp[e]) ? 0u : vp[e];
+          }
+          if (nan) nan_met = 1;
+        }
         if (!wait_warp(v_empty0 + 8 * vs, parity(k, kVTiles) ^ 1, abort_v, f.status)) break;
 #pragma unroll
         for (int e = 0; e < PER; ++e) turn(vc[e], vp[e], M::kV + vs * M::kTensor + e * DST_STEP);
@@ -925,6 +939,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (nan_met) {
+    begin();
+    put_nans<D, ROWS, kTile, true>(p, f, sg, u0, u1);
   }
 }
 

@@ -14,6 +14,9 @@ namespace dllm {
 constexpr int kKv4Group = 32;
 constexpr uint32_t kKv4NaNParam = 0x7FE0u;  // step of a group that held a NaN or an infinity
 
+// The group of this param word reads as NaN (its step is no finite number).
+__device__ __forceinline__ bool kv4_nan(uint32_t param) { return (param & 0x7F80u) == 0x7F80u; }
+
 // packed bf16 arithmetic on raw words
 __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;

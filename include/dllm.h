@@ -503,8 +503,10 @@ dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, cons
  *   j < len_b = min(lens[b], max_len)  (lens NULL: max_len),  key_mask[b*mask_stride + j] != 0
  *   (key_mask NULL: all),  its page is present, and, with `causal`, j <= len_b - n + i;
  *   lse = ln sum_j exp(scale * q.K_j),  out = sum_j exp(scale * q.K_j - lse) V_j.
- * A query that sees nothing gets out = 0 and lse = -inf.  Entries that no query sees are never
- * used, whatever their codes, params and mask neighbours hold.  Scores, the softmax statistics and
+ * A query that sees nothing gets out = 0 and lse = -inf.  Entries that a query does not see have no
+ * effect on it, whatever their codes, params and mask neighbours hold.  A score that is NaN makes
+ * out and lse of its query NaN, a group of V that reads as NaN its 32 channels of every query that
+ * sees the entry.  Scores, the softmax statistics and
  * sums are fp32; the weights exp(.) are rounded to bf16 for their product with V, which is exact
  * bf16, and out is rounded once to bf16.  The order of all sums is fixed: repeated calls agree
  * bit for bit.

@@ -92,3 +92,37 @@ def test_nan_keys(n, G, D, ps, T, at):
     lone[1, at + 1:at + 300] = 0
     out, lse = run(c, q, None, T, mask=lone)
     check(out, lse, q, k, v, seen_of(B, n, T, [T] * B, lone, False, c), D ** -0.5)
+
+
+@pytest.mark.parametrize("n,G,D,ps", ROWS + [(70, 8, 128, 32), (300, 1, 64, 16), (200, 2, 256, 48), (4, 4, 64, 48)])
+@pytest.mark.parametrize("T", [310, 2500])
+@pytest.mark.parametrize("masked", [False, True])
+def test_nan_values_and_causal_rows(n, G, D, ps, T, masked):
+    # a value that only later rows see leaves the earlier ones alone, whatever tile they share
+    g = gen(T + n)
+    B, H = 2, 2
+    lens = [T, T - 41]
+    c = make_cache(g, B, T, H, D, ps)
+    first = T - n
+    at = {lens[0] - 1, max(0, first), max(0, first) + n // 2, max(0, first - 1), max(0, first - 130), 5}
+    nan_v = [(0, j, h, (37 * (i + h)) % D) for i, j in enumerate(sorted(at)) for h in (0, 1) if (i + h) % 3]
+    nan_v += [(1, lens[1] - 1, 0, 0), (1, lens[1] - 1 - n // 3, 1, D - 1)]
+    k, v = store(g, c, T, nan_v=nan_v)
+    q = (1.5 * randn(g, B, n, H * G, D)).to(torch.bfloat16)
+    mask = None
+    if masked:
+        mask = (torch.rand(B, T, generator=g, device=DEV) < 0.7).to(torch.uint8)
+    for causal in (True, False):
+        out, lse = run(c, q, lens, T, causal=causal, mask=mask)
+        check(out, lse, q, k, v, seen_of(B, n, T, lens, mask, causal, c), D ** -0.5)
+
+
+@pytest.mark.parametrize("n,G,D,ps", ROWS + [(300, 1, 64, 16)])
+def test_nan_keys_and_causal_rows(n, G, D, ps):
+    g = gen(n)
+    B, H, T = 1, 2, 400
+    c = make_cache(g, B, T, H, D, ps)
+    k, v = store(g, c, T, nan_k=[(0, T - 1 - n // 2, 1, 7), (0, T - 1, 0, 0)])
+    q = (1.5 * randn(g, B, n, H * G, D)).to(torch.bfloat16)
+    out, lse = run(c, q, None, T, causal=True)
+    check(out, lse, q, k, v, seen_of(B, n, T, [T], None, True, c), D ** -0.5)
