@@ -563,7 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1);
         const int row_tile = r - sg.rt * ROWS;
-        float keep0 = count > 0 ? 1.f : 0.f, keep1 = 0.f;  // this group's and the other's
+        float keep0 = 1.f, keep1 = 0.f;  // this group's and the other's
+        // An accumulator without a tile holds nothing yet; all others count however small their weight
+        // is (0 * NaN is NaN).
+        const bool other = kSame && pc.tiles > 1 - first;
         if constexpr (kSame) {
           const float2 ml = ml_s[grp ^ 1][row_in];
           const float mn = fmaxf(m, ml.x);
@@ -587,16 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld();
             }
           } else {
-            float x[32];
+            float x[32] = {};
             if (count > 0) tmem_ld32(t_o + c, o);
-            tmem_ld32(t_other + c, x);
+            if (other) tmem_ld32(t_other + c, x);
             tmem_wait_ld();
-            {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = keep0 == 0.f ? 0.f : o[e] * keep0;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = keep1 == 0.f ? o[e] : fmaf(x[e], keep1, o[e]);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(x[e], keep1, o[e] * keep0);
           }
           // channels back in order: the word holds 0, 4, 1, 5, 2, 6, 3, 7
           if (r < rows && !direct) {

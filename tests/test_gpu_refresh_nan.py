@@ -126,3 +126,21 @@ def test_nan_keys_and_causal_rows(n, G, D, ps):
     q = (1.5 * randn(g, B, n, H * G, D)).to(torch.bfloat16)
     out, lse = run(c, q, None, T, causal=True)
     check(out, lse, q, k, v, seen_of(B, n, T, [T], None, True, c), D ** -0.5)
+
+
+@pytest.mark.parametrize("n,G,D", [(1, 4, 128), (48, 2, 128), (40, 1, 256), (90, 4, 64)])
+def test_nan_value_of_a_vanishing_weight(n, G, D):
+    # a value that is seen counts, however small its weight: 0 * NaN is NaN wherever the sum is joined
+    g = gen(n)
+    T = 700
+    c = make_cache(g, 1, T, 1, D, 64)
+    k = torch.zeros(1, T, 1, D, device=DEV, dtype=torch.bfloat16)
+    k[:, 65] = 100.0  # one entry takes all of the weight
+    v = randn(g, 1, T, 1, D).to(torch.bfloat16)
+    v[0, 3, 0, 0] = v[0, 140, 0, D - 1] = math.nan
+    import diffusion_decoding_gb300 as dd
+    dd.dllm_kv4_write(c, k, v, torch.arange(T, dtype=torch.int32, device=DEV)[None])
+    kk, vv = entries(c, c.k_codes, c.k_params, T), entries(c, c.v_codes, c.v_params, T)
+    q = torch.ones(1, n, G, D, device=DEV, dtype=torch.bfloat16)
+    out, lse = run(c, q, None, T, scale=1.0)
+    check(out, lse, q, kk, vv, torch.ones(1, n, T, dtype=torch.bool, device=DEV), 1.0)
