@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(32 * WARPS)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  const int64_t seg = blockIdx.x / ROWS;
-  const int r = blockIdx.x % ROWS;
+  const int64_t seg = blockIdx.x;
+  const int r = blockIdx.y;
   const int2 info = f.parts[seg];
   if (info.x < 0) return;
   const int h = static_cast<int>(seg % p.heads), item = static_cast<int>(seg / p.heads);
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(32 * WARPS)
 template <int D, int ROWS>
 cudaError_t launch_join(const AttnParams& p, const AttnPlan& f, cudaStream_t stream) {
   const int64_t segments = static_cast<int64_t>(p.B) * f.row_tiles * p.heads;
-  const dim3 blocks(static_cast<unsigned>(segments * ROWS));
+  const dim3 blocks(static_cast<unsigned>(segments), ROWS);  // up to 2^30 segments
   if (f.ctas > 16 * segments)
     return launch_dependent(attention_join_kernel<D, ROWS, 16>, blocks, dim3(512), 0, stream, p, f);
   return launch_dependent(attention_join_kernel<D, ROWS, 4>, blocks, dim3(128), 0, stream, p, f);

@@ -1104,6 +1104,7 @@ static cudaError_t launch_tc(const AttnParams& p, void* ws, int sm_count, cudaSt
   e = launch_dependent(attention_tc_kernel<D, kShare>, dim3(f.ctas), dim3(kThreads),
                        Smem<D, kShare>::kBytes, stream, p, f);
   if (e != cudaSuccess || f.whole) return e;
+  // (below 2^31: more than 8 rows to each of 2^30 / rows segments, 16 CTAs a segment at most)
   const int64_t joins = static_cast<int64_t>(p.B) * f.row_tiles * p.heads * (R / 32) * (D / 64);
   return launch_dependent(attention_tc_join_kernel<D, R>, dim3(static_cast<unsigned>(joins)),
                           dim3(128), 0, stream, p, f);
