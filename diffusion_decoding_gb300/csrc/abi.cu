@@ -715,6 +715,11 @@ dllm_status dllm_qk_norm_rope(const dllm_heads* q, const dllm_heads* q_out, cons
       return fail(DLLM_ERR_INVALID_ARG, "the tensors differ in dtype");
   }
   DLLM_TRY(check_tokens(B, n));
+  // a warp each in the largest grid of four-warp blocks
+  const int64_t rows = static_cast<int64_t>(B) * n * ((q ? q->heads : 0) + (k ? k->heads : 0));
+  if (rows > (int64_t{1} << 33) - 4)
+    return fail(DLLM_ERR_UNSUPPORTED, "B*n tokens of all heads: %lld exceeds 2^33 - 4",
+                static_cast<long long>(rows));
   if (head_dim < 1 || head_dim > 1024)
     return fail(head_dim < 1 ? DLLM_ERR_INVALID_ARG : DLLM_ERR_UNSUPPORTED,
                 "head_dim=%d outside [1, 1024]", head_dim);

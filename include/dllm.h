@@ -440,7 +440,8 @@ dllm_status dllm_rope_phases(const dllm_rope* rope, int64_t* phases, dllm_stream
  * heads; they may be the same memory with the same strides, and must not overlap otherwise.
  * q, q_out or k, k_out may be NULL (both of a pair): only the other is done.  One dtype for all
  * tensors and weights (fp32 or bf16).  1 <= head_dim <= 1024; rotary_dim even, <= head_dim, 0: no
- * rotation (phases may be NULL, and pos too: every token is done).  B, n >= 1, B*n <= 2^20.
+ * rotation (phases may be NULL, and pos too: every token is done).  B, n >= 1, B*n <= 2^20, and
+ * B*n times the heads of q and k together <= 2^33 - 4.
  */
 dllm_status dllm_qk_norm_rope(const dllm_heads* q, const dllm_heads* q_out, const dllm_heads* k,
                               const dllm_heads* k_out, int32_t B, int32_t n, int32_t head_dim,

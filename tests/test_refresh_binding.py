@@ -1,0 +1,19 @@
+"""Host-side checks of the refresh operators beyond test_refresh_host.py: sizes at the far end of the
+limits, and tensors that the binding must not take (no GPU needed: every call is refused or only asks
+for sizes)."""
+import pytest
+import torch
+
+import diffusion_decoding_gb300 as dd
+from test_refresh_host import BAD, INV, UNS, cache, heads, lib, norm_rope, ref  # noqa: F401
+
+
+@pytest.mark.parametrize("q,k,B,n", [
+    (65536, 65536, 1 << 10, 1 << 6),   # 2^33 heads
+    (65536, 65536, 1 << 20, 1), (8192, None, 1 << 20, 1), (None, 8192, 1, 1 << 20),
+    (8191, 1, 1 << 10, 1 << 10)])
+@pytest.mark.parametrize("D,R", [(1, 0), (64, 64), (1024, 0)])
+def test_norm_rope_refuses_more_heads_than_a_grid_has_warps(lib, q, k, B, n, D, R):
+    hq, hk = (None if h is None else heads(heads=h) for h in (q, k))
+    assert norm_rope(lib, q=hq, qo=hq, k=hk, ko=hk, B=B, n=n, D=D, R=R) == UNS
+    assert b"heads" in lib.dllm_last_error()
