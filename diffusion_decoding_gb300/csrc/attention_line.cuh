@@ -29,10 +29,15 @@ struct AttnPlan {
   int32_t* status;
 };
 
-// log2 of the entries of a unit: at least `least`, and so many that no line reaches 2^31 units.
+// log2 of the entries of a unit: at least `least`, and so many that no line reaches 2^31 units (2^30 at
+// most, for up to 2^30 segments of up to 2^30 entries).
 inline int unit_log2_of(int64_t segments, int max_len, int least) {
   int lg = least;
-  while (segments * ((static_cast<int64_t>(max_len) >> lg) + 1) >= (int64_t{1} << 31)) ++lg;
+  auto units = [&] {
+    const int64_t n = (static_cast<int64_t>(max_len) + (int64_t{1} << lg) - 1) >> lg;
+    return segments * (n > 1 ? n : 1);
+  };
+  while (units() >= (int64_t{1} << 31)) ++lg;
   return lg;
 }
 
