@@ -484,8 +484,10 @@ def dllm_rope_phases(rotary_dim: int, phases: torch.Tensor, base: float = 10000.
                      original_len: float = 0.0, slow_turns: float = 1.0, fast_turns: float = 32.0,
                      stream=None) -> None:
     """Fill phases ([rotary_dim / 2] int64) with each pair's turns per position in 2^-64."""
-    if phases.dtype != torch.int64 or phases.numel() < rotary_dim // 2:
-        raise ValueError("phases must hold rotary_dim / 2 int64 words")
+    # as many words as pairs: dllm_qk_norm_rope rotates two channels for every word it is given
+    if phases.dtype is not torch.int64 or phases.numel() != rotary_dim // 2 \
+            or not phases.is_contiguous():
+        raise ValueError("phases must be rotary_dim / 2 int64 words, contiguous")
     r = dllm_rope(rotary_dim, scaling, base, factor, original_len, slow_turns, fast_turns)
     _check(lib().dllm_rope_phases(ctypes.byref(r), _ptr(phases), _stream(stream)),
            "dllm_rope_phases")
@@ -515,6 +517,8 @@ def dllm_qk_norm_rope(q, k, q_out, k_out, pos, phases, q_weight=None, k_weight=N
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype is not dtype or w.numel() != D or not w.is_contiguous()):
             raise ValueError("weights must be contiguous, [head_dim], of the tensors' dtype")
+    if phases is not None and (phases.dtype is not torch.int64 or not phases.is_contiguous()):
+        raise ValueError("phases must be a contiguous int64 table")
     hq = hqo = hk = hko = None
     if q is not None:
         hq = _rows(q, B, n, D)

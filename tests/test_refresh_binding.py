@@ -17,3 +17,14 @@ def test_norm_rope_refuses_more_heads_than_a_grid_has_warps(lib, q, k, B, n, D, 
     hq, hk = (None if h is None else heads(heads=h) for h in (q, k))
     assert norm_rope(lib, q=hq, qo=hq, k=hk, ko=hk, B=B, n=n, D=D, R=R) == UNS
     assert b"heads" in lib.dllm_last_error()
+
+
+def test_phase_tables_are_whole_and_of_their_type():
+    x, pos = torch.zeros(2, 3, 2, 64), torch.zeros(2, 3, dtype=torch.int32)
+    table = torch.zeros(64, dtype=torch.int64)
+    for bad in (table[:33], table[::2], table[:32].int(), table[:32].double()):  # 64 channels: 32 words
+        with pytest.raises(ValueError):
+            dd.dllm_rope_phases(64, bad)
+    for bad in (table[::2], table[:32].int(), table[:32].double(), table[:32].float()):
+        with pytest.raises(ValueError):
+            dd.dllm_qk_norm_rope(x, None, x, None, pos, bad)
