@@ -248,12 +248,20 @@ class BlockState:
         dllm_block_state_reset(self, stream=stream)
 
 
+def _kept(i: int) -> property:
+    """Array i of a cache: its descriptor holds the address, so no other tensor can be assigned."""
+    def put(self, t):
+        if t is not self._arrays[i]:
+            raise AttributeError("a cache keeps its arrays; Kv4Cache.of makes one over others")
+    return property(lambda self: self._arrays[i], put)
+
+
 class Kv4Cache:
     """Device arrays of a paged 4-bit key/value cache (format: include/dllm.h) and its page table.
 
     pages: pages in the pool; table: [B, pages per sequence] int32 page ids (a word outside
-    [0, pages) is an absent page).  The table may be changed between calls; codes and params need
-    no initial values."""
+    [0, pages) is an absent page).  The table's words may be changed between calls, and `table` may be
+    set to another tensor; codes and params need no initial values and stay the same tensors."""
 
     def __init__(self, pages: int, heads: int, page_size: int, head_dim: int, B: int,
                  pages_per_seq: int, device=None):
@@ -274,22 +282,32 @@ class Kv4Cache:
         for name, t, shape, es in (("k_codes", k_codes, k_codes.shape, 1),
                                    ("v_codes", v_codes, k_codes.shape, 1),
                                    ("k_params", k_params, (pages, heads, page_size, half // 16), 2),
-                                   ("v_params", v_params, (pages, heads, page_size, half // 16), 2),
-                                   ("table", table, (table.shape[0], table.shape[-1]), 4)):
+                                   ("v_params", v_params, (pages, heads, page_size, half // 16), 2)):
             if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.element_size() != es:
                 raise ValueError(f"{name} must be contiguous, {tuple(shape)}, {es} bytes a value")
         self._set(k_codes, k_params, v_codes, v_params, table)
         return self
 
     def _set(self, k_codes, k_params, v_codes, v_params, table) -> None:
-        self.k_codes, self.k_params = k_codes, k_params
-        self.v_codes, self.v_params = v_codes, v_params
-        self.table = table
+        self._arrays = (k_codes, k_params, v_codes, v_params)
         pages, heads, page_size, half = k_codes.shape
         self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
-        self._c = dllm_kv4_cache(_ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params),
-                                 _ptr(table), pages, heads, page_size, 2 * half, table.shape[1])
-        self.B, self.ref = table.shape[0], _byref(self._c)
+        self._c = dllm_kv4_cache(*map(_ptr, self._arrays), None, pages, heads, page_size, 2 * half, 0)
+        self.ref = _byref(self._c)
+        self.table = table
+
+    k_codes, k_params, v_codes, v_params = map(_kept, range(4))
+
+    @property
+    def table(self) -> torch.Tensor:
+        return self._table
+
+    @table.setter
+    def table(self, table: torch.Tensor) -> None:
+        if table.dtype is not torch.int32 or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be [B, pages of a sequence] int32, contiguous")
+        self._table, self.B = table, table.shape[0]
+        self._c.page_table, self._c.table_stride = _ptr(table), table.shape[1]
 
     def c(self) -> dllm_kv4_cache:
         return self._c

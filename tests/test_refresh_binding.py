@@ -28,3 +28,20 @@ def test_phase_tables_are_whole_and_of_their_type():
     for bad in (table[::2], table[:32].int(), table[:32].double(), table[:32].float()):
         with pytest.raises(ValueError):
             dd.dllm_qk_norm_rope(x, None, x, None, pos, bad)
+
+
+def test_a_cache_follows_the_table_it_is_given():
+    c = dd.Kv4Cache(4, 2, 16, 64, 2, 2, device="cpu")
+    other = torch.zeros(3, 5, dtype=torch.int32)
+    c.table = other
+    assert c.table is other and c.B == 3
+    assert c.c().page_table == other.data_ptr() and c.c().table_stride == 5
+    assert c.ref._obj.page_table == other.data_ptr()
+    for bad in (other.float(), other.long(), other[:, ::2], other[0], other.t()):
+        with pytest.raises(ValueError):
+            c.table = bad
+    assert c.table is other
+    for name in ("k_codes", "k_params", "v_codes", "v_params"):  # a cache over others is made by `of`
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name).clone())
+    c.k_codes += 1  # in place is no other tensor
