@@ -279,12 +279,13 @@ class Kv4Cache:
         """A cache over existing contiguous device tensors (shapes as the constructor makes)."""
         self = cls.__new__(cls)
         pages, heads, page_size, half = k_codes.shape
-        for name, t, shape, es in (("k_codes", k_codes, k_codes.shape, 1),
-                                   ("v_codes", v_codes, k_codes.shape, 1),
-                                   ("k_params", k_params, (pages, heads, page_size, half // 16), 2),
-                                   ("v_params", v_params, (pages, heads, page_size, half // 16), 2)):
-            if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.element_size() != es:
-                raise ValueError(f"{name} must be contiguous, {tuple(shape)}, {es} bytes a value")
+        codes, params = (torch.uint8,), (torch.int16, torch.uint16)
+        for name, t, shape, types in (
+                ("k_codes", k_codes, k_codes.shape, codes), ("v_codes", v_codes, k_codes.shape, codes),
+                ("k_params", k_params, (pages, heads, page_size, half // 16), params),
+                ("v_params", v_params, (pages, heads, page_size, half // 16), params)):
+            if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.dtype not in types:
+                raise ValueError(f"{name} must be contiguous, {tuple(shape)}, {types[0]}")
         self._set(k_codes, k_params, v_codes, v_params, table)
         return self
 

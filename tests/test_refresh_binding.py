@@ -45,3 +45,16 @@ def test_a_cache_follows_the_table_it_is_given():
         with pytest.raises(AttributeError):
             setattr(c, name, getattr(c, name).clone())
     c.k_codes += 1  # in place is no other tensor
+
+
+def test_a_cache_over_arrays_of_other_types_is_refused():
+    c = dd.Kv4Cache(4, 2, 16, 64, 2, 2, device="cpu")
+    arrays = dict(k_codes=c.k_codes, k_params=c.k_params, v_codes=c.v_codes, v_params=c.v_params,
+                  table=c.table)
+    dd.Kv4Cache.of(**arrays)
+    for name, dtype in (("k_codes", torch.bool), ("v_codes", torch.int8), ("k_params", torch.bfloat16),
+                        ("v_params", torch.float16), ("table", torch.float32)):
+        with pytest.raises(ValueError):
+            dd.Kv4Cache.of(**{**arrays, name: arrays[name].to(dtype)})
+    for name in ("k_params", "v_params"):  # the same words, unsigned
+        dd.Kv4Cache.of(**{**arrays, name: arrays[name].view(torch.uint16)})
