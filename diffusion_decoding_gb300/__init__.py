@@ -585,8 +585,8 @@ def dllm_attention_kv4_workspace_bytes(cache: Kv4Cache, B: int, n: int, q_heads:
 def dllm_attention_kv4(q, cache: Kv4Cache, lens, max_len: int, out, ws, lse=None, key_mask=None,
                        scale: float | None = None, causal: bool = False, stream=None) -> None:
     """q, out: [B, n, heads, head_dim] bf16; lens: [B] int32 (None: max_len everywhere); lse:
-    [B, heads, n] fp32 or None; key_mask: [B, >= max_len] uint8 or bool, 0 = hidden; scale: None
-    for head_dim ** -0.5."""
+    [B, heads, n] fp32 or None; key_mask: [B, >= max_len] uint8 or bool with contiguous rows (it may
+    be one row expanded to all sequences), 0 = hidden; scale: None for head_dim ** -0.5."""
     B, n, H, D = q.shape
     if D != cache.head_dim or B != cache.B:
         raise ValueError("q and out must be [B, n, heads, head_dim] of the cache")
@@ -599,7 +599,7 @@ def dllm_attention_kv4(q, cache: Kv4Cache, lens, max_len: int, out, ws, lse=None
     mask_stride = 0
     if key_mask is not None:
         if key_mask.element_size() != 1 or key_mask.dim() != 2 or key_mask.shape[0] != B \
-                or key_mask.shape[1] < max_len or key_mask.stride(1) != 1:
+                or key_mask.shape[1] < max_len or (key_mask.stride(1) != 1 and key_mask.shape[1] != 1):
             raise ValueError("key_mask must be [B, >= max_len] uint8 or bool with contiguous rows")
         mask_stride = key_mask.stride(0)
     status = lib().dllm_attention_kv4(

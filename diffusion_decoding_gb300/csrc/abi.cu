@@ -791,7 +791,7 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
   if (q->heads != out->heads)
     return fail(DLLM_ERR_INVALID_ARG, "q has %d heads, out %d", q->heads, out->heads);
   if (!std::isfinite(scale)) return fail(DLLM_ERR_INVALID_ARG, "scale is not finite");
-  if (key_mask && mask_stride < max_len)
+  if (key_mask && B > 1 && mask_stride != 0 && mask_stride < max_len)
     return fail(DLLM_ERR_INVALID_ARG, "mask_stride %lld < max_len %d",
                 static_cast<long long>(mask_stride), max_len);
   if (!aligned(lens, 4) || !aligned(lse, 4))

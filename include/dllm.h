@@ -502,7 +502,8 @@ dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, cons
  * token, a piece of a prompt).  Query head h reads key/value head h / (q->heads / cache->heads).
  * Query i of sequence b sees entry j when
  *   j < len_b = min(lens[b], max_len)  (lens NULL: max_len),  key_mask[b*mask_stride + j] != 0
- *   (key_mask NULL: all),  its page is present, and, with `causal`, j <= len_b - n + i;
+ *   (key_mask NULL: all; mask_stride >= max_len, or 0: one mask for all sequences),  its page is
+ *   present, and, with `causal`, j <= len_b - n + i;
  *   lse = ln sum_j exp(scale * q.K_j),  out = sum_j exp(scale * q.K_j - lse) V_j.
  * A query that sees nothing gets out = 0 and lse = -inf.  Entries that a query does not see have no
  * effect on it, whatever their codes, params and mask neighbours hold.  A score that is NaN makes
