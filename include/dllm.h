@@ -508,11 +508,11 @@ dllm_status dllm_kv4_read(const dllm_kv4_cache* cache, const dllm_heads* k, cons
  * A query that sees nothing gets out = 0 and lse = -inf.  Entries that a query does not see have no
  * effect on it, whatever their codes, params and mask neighbours hold.  A score that is NaN makes
  * out and lse of its query NaN, a group of V that reads as NaN its 32 channels of every query that
- * sees the entry.  Scores, the softmax statistics and
- * sums are fp32; the weights exp(.) are rounded to bf16 for their product with V, which is exact
- * bf16, and out is rounded once to bf16.  The order of all sums is fixed: repeated calls agree
- * bit for bit.
- * q, out: bf16, same heads (a multiple of cache->heads).  lse: [B, q->heads, n] fp32 or NULL.
+ * sees the entry.  Scores, the softmax statistics and sums are fp32; the weights exp(.) are rounded
+ * to bf16 for their product with V, which is exact bf16, and out is rounded once to bf16.  The order
+ * of all sums is fixed: repeated calls agree bit for bit.
+ * q, out: bf16, same heads (a multiple of cache->heads); they may be the same memory with the same
+ * strides, and must not overlap otherwise.  lse: [B, q->heads, n] fp32 or NULL.
  * head_dim 64, 128, 192 or 256; 0 <= max_len <= table_stride * page_size and 2^30; scale finite;
  * B*n <= 2^20, B*n*heads <= 2^30.
  * ws: dllm_attention_kv4_workspace_bytes(...) bytes (0 on invalid sizes); max_len is the bound the
