@@ -17,11 +17,13 @@
 // barrier), and page ids one tile further ahead.
 //
 // Measured: one token of each of 32 sequences of up to 8192 entries, 4 query heads to each of 8 cache
-// heads of 128 channels: 66.8 us, 3.4 TB/s of cache.  The rate is set by the integer work that turns
-// codes into values: about 450 instructions a warp and tile of 16 entries, 66 % of the issue slots and
-// 63 % of the integer pipe busy, at four warps a scheduler (123 registers; five CTAs an SM spill and
-// take 72.7 us; shifts done by the multiplier 69.5 to 76.5).  One sequence of 65536 entries: 21 us, of
-// which the join takes a third.
+// heads of 128 channels: 65.5 us, 3.5 TB/s of cache, 0.51 of the copy rate.  No unit is full: 66 % of the
+// issue slots and 63 % of the integer pipe are busy, and warps that could issue wait for one another
+// or for that pipe.  A warp issues 452 instructions for a tile of 16 entries.  Turning its codes takes
+// 192 of them (64 pairs a lane at a shift, a mask and a packed fma); the rest is the walk through the
+// pages, copies, loads from the ring, votes, scores and products, and is paid for every 16 entries.
+// Registers (121) allow four warps a scheduler; five CTAs an SM spill (72.7 us).  One sequence of
+// 65536 entries: 21 us, of which the join takes a third.
 #include "attention.h"
 
 #include <algorithm>

@@ -190,8 +190,9 @@ __device__ __forceinline__ void note_segment(const AttnPlan& f, const AttnParams
 // see.  Entries in tiles of `TILE` that not all rows see alike therefore count as 0 in the products where
 // their group of V is NaN; a CTA that met one runs this when it is done (all its threads, its stores made
 // visible to each other): the rows that do see such an entry get their NaN.  It stands at the end,
-// out of the way: the same look-up in a segment's own end cost every call 1 to 9 %, as it is single tokens
-// over a masked cache take 62.5 us (61.4 without), pieces of 256 channels 44.4 (43.7), others the same.
+// out of the way: the same look-up at the end of each segment cost every call 1 to 9 %.  Here causal
+// pieces of 256 channels take 44.4 us (43.8 without), of 192 41.4 (40.9), blocks of 32 tokens 18.5 (18.3),
+// other calls the same.
 template <int D, int ROWS, int TILE, bool kRowsTogether>
 __device__ __forceinline__ void put_nans(const AttnParams& p, const AttnPlan& f, Segment<ROWS> sg, int u0,
                                          int u1) {

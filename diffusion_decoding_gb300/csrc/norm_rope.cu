@@ -337,10 +337,13 @@ template <int DT, int GL>
 cudaError_t launch_vec(NormRopeParams& p, int sm_count, cudaStream_t stream) {
   constexpr int HPW = 32 / GL;
   // With at most half a warp's heads, tokens share a warp (9944 tokens of 1 + 1 heads of 80 channels:
-  // 5.6 us, 19.1 with a token a warp; 16384 of 2 + 1 heads of 128: 12.2, 29.2).  Otherwise as many sets of heads a warp (more loads on the way,
-  // sines and cosines used more often) as leave 12 warps an SM; a call with fewer tokens spreads each
-  // over more warps.  512 tokens of 32 + 8 heads take 3.9 us in 17 warps an SM of one set, 4.4 in 8 of
-  // two; 999 tokens of 7 + 7 heads of 80 fp32 channels 4.6 us in 13 warps of two, 5.4 in 26 of one.
+  // 5.6 us, 19.1 with a token a warp; 16384 of 2 + 1 heads of 128: 12.2, 29.2).  Otherwise as many sets of
+  // heads a warp (more loads on the way, sines and cosines used more often) as leave 12 warps an SM; a
+  // call with fewer tokens spreads each over more warps.  512 tokens of 32 + 8 heads take 3.9 us in 17
+  // warps an SM of one set, 4.4 in 8 of two; 999 tokens of 7 + 7 heads of 80 fp32 channels 4.6 us in 13
+  // warps of two, 5.4 in 26 of one.  Over 54 sizes of 128 to 4096 tokens the other thresholds come to
+  // (mean, best, worst, as parts of the time with 12): 6: 0.99, 0.84, 1.28; 8: 1.01, 0.93, 1.28;
+  // 16: 1.03, 0.84, 1.31; 24: 1.04, 0.79, 1.34.
   const int most = p.s[0].heads > p.s[1].heads ? p.s[0].heads : p.s[1].heads;
   p.pack_log2 = 0;
   while ((most << (p.pack_log2 + 1)) <= HPW) ++p.pack_log2;
