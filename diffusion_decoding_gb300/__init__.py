@@ -531,6 +531,8 @@ def dllm_qk_norm_rope(q, k, q_out, k_out, pos, phases, q_weight=None, k_weight=N
     k with its output may be None); pos: [B, >= n] int32, < 0: token skipped; phases: the
     dllm_rope_phases table, two channels per entry are rotated (None: no rotation)."""
     x = q if q is not None else k
+    if x is None:
+        raise ValueError("need q with q_out, or k with k_out, or both pairs")
     B, n, _, D = x.shape
     dtype = x.dtype
     for w in (q_weight, k_weight):

@@ -58,3 +58,8 @@ def test_a_cache_over_arrays_of_other_types_is_refused():
             dd.Kv4Cache.of(**{**arrays, name: arrays[name].to(dtype)})
     for name in ("k_params", "v_params"):  # the same words, unsigned
         dd.Kv4Cache.of(**{**arrays, name: arrays[name].view(torch.uint16)})
+
+
+def test_norm_rope_of_nothing_is_refused():
+    with pytest.raises(ValueError):
+        dd.dllm_qk_norm_rope(None, None, None, None, None, None)
