@@ -62,6 +62,10 @@ class dllm_rope(ctypes.Structure):
                 ("slow_turns", ctypes.c_double), ("fast_turns", ctypes.c_double)]
 
 
+class dllm_sampling(ctypes.Structure):
+    _fields_ = [("temperature", _c_f32), ("top_k", _c_i32), ("top_p", _c_f32), ("min_p", _c_f32)]
+
+
 class dllm_kv4_cache(ctypes.Structure):
     _fields_ = [("k_codes", _c_vp), ("k_params", _c_vp), ("v_codes", _c_vp), ("v_params", _c_vp),
                 ("page_table", _c_vp), ("pages", _c_i32), ("heads", _c_i32),
@@ -77,6 +81,8 @@ _SIGS = {
     "dllm_workspace_bytes": (_c_sz, [ctypes.POINTER(dllm_shape)]),
     "dllm_decode_stats": (_c_i32, [_c_vp, ctypes.POINTER(dllm_shape), _c_vp,
                                    ctypes.POINTER(dllm_stats), _c_vp, _c_vp]),
+    "dllm_sample": (_c_i32, [_c_vp, ctypes.POINTER(dllm_shape), _c_vp, _c_vp,
+                             ctypes.POINTER(dllm_sampling), ctypes.POINTER(dllm_stats), _c_vp]),
     "dllm_commit_threshold": (_c_i32, [_c_vp, ctypes.POINTER(dllm_shape),
                                        ctypes.POINTER(dllm_stats),
                                        ctypes.POINTER(dllm_block_state), _c_f32, _c_i32, _c_vp,
@@ -131,6 +137,13 @@ _SIGS = {
     "dllm_attention_kv4": (_c_i32, [_P_HEADS, _P_CACHE, _c_vp, _c_i32, _c_vp, _c_i64, _c_f32,
                                     _c_i32, _P_HEADS, _c_vp, _c_i32, _c_i32, _c_vp, _c_sz,
                                     _c_vp]),
+    "dllm_attention_kv4_weights_workspace_bytes": (_c_sz, [_P_CACHE, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "dllm_attention_kv4_weights": (_c_i32, [_P_HEADS, _P_CACHE, _c_vp, _c_i32, _c_vp, _c_i64, _c_f32,
+                                            _c_i32, _c_vp, _c_vp, _c_i64, _c_f32, _c_vp, _c_i64,
+                                            _c_i32, _c_i32, _c_vp, _c_sz, _c_vp]),
+    "dllm_kv4_evict_workspace_bytes": (_c_sz, [_P_CACHE, _c_i32, _c_i32]),
+    "dllm_kv4_evict": (_c_i32, [_P_CACHE, _c_vp, _c_i64, _c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp,
+                                _c_i64, _c_vp, _c_vp, _c_i64, _c_i32, _c_vp, _c_sz, _c_vp]),
     "dllm_get_status": (_c_i32, [_c_vp, _c_vp, ctypes.POINTER(_c_i32)]),
     "dllm_merge_shard_stats": (_c_i32, [ctypes.POINTER(dllm_shard_stats), _c_i32, _c_i64,
                                         ctypes.POINTER(dllm_stats), _c_vp]),
@@ -360,6 +373,23 @@ def dllm_decode_stats(logits, shape, masked, stats: StatsBuffers, ws, stream=Non
     _check(lib().dllm_decode_stats(_ptr(logits), ctypes.byref(shape), _ptr(masked),
                                    ctypes.byref(st), _ptr(ws), _stream(stream)),
            "dllm_decode_stats")
+
+
+def dllm_sample(logits, shape, masked, uniform, stats: StatsBuffers, temperature: float = 1.0,
+                top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0, stream=None) -> None:
+    """Draw a token per row (into stats.argmax, its model probability into stats.conf); uniform:
+    [B*L] fp32 numbers in [0, 1); masked: [B*L] uint8 or None; filters: see include/dllm.h."""
+    rows = shape.B * shape.L
+    if uniform.dtype is not torch.float32 or uniform.numel() != rows or not uniform.is_contiguous():
+        raise ValueError("uniform must be [B*L] float32, contiguous")
+    if masked is not None and (masked.element_size() != 1 or masked.numel() != rows
+                               or not masked.is_contiguous()):
+        raise ValueError("masked must be [B*L] uint8, contiguous")
+    how, st = dllm_sampling(temperature, top_k, top_p, min_p), stats.c()
+    status = lib().dllm_sample(_ptr(logits), _byref(shape), _ptr(masked), _ptr(uniform), _byref(how),
+                               _byref(st), _stream(stream))
+    if status:
+        _check(status, "dllm_sample")
 
 
 def dllm_commit_threshold(logits, shape, stats: StatsBuffers, state: BlockState, tau: float,
@@ -610,6 +640,76 @@ def dllm_attention_kv4(q, cache: Kv4Cache, lens, max_len: int, out, ws, lse=None
         _ptr(ws), ws.numel(), _stream(stream))
     if status:
         _check(status, "dllm_attention_kv4")
+
+
+def _word_rows(t, name: str, B: int, max_len: int, dtype=torch.float32) -> int:
+    """Stride of the rows of a [B, >= max_len] tensor of 32-bit words (0: none)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != B or t.shape[1] < max_len \
+            or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be [B, >= max_len] {dtype} with contiguous rows")
+    return t.stride(0)
+
+
+def _lens(lens, name: str, B: int):
+    if lens is not None and (lens.dtype is not torch.int32 or lens.numel() != B
+                             or not lens.is_contiguous()):
+        raise ValueError(f"{name} must be [B] int32, contiguous")
+    return _ptr(lens)
+
+
+def dllm_attention_kv4_weights_workspace_bytes(cache: Kv4Cache, B: int, n: int, q_heads: int,
+                                               max_len: int) -> int:
+    return int(lib().dllm_attention_kv4_weights_workspace_bytes(cache.ref, B, n, q_heads, max_len))
+
+
+def dllm_attention_kv4_weights(q, cache: Kv4Cache, lens, max_len: int, lse, weights, ws, prior=None,
+                               keep: float = 1.0, key_mask=None, scale: float | None = None,
+                               causal: bool = False, stream=None) -> None:
+    """weights[b, j] = keep * prior[b, j] + the attention that entry j receives from all queries and
+    heads; q, lens, max_len, key_mask, scale, causal as given to dllm_attention_kv4, lse ([B, heads, n])
+    as it wrote it; weights, prior: [B, >= max_len] fp32 (prior may be weights, or None)."""
+    B, n, H, D = q.shape
+    if D != cache.head_dim or B != cache.B:
+        raise ValueError("q must be [B, n, heads, head_dim] of the cache")
+    if lse.dtype is not torch.float32 or lse.shape != (B, H, n) or not lse.is_contiguous():
+        raise ValueError("lse must be [B, heads, n] float32, contiguous")
+    mask_stride = 0
+    if key_mask is not None:
+        if key_mask.element_size() != 1 or key_mask.dim() != 2 or key_mask.shape[0] != B \
+                or key_mask.shape[1] < max_len or (key_mask.stride(1) != 1 and key_mask.shape[1] != 1):
+            raise ValueError("key_mask must be [B, >= max_len] uint8 or bool with contiguous rows")
+        mask_stride = key_mask.stride(0)
+    status = lib().dllm_attention_kv4_weights(
+        _rows(q, B, n, D), cache.ref, _lens(lens, "lens", B), max_len, _ptr(key_mask), mask_stride,
+        D ** -0.5 if scale is None else scale, causal, _ptr(lse), _ptr(prior),
+        _word_rows(prior, "prior", B, max_len), keep, _ptr(weights),
+        _word_rows(weights, "weights", B, max_len), B, n, _ptr(ws), ws.numel(), _stream(stream))
+    if status:
+        _check(status, "dllm_attention_kv4_weights")
+
+
+def dllm_kv4_evict_workspace_bytes(cache: Kv4Cache, B: int, max_len: int) -> int:
+    return int(lib().dllm_kv4_evict_workspace_bytes(cache.ref, B, max_len))
+
+
+def dllm_kv4_evict(cache: Kv4Cache, weights, lens, max_len: int, budget: int, slots, lens_out, ws,
+                   first: int = 0, last: int = 0, weights_out=None, stream=None) -> None:
+    """Cut every sequence to its `budget` entries of largest weight ([B, >= max_len] fp32; the first
+    `first` and last `last` always stay).  slots ([B, >= max_len] int32): where each entry is now, -1
+    if dropped; lens_out ([B] int32; may be lens): the new lengths; weights_out (may be weights): the
+    weights in the new order."""
+    B = cache.B
+    if weights is None or slots is None or lens_out is None:
+        raise ValueError("weights, slots and lens_out are needed")
+    status = lib().dllm_kv4_evict(
+        cache.ref, _ptr(weights), _word_rows(weights, "weights", B, max_len), _lens(lens, "lens", B),
+        max_len, budget, first, last, _ptr(slots), _word_rows(slots, "slots", B, max_len, torch.int32),
+        _lens(lens_out, "lens_out", B), _ptr(weights_out),
+        _word_rows(weights_out, "weights_out", B, max_len), B, _ptr(ws), ws.numel(), _stream(stream))
+    if status:
+        _check(status, "dllm_kv4_evict")
 
 
 def dllm_capture_condition(default_value: int = 0, stream=None) -> int:

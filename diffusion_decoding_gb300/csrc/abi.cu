@@ -224,6 +224,59 @@ dllm_status check_attention(const dllm_kv4_cache* cache, int32_t B, int32_t n, i
   return DLLM_OK;
 }
 
+// What a call says of its queries and what they see, checked before.
+dllm::AttnParams attention_params(const dllm_heads* q, const dllm_kv4_cache* cache, const int32_t* lens,
+                                  int32_t max_len, const uint8_t* key_mask, int64_t mask_stride,
+                                  float scale, int32_t causal, int32_t B, int32_t n) {
+  dllm::AttnParams p{};
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.qb = q->batch_stride, p.qt = q->token_stride, p.qh = q->head_stride;
+  p.k_codes = cache->k_codes, p.k_params = cache->k_params;
+  p.v_codes = cache->v_codes, p.v_params = cache->v_params;
+  p.table = cache->page_table;
+  p.table_stride = cache->table_stride;
+  p.pages = cache->pages;
+  p.page_size = cache->page_size;
+  p.heads = cache->heads;
+  p.G = q->heads / cache->heads;
+  p.g_magic = p.G > 1 && static_cast<int64_t>(n) * p.G * p.G < (int64_t{1} << 32)
+                  ? static_cast<uint32_t>((uint64_t{1} << 32) / p.G + 1)
+                  : 0u;
+  p.lens = lens;
+  p.max_len = max_len;
+  p.key_mask = key_mask;
+  p.mask_stride = mask_stride;
+  p.scale_log2 = scale * dllm::kLog2e;
+  p.causal = causal != 0;
+  p.B = B;
+  p.n = n;
+  return p;
+}
+
+// A matrix of words, one row a sequence.
+dllm_status check_rows(const void* x, int64_t stride, int32_t B, int32_t max_len, const char* what) {
+  if (!aligned(x, 4)) return fail(DLLM_ERR_INVALID_ARG, "%s must be 4-byte aligned", what);
+  if (x && B > 1 && stride < max_len)
+    return fail(DLLM_ERR_INVALID_ARG, "%s: stride %lld < max_len %d", what,
+                static_cast<long long>(stride), max_len);
+  return DLLM_OK;
+}
+
+dllm_status check_entries(int32_t B, int32_t max_len) {
+  if (static_cast<int64_t>(B) * max_len > (int64_t{1} << 36))
+    return fail(DLLM_ERR_UNSUPPORTED, "B * max_len exceeds 2^36");
+  return DLLM_OK;
+}
+
+dllm_status check_evict(const dllm_kv4_cache* cache, int32_t B, int32_t max_len) {
+  DLLM_TRY(check_cache(cache));
+  DLLM_TRY(check_tokens(B, 1));
+  if (max_len < 0 || max_len > static_cast<int64_t>(cache->table_stride) * cache->page_size)
+    return fail(DLLM_ERR_INVALID_ARG, "max_len=%d outside [0, table_stride * page_size]", max_len);
+  if (max_len > (1 << 30)) return fail(DLLM_ERR_UNSUPPORTED, "max_len=%d exceeds 2^30", max_len);
+  return check_entries(B, max_len);
+}
+
 }  // namespace
 
 namespace dllm {
@@ -258,6 +311,31 @@ dllm_status dllm_decode_stats(const void* logits, const dllm_shape* shape, const
   cudaError_t e = dllm::launch_stats_commit(logits, *shape, masked, *out, nullptr, ca, w,
                                             sm_count(), reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dllm_decode_stats");
+  return ok();
+}
+
+dllm_status dllm_sample(const void* logits, const dllm_shape* shape, const uint8_t* masked,
+                        const float* uniform, const dllm_sampling* how, const dllm_stats* out,
+                        dllm_stream_t stream) {
+  CallRange range_("dllm_sample");
+  if (!logits) return fail(DLLM_ERR_INVALID_ARG, "logits is null");
+  DLLM_TRY(check_shape(shape));
+  DLLM_TRY(check_logits(logits, shape));
+  DLLM_TRY(check_stats(out));
+  if (!how || !uniform) return fail(DLLM_ERR_INVALID_ARG, "how and uniform must not be null");
+  if (!aligned(uniform, 4)) return fail(DLLM_ERR_INVALID_ARG, "uniform must be 4-byte aligned");
+  if (shape->V > (1 << 20)) return fail(DLLM_ERR_UNSUPPORTED, "V=%d exceeds 2^20", shape->V);
+  const float t = how->temperature;
+  if (t != 0.f && !(t >= 0x1p-10f && t <= 0x1p10f))
+    return fail(DLLM_ERR_INVALID_ARG, "temperature %g is neither 0 nor in [2^-10, 2^10]", t);
+  if (how->top_k < 0) return fail(DLLM_ERR_INVALID_ARG, "top_k=%d is negative", how->top_k);
+  if (!(how->top_p > 0.f && how->top_p <= 1.f))
+    return fail(DLLM_ERR_INVALID_ARG, "top_p %g is not in (0, 1]", how->top_p);
+  if (!(how->min_p >= 0.f && how->min_p <= 1.f))
+    return fail(DLLM_ERR_INVALID_ARG, "min_p %g is not in [0, 1]", how->min_p);
+  cudaError_t e = dllm::launch_sample(logits, *shape, masked, uniform, *how, *out, sm_count(),
+                                      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_sample");
   return ok();
 }
 
@@ -801,34 +879,103 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
   if (ws_bytes < need)
     return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed",
                 ws_bytes, need);
-  dllm::AttnParams p{};
-  p.q = static_cast<const uint16_t*>(q->data);
-  p.qb = q->batch_stride, p.qt = q->token_stride, p.qh = q->head_stride;
+  dllm::AttnParams p = attention_params(q, cache, lens, max_len, key_mask, mask_stride, scale, causal, B, n);
   p.out = static_cast<uint16_t*>(out->data);
   p.ob = out->batch_stride, p.ot = out->token_stride, p.oh = out->head_stride;
   p.lse = lse;
-  p.k_codes = cache->k_codes, p.k_params = cache->k_params;
-  p.v_codes = cache->v_codes, p.v_params = cache->v_params;
-  p.table = cache->page_table;
-  p.table_stride = cache->table_stride;
-  p.pages = cache->pages;
-  p.page_size = cache->page_size;
-  p.heads = cache->heads;
-  p.G = q->heads / cache->heads;
-  p.g_magic = p.G > 1 && static_cast<int64_t>(n) * p.G * p.G < (int64_t{1} << 32)
-                  ? static_cast<uint32_t>((uint64_t{1} << 32) / p.G + 1)
-                  : 0u;
-  p.lens = lens;
-  p.max_len = max_len;
-  p.key_mask = key_mask;
-  p.mask_stride = mask_stride;
-  p.scale_log2 = scale * dllm::kLog2e;
-  p.causal = causal != 0;
-  p.B = B;
-  p.n = n;
   cudaError_t e = dllm::launch_attention(p, cache->head_dim, ws, sm_count(),
                                          reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dllm_attention_kv4");
+  return ok();
+}
+
+size_t dllm_attention_kv4_weights_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t n,
+                                                  int32_t q_heads, int32_t max_len) {
+  if (check_attention(cache, B, n, q_heads, max_len) != DLLM_OK || check_entries(B, max_len) != DLLM_OK)
+    return 0;
+  return dllm::attention_weights_ws_bytes(B, n, q_heads / cache->heads, cache->heads, cache->head_dim,
+                                          max_len, sm_count());
+}
+
+dllm_status dllm_attention_kv4_weights(const dllm_heads* q, const dllm_kv4_cache* cache,
+                                       const int32_t* lens, int32_t max_len,
+                                       const uint8_t* key_mask, int64_t mask_stride, float scale,
+                                       int32_t causal, const float* lse, const float* prior,
+                                       int64_t prior_stride, float keep, float* weights,
+                                       int64_t weights_stride, int32_t B, int32_t n, void* ws,
+                                       size_t ws_bytes, dllm_stream_t stream) {
+  CallRange range_("dllm_attention_kv4_weights");
+  DLLM_TRY(check_heads(q, "q"));
+  DLLM_TRY(check_attention(cache, B, n, q->heads, max_len));
+  DLLM_TRY(check_entries(B, max_len));
+  DLLM_TRY(check_ws(ws));
+  if (q->dtype != DLLM_BF16) return fail(DLLM_ERR_UNSUPPORTED, "q must be bf16");
+  if (!lse || !weights) return fail(DLLM_ERR_INVALID_ARG, "lse and weights must not be null");
+  if (!std::isfinite(scale)) return fail(DLLM_ERR_INVALID_ARG, "scale is not finite");
+  if (prior && !std::isfinite(keep)) return fail(DLLM_ERR_INVALID_ARG, "keep is not finite");
+  if (key_mask && B > 1 && mask_stride != 0 && mask_stride < max_len)
+    return fail(DLLM_ERR_INVALID_ARG, "mask_stride %lld < max_len %d",
+                static_cast<long long>(mask_stride), max_len);
+  if (!aligned(lens, 4) || !aligned(lse, 4))
+    return fail(DLLM_ERR_INVALID_ARG, "lens and lse must be 4-byte aligned");
+  DLLM_TRY(check_rows(weights, weights_stride, B, max_len, "weights"));
+  DLLM_TRY(check_rows(prior, prior_stride, B, max_len, "prior"));
+  if (prior == weights && prior_stride != weights_stride && B > 1)
+    return fail(DLLM_ERR_INVALID_ARG, "prior and weights are one memory with two strides");
+  const size_t need = dllm::attention_weights_ws_bytes(B, n, q->heads / cache->heads, cache->heads,
+                                                       cache->head_dim, max_len, sm_count());
+  if (ws_bytes < need)
+    return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
+                need);
+  const dllm::AttnParams p =
+      attention_params(q, cache, lens, max_len, key_mask, mask_stride, scale, causal, B, n);
+  dllm::AttnWeights x{};
+  x.lse = lse;
+  x.prior = prior;
+  x.prior_stride = prior_stride;
+  x.out = weights;
+  x.out_stride = weights_stride;
+  x.keep = keep;
+  cudaError_t e = dllm::launch_attention_weights(p, x, cache->head_dim, ws, sm_count(),
+                                                 reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_attention_kv4_weights");
+  return ok();
+}
+
+size_t dllm_kv4_evict_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t max_len) {
+  return check_evict(cache, B, max_len) == DLLM_OK ? dllm::kv4_evict_ws_bytes(B, max_len) : 0;
+}
+
+dllm_status dllm_kv4_evict(const dllm_kv4_cache* cache, const float* weights, int64_t weights_stride,
+                           const int32_t* lens, int32_t max_len, int32_t budget, int32_t first,
+                           int32_t last, int32_t* slots, int64_t slots_stride, int32_t* lens_out,
+                           float* weights_out, int64_t weights_out_stride, int32_t B, void* ws,
+                           size_t ws_bytes, dllm_stream_t stream) {
+  CallRange range_("dllm_kv4_evict");
+  DLLM_TRY(check_evict(cache, B, max_len));
+  DLLM_TRY(check_ws(ws));
+  if (!weights || !slots || !lens_out)
+    return fail(DLLM_ERR_INVALID_ARG, "weights, slots and lens_out must not be null");
+  if (budget < 0 || first < 0 || last < 0 || static_cast<int64_t>(first) + last > budget)
+    return fail(DLLM_ERR_INVALID_ARG,
+                "need budget, first, last >= 0 and first + last <= budget (%d, %d, %d)", budget, first,
+                last);
+  if (!aligned(lens, 4) || !aligned(lens_out, 4))
+    return fail(DLLM_ERR_INVALID_ARG, "lens and lens_out must be 4-byte aligned");
+  DLLM_TRY(check_rows(weights, weights_stride, B, max_len, "weights"));
+  DLLM_TRY(check_rows(slots, slots_stride, B, max_len, "slots"));
+  DLLM_TRY(check_rows(weights_out, weights_out_stride, B, max_len, "weights_out"));
+  if (weights_out == weights && weights_out_stride != weights_stride && B > 1)
+    return fail(DLLM_ERR_INVALID_ARG, "weights and weights_out are one memory with two strides");
+  const size_t need = dllm::kv4_evict_ws_bytes(B, max_len);
+  if (ws_bytes < need)
+    return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
+                need);
+  cudaError_t e = dllm::launch_kv4_evict(*cache, weights, weights_stride, lens, max_len, budget, first,
+                                         last, slots, slots_stride, lens_out, weights_out,
+                                         weights_out_stride, B, ws, sm_count(),
+                                         reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dllm_kv4_evict");
   return ok();
 }
 

@@ -42,6 +42,22 @@ size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream);
 
+// Accumulated weights (attention_weights.cu): the call's queries, cache and masks are an AttnParams
+// (out and lse unused).
+struct AttnWeights {
+  const float* lse;    // [B, heads * G, n]
+  const float* prior;  // null: 0
+  int64_t prior_stride;
+  float* out;
+  int64_t out_stride;
+  float keep;
+  int ctas_per_seq;
+  int q_aligned;
+};
+size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
+cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, void* ws, int sm_count,
+                                     cudaStream_t stream);
+
 // Rows of a bf16 tensor (strides in elements) all start on 16-byte boundaries.
 bool attention_rows_aligned(const void* x, int64_t sb, int64_t st, int64_t sh);
 

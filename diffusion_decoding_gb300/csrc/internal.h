@@ -151,6 +151,19 @@ cudaError_t launch_kv4_read(const dllm_kv4_cache& cache, const dllm_heads& k, co
                             int B, int n, const int32_t* pos, int64_t pos_stride, int sm_count,
                             cudaStream_t stream);
 
+// Sampling: a token per row from its filtered softmax.
+cudaError_t launch_sample(const void* logits, const dllm_shape& sh, const uint8_t* masked,
+                          const float* uniform, const dllm_sampling& how, const dllm_stats& out,
+                          int sm_count, cudaStream_t stream);
+
+// Eviction from the 4-bit cache (accumulated weights: attention.h).
+size_t kv4_evict_ws_bytes(int B, int max_len);
+cudaError_t launch_kv4_evict(const dllm_kv4_cache& cache, const float* weights, int64_t weights_stride,
+                             const int32_t* lens, int max_len, int budget, int first, int last,
+                             int32_t* slots, int64_t slots_stride, int32_t* lens_out,
+                             float* weights_out, int64_t weights_out_stride, int B, void* ws,
+                             int sm_count, cudaStream_t stream);
+
 // Record a message for dllm_last_error() on this thread (with a CUDA error string if e != 0).
 void set_last_error(const char* msg, cudaError_t e);
 

@@ -135,6 +135,38 @@ dllm_status dllm_decode_stats(const void* logits, const dllm_shape* shape, const
                               const dllm_stats* out, void* ws, dllm_stream_t stream);
 
 /*
+ * Sampling (dInfer explainer, decoding strategies: a strategy takes each position's token and the
+ * model's confidence in it): one token per row, drawn from the row's filtered softmax with a given
+ * uniform number, in place of the most probable one.  For a computed row z of maximum m:
+ *   candidates are ordered by falling z, lower ids first among equals, with weight
+ *   w_v = exp((z_v - m) / temperature); each filter keeps a prefix of that order:
+ *     top_k:  the first top_k (0, or V and more: all);
+ *     top_p:  the shortest prefix that weighs at least top_p of what top_k keeps (1: all);
+ *     min_p:  those with w_v >= min_p, that is z_v >= m + temperature * ln(min_p) (0: all);
+ *   of the shortest of these prefixes the token is the lowest id at which the sum of the kept
+ *   weights by rising id exceeds uniform[r] times their sum;
+ *   row_max and lse as dllm_decode_stats;  argmax = the token;  conf = exp(z_token - lse), its
+ *   probability under the model itself (no temperature, no filter).
+ * The commit calls take these statistics with logits = NULL and so commit sampled tokens.
+ * temperature 0 takes the most probable token (lowest id on ties), whatever the other fields.
+ * Sums of weights are exact to 2^-36 of their terms, and weights below 2^-43 count as 0; the token
+ * does not depend on how the work was split.  Rows with masked[r] = 0 are not read and get -inf,
+ * -inf, 0, -1; so does a row without a finite logit, its lse and row_max being what they are.
+ * masked: [B*L] uint8 or NULL (every row).  uniform: [B*L] fp32 in [0, 1) (others count as the
+ * nearest in range, a NaN as 0).  temperature 0 or in [2^-10, 2^10]; top_k >= 0; 0 < top_p <= 1;
+ * 0 <= min_p <= 1; V <= 2^20.  Logits are finite or -inf.  No workspace.
+ */
+typedef struct {
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+} dllm_sampling;
+dllm_status dllm_sample(const void* logits, const dllm_shape* shape, const uint8_t* masked,
+                        const float* uniform, const dllm_sampling* how, const dllm_stats* out,
+                        dllm_stream_t stream);
+
+/*
  * Threshold decoding (dInfer explainer, decoding strategies, method 1: fix a position at once
  * when the model is confident in it).  Per sequence that is not stopped:
  *   C = { masked i : conf_i > tau };  if C is empty, C = { the masked i of largest conf,
@@ -525,6 +557,59 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
                                int64_t mask_stride, float scale, int32_t causal,
                                const dllm_heads* out, float* lse, int32_t B, int32_t n, void* ws,
                                size_t ws_bytes, dllm_stream_t stream);
+
+/*
+ * How much attention each cache entry receives from the queries of one dllm_attention_kv4 call, added
+ * to what earlier calls left (dInfer explainer, KV-cache manager: which entries a cache keeps).  For
+ * j < len_b:
+ *   weights[b, j] = keep * prior[b, j] + sum over queries i and heads h that see j of
+ *                   exp(scale * q_ih.K_j - lse_ih)
+ * with the visibility, q, cache, lens, key_mask, scale and causal of that call and the lse it wrote.
+ * weights and prior: fp32, row b from b * their stride on (strides >= max_len); they may be the same
+ * memory with the same stride, and must not overlap otherwise; prior NULL: nothing is added, and keep
+ * is not used.  Words of weights from len_b on are left as they are.  A query whose lse is -inf saw
+ * nothing and adds nothing; a score that is NaN makes the weight of its entry NaN, a NaN of lse those
+ * of all entries its query sees.  All in fp32, in a fixed order: repeated calls agree bit for bit.
+ * Limits as dllm_attention_kv4, and B * max_len <= 2^36.
+ * ws: dllm_attention_kv4_weights_workspace_bytes(...) bytes (0 on invalid sizes).
+ */
+size_t dllm_attention_kv4_weights_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t n,
+                                                  int32_t q_heads, int32_t max_len);
+dllm_status dllm_attention_kv4_weights(const dllm_heads* q, const dllm_kv4_cache* cache,
+                                       const int32_t* lens, int32_t max_len,
+                                       const uint8_t* key_mask, int64_t mask_stride, float scale,
+                                       int32_t causal, const float* lse, const float* prior,
+                                       int64_t prior_stride, float keep, float* weights,
+                                       int64_t weights_stride, int32_t B, int32_t n, void* ws,
+                                       size_t ws_bytes, dllm_stream_t stream);
+
+/*
+ * Eviction (dInfer explainer, KV-cache manager): cut every sequence to at most `budget` entries, by
+ * the weights that dllm_attention_kv4_weights adds up.  With len_b = min(lens[b], max_len) (lens NULL:
+ * max_len) and new_b = min(len_b, budget), a sequence of more than `budget` entries keeps its first
+ * `first` and last `last` entries and, of the others, those of largest weight (lower entries first
+ * among equals; a NaN is less than every number), new_b in all.  Kept entries before new_b stay where
+ * they are; the k-th kept entry from new_b on moves to the place of the k-th dropped entry before
+ * new_b, codes and params of all heads.  Attention does not depend on the order of entries: keys hold
+ * their rotation.  (A `causal` call does: it takes the last n entries for its queries'.  Write those
+ * after an eviction.)
+ *   slots[b*slots_stride + j], j < max_len: where entry j is now, -1 if it was dropped or j >= len_b
+ *     (a list of positions goes through it before dllm_kv4_write);
+ *   lens_out[b] = new_b; it may be lens;
+ *   weights_out (or NULL), j < max_len: the weights in the entries' new order, 0 from new_b on; it may
+ *     be weights with the same stride, and must not overlap it otherwise.
+ * Entries from new_b on and pages are left as they are; pages wholly behind new_b may be reused.  The
+ * pages of a sequence's first len_b entries must be its own; a move from or to an absent page is not
+ * made.  budget, first, last >= 0, first + last <= budget; 0 <= max_len <= table_stride * page_size
+ * and 2^30; B >= 1, B <= 2^20, B * max_len <= 2^36; strides >= max_len.
+ * ws: dllm_kv4_evict_workspace_bytes(cache, B, max_len) bytes (0 on invalid sizes).
+ */
+size_t dllm_kv4_evict_workspace_bytes(const dllm_kv4_cache* cache, int32_t B, int32_t max_len);
+dllm_status dllm_kv4_evict(const dllm_kv4_cache* cache, const float* weights, int64_t weights_stride,
+                           const int32_t* lens, int32_t max_len, int32_t budget, int32_t first,
+                           int32_t last, int32_t* slots, int64_t slots_stride, int32_t* lens_out,
+                           float* weights_out, int64_t weights_out_stride, int32_t B, void* ws,
+                           size_t ws_bytes, dllm_stream_t stream);
 
 /*
  * Self-test of failure detection (no counterpart in the pages): runs the bounded wait the
