@@ -45,7 +45,7 @@ __device__ const float2 kPow2Table[32] = {
 // How far z lies below m, in octaves of weight (to 32 bits; monotone in z).  NaN for a NaN.
 __device__ __forceinline__ float octaves_below(float z, float m, InvTemp t) { return (m - z) * t.hi; }
 
-// The weight of z; 0 where it is below half a unit, and for a NaN.  `table`: kPow2Table, in shared
+// The weight of z; 0 where it is below a unit, and for a NaN.  `table`: kPow2Table, in shared
 // memory.
 __device__ __forceinline__ uint64_t weight_fixed(float z, float m, InvTemp t, const float2* table) {
   const float dh = z - m;                      // z - m = dh + dl
@@ -53,7 +53,7 @@ __device__ __forceinline__ uint64_t weight_fixed(float z, float m, InvTemp t, co
   const float dl = (z - back) + ((back - dh) - m);
   const float yh = dh * t.hi;                  // (z - m) log2(e) / T = yh + yl
   const float yl = fmaf(dh, t.hi, -yh) + fmaf(dh, t.lo, dl * t.hi);
-  if (!(yh > -(kWeightBits + 1.f))) return 0;
+  if (!(yh > -static_cast<float>(kWeightBits))) return 0;
   const int n = __float2int_rn(yh * 32.f);     // yh = n / 32 + g
   const float g = fmaf(static_cast<float>(n), -0.03125f, yh);
   const float2 p = table[n & 31];
@@ -70,7 +70,7 @@ __device__ __forceinline__ uint64_t weight_fixed(float z, float m, InvTemp t, co
   // hi is a multiple of 2^-24 in (0.98, 2.02)
   const int64_t whole = static_cast<int64_t>(static_cast<int>(hi * 0x1p24f)) * (int64_t{1} << (kWeightBits - 24)) +
                         __float2int_rn(lo * static_cast<float>(int64_t{1} << kWeightBits));
-  const int down = -(n >> 5);                  // 0 .. 43
+  const int down = -(n >> 5);                  // 0 .. 42
   return static_cast<uint64_t>(down > 0 ? (whole + (int64_t{1} << (down - 1))) >> down : whole);
 }
 
