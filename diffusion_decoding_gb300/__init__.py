@@ -81,8 +81,7 @@ _SIGS = {
     "dllm_workspace_bytes": (_c_sz, [ctypes.POINTER(dllm_shape)]),
     "dllm_decode_stats": (_c_i32, [_c_vp, ctypes.POINTER(dllm_shape), _c_vp,
                                    ctypes.POINTER(dllm_stats), _c_vp, _c_vp]),
-    "dllm_sample": (_c_i32, [_c_vp, ctypes.POINTER(dllm_shape), _c_vp, _c_vp,
-                             ctypes.POINTER(dllm_sampling), ctypes.POINTER(dllm_stats), _c_vp]),
+    "dllm_sample": (_c_i32, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "dllm_commit_threshold": (_c_i32, [_c_vp, ctypes.POINTER(dllm_shape),
                                        ctypes.POINTER(dllm_stats),
                                        ctypes.POINTER(dllm_block_state), _c_f32, _c_i32, _c_vp,
@@ -330,6 +329,9 @@ class Kv4Cache:
 _DTYPES = {torch.float32: DLLM_F32, torch.bfloat16: DLLM_BF16}
 _pack_heads = struct.Struct("Pii3q").pack  # dllm_heads
 assert struct.calcsize("Pii3q") == ctypes.sizeof(dllm_heads)
+_pack_stats = struct.Struct("4P").pack  # dllm_stats
+_pack_sampling = struct.Struct("fi2f").pack  # dllm_sampling
+assert struct.calcsize("fi2f") == ctypes.sizeof(dllm_sampling)
 
 
 def heads_of(t: torch.Tensor) -> dllm_heads:
@@ -379,15 +381,17 @@ def dllm_sample(logits, shape, masked, uniform, stats: StatsBuffers, temperature
                 top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0, stream=None) -> None:
     """Draw a token per row (into stats.argmax, its model probability into stats.conf); uniform:
     [B*L] fp32 numbers in [0, 1); masked: [B*L] uint8 or None; filters: see include/dllm.h."""
-    rows = shape.B * shape.L
+    rows, open_ = shape.B * shape.L, None
     if uniform.dtype is not torch.float32 or uniform.numel() != rows or not uniform.is_contiguous():
         raise ValueError("uniform must be [B*L] float32, contiguous")
-    if masked is not None and (masked.element_size() != 1 or masked.numel() != rows
-                               or not masked.is_contiguous()):
-        raise ValueError("masked must be [B*L] uint8, contiguous")
-    how, st = dllm_sampling(temperature, top_k, top_p, min_p), stats.c()
-    status = lib().dllm_sample(_ptr(logits), _byref(shape), _ptr(masked), _ptr(uniform), _byref(how),
-                               _byref(st), _stream(stream))
+    if masked is not None:
+        if masked.element_size() != 1 or masked.numel() != rows or not masked.is_contiguous():
+            raise ValueError("masked must be [B*L] uint8, contiguous")
+        open_ = masked.data_ptr()
+    out = _pack_stats(stats.row_max.data_ptr(), stats.lse.data_ptr(), stats.conf.data_ptr(),
+                      stats.argmax.data_ptr())
+    status = lib().dllm_sample(_ptr(logits), _byref(shape), open_, uniform.data_ptr(),
+                               _pack_sampling(temperature, top_k, top_p, min_p), out, _stream(stream))
     if status:
         _check(status, "dllm_sample")
 
