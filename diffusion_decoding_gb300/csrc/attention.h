@@ -51,12 +51,18 @@ struct AttnWeights {
   float* out;
   int64_t out_stride;
   float keep;
-  int ctas_per_seq;
   int q_aligned;
+  int ctas_per_seq, split_log2, heads_at_once;  // few rows: attention_weights.cu
 };
 size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
 cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, void* ws, int sm_count,
                                      cudaStream_t stream);
+
+// Many rows per cache head (attention_weights_tc.cu).
+bool weights_tc_takes(int B, int n, int G, int heads, int max_len);
+size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
+cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,
+                              cudaStream_t stream);
 
 // Rows of a bf16 tensor (strides in elements) all start on 16-byte boundaries.
 bool attention_rows_aligned(const void* x, int64_t sb, int64_t st, int64_t sh);

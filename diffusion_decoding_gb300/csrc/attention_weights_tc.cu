@@ -1,0 +1,512 @@
+// How much attention each cache entry receives (attention_weights.cu), for many query rows per cache
+// head, on the 5th-generation tensor cores.
+//
+// S^T [128 entries x 64 rows] = K Q^T with the entries as the rows of the product: an entry's scores
+// then lie in one lane of tensor memory, and its sum over the queries needs no other thread.  A CTA
+// takes 256 entries (two tiles) of one head and walks through the queries in chunks of 64.
+//
+// Warps 0-7: an entry a thread.  At first they turn its codes to bf16 and store them in tensor memory
+// (left operands may lie there), then add up exp2(scale * s - lse) of every chunk.  Warp 8 issues the
+// products, warp 9 has the chunks copied in (bulk copies of tiles that weights_queries_kernel has laid
+// out: 64 rows in the 128-byte swizzled layout, channels in the order in which codes come out, and the
+// rows' -lse and tokens).  Sums of an entry over heads (and over parts of the rows) are partial results
+// that weights_join_kernel adds in order.
+//
+// TMEM, 512 columns: K 2 x D/2, scores 2 tiles x 2 buffers x 64.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "attention.h"
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "mbarrier.cuh"
+#include "vec_math.cuh"
+
+namespace dllm {
+namespace {
+
+constexpr int kTile = 128;                // entries of a tile
+constexpr int kPair = 2 * kTile;          // entries of a CTA at a time
+constexpr int kChunk = 64;                // query rows of a product
+constexpr int kThreads = 320;
+constexpr int kTmemCols = 512;
+
+struct WeightsPlan {
+  int rows, chunks, pairs;  // query rows of a head, chunks of them, pairs of entry tiles (of max_len)
+  int parts, per_part;      // the chunks are cut into parts
+  int64_t items;            // pairs * parts * heads * B
+  uint8_t* queries;         // [B][heads][chunks] records
+  float* sums;              // [B][heads * parts][pairs * kPair]
+  int32_t* status;
+};
+
+// A record: D / 64 slabs of 64 rows x 128 bytes, 64 floats -lse log2(e), 64 ints token.
+__host__ __device__ constexpr uint32_t record_bytes(int D) { return D * 128 + 512; }
+__host__ __device__ constexpr uint32_t stage_bytes(int D) { return D * 128 + 1024; }
+__host__ __device__ constexpr int stages(int D) { return D <= 64 ? 8 : D <= 128 ? 6 : 4; }
+
+// ---- tcgen05, one CTA
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// (whole warps issue with uniform operands, one elected lane executes: see attention_tc.cu)
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(kFull, x); }
+__device__ __forceinline__ int uniform(int x) { return static_cast<int>(uniform(static_cast<uint32_t>(x))); }
+// D [128 x 64] (+)= A [128 x 16] B [16 x 64], A in TMEM, B in shared memory
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory descriptor, 128-byte swizzle, K-major (attention_tc.cu).
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint64_t desc_of(uint32_t saddr) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(((saddr & 0x3FFFFu) >> 4) | (1u << 16)), "r"(kDescHigh));
+  return d;
+}
+// D fp32, A and B bf16, M = 128, N = 64, both K-major
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kChunk >> 3) << 17) |
+                            (static_cast<uint32_t>(kTile >> 4) << 24);
+
+// A whole warp's wait (attention_tc.cu).
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status)) != 0;
+}
+
+__device__ __forceinline__ int length_of(const AttnParams& p, int b) {
+  return p.lens ? max(0, min(__ldg(p.lens + b), p.max_len)) : p.max_len;
+}
+
+// ---- the queries, once per call
+
+// A thread: eight channels of a row, or a row's -lse and token.
+__global__ void __launch_bounds__(256)
+    weights_queries_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWeights x,
+                           const __grid_constant__ WeightsPlan f, int D) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t rec = blockIdx.x;  // (b, head, chunk)
+  const int chunk = static_cast<int>(rec % f.chunks);
+  const int64_t bh = rec / f.chunks;
+  const int h = static_cast<int>(bh % p.heads), b = static_cast<int>(bh / p.heads);
+  uint8_t* out = f.queries + rec * record_bytes(D);
+  const int words = D / 8;
+  for (int k = threadIdx.x; k < kChunk * words; k += blockDim.x) {
+    const int row = k / words, w = k - row * words, r = chunk * kChunk + row, i = r / p.G;
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (r < f.rows) {
+      const uint16_t* s8 =
+          p.q + b * p.qb + i * p.qt + (static_cast<int64_t>(h) * p.G + r - i * p.G) * p.qh + 8 * w;
+      if (x.q_aligned) {
+        const uint4 y = *reinterpret_cast<const uint4*>(s8);
+        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+      } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) v[m] = s8[2 * m] | static_cast<uint32_t>(s8[2 * m + 1]) << 16;
+      }
+    }
+    // channels of a code word come out in pairs (m, m + 4)
+    *reinterpret_cast<uint4*>(out + (w >> 3) * (kChunk * 128) + row * 128 + (((w & 7) ^ (row & 7)) << 4)) =
+        make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
+                   __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+  }
+  for (int row = threadIdx.x; row < kChunk; row += blockDim.x) {
+    const int r = chunk * kChunk + row, i = r / p.G;
+    float l = -INFINITY;  // adds nothing
+    if (r < f.rows) l = x.lse[(static_cast<int64_t>(b) * p.heads * p.G + h * p.G + r - i * p.G) * p.n + i];
+    reinterpret_cast<float*>(out + D * 128)[row] = l == -INFINITY ? l : -l * kLog2e;
+    reinterpret_cast<int32_t*>(out + D * 128 + 256)[row] = r < f.rows ? i : INT_MIN / 2;
+  }
+}
+
+// ---- what a CTA does at a time
+
+struct Item {
+  int b, h, j0, len, tiles;  // first entry; tiles with entries (0: none)
+  int c0, c1;                // chunks
+  int part;
+  __device__ __forceinline__ Item(const AttnParams& p, const WeightsPlan& f, int64_t at) {
+    const int pair = static_cast<int>(at % f.pairs);
+    at /= f.pairs;
+    part = static_cast<int>(at % f.parts);
+    at /= f.parts;
+    h = static_cast<int>(at % p.heads);
+    b = static_cast<int>(at / p.heads);
+    j0 = pair * kPair;
+    len = length_of(p, b);
+    tiles = j0 >= len ? 0 : j0 + kTile >= len ? 1 : 2;
+    c0 = part * f.per_part;
+    c1 = min(c0 + f.per_part, f.chunks);
+    // chunks whose last row sees nothing of these entries are passed over: row r sees the entries below
+    // len - n + r / G + 1
+    if (p.causal && tiles > 0) {
+      const int64_t token = static_cast<int64_t>(j0) - (len - p.n);  // the first that sees entry j0
+      if (token > 0) c0 = max(c0, static_cast<int>(min(token * p.G / kChunk, static_cast<int64_t>(f.chunks))));
+    }
+    c1 = tiles > 0 ? max(c0, c1) : c0;  // (all roles count the same chunks)
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_weights_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WeightsPlan f) {
+  constexpr int S = stages(D);
+  constexpr uint32_t kScores = D;  // first column of the scores
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t bars[2 * S + 2 + 8 + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t q_full = smem_u32(&bars[0]), q_empty = q_full + 8 * S;
+  const uint32_t k_full = q_empty + 8 * S;  // of a tile: K is there
+  const uint32_t s_full = k_full + 16;      // of a buffer (tile + 2 * parity): scores are there, have been read
+  const uint32_t s_empty = s_full + 32, done = s_empty + 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(q_full + 8 * s, 1);
+      mbar_init(q_empty + 8 * s, 9);  // the products, and the eight warps that read the rows' words
+    }
+    for (int t = 0; t < 2; ++t) mbar_init(k_full + 8 * t, 4);
+    for (int a = 0; a < 4; ++a) mbar_init(s_full + 8 * a, 1), mbar_init(s_empty + 8 * a, 4);
+    mbar_init(done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();  // (before tensor memory is taken: the kernel before may wait for some)
+  pdl_trigger();
+  if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_v = &abort_flag;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- an entry a thread
+    const int tile = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t t_k = tmem + lanes + tile * (D / 2), t_s = tmem + lanes + kScores + tile * kChunk;
+    uint32_t chunk = 0;  // of all items: stage and phase of the ring
+    uint32_t mine = 0;   // of those with this tile: buffer and phase
+    bool ok = true;
+    uint32_t code[D / 8], par[D / 32];
+    auto load = [&](int64_t at) {
+      // codes of this thread's entry; whether it counts
+      bool there = false;
+      if (at < f.items) {
+        const Item it(p, f, at);
+        const int j = it.j0 + tile * kTile + 32 * (warp & 3) + lane;
+        if (j < it.len && it.c1 > it.c0) {
+          const int t = j / p.page_size;
+          const int page = __ldg(p.table + static_cast<int64_t>(it.b) * p.table_stride + t);
+          there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
+          if (there && p.key_mask) there = __ldg(p.key_mask + it.b * p.mask_stride + j) != 0;
+          if (there) {
+            const int64_t row = (static_cast<int64_t>(page) * p.heads + it.h) * p.page_size + j - t * p.page_size;
+            const uint4* src = reinterpret_cast<const uint4*>(p.k_codes + row * (D / 2));
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+              const uint4 v = __ldg(src + w);
+              code[4 * w] = v.x, code[4 * w + 1] = v.y, code[4 * w + 2] = v.z, code[4 * w + 3] = v.w;
+              par[w] = __ldg(p.k_params + row * (D / 32) + w);
+            }
+          }
+        }
+      }
+      if (!there) {
+#pragma unroll
+        for (int w = 0; w < D / 8; ++w) code[w] = 0u;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) par[w] = 0u;
+      }
+      return there;
+    };
+    bool next_shown = load(blockIdx.x);
+    for (int64_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
+      const Item it(p, f, at);
+      const bool shown = next_shown;
+      const int j = it.j0 + tile * kTile + 32 * (warp & 3) + lane;
+      const bool here = tile < it.tiles && it.c1 > it.c0;
+      if (here) {
+        // (all products that read this tile's K before are complete: their scores have been read)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t v[32];
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            const uint32_t x2 = par[2 * c + w / 4];
+            const Kv4Scale sc = kv4_scale(__byte_perm(x2, x2, 0x1010));
+            v[4 * w] = kv4_pair<0>(code[8 * c + w], sc);
+            v[4 * w + 1] = kv4_pair<1>(code[8 * c + w], sc);
+            v[4 * w + 2] = kv4_pair<2>(code[8 * c + w], sc);
+            v[4 * w + 3] = kv4_pair<3>(code[8 * c + w], sc);
+          }
+          tmem_st32(t_k + 32 * c, v);
+        }
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + 8 * tile);
+      }
+      next_shown = load(at + gridDim.x);
+      float sum = 0.f;
+      for (int c = it.c0; c < it.c1; ++c, ++chunk) {
+        const int st = chunk % S;
+        const uint32_t phase = chunk / S & 1;
+        ok = wait_warp(q_full + 8 * st, phase, abort_v, f.status);
+        if (!ok) break;
+        if (here) {
+          const int a = tile + 2 * (mine & 1);
+          ok = wait_warp(s_full + 8 * a, mine >> 1 & 1, abort_v, f.status);
+          if (!ok) break;
+          tc_after();
+          float s[kChunk];
+          tmem_ld32(t_s + (mine & 1) * 2 * kChunk, s);
+          tmem_ld32(t_s + (mine & 1) * 2 * kChunk + 32, s + 32);
+          tmem_wait_ld();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_empty + 8 * a);
+          ++mine;
+          const uint32_t row = sbase + st * stage_bytes(D) + D * 128;
+          const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+          uint64_t l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+          if (!p.causal || it.len - p.n + c * kChunk / p.G + 1 >= min(it.len, it.j0 + (tile + 1) * kTile)) {
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 4) {
+              const uint4 l = ld_shared_v4(row + 4 * e);
+              float a0, a1, a2, a3;
+              unpack2(fma2(pack2(s[e], s[e + 1]), scale2, pack2(__uint_as_float(l.x), __uint_as_float(l.y))), a0, a1);
+              unpack2(fma2(pack2(s[e + 2], s[e + 3]), scale2, pack2(__uint_as_float(l.z), __uint_as_float(l.w))), a2,
+                      a3);
+              l2[0] = add2(l2[0], pack2(ex2(a0), ex2(a1)));
+              l2[1] = add2(l2[1], pack2(ex2(a2), ex2(a3)));
+            }
+          } else {
+            float part = 0.f;
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 4) {
+              const uint4 l = ld_shared_v4(row + 4 * e), t = ld_shared_v4(row + 256 + 4 * e);
+              const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, tw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float w = ex2(fmaf(s[e + y], p.scale_log2, __uint_as_float(lw[y])));
+                part += j <= it.len - p.n + static_cast<int>(tw[y]) ? w : 0.f;
+              }
+            }
+            l2[0] = pack2(part, 0.f);
+          }
+          float a0, a1;
+          unpack2(add2(l2[0], l2[1]), a0, a1);
+          sum += a0 + a1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + 8 * st);
+      }
+      if (ok && j < it.len && tile < it.tiles)
+        f.sums[((static_cast<int64_t>(it.b) * p.heads + it.h) * f.parts + it.part) * f.pairs * kPair + j] =
+            shown ? sum : 0.f;
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- products
+    const uint32_t lead = elect_lane();
+    uint32_t chunk = 0, mine[2] = {0u, 0u}, k_phase[2] = {0u, 0u};
+    bool ok = true;
+    for (int64_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
+      const Item it(p, f, at);
+      if (it.c1 <= it.c0) continue;
+      for (int t = 0; t < it.tiles && ok; ++t) {
+        ok = wait_warp(k_full + 8 * t, k_phase[t] & 1, abort_v, f.status);
+        ++k_phase[t];
+      }
+      if (!ok) break;
+      tc_after();
+      for (int c = it.c0; c < it.c1; ++c, ++chunk) {
+        const int st = uniform(static_cast<int>(chunk % S));
+        ok = wait_warp(q_full + 8 * st, chunk / S & 1, abort_v, f.status);
+        if (!ok) break;
+        const uint32_t q = uniform(sbase + st * stage_bytes(D));
+        for (int t = 0; t < it.tiles; ++t) {
+          const uint32_t a = uniform(t + 2 * (mine[t] & 1));
+          ok = wait_warp(s_empty + 8 * a, (mine[t] >> 1 & 1) ^ 1, abort_v, f.status);
+          if (!ok) break;
+          tc_after();
+          const uint32_t d = uniform(tmem + kScores + a * kChunk), k = uniform(tmem + t * (D / 2));
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ts(lead, d, k + 8 * ks, desc_of(q + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32), kIdesc, ks > 0);
+          mma_commit(lead, s_full + 8 * a);
+          ++mine[t];
+        }
+        if (!ok) break;
+        mma_commit(lead, q_empty + 8 * st);
+      }
+    }
+    mma_commit(lead, done);
+  } else {
+    // ---------------------------------------------------------------- copies
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (int64_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
+      const Item it(p, f, at);
+      const uint8_t* src =
+          f.queries + ((static_cast<int64_t>(it.b) * p.heads + it.h) * f.chunks + it.c0) * record_bytes(D);
+      for (int c = it.c0; c < it.c1; ++c, ++chunk, src += record_bytes(D)) {
+        const int st = chunk % S;
+        ok = wait_warp(q_empty + 8 * st, (chunk / S & 1) ^ 1, abort_v, f.status);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(q_full + 8 * st, record_bytes(D));
+          bulk_g2s(sbase + st * stage_bytes(D), src, record_bytes(D), q_full + 8 * st);
+        }
+        __syncwarp();
+      }
+    }
+    // after an abort: copies in flight land before shared memory goes
+    if (!ok && lane < S && static_cast<int>(chunk) > lane) {
+      const uint32_t uses = (chunk - lane + S - 1) / S;  // of this stage
+      drain_bar(q_full + 8 * lane, (uses - 1) & 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    if (lane == 0) drain_bar(done, 0);
+    __syncwarp();
+    tc_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Partial sums in order, and what was there before.
+__global__ void __launch_bounds__(256)
+    weights_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWeights x,
+                        const __grid_constant__ WeightsPlan f) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t stride = static_cast<int64_t>(f.pairs) * kPair;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int b = static_cast<int>(at / stride), j = static_cast<int>(at - b * stride);
+  if (j >= length_of(p, b)) return;
+  const int parts = p.heads * f.parts;
+  const float* src = f.sums + static_cast<int64_t>(b) * parts * stride + j;
+  float v = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k) v += src[k * stride];
+  x.out[b * x.out_stride + j] = x.prior ? fmaf(x.keep, x.prior[b * x.prior_stride + j], v) : v;
+}
+
+WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int sm_count) {
+  WeightsPlan f{};
+  f.rows = n * G;
+  f.chunks = (f.rows + kChunk - 1) / kChunk;
+  f.pairs = (max_len + kPair - 1) / kPair;
+  f.parts = 1;
+  f.per_part = f.chunks;
+  f.items = static_cast<int64_t>(B) * heads * f.parts * f.pairs;
+  return f;
+}
+
+size_t sums_at(const WeightsPlan& f, int B, int heads, int D) {
+  return align_up(kWsHeader + static_cast<size_t>(B) * heads * f.chunks * record_bytes(D), 256);
+}
+
+template <int D>
+cudaError_t launch(const AttnParams& p, const AttnWeights& x, const WeightsPlan& f, int sm_count,
+                   cudaStream_t stream) {
+  constexpr size_t smem = stages(D) * stage_bytes(D) + 1024;
+  cudaError_t e = allow_smem<attention_weights_tc_kernel<D>>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t records = static_cast<int64_t>(p.B) * p.heads * f.chunks;
+  e = launch_dependent(weights_queries_kernel, dim3(static_cast<unsigned>(records)), dim3(256), 0, stream, p, x, f, D);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(attention_weights_tc_kernel<D>,
+                       dim3(static_cast<unsigned>(std::min<int64_t>(f.items, sm_count))), dim3(kThreads), smem, stream,
+                       p, f);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(weights_join_kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * f.pairs)),
+                          dim3(256), 0, stream, p, x, f);
+}
+
+}  // namespace
+
+bool weights_tc_takes(int B, int n, int G, int heads, int max_len) {
+  const int64_t rows = static_cast<int64_t>(n) * G;
+  return rows >= 64 && static_cast<int64_t>(B) * heads * max_len <= (int64_t{1} << 34);
+}
+
+size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
+  const WeightsPlan f = make_plan(B, n, G, heads, max_len, sm_count);
+  return sums_at(f, B, heads, D) +
+         static_cast<size_t>(B) * heads * f.parts * static_cast<size_t>(f.pairs) * kPair * 4;
+}
+
+cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,
+                              cudaStream_t stream) {
+  WeightsPlan f = make_plan(p.B, p.n, p.G, p.heads, p.max_len, sm_count);
+  f.status = static_cast<int32_t*>(ws);
+  f.queries = static_cast<uint8_t*>(ws) + kWsHeader;
+  f.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sums_at(f, p.B, p.heads, D));
+  switch (D) {
+    case 64: return launch<64>(p, x, f, sm_count, stream);
+    case 128: return launch<128>(p, x, f, sm_count, stream);
+    case 192: return launch<192>(p, x, f, sm_count, stream);
+    default: return launch<256>(p, x, f, sm_count, stream);
+  }
+}
+
+}  // namespace dllm
