@@ -4,10 +4,15 @@
 // rotated before they are stored), so no other entry has to move: sources lie behind the new length
 // and destinations before it, and all copies are independent.
 //
-// kv4_evict_select_kernel, a cluster a sequence: the K-th largest weight by a radix search (11 + 11 +
-// 10 bits of the weights' order, histograms in shared memory, summed over the cluster), the places of
-// kept and dropped entries by counting in order.  It leaves the list of moves in the workspace.
-// kv4_evict_move_kernel, a warp a move: codes and params of all heads.
+// kv4_evict_select_kernel, a cluster of CTAs a sequence: a histogram of the upper 11 bits of the weights'
+// order finds the bin in which the K-th largest weight lies; the entries of that bin are listed and
+// sorted in one CTA (a bin of more entries than the list holds is narrowed down by the other bits, and
+// equal weights by counting in order), which gives the border: the last entry kept.  Kept and dropped
+// entries are then numbered by counting in order, and the moves left in the workspace.
+// kv4_evict_move_kernel copies 16 bytes of codes and a param word a thread and step, eight steps at a
+// time so that enough loads are under way, and finishes slots and weights of the entries it moves.
+#include <limits.h>
+
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -20,10 +25,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;
 constexpr int kMaxRanks = 8;
-constexpr int kDigits = 2048;
-constexpr int kDigitsPerThread = kDigits / kThreads;
+constexpr int kHeld = 8;         // entries a thread keeps in registers
+constexpr int kDigits = 2048;    // upper 11 bits, middle 11, lower 10
+constexpr int kList = 2048;      // entries that are listed
+constexpr int kSorted = 64;      // entries that are sorted as they are
 
 struct EvictParams {
   const float* weights;
@@ -44,41 +51,109 @@ struct EvictParams {
 
 // Rising order of weights as integers; a NaN comes first, both zeros are alike.
 __device__ __forceinline__ uint32_t order_of(float w) {
-  if (w != w) return 0u;
   const uint32_t b = __float_as_uint(w + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return w == w ? o : 0u;
 }
 
 struct Shared {
-  int bins[2][kDigits];
-  int warp_total[kWarps];
-  int digit, above;           // the digit found, entries above it
-  int ties[kWarps];           // of each warp: entries of the border weight;
-  int holes[kWarps], tails[kWarps];  // dropped before, kept behind the new length
+  int bins[kDigits];
+  uint64_t list[kList];            // ~order << 32 | entry
+  int warp_total[kMaxThreads / 32];
+  int digit, above, in_digit;      // the digit found, entries above it and in it
+  int listed;
+  int2 mine;                       // this CTA's holes and tails (or equal weights), read by the others
+  int2 of_warp[kMaxThreads / 32];
+  uint32_t border;                 // order of the last entry kept
+  int border_entry;
 };
 
+// kHeldAll: a thread's entries fit its registers.
+template <int kThreads, bool kHeldAll>
 struct Selector {
+  static constexpr int kWarps = kThreads / 32;
   const EvictParams& p;
   Shared& s;
   int rank, ranks, lane, warp;
   const float* w;
   int len, from, to;  // entries of this warp: [from, to)
+  uint32_t held[kHeldAll ? kHeld : 1];  // order of the weights
+  uint32_t open;  // bit k: entry k of the thread may be dropped
 
-  __device__ __forceinline__ const Shared& of(int r) const {
-    return *cg::this_cluster().map_shared_rank(&s, r);
+  __device__ __forceinline__ Selector(const EvictParams& p_, Shared& s_) : p(p_), s(s_) {}
+  __device__ __forceinline__ Shared& of(int r) const { return *cg::this_cluster().map_shared_rank(&s, r); }
+  __device__ __forceinline__ void sync() const {
+    if (ranks > 1)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
   }
-  __device__ __forceinline__ void sync() const { cg::this_cluster().sync(); }
-  __device__ __forceinline__ bool fixed(int j) const { return j < p.first || j >= len - p.last; }
+  // entry j may be dropped
+  __device__ __forceinline__ bool may_go(int j) const {
+    return static_cast<unsigned>(j - p.first) < static_cast<unsigned>(max(len - p.last - p.first, 0));
+  }
 
-  // The digit in which the count from the top reaches `need`, and the entries above it.
-  __device__ __forceinline__ void find_digit(int buffer, int need) {
-    int own[kDigitsPerThread], sum = 0;
-    const int d0 = kDigits - 1 - threadIdx.x * kDigitsPerThread;  // from the top
+  // f(j, order of the weight, whether the entry may be dropped) of the warp's entries, 32 at a time and
+  // all lanes together.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if constexpr (kHeldAll) {
 #pragma unroll
-    for (int k = 0; k < kDigitsPerThread; ++k) {
-      own[k] = 0;
-      for (int r = 0; r < ranks; ++r) own[k] += of(r).bins[buffer][d0 - k];
-      sum += own[k];
+      for (int k = 0; k < kHeld; ++k)
+        if (from + 32 * k < to) f(from + 32 * k + lane, held[k], (open >> k & 1u) != 0u);
+    } else {
+      for (int j0 = from; j0 < to; j0 += 32) {
+        const int j = j0 + lane;
+        const bool may = may_go(j);
+        f(j, may ? order_of(w[j]) : 0u, may);
+      }
+    }
+  }
+  __device__ __forceinline__ void load() {
+    if constexpr (kHeldAll) {
+      open = 0u;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int j = from + 32 * k + lane;
+        const bool may = may_go(j) && j < to;
+        held[k] = may ? order_of(w[j]) : 0u;
+        open |= may ? 1u << k : 0u;
+      }
+    }
+  }
+
+  // Histogram of the digit at `shift` of the open entries whose upper bits are `known`, over the row.
+  __device__ __forceinline__ void histogram(uint32_t known, uint32_t mask, int shift, uint32_t digits) {
+    for (int d = threadIdx.x; d < kDigits; d += kThreads) s.bins[d] = 0;
+    __syncthreads();
+    each([&](int, uint32_t key, bool may) {
+      if (may && (key & mask) == known) atomicAdd(&s.bins[key >> shift & digits], 1);
+    });
+    sync();
+  }
+  // The digit in which the count from the top reaches `need`, and the entries above it and in it; by the
+  // histograms of all CTAs, or (kOwn) this one's alone.
+  template <bool kOwn>
+  __device__ __forceinline__ void find_digit(int need) {
+    constexpr int kEach = kDigits / kThreads;
+    const int top = kDigits - 1 - threadIdx.x * kEach;  // this thread's digits from the top
+    int own[kEach], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; k += 2) {
+      int2 o = *reinterpret_cast<const int2*>(&s.bins[top - k - 1]);
+      if (!kOwn && ranks > 1) {
+        o = make_int2(0, 0);
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r) {
+          if (r >= ranks) break;
+          const int2 y = *reinterpret_cast<const int2*>(&of(r).bins[top - k - 1]);
+          o.x += y.x;
+          o.y += y.y;
+        }
+      }
+      own[k] = o.y;
+      own[k + 1] = o.x;
+      sum += o.x + o.y;
     }
     int upto = sum;
 #pragma unroll
@@ -88,30 +163,175 @@ struct Selector {
     }
     if (lane == 31) s.warp_total[warp] = upto;
     __syncthreads();
-    int above = upto - sum;
-    for (int k = 0; k < warp; ++k) above += s.warp_total[k];
+    const int before = lane < warp ? s.warp_total[lane] : 0;
+    int above = upto - sum + static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(before)));
 #pragma unroll
-    for (int k = 0; k < kDigitsPerThread; ++k) {
-      if (above < need && above + own[k] >= need) s.digit = d0 - k, s.above = above;
+    for (int k = 0; k < kEach; ++k) {
+      if (above < need && above + own[k] >= need) s.digit = top - k, s.above = above, s.in_digit = own[k];
       above += own[k];
     }
     __syncthreads();
   }
-  // Sum of one count a warp over the warps before this one, in the order of their entries.
-  __device__ __forceinline__ int before(int (Shared::*counts)[kWarps]) const {
-    int sum = 0;
-    for (int k = lane; k < rank * kWarps + warp; k += 32) sum += (of(k / kWarps).*counts)[k % kWarps];
-    return static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(sum)));
+  // Counts of this warp in the order of entries: those of the warps before it, over the whole row.
+  __device__ __forceinline__ int2 before_of(int2 count) {
+    if (lane == 0) s.of_warp[warp] = count;
+    __syncthreads();
+    int2 own = lane < kWarps ? s.of_warp[lane] : make_int2(0, 0);
+    const int2 all = make_int2(static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(own.x))),
+                               static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(own.y))));
+    if (lane >= warp) own = make_int2(0, 0);
+    if (ranks > 1) {
+      if (threadIdx.x == 0) s.mine = all;
+      sync();
+      if (lane < rank) {
+        const int2 o = of(lane).mine;
+        own.x += o.x;
+        own.y += o.y;
+      }
+    }
+    return make_int2(static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(own.x))),
+                     static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(own.y))));
+  }
+
+  // The last entry kept of the open ones, `need` of which are kept, to border and border_entry.
+  __device__ __forceinline__ void find_border(int need, uint32_t& border, int& border_entry) {
+    if (need == 0) {
+      border = 0xFFFFFFFFu;
+      border_entry = -1;
+      return;
+    }
+    if (threadIdx.x == 0) s.listed = 0;
+    histogram(0u, 0u, 21, 2047u);
+    find_digit<false>(need);
+    const uint32_t digit = static_cast<uint32_t>(s.digit);
+    need -= s.above;
+    if (s.in_digit <= kList) {
+      if (ranks == 1) {
+        each([&](int j, uint32_t key, bool may) {
+          if (may && key >> 21 == digit)
+            s.list[atomicAdd(&s.listed, 1)] = static_cast<uint64_t>(~key) << 32 | static_cast<uint32_t>(j);
+        });
+      } else {
+        list_far(digit);
+      }
+      sync();
+      if (rank == 0) {
+        const uint64_t last = nth_listed(need - 1);
+        if (threadIdx.x == 0) s.border = ~static_cast<uint32_t>(last >> 32), s.border_entry = static_cast<int>(last & 0xFFFFFFFFu);
+      }
+      sync();
+      border = of(0).border;
+      border_entry = of(0).border_entry;
+      return;
+    }
+    border = digit << 21;
+    sync();  // the bins are counted anew
+    histogram(border, 0xFFFFFFFFu << 21, 10, 2047u);
+    find_digit<false>(need);
+    border |= static_cast<uint32_t>(s.digit) << 10;
+    need -= s.above;
+    sync();
+    histogram(border, 0xFFFFFFFFu << 10, 0, 1023u);
+    find_digit<false>(need);
+    border |= static_cast<uint32_t>(s.digit);
+    need -= s.above;
+    // the need-th entry of that weight
+    int equal = 0;
+    each([&](int, uint32_t key, bool may) { equal += __popc(__ballot_sync(kFull, may && key == border)); });
+    int seen = before_of(make_int2(equal, 0)).x;
+    each([&](int j, uint32_t key, bool may) {
+      const unsigned hit = __ballot_sync(kFull, may && key == border);
+      const int upto = seen + __popc(hit & ((2u << lane) - 1u));
+      if ((hit >> lane & 1u) && upto == need) of(0).border_entry = j;
+      seen += __popc(hit);
+    });
+    sync();
+    border_entry = of(0).border_entry;
+    sync();
+  }
+  // The entries of that digit to the first CTA's list (a place for all of a warp's, not an atomic operation
+  // on another CTA's memory for every entry).
+  __device__ __forceinline__ void list_far(uint32_t digit) {
+    Shared& first = of(0);
+    int mine = 0;
+    each([&](int, uint32_t key, bool may) { mine += __popc(__ballot_sync(kFull, may && key >> 21 == digit)); });
+    int at = 0;
+    if (lane == 0 && mine > 0) at = atomicAdd(&first.listed, mine);
+    at = __shfl_sync(kFull, at, 0);
+    if (mine > 0) {
+      each([&](int j, uint32_t key, bool may) {
+        const bool in = may && key >> 21 == digit;
+        const unsigned hit = __ballot_sync(kFull, in);
+        if (in)
+          first.list[at + __popc(hit & ((1u << lane) - 1u))] =
+              static_cast<uint64_t>(~key) << 32 | static_cast<uint32_t>(j);
+        at += __popc(hit);
+      });
+    }
+  }
+  // First CTA: element n of the list in rising order.  A long list is cut down to those that share the
+  // n-th's middle bits first.
+  __device__ __forceinline__ uint64_t nth_listed(int n) {
+    int count = s.listed;
+    if (count > kSorted) {
+      constexpr int kEach = kList / kThreads;
+      for (int d = threadIdx.x; d < kDigits; d += kThreads) s.bins[d] = 0;
+      uint64_t mine[kEach];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int at = threadIdx.x + k * kThreads;
+        mine[k] = at < count ? s.list[at] : 0;
+        if (at < count) atomicAdd(&s.bins[~static_cast<uint32_t>(mine[k] >> 32) >> 10 & 2047u], 1);
+      }
+      if (threadIdx.x == 0) s.listed = 0;
+      __syncthreads();
+      find_digit<true>(n + 1);
+      n -= s.above;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        if (threadIdx.x + k * kThreads < count &&
+            (~static_cast<uint32_t>(mine[k] >> 32) >> 10 & 2047u) == static_cast<uint32_t>(s.digit))
+          s.list[atomicAdd(&s.listed, 1)] = mine[k];
+      }
+      __syncthreads();
+      count = s.listed;
+    }
+    int size = 32;
+    while (size < count) size *= 2;
+    for (int k = count + threadIdx.x; k < size; k += kThreads) s.list[k] = ~uint64_t{0};
+    __syncthreads();
+    for (int l = 2; l <= size; l *= 2) {
+      for (int d = l / 2; d > 0; d /= 2) {
+        for (int k = threadIdx.x; k < size / 2; k += kThreads) {
+          const int i = 2 * d * (k / d) + k % d;
+          const uint64_t x = s.list[i], y = s.list[i + d];
+          if ((x > y) == ((i & l) == 0)) s.list[i] = y, s.list[i + d] = x;
+        }
+        if (size > 64)
+          __syncthreads();
+        else if (warp == 0)
+          __syncwarp();  // (it has all pairs)
+        else
+          break;
+      }
+    }
+    __syncthreads();
+    return s.list[n];
   }
 };
 
+template <int kThreads, bool kHeldAll>
 __global__ void __launch_bounds__(kThreads) kv4_evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ Shared s;
-  Selector x{p, s};
+  __shared__ __align__(16) Shared s;
+  constexpr int kWarps = kThreads / 32;
+  Selector<kThreads, kHeldAll> x{p, s};
   x.ranks = static_cast<int>(cg::this_cluster().num_blocks());
   x.rank = static_cast<int>(cg::this_cluster().block_rank());
-  x.lane = threadIdx.x & 31;
+  const int lane = x.lane = threadIdx.x & 31;
   x.warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
   const int64_t b = blockIdx.x / x.ranks;
   x.w = p.weights + b * p.weights_stride;
   const int len = x.len = p.lens ? max(0, min(p.lens[b], p.max_len)) : p.max_len;
@@ -120,107 +340,75 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_select_kernel(const __grid
   float* out = p.weights_out ? p.weights_out + b * p.weights_out_stride : nullptr;
   // every warp has as many entries, whole 32s
   const int warps = x.ranks * kWarps, chunks = (p.max_len + 31) / 32;
-  const int per = 32 * ((chunks + warps - 1) / warps);
-  const int64_t start = static_cast<int64_t>(x.rank * kWarps + x.warp) * per;
+  const int64_t per = 32 * static_cast<int64_t>((chunks + warps - 1) / warps);
+  const int64_t start = (x.rank * kWarps + x.warp) * per;
   x.from = static_cast<int>(min(start, static_cast<int64_t>(p.max_len)));
   x.to = static_cast<int>(min(start + per, static_cast<int64_t>(p.max_len)));
-
-  // the border: entries of a weight above it stay, of the border weight the first `ties`
   uint32_t border = 0u;
-  int ties = 0;
+  int border_entry = INT_MAX;  // all stay
   if (len > p.budget) {
-    int need = p.budget - p.first - p.last;
-    if (need == 0) {
-      border = 0xFFFFFFFFu;
-    } else {
-      int shift = 21;
-      for (int pass = 0; pass < 3; ++pass) {
-        const int buffer = pass & 1;
-        for (int d = threadIdx.x; d < kDigits; d += kThreads) s.bins[buffer][d] = 0;
-        __syncthreads();
-        const uint32_t known = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + (pass == 1 ? 11 : 10));
-        const uint32_t digits = pass == 2 ? 1023u : 2047u;
-        for (int j = x.from + x.lane; j < min(x.to, len); j += 32) {
-          if (x.fixed(j)) continue;
-          const uint32_t key = order_of(x.w[j]);
-          if ((key & known) == (border & known)) atomicAdd(&s.bins[buffer][key >> shift & digits], 1);
-        }
-        x.sync();
-        x.find_digit(buffer, need);
-        border |= static_cast<uint32_t>(s.digit) << shift;
-        need -= s.above;
-        shift = pass == 0 ? 10 : 0;
-      }
-      ties = need;
-    }
-    // entries of the border weight before this warp's
-    int mine = 0;
-    for (int j = x.from + x.lane; j < x.to; j += 32)
-      mine += j < len && !x.fixed(j) && order_of(x.w[j]) == border ? 1 : 0;
-    mine = static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(mine)));
-    if (x.lane == 0) s.ties[x.warp] = mine;
+    x.load();
+    x.find_border(p.budget - p.first - p.last, border, border_entry);
+  } else if constexpr (kHeldAll) {
+    x.open = 0u;
   }
-  x.sync();
-  const int ties_before = len > p.budget ? x.before(&Shared::ties) : 0;
-
-  const unsigned below = (1u << x.lane) - 1u;
-  // whether entry j stays; `seen` counts the warp's entries of the border weight
-  auto stays = [&](int j, float w, int& seen) {
-    bool stay = j < len;
-    const bool open = stay && len > p.budget && !x.fixed(j);
-    const uint32_t key = open ? order_of(w) : 0u;
-    const unsigned equal = __ballot_sync(kFull, open && key == border);
-    if (open) stay = key > border || (key == border && seen + __popc(equal & below) < ties);
-    seen += __popc(equal);
-    return stay;
+  auto stays = [&](int j, uint32_t key, bool may) {
+    return may && len > p.budget ? key > border || (key == border && j <= border_entry) : j < len;
   };
-  int holes = 0, tails = 0, seen = ties_before;
-  for (int j0 = x.from; j0 < x.to; j0 += 32) {
-    const int j = j0 + x.lane;
-    const bool stay = stays(j, j < len ? x.w[j] : 0.f, seen);
-    holes += __popc(__ballot_sync(kFull, j < fresh && !stay));
-    tails += __popc(__ballot_sync(kFull, j >= fresh && stay));
-  }
-  if (x.lane == 0) s.holes[x.warp] = holes, s.tails[x.warp] = tails;
-  x.sync();
-  holes = x.before(&Shared::holes);
-  tails = x.before(&Shared::tails);
-  seen = ties_before;
+  const unsigned below = (1u << lane) - 1u;
   int32_t* from = p.from + b * p.most;
   int32_t* to = p.to + b * p.most;
-  for (int j0 = x.from; j0 < x.to; j0 += 32) {
-    const int j = j0 + x.lane;
-    const float w = j < len ? x.w[j] : 0.f;
-    const bool stay = stays(j, w, seen);
-    const bool hole = j < fresh && !stay, tail = j >= fresh && stay;
-    const unsigned hs = __ballot_sync(kFull, hole), ts = __ballot_sync(kFull, tail);
+  // (what moves is the other kernel's: its slot, its weight here and where it goes)
+  auto put = [&](int j, bool stay, unsigned hs, unsigned ts, int& holes, int& tails) {
+    const bool hole = hs >> lane & 1u, tail = ts >> lane & 1u;
     if (hole) to[holes + __popc(hs & below)] = j;
     if (tail) from[tails + __popc(ts & below)] = j;
     holes += __popc(hs);
     tails += __popc(ts);
-    if (j < x.to) {
-      if (!tail) slots[j] = stay ? j : -1;
-      if (out && stay && !tail) out[j] = w;
+    if (j < x.to && !tail) {
+      slots[j] = stay ? j : -1;
+      if (out && !hole) out[j] = stay ? x.w[j] : 0.f;
     }
+  };
+  int holes = 0, tails = 0;
+  if constexpr (kHeldAll) {
+    unsigned hs[kHeld], ts[kHeld], stay = 0u;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int j = x.from + 32 * k + lane;
+      const bool st = stays(j, x.held[k], (x.open >> k & 1u) != 0u) && j < x.to;
+      stay |= st ? 1u << k : 0u;
+      hs[k] = __ballot_sync(kFull, j < min(fresh, x.to) && !st);
+      ts[k] = __ballot_sync(kFull, j >= fresh && st);
+      holes += __popc(hs[k]);
+      tails += __popc(ts[k]);
+    }
+    const int2 before = x.before_of(make_int2(holes, tails));
+    holes = before.x;
+    tails = before.y;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (x.from + 32 * k < x.to) put(x.from + 32 * k + lane, stay >> k & 1u, hs[k], ts[k], holes, tails);
+  } else {
+    auto count = [&](auto use) {
+      x.each([&](int j, uint32_t key, bool may) {
+        const bool st = stays(j, key, may);
+        const unsigned hs = __ballot_sync(kFull, j < fresh && !st), ts = __ballot_sync(kFull, j >= fresh && st);
+        use(j, st, hs, ts);
+      });
+    };
+    count([&](int, bool, unsigned hs, unsigned ts) { holes += __popc(hs), tails += __popc(ts); });
+    const int2 before = x.before_of(make_int2(holes, tails));
+    holes = before.x;
+    tails = before.y;
+    count([&](int j, bool st, unsigned hs, unsigned ts) { put(j, st, hs, ts, holes, tails); });
   }
   // as many holes as kept entries behind the new length: the last warp has counted them all
-  if (x.rank == x.ranks - 1 && x.warp == kWarps - 1 && x.lane == 0) {
-    s.above = tails;
+  if (x.rank == x.ranks - 1 && x.warp == kWarps - 1 && lane == 0) {
     p.count[b] = tails;
+    p.lens_out[b] = fresh;
   }
-  x.sync();
-  const int moves = x.of(x.ranks - 1).above;
-  for (int k = x.rank * kThreads + threadIdx.x; k < moves; k += x.ranks * kThreads) {
-    const int j = from[k], hole = to[k];
-    slots[j] = hole;
-    if (out) out[hole] = x.w[j];
-  }
-  x.sync();
-  if (out) {
-    for (int j = x.from + x.lane; j < x.to; j += 32)
-      if (j >= fresh) out[j] = 0.f;
-  }
-  if (x.rank == 0 && threadIdx.x == 0) p.lens_out[b] = fresh;
+  if (x.ranks > 1) x.sync();  // nobody leaves while its counts may be read
 }
 
 struct MoveParams {
@@ -228,42 +416,89 @@ struct MoveParams {
   uint16_t* params[2];
   const int32_t* table;
   int table_stride, pages, page_size, heads, groups;
-  const int32_t* count;
-  const int32_t* from;
-  const int32_t* to;
-  int64_t most;
-  int splits;
+  int units;           // groups of an entry: heads * 2 * groups
+  int lanes_log2;      // lanes that copy one move: 32, or as many as it has units
+  int rounds;          // of kSteps steps: a warp's moves
+  EvictParams e;
+  int64_t ctas_per_seq;
 };
 
 constexpr int kMoveThreads = 256;
+constexpr int kSteps = 2;  // moves, or groups of them, that a warp copies at a time
 
-__global__ void __launch_bounds__(kMoveThreads) kv4_evict_move_kernel(const __grid_constant__ MoveParams p) {
+// A warp has up to 32 moves: a lane looks up where one of them comes from and goes to, then all lanes
+// copy, each its unit (16 bytes of codes and a param word) of kSteps moves at a time, the loads of the
+// next ones before the stores of these.  An entry of fewer than 32 units shares the warp with others.
+__global__ void __launch_bounds__(kMoveThreads, 4) kv4_evict_move_kernel(const __grid_constant__ MoveParams p) {
   const int lane = threadIdx.x & 31;
-  const int b = blockIdx.x / p.splits, part = blockIdx.x - b * p.splits;
-  const int count = p.count[b];
-  const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
-  const int stride = p.splits * (kMoveThreads / 32);
-  for (int k = part * (kMoveThreads / 32) + (threadIdx.x >> 5); k < count; k += stride) {
-    const int j[2] = {p.from[b * p.most + k], p.to[b * p.most + k]};
-    int64_t row[2];
-    bool there = true;
+  pdl_wait();
+  pdl_trigger();
+  const int b = static_cast<int>(blockIdx.x / p.ctas_per_seq);
+  const int64_t task = (blockIdx.x - b * p.ctas_per_seq) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int together = 32 >> p.lanes_log2;  // moves of a step
+  const int steps = min(kSteps, 1 << p.lanes_log2);  // of a round
+  const int moves = p.rounds * steps * together;
+  const int64_t k0 = task * moves;
+  const int count = __ldg(p.e.count + b);
+  if (k0 >= count) return;
+  const int here = static_cast<int>(min(static_cast<int64_t>(moves), count - k0));
+  int64_t row[2] = {-1, -1};  // group 0 of head 0 of the lane's move, from and to
+  if (lane < here) {
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
+    const int j0 = __ldg(p.e.from + b * p.e.most + k0 + lane), j1 = __ldg(p.e.to + b * p.e.most + k0 + lane);
+    const int t0 = j0 / p.page_size, t1 = j1 / p.page_size;
+    const int page0 = __ldg(table + t0), page1 = __ldg(table + t1);
+    p.e.slots[b * p.e.slots_stride + j0] = j1;
+    if (p.e.weights_out) {
+      p.e.weights_out[b * p.e.weights_out_stride + j1] = p.e.weights[b * p.e.weights_stride + j0];
+      p.e.weights_out[b * p.e.weights_out_stride + j0] = 0.f;
+    }
+    if (static_cast<unsigned>(page0) < static_cast<unsigned>(p.pages) &&
+        static_cast<unsigned>(page1) < static_cast<unsigned>(p.pages)) {
+      row[0] = (static_cast<int64_t>(page0) * p.heads * p.page_size + j0 - t0 * p.page_size) * p.groups;
+      row[1] = (static_cast<int64_t>(page1) * p.heads * p.page_size + j1 - t1 * p.page_size) * p.groups;
+    }
+  }
+  const int of_step = lane >> p.lanes_log2, rounds = (here + steps * together - 1) / (steps * together);
+  struct Held {
+    uint4 c[kSteps];
+    uint16_t q[kSteps];
+    int64_t dst[kSteps];  // -1: nothing
+    uint4* codes;
+    uint16_t* params;
+  };
+  int round = 0, unit = lane & ((1 << p.lanes_log2) - 1), ht = unit / p.groups;
+  auto load = [&](Held& x) {
+    const int64_t off = static_cast<int64_t>(ht >> 1) * p.page_size * p.groups + unit - ht * p.groups;
+    x.codes = reinterpret_cast<uint4*>(p.codes[ht & 1]) + off;
+    x.params = p.params[ht & 1] + off;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int t = j[e] / p.page_size;
-      const int page = table[t];
-      there &= static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
-      row[e] = static_cast<int64_t>(page) * p.heads * p.page_size + (j[e] - t * p.page_size);
+    for (int i = 0; i < kSteps; ++i) {
+      const int m = (round * steps + i) * together + of_step;
+      const int64_t src = __shfl_sync(kFull, row[0], m & 31);
+      x.dst[i] = __shfl_sync(kFull, row[1], m & 31);
+      if (i >= steps || m >= here || unit >= p.units) x.dst[i] = -1;
+      if (x.dst[i] >= 0) x.c[i] = x.codes[src], x.q[i] = x.params[src];
     }
-    if (!there) continue;
-    // a lane's unit: one group of one tensor of one head
-    for (int u = lane; u < p.heads * 2 * p.groups; u += 32) {
-      const int ht = u / p.groups, group = u - ht * p.groups, tensor = ht & 1;
-      const int64_t up = static_cast<int64_t>(ht >> 1) * p.page_size;
-      const int64_t src = (row[0] + up) * p.groups + group, dst = (row[1] + up) * p.groups + group;
-      uint4* codes = reinterpret_cast<uint4*>(p.codes[tensor]);
-      codes[dst] = codes[src];
-      p.params[tensor][dst] = p.params[tensor][src];
+    if (++round == rounds) {
+      round = 0;
+      unit += 32;
+      ht = unit / p.groups;
     }
+  };
+  auto store = [&](const Held& x) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (x.dst[i] >= 0) x.codes[x.dst[i]] = x.c[i], x.params[x.dst[i]] = x.q[i];
+  };
+  const int total = rounds * ((p.units + 31) / 32);
+  Held a, z;
+  load(a);
+  for (int it = 0; it < total; it += 2) {
+    if (it + 1 < total) load(z);
+    store(a);
+    if (it + 2 < total) load(a);
+    if (it + 1 < total) store(z);
   }
 }
 
@@ -289,21 +524,28 @@ cudaError_t launch_kv4_evict(const dllm_kv4_cache& cache, const float* weights, 
   p.count = reinterpret_cast<int32_t*>(at);
   p.from = reinterpret_cast<int32_t*>(at + align_up(static_cast<size_t>(B) * 4, 256));
   p.to = p.from + B * p.most;
+  // a CTA has up to eight entries a thread; a short sequence fewer threads (barriers of eight warps take
+  // less time than of 32)
+  const int threads = max_len <= 256 * kHeld ? 256 : kMaxThreads;
   int ranks = 1;
-  while (ranks < kMaxRanks && max_len > ranks * kThreads * 2 &&
-         static_cast<int64_t>(B) * ranks * 2 <= 2 * static_cast<int64_t>(sm_count))
-    ranks *= 2;
+  while (ranks < kMaxRanks && max_len > ranks * threads * kHeld) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B * ranks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_select_kernel, p);
+  cfg.numAttrs = 2;
+  const cudaError_t e =
+      threads == 256 ? cudaLaunchKernelEx(&cfg, kv4_evict_select_kernel<256, true>, p)
+      : max_len <= ranks * threads * kHeld
+          ? cudaLaunchKernelEx(&cfg, kv4_evict_select_kernel<kMaxThreads, true>, p)
+          : cudaLaunchKernelEx(&cfg, kv4_evict_select_kernel<kMaxThreads, false>, p);
   if (e != cudaSuccess || max_len <= budget) return e;
   MoveParams m{};
   m.codes[0] = cache.k_codes, m.codes[1] = cache.v_codes;
@@ -312,14 +554,21 @@ cudaError_t launch_kv4_evict(const dllm_kv4_cache& cache, const float* weights, 
   m.table_stride = cache.table_stride, m.pages = cache.pages, m.page_size = cache.page_size;
   m.heads = cache.heads;
   m.groups = cache.head_dim / 32;
-  m.count = p.count, m.from = p.from, m.to = p.to;
-  m.most = p.most;
+  m.units = cache.heads * 2 * m.groups;
+  m.e = p;
   const int64_t most = std::min<int64_t>(max_len - budget, budget);
-  const int64_t warps = kMoveThreads / 32;
-  m.splits = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>((most + warps - 1) / warps, (8 * static_cast<int64_t>(sm_count) + B - 1) / B)));
-  kv4_evict_move_kernel<<<static_cast<unsigned>(static_cast<int64_t>(B) * m.splits), kMoveThreads, 0, stream>>>(m);
-  return cudaGetLastError();
+  if (most == 0) return cudaSuccess;
+  while (m.lanes_log2 < 5 && (1 << m.lanes_log2) < m.units) ++m.lanes_log2;
+  // many moves a warp where there are many (what it looks up first is then a small part of its time), few
+  // where that leaves SMs idle
+  const int together = 32 >> m.lanes_log2;
+  const int steps = std::min(kSteps, 1 << m.lanes_log2);
+  m.rounds = std::min(2, (1 << m.lanes_log2) / steps);
+  while (m.rounds > 1 && B * most < static_cast<int64_t>(8) * sm_count * m.rounds * steps * together) m.rounds /= 2;
+  const int64_t per_cta = (kMoveThreads / 32) * m.rounds * steps * together;
+  m.ctas_per_seq = (most + per_cta - 1) / per_cta;
+  return launch_dependent(kv4_evict_move_kernel, dim3(static_cast<unsigned>(B * m.ctas_per_seq)),
+                          dim3(kMoveThreads), 0, stream, m);
 }
 
 }  // namespace dllm
