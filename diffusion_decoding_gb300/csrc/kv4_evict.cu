@@ -49,11 +49,14 @@ struct EvictParams {
   int64_t most;
 };
 
-// Rising order of weights as integers; a NaN comes first, both zeros are alike.
+// Rising order of weights as integers; a NaN comes first, both zeros are alike.  weight_of: back.
 __device__ __forceinline__ uint32_t order_of(float w) {
   const uint32_t b = __float_as_uint(w + 0.f);
   const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
   return w == w ? o : 0u;
+}
+__device__ __forceinline__ float weight_of(uint32_t o) {
+  return o == 0u ? NAN : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
 struct Shared {
@@ -104,8 +107,7 @@ struct Selector {
     } else {
       for (int j0 = from; j0 < to; j0 += 32) {
         const int j = j0 + lane;
-        const bool may = may_go(j);
-        f(j, may ? order_of(w[j]) : 0u, may);
+        f(j, j < len ? order_of(w[j]) : 0u, may_go(j));
       }
     }
   }
@@ -115,9 +117,8 @@ struct Selector {
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
         const int j = from + 32 * k + lane;
-        const bool may = may_go(j) && j < to;
-        held[k] = may ? order_of(w[j]) : 0u;
-        open |= may ? 1u << k : 0u;
+        held[k] = j < min(len, to) ? order_of(w[j]) : 0u;
+        open |= may_go(j) && j < to ? 1u << k : 0u;
       }
     }
   }
@@ -146,7 +147,8 @@ struct Selector {
 #pragma unroll
         for (int r = 0; r < kMaxRanks; ++r) {
           if (r >= ranks) break;
-          const int2 y = *reinterpret_cast<const int2*>(&of(r).bins[top - k - 1]);
+          // (each CTA begins with its own: they do not all read the same one's at a time)
+          const int2 y = *reinterpret_cast<const int2*>(&of((rank + r) & (ranks - 1)).bins[top - k - 1]);
           o.x += y.x;
           o.y += y.y;
         }
@@ -200,41 +202,37 @@ struct Selector {
       border_entry = -1;
       return;
     }
+    uint32_t mask = 0u;
+    border = 0u;
     if (threadIdx.x == 0) s.listed = 0;
-    histogram(0u, 0u, 21, 2047u);
-    find_digit<false>(need);
-    const uint32_t digit = static_cast<uint32_t>(s.digit);
-    need -= s.above;
-    if (s.in_digit <= kList) {
-      if (ranks == 1) {
-        each([&](int j, uint32_t key, bool may) {
-          if (may && key >> 21 == digit)
-            s.list[atomicAdd(&s.listed, 1)] = static_cast<uint64_t>(~key) << 32 | static_cast<uint32_t>(j);
-        });
-      } else {
-        list_far(digit);
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+      if (mask != 0u) sync();  // the bins are counted anew
+      histogram(border, mask, shift, shift == 0 ? 1023u : 2047u);
+      find_digit<false>(need);
+      border |= static_cast<uint32_t>(s.digit) << shift;
+      mask = 0xFFFFFFFFu << shift;
+      need -= s.above;
+      if (s.in_digit <= kList) {
+        if (ranks == 1) {
+          each([&](int j, uint32_t key, bool may) {
+            if (may && (key & mask) == border)
+              s.list[atomicAdd(&s.listed, 1)] = static_cast<uint64_t>(~key) << 32 | static_cast<uint32_t>(j);
+          });
+        } else {
+          list_far(border, mask);
+        }
+        sync();
+        if (rank == 0) {
+          const uint64_t last = nth_listed(need - 1);
+          if (threadIdx.x == 0)
+            s.border = ~static_cast<uint32_t>(last >> 32), s.border_entry = static_cast<int>(last & 0xFFFFFFFFu);
+        }
+        sync();
+        border = of(0).border;
+        border_entry = of(0).border_entry;
+        return;
       }
-      sync();
-      if (rank == 0) {
-        const uint64_t last = nth_listed(need - 1);
-        if (threadIdx.x == 0) s.border = ~static_cast<uint32_t>(last >> 32), s.border_entry = static_cast<int>(last & 0xFFFFFFFFu);
-      }
-      sync();
-      border = of(0).border;
-      border_entry = of(0).border_entry;
-      return;
     }
-    border = digit << 21;
-    sync();  // the bins are counted anew
-    histogram(border, 0xFFFFFFFFu << 21, 10, 2047u);
-    find_digit<false>(need);
-    border |= static_cast<uint32_t>(s.digit) << 10;
-    need -= s.above;
-    sync();
-    histogram(border, 0xFFFFFFFFu << 10, 0, 1023u);
-    find_digit<false>(need);
-    border |= static_cast<uint32_t>(s.digit);
-    need -= s.above;
     // the need-th entry of that weight
     int equal = 0;
     each([&](int, uint32_t key, bool may) { equal += __popc(__ballot_sync(kFull, may && key == border)); });
@@ -251,16 +249,16 @@ struct Selector {
   }
   // The entries of that digit to the first CTA's list (a place for all of a warp's, not an atomic operation
   // on another CTA's memory for every entry).
-  __device__ __forceinline__ void list_far(uint32_t digit) {
+  __device__ __forceinline__ void list_far(uint32_t known, uint32_t mask) {
     Shared& first = of(0);
     int mine = 0;
-    each([&](int, uint32_t key, bool may) { mine += __popc(__ballot_sync(kFull, may && key >> 21 == digit)); });
+    each([&](int, uint32_t key, bool may) { mine += __popc(__ballot_sync(kFull, may && (key & mask) == known)); });
     int at = 0;
     if (lane == 0 && mine > 0) at = atomicAdd(&first.listed, mine);
     at = __shfl_sync(kFull, at, 0);
     if (mine > 0) {
       each([&](int j, uint32_t key, bool may) {
-        const bool in = may && key >> 21 == digit;
+        const bool in = may && (key & mask) == known;
         const unsigned hit = __ballot_sync(kFull, in);
         if (in)
           first.list[at + __popc(hit & ((1u << lane) - 1u))] =
@@ -304,7 +302,7 @@ struct Selector {
     for (int l = 2; l <= size; l *= 2) {
       for (int d = l / 2; d > 0; d /= 2) {
         for (int k = threadIdx.x; k < size / 2; k += kThreads) {
-          const int i = 2 * d * (k / d) + k % d;
+          const int i = 2 * k - (k & (d - 1));  // d is a power of two
           const uint64_t x = s.list[i], y = s.list[i + d];
           if ((x > y) == ((i & l) == 0)) s.list[i] = y, s.list[i + d] = x;
         }
@@ -346,12 +344,8 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_select_kernel(const __grid
   x.to = static_cast<int>(min(start + per, static_cast<int64_t>(p.max_len)));
   uint32_t border = 0u;
   int border_entry = INT_MAX;  // all stay
-  if (len > p.budget) {
-    x.load();
-    x.find_border(p.budget - p.first - p.last, border, border_entry);
-  } else if constexpr (kHeldAll) {
-    x.open = 0u;
-  }
+  x.load();
+  if (len > p.budget) x.find_border(p.budget - p.first - p.last, border, border_entry);
   auto stays = [&](int j, uint32_t key, bool may) {
     return may && len > p.budget ? key > border || (key == border && j <= border_entry) : j < len;
   };
@@ -359,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_select_kernel(const __grid
   int32_t* from = p.from + b * p.most;
   int32_t* to = p.to + b * p.most;
   // (what moves is the other kernel's: its slot, its weight here and where it goes)
-  auto put = [&](int j, bool stay, unsigned hs, unsigned ts, int& holes, int& tails) {
+  auto put = [&](int j, uint32_t key, bool stay, unsigned hs, unsigned ts, int& holes, int& tails) {
     const bool hole = hs >> lane & 1u, tail = ts >> lane & 1u;
     if (hole) to[holes + __popc(hs & below)] = j;
     if (tail) from[tails + __popc(ts & below)] = j;
@@ -367,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_select_kernel(const __grid
     tails += __popc(ts);
     if (j < x.to && !tail) {
       slots[j] = stay ? j : -1;
-      if (out && !hole) out[j] = stay ? x.w[j] : 0.f;
+      if (out && !hole) out[j] = stay ? weight_of(key) : 0.f;
     }
   };
   int holes = 0, tails = 0;
@@ -388,20 +382,20 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_select_kernel(const __grid
     tails = before.y;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k)
-      if (x.from + 32 * k < x.to) put(x.from + 32 * k + lane, stay >> k & 1u, hs[k], ts[k], holes, tails);
+      if (x.from + 32 * k < x.to) put(x.from + 32 * k + lane, x.held[k], stay >> k & 1u, hs[k], ts[k], holes, tails);
   } else {
     auto count = [&](auto use) {
       x.each([&](int j, uint32_t key, bool may) {
         const bool st = stays(j, key, may);
         const unsigned hs = __ballot_sync(kFull, j < fresh && !st), ts = __ballot_sync(kFull, j >= fresh && st);
-        use(j, st, hs, ts);
+        use(j, key, st, hs, ts);
       });
     };
-    count([&](int, bool, unsigned hs, unsigned ts) { holes += __popc(hs), tails += __popc(ts); });
+    count([&](int, uint32_t, bool, unsigned hs, unsigned ts) { holes += __popc(hs), tails += __popc(ts); });
     const int2 before = x.before_of(make_int2(holes, tails));
     holes = before.x;
     tails = before.y;
-    count([&](int j, bool st, unsigned hs, unsigned ts) { put(j, st, hs, ts, holes, tails); });
+    count([&](int j, uint32_t key, bool st, unsigned hs, unsigned ts) { put(j, key, st, hs, ts, holes, tails); });
   }
   // as many holes as kept entries behind the new length: the last warp has counted them all
   if (x.rank == x.ranks - 1 && x.warp == kWarps - 1 && lane == 0) {
