@@ -936,6 +936,7 @@ dllm_status dllm_attention_kv4_weights(const dllm_heads* q, const dllm_kv4_cache
   x.out = weights;
   x.out_stride = weights_stride;
   x.keep = keep;
+  x.scale = scale;
   cudaError_t e = dllm::launch_attention_weights(p, x, cache->head_dim, ws, sm_count(),
                                                  reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dllm_attention_kv4_weights");

@@ -51,6 +51,8 @@ struct AttnWeights {
   float* out;
   int64_t out_stride;
   float keep;
+  float scale;
+  float l_hi, l_lo;  // scale_log2 / scale: what a log-sum-exp is multiplied by
   int q_aligned;
   int ctas_per_seq, split_log2, heads_at_once;  // few rows: attention_weights.cu
 };
@@ -59,6 +61,7 @@ cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, 
                                      cudaStream_t stream);
 
 // Many rows per cache head (attention_weights_tc.cu).
+bool weights_tc_scale(float scale);  // whether it can have this scale
 bool weights_tc_takes(int B, int n, int G, int heads, int max_len);
 size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
 cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,

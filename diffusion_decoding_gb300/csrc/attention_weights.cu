@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "attention.h"
+#include "attention_weights.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -20,10 +21,6 @@ namespace dllm {
 namespace {
 
 constexpr int kWarps = 8;
-
-__device__ __forceinline__ void put_weight(const AttnWeights& x, int b, int j, float got) {
-  x.out[b * x.out_stride + j] = x.prior ? fmaf(x.keep, x.prior[b * x.prior_stride + j], got) : got;
-}
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -168,7 +165,7 @@ __global__ void __launch_bounds__(32 * kWarps)
         float l = -INFINITY;  // adds nothing
         if (r < rows)
           l = x.lse[(static_cast<int64_t>(b) * p.heads * p.G + h * p.G + r - i * p.G) * p.n + i];
-        l_s[k] = l == -INFINITY ? l : -l * kLog2e;
+        l_s[k] = l == -INFINITY ? l : minus_l(x, l);
       }
       __syncthreads();
       if (!some0 && !some1) continue;
@@ -288,7 +285,12 @@ cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, 
                                      cudaStream_t stream) {
   if (p.max_len == 0) return cudaSuccess;
   x.q_aligned = attention_rows_aligned(p.q, p.qb, p.qt, p.qh);
-  if (weights_tc_takes(p.B, p.n, p.G, p.heads, p.max_len))
+  // The scores are multiplied by scale_log2 = scale * log2(e) as it is rounded, so the log-sum-exps by the
+  // same number over scale: the exponent's error is then relative to the exponent itself.
+  const double ratio = x.scale != 0.f ? static_cast<double>(p.scale_log2) / x.scale : 1.4426950408889634074;
+  x.l_hi = static_cast<float>(ratio);
+  x.l_lo = static_cast<float>(ratio - static_cast<double>(x.l_hi));
+  if (weights_tc_takes(p.B, p.n, p.G, p.heads, p.max_len) && weights_tc_scale(x.scale))
     return launch_weights_tc(p, x, D, ws, sm_count, stream);
   switch (D) {
     case 64: return launch<64>(p, x, sm_count, stream);

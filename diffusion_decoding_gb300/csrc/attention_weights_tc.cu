@@ -5,19 +5,26 @@
 // then lie in one lane of tensor memory, and its sum over the queries needs no other thread.  A CTA
 // takes 256 entries (two tiles) of one head and walks through the queries in chunks of 64.
 //
-// Warps 0-7: an entry a thread.  At first they turn its codes to bf16 and store them in tensor memory
-// (left operands may lie there), then add up exp2(scale * s - lse) of every chunk.  Warp 8 issues the
-// products, warp 9 has the chunks copied in (bulk copies of tiles that weights_queries_kernel has laid
-// out: 64 rows in the 128-byte swizzled layout, channels in the order in which codes come out, and the
-// rows' -lse and tokens).  Sums of an entry over heads (and over parts of the rows) are partial results
+// The log-sum-exps go through the product too: K has a block of 16 more channels that are 1 (four of them
+// used), the queries' rows there hold -lse / scale as four bf16 terms (32 bits of it), so that a weight is
+// exp2(scale log2(e) * s) and the threads that add the weights up need nothing but the scores.
+//
+// Warps 0-15: two threads an entry, each half of the rows of a chunk.  They turn the entry's codes to bf16
+// (half of the channels each) and store them in tensor memory (left operands may lie there), then add up
+// the weights of every chunk; the next entries' K is stored, into a second place where head_dim <= 128
+// leaves room, before the last chunk's scores are read, so that the products do not stop between entries.
+// Warp 16 issues the products, warp 17 has the chunks copied in (bulk copies of tiles that
+// weights_queries_kernel has laid out: 64 rows in the 128-byte swizzled layout, channels in the order in
+// which codes come out).  Sums of an entry over heads, halves (and parts of the rows) are partial results
 // that weights_join_kernel adds in order.
 //
-// TMEM, 512 columns: K 2 x D/2, scores 2 tiles x 2 buffers x 64.
-#include <limits.h>
+// TMEM, 512 columns: K 2 tiles x 1 or 2 x D/2, scores 2 tiles x 2 buffers x 64.
+#include <math.h>
 
 #include <algorithm>
 
 #include "attention.h"
+#include "attention_weights.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -30,21 +37,22 @@ namespace {
 constexpr int kTile = 128;                // entries of a tile
 constexpr int kPair = 2 * kTile;          // entries of a CTA at a time
 constexpr int kChunk = 64;                // query rows of a product
-constexpr int kThreads = 320;
+constexpr int kSumWarps = 16;
+constexpr int kThreads = 32 * (kSumWarps + 2);
 constexpr int kTmemCols = 512;
 
 struct WeightsPlan {
   int rows, chunks, pairs;  // query rows of a head, chunks of them, pairs of entry tiles (of max_len)
   int parts, per_part;      // the chunks are cut into parts
-  int64_t items;            // pairs * parts * heads * B
+  uint32_t items;           // pairs * parts * heads * B, below 2^31
   uint8_t* queries;         // [B][heads][chunks] records
-  float* sums;              // [B][heads * parts][pairs * kPair]
+  float* sums;              // [B][heads * parts * 2][pairs * kPair]
   int32_t* status;
 };
 
-// A record: D / 64 slabs of 64 rows x 128 bytes, 64 floats -lse log2(e), 64 ints token.
-__host__ __device__ constexpr uint32_t record_bytes(int D) { return D * 128 + 512; }
-__host__ __device__ constexpr uint32_t stage_bytes(int D) { return D * 128 + 1024; }
+// A record: D / 64 slabs of 64 rows x 128 bytes, and the block of -lse / scale (64 rows x 16 channels).
+constexpr uint32_t kTermBytes = kChunk * 32, kOnesBytes = kTile * 32;
+__host__ __device__ constexpr uint32_t record_bytes(int D) { return D * 128 + kTermBytes; }
 __host__ __device__ constexpr int stages(int D) { return D <= 64 ? 8 : D <= 128 ? 6 : 4; }
 
 // ---- tcgen05, one CTA
@@ -76,6 +84,15 @@ __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, ui
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
+// the same with A in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
@@ -96,15 +113,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
         "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -116,6 +130,18 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t saddr) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(((saddr & 0x3FFFFu) >> 4) | (1u << 16)), "r"(kDescHigh));
   return d;
+}
+// The same without a swizzle, 16 channels: 8 rows x 16 bytes contiguous, the other 8 channels 128 bytes on,
+// the next 8 rows 256 bytes on.
+__device__ __forceinline__ uint64_t desc_block(uint32_t saddr) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};"
+      : "=l"(d)
+      : "r"(((saddr & 0x3FFFFu) >> 4) | ((128u >> 4) << 16)), "r"((256u >> 4) | 1u << 14));
+  return d;
+}
+__host__ __device__ constexpr uint32_t block_at(int row, int channel) {
+  return (row >> 3) * 256 + (channel >> 3) * 128 + (row & 7) * 16 + (channel & 7) * 2;
 }
 // D fp32, A and B bf16, M = 128, N = 64, both K-major
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kChunk >> 3) << 17) |
@@ -168,8 +194,21 @@ __global__ void __launch_bounds__(256)
     const int r = chunk * kChunk + row, i = r / p.G;
     float l = -INFINITY;  // adds nothing
     if (r < f.rows) l = x.lse[(static_cast<int64_t>(b) * p.heads * p.G + h * p.G + r - i * p.G) * p.n + i];
-    reinterpret_cast<float*>(out + D * 128)[row] = l == -INFINITY ? l : -l * kLog2e;
-    reinterpret_cast<int32_t*>(out + D * 128 + 256)[row] = r < f.rows ? i : INT_MIN / 2;
+    uint32_t w[8] = {};
+    if (!(fabsf(l) < INFINITY)) {
+      // infinite: the score becomes so small that the weight is 0
+      w[0] = l != l ? 0x7FFFu : x.scale > 0.f ? 0xFF80u : 0x7F80u;
+    } else {
+      double rest = -static_cast<double>(l) / static_cast<double>(x.scale);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t term = __float_as_uint(static_cast<float>(rest)) & 0xFFFF0000u;  // (cut: the rest follows)
+        rest -= static_cast<double>(__uint_as_float(term));
+        w[k >> 1] |= term >> (k & 1 ? 0 : 16);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + D * 128 + block_at(row, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(out + D * 128 + block_at(row, 8)) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -177,232 +216,259 @@ __global__ void __launch_bounds__(256)
 
 struct Item {
   int b, h, j0, len, tiles;  // first entry; tiles with entries (0: none)
-  int c0, c1;                // chunks
+  int c0, c1;                // chunks (none where no query sees an entry)
   int part;
-  __device__ __forceinline__ Item(const AttnParams& p, const WeightsPlan& f, int64_t at) {
-    const int pair = static_cast<int>(at % f.pairs);
-    at /= f.pairs;
-    part = static_cast<int>(at % f.parts);
-    at /= f.parts;
-    h = static_cast<int>(at % p.heads);
-    b = static_cast<int>(at / p.heads);
-    j0 = pair * kPair;
+  // (all roles count the same chunks)
+  __device__ __forceinline__ Item(const AttnParams& p, const WeightsPlan& f, uint32_t at) {
+    const uint32_t rest = at / static_cast<uint32_t>(f.pairs), rest2 = rest / static_cast<uint32_t>(f.parts);
+    j0 = static_cast<int>(at - rest * f.pairs) * kPair;
+    part = static_cast<int>(rest - rest2 * f.parts);
+    b = static_cast<int>(rest2 / static_cast<uint32_t>(p.heads));
+    h = static_cast<int>(rest2) - b * p.heads;
     len = length_of(p, b);
     tiles = j0 >= len ? 0 : j0 + kTile >= len ? 1 : 2;
     c0 = part * f.per_part;
-    c1 = min(c0 + f.per_part, f.chunks);
-    // chunks whose last row sees nothing of these entries are passed over: row r sees the entries below
-    // len - n + r / G + 1
-    if (p.causal && tiles > 0) {
-      const int64_t token = static_cast<int64_t>(j0) - (len - p.n);  // the first that sees entry j0
-      if (token > 0) c0 = max(c0, static_cast<int>(min(token * p.G / kChunk, static_cast<int64_t>(f.chunks))));
-    }
-    c1 = tiles > 0 ? max(c0, c1) : c0;  // (all roles count the same chunks)
+    c1 = tiles > 0 ? min(c0 + f.per_part, f.chunks) : c0;
+    // row r sees the entries below len - n + r / G + 1: chunks whose last row sees none of these are passed over
+    if (p.causal && tiles > 0) c0 = min(max(c0, first_row(p, f, j0) / kChunk), c1);
+  }
+  // The first row that sees entry j (one beyond all rows: none does).
+  __device__ __forceinline__ int first_row(const AttnParams& p, const WeightsPlan& f, int j) const {
+    const int64_t token = static_cast<int64_t>(j) - (len - p.n);
+    return token <= 0 ? 0 : static_cast<int>(min(token * p.G, static_cast<int64_t>(f.chunks) * kChunk));
   }
 };
+
+// Where the K of use n of a tile lies, from the tile's first column.
+template <int D>
+__device__ __forceinline__ constexpr uint32_t k_place(int tile, uint32_t n) {
+  return D <= 128 ? tile * D + (n & 1) * (D / 2) : tile * (D / 2);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_weights_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WeightsPlan f) {
   constexpr int S = stages(D);
-  constexpr uint32_t kScores = D;  // first column of the scores
+  constexpr bool kTwoK = D <= 128;                      // two places for K
+  constexpr uint32_t kScores = kTwoK ? 2 * D : D;       // first column of the scores
+  static_assert(kScores + 4 * kChunk <= kTmemCols, "");
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t bars[2 * S + 2 + 8 + 1];
+  __shared__ __align__(8) uint64_t bars[2 * S + 4 + 8 + 1];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t ones = sbase + S * record_bytes(D);  // K's block of 16 channels
   const uint32_t q_full = smem_u32(&bars[0]), q_empty = q_full + 8 * S;
-  const uint32_t k_full = q_empty + 8 * S;  // of a tile: K is there
-  const uint32_t s_full = k_full + 16;      // of a buffer (tile + 2 * parity): scores are there, have been read
+  const uint32_t k_full = q_empty + 8 * S;  // of a tile and place (tile + 2 * place): K is there
+  const uint32_t s_full = k_full + 32;      // of a buffer (tile + 2 * parity): scores are there, have been read
   const uint32_t s_empty = s_full + 32, done = s_empty + 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(q_full + 8 * s, 1);
-      mbar_init(q_empty + 8 * s, 9);  // the products, and the eight warps that read the rows' words
+      mbar_init(q_empty + 8 * s, 1);
     }
-    for (int t = 0; t < 2; ++t) mbar_init(k_full + 8 * t, 4);
-    for (int a = 0; a < 4; ++a) mbar_init(s_full + 8 * a, 1), mbar_init(s_empty + 8 * a, 4);
+    for (int a = 0; a < 4; ++a) {
+      mbar_init(k_full + 8 * a, kSumWarps / 2);
+      mbar_init(s_full + 8 * a, 1);
+      mbar_init(s_empty + 8 * a, kSumWarps / 2);
+    }
     mbar_init(done, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
+  for (int k = threadIdx.x; k < kTile * 2; k += kThreads) {
+    const uint32_t one2 = k & 1 ? 0u : 0x3F803F80u;  // channels 0 to 3 are 1
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ones + block_at(k >> 1, 8 * (k & 1))), "r"(one2),
+                 "r"(one2), "r"(0u), "r"(0u)
+                 : "memory");
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   pdl_wait();  // (before tensor memory is taken: the kernel before may wait for some)
   pdl_trigger();
-  if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+  if (warp == kSumWarps) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = tmem_slot;
   volatile int* abort_v = &abort_flag;
 
-  if (warp < 8) {
-    // ---------------------------------------------------------------- an entry a thread
-    const int tile = warp >> 2;
+  if (warp < kSumWarps) {
+    // ---------------------------------------------------------------- two threads an entry
+    const int tile = warp >> 2 & 1, half = warp >> 3;
+    const int in_pair = tile * kTile + 32 * (warp & 3) + lane;  // entry
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t t_k = tmem + lanes + tile * (D / 2), t_s = tmem + lanes + kScores + tile * kChunk;
-    uint32_t chunk = 0;  // of all items: stage and phase of the ring
-    uint32_t mine = 0;   // of those with this tile: buffer and phase
+    constexpr int kWords = D / 16, kParams = D / 64;  // of half an entry
+    uint32_t mine = 0, k_use = 0;  // of chunks with this tile: buffer and phase; uses of its K
     bool ok = true;
-    uint32_t code[D / 8], par[D / 32];
-    auto load = [&](int64_t at) {
-      // codes of this thread's entry; whether it counts
+    uint32_t code[kWords], par[kParams];
+    auto sums_of = [&](const Item& it) {
+      return f.sums +
+             (((static_cast<int64_t>(it.b) * p.heads + it.h) * f.parts + it.part) * 2 + half) * f.pairs * kPair +
+             it.j0 + in_pair;
+    };
+    // The next item from `at` on whose entries some query sees; the sums of others are 0.
+    auto advance = [&](uint32_t& at) {
+      for (;; at += gridDim.x) {
+        const Item it(p, f, min(at, f.items - 1));
+        if (at >= f.items || it.c1 > it.c0) return it;
+        if (it.j0 + in_pair < it.len) *sums_of(it) = 0.f;
+      }
+    };
+    // The codes of this thread's half; whether the entry counts.
+    auto load = [&](uint32_t at, const Item& it) {
       bool there = false;
-      if (at < f.items) {
-        const Item it(p, f, at);
-        const int j = it.j0 + tile * kTile + 32 * (warp & 3) + lane;
-        if (j < it.len && it.c1 > it.c0) {
-          const int t = j / p.page_size;
-          const int page = __ldg(p.table + static_cast<int64_t>(it.b) * p.table_stride + t);
-          there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
-          if (there && p.key_mask) there = __ldg(p.key_mask + it.b * p.mask_stride + j) != 0;
-          if (there) {
-            const int64_t row = (static_cast<int64_t>(page) * p.heads + it.h) * p.page_size + j - t * p.page_size;
-            const uint4* src = reinterpret_cast<const uint4*>(p.k_codes + row * (D / 2));
+      const int j = it.j0 + in_pair;
+      if (at < f.items && j < it.len) {
+        const int t = j / p.page_size;
+        const int page = __ldg(p.table + static_cast<int64_t>(it.b) * p.table_stride + t);
+        there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
+        if (there && p.key_mask) there = __ldg(p.key_mask + it.b * p.mask_stride + j) != 0;
+        if (there) {
+          const int64_t row = (static_cast<int64_t>(page) * p.heads + it.h) * p.page_size + j - t * p.page_size;
+          const uint4* src = reinterpret_cast<const uint4*>(p.k_codes + row * (D / 2) + half * (D / 4));
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-              const uint4 v = __ldg(src + w);
-              code[4 * w] = v.x, code[4 * w + 1] = v.y, code[4 * w + 2] = v.z, code[4 * w + 3] = v.w;
-              par[w] = __ldg(p.k_params + row * (D / 32) + w);
-            }
+          for (int w = 0; w < kWords / 4; ++w) {
+            const uint4 v = __ldg(src + w);
+            code[4 * w] = v.x, code[4 * w + 1] = v.y, code[4 * w + 2] = v.z, code[4 * w + 3] = v.w;
           }
+#pragma unroll
+          for (int w = 0; w < kWords / 4; ++w) par[w] = __ldg(p.k_params + row * (D / 32) + half * (D / 64) + w);
         }
       }
       if (!there) {
 #pragma unroll
-        for (int w = 0; w < D / 8; ++w) code[w] = 0u;
+        for (int w = 0; w < kWords; ++w) code[w] = 0u;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) par[w] = 0u;
+        for (int w = 0; w < kParams; ++w) par[w] = 0u;
       }
       return there;
     };
-    bool next_shown = load(blockIdx.x);
-    for (int64_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
-      const Item it(p, f, at);
-      const bool shown = next_shown;
-      const int j = it.j0 + tile * kTile + 32 * (warp & 3) + lane;
-      const bool here = tile < it.tiles && it.c1 > it.c0;
-      if (here) {
-        // (all products that read this tile's K before are complete: their scores have been read)
+    // Store K of the codes held, where its place is free.
+    auto store = [&]() {
+      const uint32_t t_k = tmem + lanes + k_place<D>(tile, k_use) + half * (D / 4);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t v[32];
+      for (int c = 0; c < kWords / 4; ++c) {
+        uint32_t v[16];
+        const Kv4Scale sc = kv4_scale(__byte_perm(par[c], par[c], 0x1010));
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const uint32_t x2 = par[2 * c + w / 4];
-            const Kv4Scale sc = kv4_scale(__byte_perm(x2, x2, 0x1010));
-            v[4 * w] = kv4_pair<0>(code[8 * c + w], sc);
-            v[4 * w + 1] = kv4_pair<1>(code[8 * c + w], sc);
-            v[4 * w + 2] = kv4_pair<2>(code[8 * c + w], sc);
-            v[4 * w + 3] = kv4_pair<3>(code[8 * c + w], sc);
-          }
-          tmem_st32(t_k + 32 * c, v);
+        for (int w = 0; w < 4; ++w) {
+          v[4 * w] = kv4_pair<0>(code[4 * c + w], sc);
+          v[4 * w + 1] = kv4_pair<1>(code[4 * c + w], sc);
+          v[4 * w + 2] = kv4_pair<2>(code[4 * c + w], sc);
+          v[4 * w + 3] = kv4_pair<3>(code[4 * c + w], sc);
         }
-        tmem_wait_st();
+        tmem_st16(t_k + 16 * c, v);
+      }
+      tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full + 8 * (tile + (kTwoK ? 2 * (k_use & 1) : 0)));
+      ++k_use;
+    };
+    uint32_t at = blockIdx.x;
+    Item it = advance(at);
+    bool shown = load(at, it);
+    if (at < f.items && tile < it.tiles) store();
+    while (at < f.items && ok) {
+      const bool here = tile < it.tiles;
+      const int j = it.j0 + in_pair;
+      uint32_t at_next = at + gridDim.x;
+      const Item next = advance(at_next);
+      const bool next_shown = load(at_next, next), next_here = at_next < f.items && tile < next.tiles;
+      // the first chunk all of whose rows see all of the tile's entries; the first row that sees this one
+      const int c_all = p.causal ? (it.first_row(p, f, min(it.len, it.j0 + (tile + 1) * kTile) - 1) + kChunk - 1) / kChunk
+                                 : 0;
+      const int own_row = p.causal ? it.first_row(p, f, j) - 32 * half : 0;
+      float sum = 0.f;
+      for (int c = it.c0; c < it.c1; ++c) {
+        // (the products that read the other place's K are complete: their scores have been read)
+        if (kTwoK && c == it.c1 - 1 && next_here) store();
+        if (!here) continue;
+        const int a = tile + 2 * (mine & 1);
+        ok = wait_warp(s_full + 8 * a, mine >> 1 & 1, abort_v, f.status);
+        if (!ok) break;
+        tc_after();
+        float s[32];
+        tmem_ld32(tmem + lanes + kScores + a * kChunk + half * 32, s);
+        tmem_wait_ld();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + 8 * tile);
-      }
-      next_shown = load(at + gridDim.x);
-      float sum = 0.f;
-      for (int c = it.c0; c < it.c1; ++c, ++chunk) {
-        const int st = chunk % S;
-        const uint32_t phase = chunk / S & 1;
-        ok = wait_warp(q_full + 8 * st, phase, abort_v, f.status);
-        if (!ok) break;
-        if (here) {
-          const int a = tile + 2 * (mine & 1);
-          ok = wait_warp(s_full + 8 * a, mine >> 1 & 1, abort_v, f.status);
-          if (!ok) break;
-          tc_after();
-          float s[kChunk];
-          tmem_ld32(t_s + (mine & 1) * 2 * kChunk, s);
-          tmem_ld32(t_s + (mine & 1) * 2 * kChunk + 32, s + 32);
-          tmem_wait_ld();
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_empty + 8 * a);
-          ++mine;
-          const uint32_t row = sbase + st * stage_bytes(D) + D * 128;
+        if (lane == 0) mbar_arrive(s_empty + 8 * a);
+        ++mine;
+        if (c >= c_all) {
           const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-          uint64_t l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-          if (!p.causal || it.len - p.n + c * kChunk / p.G + 1 >= min(it.len, it.j0 + (tile + 1) * kTile)) {
+          uint64_t l2[4] = {pack2(0.f, 0.f), pack2(0.f, 0.f), pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-            for (int e = 0; e < kChunk; e += 4) {
-              const uint4 l = ld_shared_v4(row + 4 * e);
-              float a0, a1, a2, a3;
-              unpack2(fma2(pack2(s[e], s[e + 1]), scale2, pack2(__uint_as_float(l.x), __uint_as_float(l.y))), a0, a1);
-              unpack2(fma2(pack2(s[e + 2], s[e + 3]), scale2, pack2(__uint_as_float(l.z), __uint_as_float(l.w))), a2,
-                      a3);
-              l2[0] = add2(l2[0], pack2(ex2(a0), ex2(a1)));
-              l2[1] = add2(l2[1], pack2(ex2(a2), ex2(a3)));
-            }
-          } else {
-            float part = 0.f;
-#pragma unroll
-            for (int e = 0; e < kChunk; e += 4) {
-              const uint4 l = ld_shared_v4(row + 4 * e), t = ld_shared_v4(row + 256 + 4 * e);
-              const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, tw[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float w = ex2(fmaf(s[e + y], p.scale_log2, __uint_as_float(lw[y])));
-                part += j <= it.len - p.n + static_cast<int>(tw[y]) ? w : 0.f;
-              }
-            }
-            l2[0] = pack2(part, 0.f);
+          for (int e = 0; e < 32; e += 2) {
+            float a0, a1;
+            unpack2(mul2(pack2(s[e], s[e + 1]), scale2), a0, a1);
+            l2[e >> 1 & 3] = add2(l2[e >> 1 & 3], pack2(ex2(a0), ex2(a1)));
           }
           float a0, a1;
-          unpack2(add2(l2[0], l2[1]), a0, a1);
+          unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), a0, a1);
           sum += a0 + a1;
+        } else {
+          float part = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float w = ex2(s[e] * p.scale_log2);
+            part += c * kChunk + e >= own_row ? w : 0.f;
+          }
+          sum += part;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty + 8 * st);
-      }
-      if (ok && j < it.len && tile < it.tiles)
-        f.sums[((static_cast<int64_t>(it.b) * p.heads + it.h) * f.parts + it.part) * f.pairs * kPair + j] =
-            shown ? sum : 0.f;
-    }
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- products
-    const uint32_t lead = elect_lane();
-    uint32_t chunk = 0, mine[2] = {0u, 0u}, k_phase[2] = {0u, 0u};
-    bool ok = true;
-    for (int64_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
-      const Item it(p, f, at);
-      if (it.c1 <= it.c0) continue;
-      for (int t = 0; t < it.tiles && ok; ++t) {
-        ok = wait_warp(k_full + 8 * t, k_phase[t] & 1, abort_v, f.status);
-        ++k_phase[t];
       }
       if (!ok) break;
+      if (j < it.len && here) *sums_of(it) = shown ? sum : 0.f;
+      if (!kTwoK && next_here) store();
+      at = at_next;
+      it = next;
+      shown = next_shown;
+    }
+  } else if (warp == kSumWarps) {
+    // ---------------------------------------------------------------- products
+    const uint32_t lead = elect_lane(), ones_u = uniform(ones);
+    int stage = 0;
+    uint32_t phase = 0, mine[2] = {0u, 0u}, k_use[2] = {0u, 0u};
+    bool ok = true;
+    for (uint32_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
+      const Item it(p, f, at);
+      if (it.c1 <= it.c0) continue;
+      for (int t = 0; t < it.tiles && ok; ++t)
+        ok = wait_warp(k_full + 8 * (t + (kTwoK ? 2 * (k_use[t] & 1) : 0)), (kTwoK ? k_use[t] >> 1 : k_use[t]) & 1,
+                       abort_v, f.status);
+      if (!ok) break;
       tc_after();
-      for (int c = it.c0; c < it.c1; ++c, ++chunk) {
-        const int st = uniform(static_cast<int>(chunk % S));
-        ok = wait_warp(q_full + 8 * st, chunk / S & 1, abort_v, f.status);
+      for (int c = it.c0; c < it.c1; ++c) {
+        const int st = uniform(stage);
+        ok = wait_warp(q_full + 8 * st, phase, abort_v, f.status);
         if (!ok) break;
-        const uint32_t q = uniform(sbase + st * stage_bytes(D));
+        const uint32_t q = uniform(sbase + st * record_bytes(D));
         for (int t = 0; t < it.tiles; ++t) {
           const uint32_t a = uniform(t + 2 * (mine[t] & 1));
           ok = wait_warp(s_empty + 8 * a, (mine[t] >> 1 & 1) ^ 1, abort_v, f.status);
           if (!ok) break;
           tc_after();
-          const uint32_t d = uniform(tmem + kScores + a * kChunk), k = uniform(tmem + t * (D / 2));
+          const uint32_t d = uniform(tmem + kScores + a * kChunk), k = uniform(tmem + k_place<D>(t, k_use[t]));
+          mma_ss(lead, d, desc_block(ones_u), desc_block(q + D * 128), kIdesc, 0u);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_ts(lead, d, k + 8 * ks, desc_of(q + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32), kIdesc, ks > 0);
+            mma_ts(lead, d, k + 8 * ks, desc_of(q + (ks >> 2) * (kChunk * 128) + (ks & 3) * 32), kIdesc, 1u);
           mma_commit(lead, s_full + 8 * a);
           ++mine[t];
         }
         if (!ok) break;
         mma_commit(lead, q_empty + 8 * st);
+        if (++stage == S) stage = 0, phase ^= 1;
       }
+      for (int t = 0; t < it.tiles; ++t) ++k_use[t];
     }
     mma_commit(lead, done);
   } else {
     // ---------------------------------------------------------------- copies
     uint32_t chunk = 0;
     bool ok = true;
-    for (int64_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
+    for (uint32_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
       const Item it(p, f, at);
       const uint8_t* src =
           f.queries + ((static_cast<int64_t>(it.b) * p.heads + it.h) * f.chunks + it.c0) * record_bytes(D);
@@ -412,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           mbar_expect_tx(q_full + 8 * st, record_bytes(D));
-          bulk_g2s(sbase + st * stage_bytes(D), src, record_bytes(D), q_full + 8 * st);
+          bulk_g2s(sbase + st * record_bytes(D), src, record_bytes(D), q_full + 8 * st);
         }
         __syncwarp();
       }
@@ -424,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSumWarps) {
     if (lane == 0) drain_bar(done, 0);
     __syncwarp();
     tc_after();
@@ -442,12 +508,12 @@ __global__ void __launch_bounds__(256)
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int b = static_cast<int>(at / stride), j = static_cast<int>(at - b * stride);
   if (j >= length_of(p, b)) return;
-  const int parts = p.heads * f.parts;
+  const int parts = p.heads * f.parts * 2;
   const float* src = f.sums + static_cast<int64_t>(b) * parts * stride + j;
   float v = 0.f;
 #pragma unroll 8
   for (int k = 0; k < parts; ++k) v += src[k * stride];
-  x.out[b * x.out_stride + j] = x.prior ? fmaf(x.keep, x.prior[b * x.prior_stride + j], v) : v;
+  put_weight(x, b, j, v);
 }
 
 WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int sm_count) {
@@ -457,7 +523,7 @@ WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int sm_count)
   f.pairs = (max_len + kPair - 1) / kPair;
   f.parts = 1;
   f.per_part = f.chunks;
-  f.items = static_cast<int64_t>(B) * heads * f.parts * f.pairs;
+  f.items = static_cast<uint32_t>(static_cast<int64_t>(B) * heads * f.parts * f.pairs);
   return f;
 }
 
@@ -468,7 +534,7 @@ size_t sums_at(const WeightsPlan& f, int B, int heads, int D) {
 template <int D>
 cudaError_t launch(const AttnParams& p, const AttnWeights& x, const WeightsPlan& f, int sm_count,
                    cudaStream_t stream) {
-  constexpr size_t smem = stages(D) * stage_bytes(D) + 1024;
+  constexpr size_t smem = stages(D) * record_bytes(D) + kOnesBytes + 1024;
   cudaError_t e = allow_smem<attention_weights_tc_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t records = static_cast<int64_t>(p.B) * p.heads * f.chunks;
@@ -484,15 +550,17 @@ cudaError_t launch(const AttnParams& p, const AttnWeights& x, const WeightsPlan&
 
 }  // namespace
 
+bool weights_tc_scale(float scale) { return fabsf(scale) >= 0x1p-20f && fabsf(scale) <= 0x1p20f; }
+
 bool weights_tc_takes(int B, int n, int G, int heads, int max_len) {
   const int64_t rows = static_cast<int64_t>(n) * G;
-  return rows >= 64 && static_cast<int64_t>(B) * heads * max_len <= (int64_t{1} << 34);
+  return rows >= 64 && static_cast<int64_t>(B) * heads * (static_cast<int64_t>(max_len) + kPair) <= (int64_t{1} << 34);
 }
 
 size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
   const WeightsPlan f = make_plan(B, n, G, heads, max_len, sm_count);
   return sums_at(f, B, heads, D) +
-         static_cast<size_t>(B) * heads * f.parts * static_cast<size_t>(f.pairs) * kPair * 4;
+         static_cast<size_t>(B) * heads * f.parts * 2 * static_cast<size_t>(f.pairs) * kPair * 4;
 }
 
 cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,

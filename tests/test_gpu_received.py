@@ -57,7 +57,11 @@ def check(cache, q, lens, T, key_mask=None, causal=False, prior=None, keep=1.0, 
     # a term's exponent: the products' sum (2^-20 of their magnitudes' sum), the rounding of lse and of
     # the exponent itself; then one addition a term and one of the prior
     top = float(lse[lse.isfinite()].abs().max()) if bool(lse.isfinite().any()) else 0.0
-    tol = want.abs() * (2.0 ** -20 * size + 2.0 ** -22 * (top + size) + 2.0 ** -21 + n * H * 2.0 ** -24) + 1e-37
+    # The terms' errors are relative to their sum, which is want - keep * prior and not want: with a negative
+    # keep the two may cancel.  keep * prior + sum is one fused operation, off by half an ulp of itself.
+    gain = want if prior is None else want - float(torch.tensor(keep)) * held[:, :T].double()
+    tol = gain.abs() * (2.0 ** -20 * size + 2.0 ** -22 * (top + size) + 2.0 ** -21 + n * H * 2.0 ** -24) \
+        + want.abs() * 2.0 ** -24 + 1e-37
     bad = there & ~((got.double() - want).abs() <= tol) & ~(got.isnan() & want.isnan())
     assert not bool(bad.any()), (got[bad][:5], want[bad][:5])
     return got
