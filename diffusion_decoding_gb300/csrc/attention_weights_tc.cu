@@ -41,7 +41,21 @@ constexpr int kSumWarps = 16;
 constexpr int kThreads = 32 * (kSumWarps + 2);
 constexpr int kTmemCols = 512;
 
+// Division of n < 2^31 by a number known on the host: a multiplication (of at most 2^32 / 2^l * (1 + 2^-31)
+// for 2^(l-1) < d <= 2^l) and a shift.
+struct Divisor {
+  uint32_t d, m, shift;  // d = 1: m = 0
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
+};
+Divisor divisor(uint32_t d) {
+  if (d <= 1) return Divisor{1u, 0u, 0u};
+  uint32_t l = 1;
+  while ((uint64_t{1} << l) < d) ++l;
+  return Divisor{d, static_cast<uint32_t>(((uint64_t{1} << (31 + l)) + d - 1) / d), l - 1};
+}
+
 struct WeightsPlan {
+  Divisor by_pairs, by_parts, by_heads, by_page;
   int rows, chunks, pairs;  // query rows of a head, chunks of them, pairs of entry tiles (of max_len)
   int parts, per_part;      // the chunks are cut into parts
   uint32_t items;           // pairs * parts * heads * B, below 2^31
@@ -220,10 +234,10 @@ struct Item {
   int part;
   // (all roles count the same chunks)
   __device__ __forceinline__ Item(const AttnParams& p, const WeightsPlan& f, uint32_t at) {
-    const uint32_t rest = at / static_cast<uint32_t>(f.pairs), rest2 = rest / static_cast<uint32_t>(f.parts);
+    const uint32_t rest = f.by_pairs(at), rest2 = f.by_parts(rest);
     j0 = static_cast<int>(at - rest * f.pairs) * kPair;
     part = static_cast<int>(rest - rest2 * f.parts);
-    b = static_cast<int>(rest2 / static_cast<uint32_t>(p.heads));
+    b = static_cast<int>(f.by_heads(rest2));
     h = static_cast<int>(rest2) - b * p.heads;
     len = length_of(p, b);
     tiles = j0 >= len ? 0 : j0 + kTile >= len ? 1 : 2;
@@ -284,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  pdl_wait();  // (before tensor memory is taken: the kernel before may wait for some)
+  // Only the copies read what weights_queries_kernel writes.  That kernel's CTAs have all waited for the
+  // kernels before it when this one may start: the cache, lengths and sums of those are complete, and
+  // none of them holds tensor memory.
   pdl_trigger();
   if (warp == kSumWarps) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   tc_before();
@@ -320,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool there = false;
       const int j = it.j0 + in_pair;
       if (at < f.items && j < it.len) {
-        const int t = j / p.page_size;
+        const int t = static_cast<int>(f.by_page(static_cast<uint32_t>(j)));
         const int page = __ldg(p.table + static_cast<int64_t>(it.b) * p.table_stride + t);
         there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pages);
         if (there && p.key_mask) there = __ldg(p.key_mask + it.b * p.mask_stride + j) != 0;
@@ -468,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- copies
     uint32_t chunk = 0;
     bool ok = true;
+    pdl_wait();
     for (uint32_t at = blockIdx.x; at < f.items && ok; at += gridDim.x) {
       const Item it(p, f, at);
       const uint8_t* src =
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(256)
   put_weight(x, b, j, v);
 }
 
-WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int sm_count) {
+WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int page_size, int sm_count) {
   WeightsPlan f{};
   f.rows = n * G;
   f.chunks = (f.rows + kChunk - 1) / kChunk;
@@ -524,6 +541,8 @@ WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int sm_count)
   f.parts = 1;
   f.per_part = f.chunks;
   f.items = static_cast<uint32_t>(static_cast<int64_t>(B) * heads * f.parts * f.pairs);
+  f.by_pairs = divisor(f.pairs), f.by_parts = divisor(f.parts), f.by_heads = divisor(heads);
+  f.by_page = divisor(page_size);
   return f;
 }
 
@@ -558,14 +577,14 @@ bool weights_tc_takes(int B, int n, int G, int heads, int max_len) {
 }
 
 size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
-  const WeightsPlan f = make_plan(B, n, G, heads, max_len, sm_count);
+  const WeightsPlan f = make_plan(B, n, G, heads, max_len, 1, sm_count);
   return sums_at(f, B, heads, D) +
          static_cast<size_t>(B) * heads * f.parts * 2 * static_cast<size_t>(f.pairs) * kPair * 4;
 }
 
 cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,
                               cudaStream_t stream) {
-  WeightsPlan f = make_plan(p.B, p.n, p.G, p.heads, p.max_len, sm_count);
+  WeightsPlan f = make_plan(p.B, p.n, p.G, p.heads, p.max_len, p.page_size, sm_count);
   f.status = static_cast<int32_t*>(ws);
   f.queries = static_cast<uint8_t*>(ws) + kWsHeader;
   f.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sums_at(f, p.B, p.heads, D));
