@@ -42,6 +42,19 @@ size_t attention_tc_ws_bytes(int B, int n, int G, int heads, int D, int sm_count
 cudaError_t launch_attention_tc(const AttnParams& p, int D, void* ws, int sm_count,
                                 cudaStream_t stream);
 
+// Division of n < 2^31 by a number known on the host: a multiplication (of at most 2^32 / 2^l * (1 + 2^-31)
+// for 2^(l-1) < d <= 2^l) and a shift.
+struct Divisor {
+  uint32_t d, m, shift;  // d = 1: m = 0
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
+};
+inline Divisor divisor(uint32_t d) {
+  if (d <= 1) return Divisor{1u, 0u, 0u};
+  uint32_t l = 1;
+  while ((uint64_t{1} << l) < d) ++l;
+  return Divisor{d, static_cast<uint32_t>(((uint64_t{1} << (31 + l)) + d - 1) / d), l - 1};
+}
+
 // Accumulated weights (attention_weights.cu): the call's queries, cache and masks are an AttnParams
 // (out and lse unused).
 struct AttnWeights {
@@ -54,7 +67,8 @@ struct AttnWeights {
   float scale;
   float l_hi, l_lo;  // scale_log2 / scale: what a log-sum-exp is multiplied by
   int q_aligned;
-  int ctas_per_seq, split_log2, heads_at_once;  // few rows: attention_weights.cu
+  Divisor by_page;
+  int ctas_per_seq, split_log2, heads_at_once, tiles_per_warp;  // few rows: attention_weights.cu
 };
 size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
 cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, void* ws, int sm_count,

@@ -41,19 +41,6 @@ constexpr int kSumWarps = 16;
 constexpr int kThreads = 32 * (kSumWarps + 2);
 constexpr int kTmemCols = 512;
 
-// Division of n < 2^31 by a number known on the host: a multiplication (of at most 2^32 / 2^l * (1 + 2^-31)
-// for 2^(l-1) < d <= 2^l) and a shift.
-struct Divisor {
-  uint32_t d, m, shift;  // d = 1: m = 0
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
-};
-Divisor divisor(uint32_t d) {
-  if (d <= 1) return Divisor{1u, 0u, 0u};
-  uint32_t l = 1;
-  while ((uint64_t{1} << l) < d) ++l;
-  return Divisor{d, static_cast<uint32_t>(((uint64_t{1} << (31 + l)) + d - 1) / d), l - 1};
-}
-
 struct WeightsPlan {
   Divisor by_pairs, by_parts, by_heads, by_page;
   int rows, chunks, pairs;  // query rows of a head, chunks of them, pairs of entry tiles (of max_len)
