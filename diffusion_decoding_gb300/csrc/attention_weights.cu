@@ -80,7 +80,7 @@ struct Stage {
 
 // Rows of a row tile: 8 * NT.
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, D <= 128 && NT == 1 ? 3 : D == 256 && NT == 4 ? 1 : 2)
+__global__ void __launch_bounds__(32 * kWarps, D <= 128 && NT == 1 ? 3 : 2)
     attention_weights_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWeights x) {
   using R = Stage<D>;
   constexpr int KW = R::KW, ROWS = 8 * NT;
@@ -364,14 +364,15 @@ template <int D>
 cudaError_t launch(const AttnParams& p, const AttnWeights& x, int sm_count, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.n) * p.G;
   if (rows <= 8) return launch_nt<D, 1>(p, x, sm_count, stream);
-  if (rows <= 16) return launch_nt<D, 2>(p, x, sm_count, stream);
-  return launch_nt<D, 4>(p, x, sm_count, stream);
+  // (more rows come here with 64 channels, or with a scale that the other kernel cannot have)
+  if (rows <= 16 || D > 64) return launch_nt<D, 2>(p, x, sm_count, stream);
+  return launch_nt<D, D == 64 ? 4 : 2>(p, x, sm_count, stream);
 }
 
 }  // namespace
 
 size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
-  return weights_tc_takes(B, n, G, heads, max_len)
+  return weights_tc_takes(B, n, G, heads, D, max_len)
              ? weights_tc_ws_bytes(B, n, G, heads, D, max_len, sm_count)
              : kWsHeader;
 }
@@ -386,7 +387,7 @@ cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, 
   const double ratio = x.scale != 0.f ? static_cast<double>(p.scale_log2) / x.scale : 1.4426950408889634074;
   x.l_hi = static_cast<float>(ratio);
   x.l_lo = static_cast<float>(ratio - static_cast<double>(x.l_hi));
-  if (weights_tc_takes(p.B, p.n, p.G, p.heads, p.max_len) && weights_tc_scale(x.scale))
+  if (weights_tc_takes(p.B, p.n, p.G, p.heads, D, p.max_len) && weights_tc_scale(x.scale))
     return launch_weights_tc(p, x, D, ws, sm_count, stream);
   switch (D) {
     case 64: return launch<64>(p, x, sm_count, stream);

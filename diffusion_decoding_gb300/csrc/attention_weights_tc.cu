@@ -558,9 +558,15 @@ cudaError_t launch(const AttnParams& p, const AttnWeights& x, const WeightsPlan&
 
 bool weights_tc_scale(float scale) { return fabsf(scale) >= 0x1p-20f && fabsf(scale) <= 0x1p20f; }
 
-bool weights_tc_takes(int B, int n, int G, int heads, int max_len) {
+// From 9 rows of 192 and 256 channels on, 17 of 128, 33 of 64 (us here and in attention_weights.cu; heads
+// x entries, sequences in brackets: 12 rows of 256 channels, 8 x 2000 (8) 16 and 26; 9 of 192 14 and 24;
+// 8 of 256, 8 x 4096 (32) 79 and 66; 16 of 128, 8 x 2000 (8) 13 and 9; 17 of 128, 8 x 4000 (8) 19.3 and 18.8, 48 of
+// 128 19.5 and 33; 17 of 128, 8 x 777 (1) 7.8 and 11; 20 of 64, 8 x 2000 (32) 27 and 16; 33 of 64, 6 x 777 (3)
+// 8.1 and 10).
+bool weights_tc_takes(int B, int n, int G, int heads, int D, int max_len) {
   const int64_t rows = static_cast<int64_t>(n) * G;
-  return rows >= 64 && static_cast<int64_t>(B) * heads * (static_cast<int64_t>(max_len) + kPair) <= (int64_t{1} << 34);
+  return rows > (D == 64 ? 32 : D == 128 ? 16 : 8) &&
+         static_cast<int64_t>(B) * heads * (static_cast<int64_t>(max_len) + kPair) <= (int64_t{1} << 34);
 }
 
 size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
