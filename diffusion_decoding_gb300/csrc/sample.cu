@@ -21,13 +21,12 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kLaneVecs = 8;                // 16-byte vectors a lane takes of a tile
+constexpr int kLaneVecs = 8, kLaneVecsLog2 = 3;  // 16-byte vectors a lane takes of a tile
 constexpr int kTileVecs = 32 * kLaneVecs;   // a tile: 4 KB of a row, one warp's
-constexpr int kCap = 1024;                  // candidates that are listed and ordered
-constexpr int kListK = 512;                 // largest top_k that is tried with a list
+constexpr int kCap = 2048;                  // candidates that are listed and ordered, at most
 constexpr int kFew = 128;                   // candidates ordered by counting, more by sorting
 constexpr int kMaxGroups = 256;             // chunks of a CTA / 32
-constexpr int kQueue = kCap;                // chunks that are looked through again
+constexpr int kMaxRanks = 8;                // CTAs of a row
 // Histogram of chunk maxima: 8 bins an octave.
 constexpr int kCoarse = 8, kCoarseBins = kWeightBits * kCoarse;
 // Histogram of weights: 32 bins an octave, down to where a weight is a unit.
@@ -40,7 +39,8 @@ struct SampleParams {
   int64_t row_stride_bytes;
   int V;
   int span_log2;           // tiles of a group
-  uint32_t tops_bytes, sums_at;  // in shared memory
+  uint32_t sums_at, keys_at;  // in shared memory
+  int cap;                 // candidates that are listed, a power of two
   const uint8_t* masked;   // null: every row
   const float* uniform;
   dllm_stats out;
@@ -90,8 +90,8 @@ struct Control {
 struct Summary {
   float m, sum;      // maximum, sum of exp(z - m)
   float some, all;   // logits that its share of top_k, and all of top_k, of its chunks reach
-  uint64_t mass;     // weights, those of light chunks in 32 bits
-  uint64_t light;    // of that: light chunks
+  uint64_t mass;     // weights
+  uint64_t light;    // of that: by sums of chunks in 32 bits
 };
 
 struct Shared {
@@ -104,15 +104,15 @@ struct Shared {
   uint64_t total[2];        // of this CTA: mass, count; read by the others
   uint64_t group_before;    // find_group's
   int group;
-  int coarse[kCoarseBins];
-  uint64_t keys[kCap];      // candidates: ~order(z) << 32 | id
+  int coarse[kCoarseBins];  // of this CTA's part
+  int row_coarse[kCoarseBins];
   ulonglong2 few[kFew];     // key, weight
   int queued;
-  uint16_t queue[kQueue];   // chunks
   uint64_t goal, goal_error;  // what one thread worked out for all: a mass in units
   float least, from;
+  bool sure;
 };
-// The histogram of all weights, where the chunk sums were.
+// The histogram of all weights, where the chunks' maxima and sums were.
 struct Fine {
   uint64_t bins_lo_hi[kBins];  // mass of a bin: low word, high word
   int bins[kBins];
@@ -141,6 +141,14 @@ struct Row {
   __device__ __forceinline__ uint4 load(int vec) const {
     const int e = id(vec);
     if (e >= 0 && e + VEC <= V) return ld_stream_v4(base + static_cast<int64_t>(vec) * 16);
+    return e < V ? load_edge(base, vec, e, V) : none();
+  }
+  static __device__ __forceinline__ uint4 none() {
+    constexpr uint32_t x = DT == DLLM_BF16 ? 0xFF80FF80u : 0xFF800000u;
+    return make_uint4(x, x, x, x);
+  }
+  // (a function of its own: eight of it in a row take longer to fetch than to run)
+  static __device__ __noinline__ uint4 load_edge(const char* base, int vec, int e, int V) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -155,6 +163,16 @@ struct Row {
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // The first two elements of q, which go from it.
+  static __device__ __forceinline__ void take2(uint4& q, float& a, float& b) {
+    if constexpr (DT == DLLM_BF16) {
+      a = bf16lo(q.x), b = bf16hi(q.x);
+      q.x = q.y, q.y = q.z, q.z = q.w;
+    } else {
+      a = __uint_as_float(q.x), b = __uint_as_float(q.y);
+      q.x = q.z, q.y = q.w;
+    }
   }
 };
 
@@ -178,6 +196,69 @@ __device__ __forceinline__ T warp_scan(T x) {  // inclusive
   return x;
 }
 
+// Bitonic sort of kThreads * E keys, E a thread, rising: neighbours in a thread's registers, then lanes of
+// a warp by shuffles, then warps through `keys`.  (A row of 1500 with top_k 900, two sorts: 33 us; with
+// every step through shared memory 63.)
+template <int E>
+__device__ __noinline__ void sort_block(uint64_t* keys, int n) {
+  const int t = threadIdx.x;
+  uint64_t k[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) k[e] = t * E + e < n ? keys[t * E + e] : ~uint64_t{0};
+#pragma unroll 1
+  for (int len = 2; len <= kThreads * E; len *= 2) {
+#pragma unroll 1
+    for (int d = len / 2; d >= E; d /= 2) {
+      const int far = d / E;  // threads apart
+      // the lower of a pair keeps the smaller key in a rising run (E <= d < len: a thread's run is one)
+      const bool small = ((t & far) == 0) == ((t * E & len) == 0);
+      if (far < 32) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint64_t o = __shfl_xor_sync(kFull, k[e], far);
+          k[e] = (o < k[e]) == small ? o : k[e];
+        }
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) keys[e * kThreads + t] = k[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint64_t o = keys[e * kThreads + (t ^ far)];
+          k[e] = (o < k[e]) == small ? o : k[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int d = E / 2; d > 0; d /= 2) {
+      if (d >= len) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (e & d) continue;
+        const uint64_t x = k[e], y = k[e | d];
+        if ((x > y) == (((t * E + e) & len) == 0)) k[e] = y, k[e | d] = x;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) keys[t * E + e] = k[e];
+  __syncthreads();
+}
+// Sort keys[0, n), n <= kCap; behind them come the largest ones.
+__device__ __forceinline__ void sort_keys(uint64_t* keys, int n) {
+  static_assert(kCap == 8 * kThreads, "");
+  if (n <= kThreads)
+    sort_block<1>(keys, n);
+  else if (n <= 2 * kThreads)
+    sort_block<2>(keys, n);
+  else if (n <= 4 * kThreads)
+    sort_block<4>(keys, n);
+  else
+    sort_block<8>(keys, n);
+}
+
 // One row, by the CTAs of a cluster (kCluster) or one CTA: each has a contiguous range of tiles.
 template <int DT, bool kCluster>
 struct Sampler {
@@ -185,13 +266,17 @@ struct Sampler {
   Shared& s;
   Shared& first;    // of the cluster's first CTA
   Fine& fine;
-  uint64_t* sums;   // [tiles of a CTA], behind fine
+  uint64_t* sums;   // of groups of tiles, or of strips; behind fine
   float* tops;      // [groups * 32] maximum of a chunk
-  float* masses;    // [groups * 32] weights of a chunk, to the reference refs[group]; where fine is
+  float* masses;    // [groups * 32] weights of a chunk, to the reference refs[group]
   float* refs;      // [groups]
+  uint64_t* keys;   // [cap] candidates: ~order(z) << 32 | id
+  uint64_t* first_keys;  // the first CTA's
+  uint16_t* queue;  // [cap] chunks that are looked through again
   Row<DT> row;
   int rank, ranks;
   int tile0, tiles, groups;
+  int strips_log2;  // strips that are summed up together
   float m, total;   // of the row: maximum, sum of exp(z - m)
   float highest;    // of this thread's elements
 
@@ -199,6 +284,27 @@ struct Sampler {
                                      const char* r)
       : p(p_), s(s_), first(f_), fine(fine_), row(r, p_.V) {}
 
+  // Its part of the row, and of the shared memory.
+  __device__ __forceinline__ void place(uint8_t* dyn, int rank_, int ranks_) {
+    rank = rank_;
+    ranks = ranks_;
+    const int all = (row.vecs + kTileVecs - 1) / kTileVecs;
+    tile0 = static_cast<int>(static_cast<int64_t>(all) * rank / ranks);
+    tiles = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / ranks) - tile0;
+    groups = (tiles + (1 << p.span_log2) - 1) >> p.span_log2;
+    // single strips where there are few (32 rows of 1500: 25 us, by whole tiles 34), else so many together
+    // that every warp has four sums or more (200 rows of 120000: 100 us, by single strips 129)
+    strips_log2 = 0;
+    while ((2 << strips_log2) <= kLaneVecs && tiles * kLaneVecs >> strips_log2 >= 8 * kWarps) ++strips_log2;
+    tops = reinterpret_cast<float*>(dyn + sizeof(Shared));
+    masses = tops + groups * 32;
+    refs = masses + groups * 32;
+    sums = reinterpret_cast<uint64_t*>(dyn + p.sums_at);
+    keys = reinterpret_cast<uint64_t*>(dyn + p.keys_at);
+    queue = reinterpret_cast<uint16_t*>(keys + p.cap);
+    first_keys = keys;
+    if constexpr (kCluster) first_keys = cg::this_cluster().map_shared_rank(keys, 0);
+  }
   __device__ __forceinline__ void sync() const {
     if constexpr (kCluster)
       cg::this_cluster().sync();
@@ -212,27 +318,51 @@ struct Sampler {
       return s;
   }
 
-  // f(z, id) of the elements of a tile, by one warp (every lane calls it as often; elements outside
-  // the row come as -inf with an id outside [0, V)).
-  // (A vector at a time: unrolled over a tile, an f of fifty instructions runs out of the instruction
-  // cache, and a row takes 50 us instead of 20.)
-  template <typename F>
-  __device__ __forceinline__ void each_of_tile(int tile, F f) const {
-    const int v0 = tile * kTileVecs + (threadIdx.x & 31);
-    uint4 next = row.load(v0);
-#pragma unroll 1
-    for (int u = 0; u < kLaneVecs; ++u) {
-      const uint4 q = next;
-      if (u + 1 < kLaneVecs) next = row.load(v0 + 32 * (u + 1));
-      float x[Row<DT>::VEC];
-      unpack_vec<DT>(q, x);
+  // f(z, id) of the elements of this CTA's part, a strip (32 vectors) at a time, 2^strips_log2 in a row by
+  // one warp; after(these strips' number) by every lane (elements outside the row come as -inf with an id
+  // outside [0, V)).
+  // (Two elements at a time: unrolled further, the code of an f of sixty instructions takes longer to
+  // fetch than to run.)
+  template <typename F, typename G>
+  __device__ __forceinline__ void each(F f, G after) const {
+    constexpr int kAhead = 3;  // vectors on their way
+    const int warp = threadIdx.x >> 5, mask = (1 << strips_log2) - 1, strips = tiles * kLaneVecs;
+    const int v0 = tile0 * kTileVecs + (threadIdx.x & 31);
+    // the i-th strip of this warp
+    auto strip_of = [&](int i) { return (warp + (i >> strips_log2) * kWarps) << strips_log2 | (i & mask); };
+    auto fetch = [&](int strip, uint4& q) {
+      const int vec = v0 + 32 * strip;
+      if (strip >= strips) return;
+      if (vec - (threadIdx.x & 31) > 0 && vec - (threadIdx.x & 31) + 32 < row.vecs)
+        q = row.whole(vec);
+      else
+        q = row.load(vec);
+    };
+    uint4 next[kAhead];
 #pragma unroll
-      for (int j = 0; j < Row<DT>::VEC; ++j) f(x[j], row.id(v0 + 32 * u) + j);
+    for (int u = 0; u < kAhead; ++u) fetch(strip_of(u), next[u]);
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const int k = strip_of(i);
+      if (k >= strips) break;
+      uint4 q = next[0];
+#pragma unroll
+      for (int u = 0; u + 1 < kAhead; ++u) next[u] = next[u + 1];
+      fetch(strip_of(i + kAhead), next[kAhead - 1]);
+      int id = row.id(v0 + 32 * k);
+#pragma unroll 1
+      for (int j = 0; j < Row<DT>::VEC; j += 2, id += 2) {
+        float a, b;
+        Row<DT>::take2(q, a, b);
+        f(a, id);
+        f(b, id + 1);
+      }
+      if ((i & mask) == mask) after(k >> strips_log2);
     }
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int t = threadIdx.x >> 5; t < tiles; t += kWarps) each_of_tile(tile0 + t, f);
+    each(f, [](int) {});
   }
 
   __device__ __forceinline__ uint64_t weight(float z) const { return weight_fixed(z, m, p.t, s.pow2); }
@@ -372,6 +502,14 @@ struct Sampler {
       }
     }
   }
+  // A value of every CTA of the row, summed up, and of those before this one; every lane calls it.
+  template <typename F>
+  __device__ __forceinline__ uint64_t sum_of_ranks(F get, uint64_t& before) const {
+    const int lane = threadIdx.x & 31;
+    const uint64_t x = lane < ranks ? get(lane) : 0;
+    before = warp_sum(lane < rank ? x : 0);
+    return warp_sum(x);
+  }
   // (reference, sum) pairs of up to 32 parts, joined; every warp calls it.
   template <typename F>
   __device__ __forceinline__ float2 joined(int n, F get) const {
@@ -432,8 +570,8 @@ struct Sampler {
     b1 = static_cast<int>(__reduce_min_sync(kFull, static_cast<unsigned>(b1)));
   }
 
-  // The weights of this CTA's part by groups, and how much of that is known to 32 bits only: all of it,
-  // or (kRefine) what lies in chunks that weigh little; the others are summed up element by element.
+  // The weights of this CTA's groups, from the sums of chunks; kRefine: those of chunks that weigh much
+  // element by element.
   template <bool kRefine>
   __device__ __forceinline__ void weigh_chunks() {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -465,6 +603,7 @@ struct Sampler {
         todo &= todo - 1;
         const int t1 = min((g + 1) << p.span_log2, tiles);
         for (int t = g << p.span_log2; t < t1; ++t) {
+#pragma unroll 1
           for (int e = lane; e < kLaneVecs * Row<DT>::VEC; e += 32) {
             const int id = row.id((tile0 + t) * kTileVecs + 32 * (e / Row<DT>::VEC) + l) + e % Row<DT>::VEC;
             if (id >= 0 && id < p.V) in_heavy += weight(row.at(id));
@@ -476,17 +615,21 @@ struct Sampler {
       light += in_light;
       mass += in_light + in_heavy;
     }
-    if (lane == 0) s.warp_mass[warp] = mass, s.warp_light[warp] = light;
+    set_mass(mass, light);
+  }
+  static constexpr float kHeavy = 0x1p-8f;  // of this CTA's weights
+  __device__ __forceinline__ void set_mass(uint64_t of_warp, uint64_t light) {
+    if ((threadIdx.x & 31) == 0) s.warp_mass[threadIdx.x >> 5] = of_warp, s.warp_light[threadIdx.x >> 5] = light;
     __syncthreads();
     if (threadIdx.x == 0) {
-      mass = light = 0;
+      uint64_t mass = 0;
+      light = 0;
       for (int w = 0; w < kWarps; ++w) mass += s.warp_mass[w], light += s.warp_light[w];
       s.mine.mass = mass;
       s.mine.light = light;
     }
     __syncthreads();
   }
-  static constexpr float kHeavy = 0x1p-8f;  // of this CTA's weights
   // A sum over chunks is off by less than this share of the light ones among them (at most 2^20 terms
   // of at least 2^-20 each make up half of a sum that is at least 1): 20 * 2^-23 * ln 2 of the
   // exponents, 2^-22 of each term and of the factors, and the additions.
@@ -502,30 +645,93 @@ struct Sampler {
       for (int g = warp; g < groups; g += kWarps) {
         if (!(tops[g * 32 + lane] >= t)) continue;
         const int at = atomicAdd(&s.queued, 1);
-        if (at < kQueue) s.queue[at] = static_cast<uint16_t>(g * 32 + lane);
+        if (at < p.cap) queue[at] = static_cast<uint16_t>(g * 32 + lane);
       }
     }
     __syncthreads();
     // more chunks than the list holds: no need to look
     const int queued = s.queued;
-    if (queued > kQueue) {
-      if (threadIdx.x == 0) atomicAdd(&first.ctl.listed, kCap + 1);
+    if (queued > p.cap) {
+      if (threadIdx.x == 0) atomicAdd(&first.ctl.listed, p.cap + 1);
       return;
     }
-    for (int k = threadIdx.x; k < queued * kLaneVecs; k += kThreads) {
-      const int chunk = s.queue[k / kLaneVecs], g = chunk >> 5;
-      const int t1 = min((g + 1) << p.span_log2, tiles);
-      for (int tile = g << p.span_log2; tile < t1; ++tile) {
-        const int vec = (tile0 + tile) * kTileVecs + 32 * (k % kLaneVecs) + (chunk & 31);
-        const uint4 q = row.load(vec);
-        if (!(vec_max<DT>(q) >= t)) continue;
-        float x[Row<DT>::VEC];
-        unpack_vec<DT>(q, x);
+    constexpr int kAhead = 4;  // vectors on their way
+    const int each_log2 = kLaneVecsLog2 + p.span_log2, all = queued << each_log2;
+    for (int k0 = threadIdx.x; k0 < all; k0 += kAhead * kThreads) {
+      uint4 q[kAhead];
+      int vec[kAhead];
 #pragma unroll
-        for (int j = 0; j < Row<DT>::VEC; ++j)
-          if (x[j] >= t && x[j] > -INFINITY) append(x[j], row.id(vec) + j);
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u * kThreads;
+        q[u] = Row<DT>::none();
+        vec[u] = 0;
+        if (k >= all) continue;
+        const int chunk = queue[k >> each_log2];
+        const int tile = ((chunk >> 5) << p.span_log2) + (k >> kLaneVecsLog2 & ((1 << p.span_log2) - 1));
+        vec[u] = (tile0 + tile) * kTileVecs + 32 * (k & (kLaneVecs - 1)) + (chunk & 31);
+        if (tile < tiles) q[u] = row.load(vec[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (!(vec_max<DT>(q[u]) >= t)) continue;
+        int id = row.id(vec[u]);
+#pragma unroll 1
+        for (int j = 0; j < Row<DT>::VEC; j += 2, id += 2) {
+          float a, b;
+          Row<DT>::take2(q[u], a, b);
+          if (a >= t && a > -INFINITY) append(a, id);
+          if (b >= t && b > -INFINITY) append(b, id + 1);
+        }
       }
     }
+  }
+
+  // First CTA: drops listed candidates that come behind the k-th (by_k) or behind the mass `goal`, as far as
+  // coarse bins tell; how many are left.  (The list began with what the largest of chunks alone reach.)
+  __device__ __forceinline__ int drop_behind(int n, bool by_k, uint64_t goal) const {
+    constexpr int kEach = kCap / kThreads;
+    int* const low = s.coarse;   // of weights in a bin (or their number): the lower 21 bits' sum
+    int* const high = s.row_coarse;
+    for (int b = threadIdx.x; b < kCoarseBins; b += kThreads) low[b] = high[b] = 0;
+    if (threadIdx.x == 0) s.queued = 0;
+    __syncthreads();
+    static_assert(kCap <= 1 << 11 && kWeightBits - 21 + 11 <= 32, "sums of 2048 in 32 bits");
+#pragma unroll 1
+    for (int k = threadIdx.x; k < n; k += kThreads) {
+      const float y = octaves_below(listed_z(k), m, p.t) * kCoarse;
+      if (!(y < kCoarseBins)) continue;
+      const int b = static_cast<int>(y);
+      if (by_k) {
+        atomicAdd(low + b, 1);
+      } else {
+        const uint64_t w = weight(listed_z(k));
+        atomicAdd(reinterpret_cast<unsigned*>(low + b), static_cast<unsigned>(w & ((1u << 21) - 1)));
+        atomicAdd(reinterpret_cast<unsigned*>(high + b), static_cast<unsigned>(w >> 21));
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int b0, b1;
+      coarse_reach(
+          [&](int b) {
+            return static_cast<float>(static_cast<unsigned>(low[b])) +
+                   static_cast<float>(static_cast<unsigned>(high[b])) * 0x1p21f;
+          },
+          by_k ? static_cast<float>(p.top_k) : static_cast<float>(goal) * 1.0001f, INFINITY, b0, b1);
+      if (threadIdx.x == 0) s.from = b0 < kCoarseBins ? logit_of(m, b0) : -INFINITY;
+    }
+    uint64_t mine[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) mine[e] = e * kThreads + threadIdx.x < n ? keys[e * kThreads + threadIdx.x] : 0;
+    __syncthreads();
+    const float from = s.from;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (e * kThreads + threadIdx.x < n && of_order(~static_cast<uint32_t>(mine[e] >> 32)) >= from)
+        keys[atomicAdd(&s.queued, 1)] = mine[e];
+    }
+    __syncthreads();
+    return s.queued;
   }
 
   // x rounded up (down) to whole units, in every thread: the doubles cost one warp's time, not eight's
@@ -546,7 +752,7 @@ struct Sampler {
     const int i = threadIdx.x >> sh, part = threadIdx.x & (step - 1);
     if (threadIdx.x == 0) s.ctl.found = INT_MAX, s.ctl.bin = n - 1, s.ctl.mass = 0, s.ctl.lo = 0u;
     if (threadIdx.x < n) {
-      const uint64_t key = s.keys[threadIdx.x];
+      const uint64_t key = keys[threadIdx.x];
       s.few[threadIdx.x] = make_ulonglong2(key, weight(listed_z(threadIdx.x)));
     }
     __syncthreads();
@@ -610,41 +816,35 @@ struct Sampler {
     return s.ctl.found == INT_MAX ? -1 : s.ctl.found;
   }
 
-  // The same for up to kCap candidates, by sorting.
-  __device__ __noinline__ int draw_listed(int n, float u, uint64_t goal_p, uint64_t error, float least,
-                                          bool reaches) {
-    constexpr int kEach = kCap / kThreads;
+  // The same for up to kCap candidates, by sorting.  (Weights are computed again where they are needed
+  // again: a thread has eight at most, and loops are short to fetch.)
+  __device__ __forceinline__ int draw_listed(int n, float u, uint64_t goal_p, uint64_t error, float least,
+                                             bool reaches) {
     sort_list(n);
-    uint64_t w[kEach], mass = 0;
+    const int each = (n + kThreads - 1) / kThreads, at0 = threadIdx.x * each, at1 = min(at0 + each, n);
+    uint64_t mass = 0;
     int count = 0;
     if (threadIdx.x == 0) s.ctl.bin = n - 1, s.ctl.lo = 0u, s.ctl.found = -1;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int at = threadIdx.x * kEach + k;
-      w[k] = at < n ? weight(listed_z(at)) : 0;
-      mass += w[k];
-    }
-    block_scan(mass, count);
     const int limit = min(n, p.top_k);
     if (p.top_p < 1.0) {
-      uint64_t upto = mass;
+#pragma unroll 1
+      for (int at = at0; at < at1; ++at) mass += weight(listed_z(at));
+      block_scan(mass, count);
       if (p.top_k < p.V) {
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          upto += w[k];
-          if (threadIdx.x * kEach + k == limit - 1)
-            s.goal = static_cast<uint64_t>(ceil(p.top_p * static_cast<double>(upto)));
+        if (at0 < limit && at1 >= limit) {
+          uint64_t upto = mass;
+#pragma unroll 1
+          for (int at = at0; at < limit; ++at) upto += weight(listed_z(at));
+          s.goal = static_cast<uint64_t>(ceil(p.top_p * static_cast<double>(upto)));
         }
         __syncthreads();
         goal_p = s.goal;
-        upto = mass;
       }
-#pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        const int at = threadIdx.x * kEach + k;
+      uint64_t upto = mass;
+#pragma unroll 1
+      for (int at = at0; at < at1; ++at) {
         const uint64_t before = upto;
-        upto += w[k];
-        if (at >= n) continue;
+        upto += weight(listed_z(at));
         if (before < goal_p && upto >= goal_p) s.ctl.bin = at;
         if (error != 0 && ((upto + error >= goal_p && upto <= goal_p + error) ||
                            (reaches && at == limit - 1 && upto < goal_p + error)))
@@ -653,79 +853,71 @@ struct Sampler {
       __syncthreads();
       if (s.ctl.lo != 0u) return -2;
     }
+    __syncthreads();
     const int last = min(s.ctl.bin, limit - 1);
-    __syncthreads();
     // the kept by id: key id << 32 | order(z)
-    uint64_t keys[kEach];
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int at = threadIdx.x * kEach + k;
-      const bool keep = at <= last && listed_z(at) >= least;
-      keys[k] = keep ? static_cast<uint64_t>(listed_id(at)) << 32 | order_of(listed_z(at)) : ~uint64_t{0};
+#pragma unroll 1
+    for (int at = at0; at < min(at1, last + 1); ++at) {
+      const float z = listed_z(at);
+      keys[at] = z >= least ? static_cast<uint64_t>(listed_id(at)) << 32 | order_of(z) : ~uint64_t{0};
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int at = threadIdx.x * kEach + k;
-      if (at <= last) s.keys[at] = keys[k];
-    }
-    __syncthreads();
     sort_list(last + 1);
+    auto weight_at = [&](int at) {
+      return keys[at] != ~uint64_t{0} ? weight(of_order(static_cast<uint32_t>(keys[at]))) : 0;
+    };
+    const int end = min(at1, last + 1);
     mass = 0;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int at = threadIdx.x * kEach + k;
-      const bool there = at <= last && s.keys[at] != ~uint64_t{0};
-      w[k] = there ? weight(of_order(static_cast<uint32_t>(s.keys[at]))) : 0;
-      mass += w[k];
-    }
+#pragma unroll 1
+    for (int at = at0; at < end; ++at) mass += weight_at(at);
     const uint64_t own = mass;
     block_scan(mass, count);
     if (threadIdx.x == kThreads - 1)
       s.goal = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(mass + own));
     __syncthreads();
     const uint64_t goal = s.goal;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const bool was = mass > goal;
-      mass += w[k];
-      if (!was && mass > goal) s.ctl.found = static_cast<int>(s.keys[threadIdx.x * kEach + k] >> 32);
+    if (!(mass > goal) && mass + own > goal) {
+#pragma unroll 1
+      for (int at = at0; at < end; ++at) {
+        mass += weight_at(at);
+        if (mass > goal) {
+          s.ctl.found = static_cast<int>(keys[at] >> 32);
+          break;
+        }
+      }
     }
     __syncthreads();
     return s.ctl.found;
   }
 
-  // The id in tiles [t, t1) at which the sum of f(z, id) by rising id, `before` before them, exceeds
-  // `goal` (it does); by the whole CTA, a tile at a time, a warp each 32 of its vectors.  -2 where that
-  // sum comes within `error` of the goal before or behind the token.  T: uint64_t, or float for weights
-  // relative to the largest.
-  template <typename T, typename F>
-  __device__ __forceinline__ void find_in_tiles(int t, int t1, T before, T goal, T error, F f) {
+  // The id in tiles [t, t1) at which the sum of weights relative to the largest exceeds `goal` (it does);
+  // by the whole CTA, a tile at a time, a warp each 32 of its vectors.  Left as it is where that sum comes
+  // within `error` of the goal before or behind the token.
+  __device__ __forceinline__ void find_in_tiles(int t, int t1, float goal, float error) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* of_warp = reinterpret_cast<T*>(s.warp_mass);
+    float before = 0.f;
     for (; t < t1; ++t) {
       const int vec = (tile0 + t) * kTileVecs + 32 * warp + lane;
       float x[Row<DT>::VEC];
       unpack_vec<DT>(row.load(vec), x);
-      T w[Row<DT>::VEC], sum = 0;
+      float w[Row<DT>::VEC], sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < Row<DT>::VEC; ++j) w[j] = f(x[j], row.id(vec) + j), sum += w[j];
-      T upto = warp_scan(sum);
-      if (lane == 31) of_warp[warp] = upto;
+      for (int j = 0; j < Row<DT>::VEC; ++j) w[j] = ex2((x[j] - m) * p.t.hi), sum += w[j];
+      float upto = warp_scan(sum);
+      if (lane == 31) s.part[warp].x = upto;
       __syncthreads();
-      T from = before;
+      float from = before;
       for (int k = 0; k < kWarps; ++k) {
         if (k == warp) from = before;
-        before += of_warp[k];
+        before += s.part[k].x;
       }
       upto += from;
       if (upto > goal && !(upto - sum > goal)) {
         upto -= sum;
 #pragma unroll
         for (int j = 0; j < Row<DT>::VEC; ++j) {
-          const T low = upto;
+          const float low = upto;
           upto += w[j];
-          if (!(low > goal) && upto > goal && w[j] > 0 && (error == 0 || (upto > goal + error && low + error < goal)))
+          if (!(low > goal) && w[j] > 0.f && upto > goal + error && low + error < goal)
             first.ctl.found = row.id(vec) + j;
         }
       }
@@ -751,39 +943,28 @@ struct Sampler {
 
   // No filter: the group of tiles, then the token in it, by the weights of chunks; -2 where their error
   // leaves either open.
-  template <bool kRefine>
   __device__ __forceinline__ int draw_whole(float u) {
     constexpr float kOfUnit = 1.f / static_cast<float>(int64_t{1} << kWeightBits);
+    uint64_t before_own;
+    uint64_t none;
+    const uint64_t all = sum_of_ranks([&](int r) { return of(r).mine.mass; }, before_own);
+    const uint64_t light = sum_of_ranks([&](int r) { return of(r).mine.light; }, none);
     if (threadIdx.x == 0) {
-      uint64_t before = 0, all = 0, light = 0;
-      for (int r = 0; r < ranks; ++r) {
-        const Summary& o = of(r).mine;
-        if (r < rank) before += o.mass;
-        all += o.mass;
-        light += o.light;
-      }
       s.goal = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(all));
       // u * all, the sum before a tile and the sum in it
       s.goal_error = static_cast<uint64_t>(2.0 * kError * static_cast<double>(light)) + 2 * kRounding * ranks;
-      s.group_before = before;
+      s.group_before = before_own;
       if (rank == 0) s.ctl.found = -2;
     }
     sync();
-    const uint64_t goal = s.goal, error = s.goal_error;
-    uint64_t before = s.group_before;
+    const uint64_t goal = s.goal, before = s.group_before;
     if (before <= goal && before + s.mine.mass > goal) {
       __syncthreads();
       if (threadIdx.x < 32) find_group(sums, groups, before, goal);
       __syncthreads();
-      const int group = s.group;
-      before = s.group_before;
-      const int t0 = group << p.span_log2, t1 = min((group + 1) << p.span_log2, tiles);
-      if constexpr (kRefine)
-        find_in_tiles<uint64_t>(t0, t1, before, goal, error, [&](float z, int) { return weight(z); });
-      else
-        find_in_tiles<float>(t0, t1, 0.f, static_cast<float>(goal - before) * kOfUnit,
-                             static_cast<float>(error) * kOfUnit,
-                             [&](float z, int) { return ex2((z - m) * p.t.hi); });
+      find_in_tiles(s.group << p.span_log2, min((s.group + 1) << p.span_log2, tiles),
+                    static_cast<float>(goal - s.group_before) * kOfUnit,
+                    static_cast<float>(s.goal_error) * kOfUnit);
     }
     sync();
     return first.ctl.found;
@@ -795,34 +976,64 @@ struct Sampler {
   template <typename F, typename G>
   __device__ __forceinline__ int locate(F f, G goal_of) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int t = warp; t < tiles; t += kWarps) {
-      uint64_t sum = 0;
-      each_of_tile(tile0 + t, [&](float z, int id) { sum += f(z, id); });
-      sum = warp_sum(sum);
-      if (lane == 0) sums[t] = sum;
-    }
-    if (threadIdx.x == 0 && rank == 0) s.ctl.found = -1;
+    uint64_t sum = 0, of_warp = 0;
+    each([&](float z, int id) { sum += f(z, id); },
+         [&](int unit) {
+           sum = warp_sum(sum);
+           if (lane == 0) sums[unit] = sum;
+           of_warp += sum;
+           sum = 0;
+         });
+    if (lane == 0) s.warp_mass[warp] = of_warp;
     __syncthreads();
-    if (warp == 0) {
-      uint64_t sum = 0;
-      for (int t = lane; t < tiles; t += 32) sum += sums[t];
-      sum = warp_sum(sum);
-      if (lane == 0) s.total[0] = sum;
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kWarps; ++w) of_warp += s.warp_mass[w];
+      s.total[0] = of_warp;
+      if (rank == 0) s.ctl.found = -1;
     }
     sync();
-    uint64_t before = 0, all = 0;
-    for (int r = 0; r < ranks; ++r) {
-      const uint64_t x = of(r).total[0];
-      if (r < rank) before += x;
-      all += x;
-    }
+    uint64_t before;
+    const uint64_t all = sum_of_ranks([&](int r) { return of(r).total[0]; }, before);
     set_goal([&] { s.goal = goal_of(all); });
     const uint64_t goal = s.goal;
-    if (before <= goal && before + s.total[0] > goal) {
-      __syncthreads();
-      if (warp == 0) find_group(sums, tiles, before, goal);
-      __syncthreads();
-      find_in_tiles<uint64_t>(s.group, s.group + 1, s.group_before, goal, uint64_t{0}, f);
+    if (warp == 0 && before <= goal && before + s.total[0] > goal) {
+      find_group(sums, tiles * kLaneVecs >> strips_log2, before, goal);
+      __syncwarp();
+      uint64_t upto = s.group_before;
+      const int vec0 = tile0 * kTileVecs + (32 * s.group << strips_log2) + lane;
+#pragma unroll 1
+      for (int u = 0; u < 1 << strips_log2; ++u) {
+        const int vec = vec0 + 32 * u;
+        const uint4 q = row.load(vec);
+        const int id = row.id(vec);
+        sum = 0;
+        uint4 left = q;
+        float a, b;
+#pragma unroll 1
+        for (int j = 0; j < Row<DT>::VEC; j += 2) {
+          Row<DT>::take2(left, a, b);
+          sum += f(a, id + j) + f(b, id + j + 1);
+        }
+        const uint64_t scan = warp_scan(sum);
+        uint64_t here = upto + scan - sum;
+        if (!(here > goal) && here + sum > goal) {
+          left = q;
+#pragma unroll 1
+          for (int j = 0; j < Row<DT>::VEC; j += 2) {
+            Row<DT>::take2(left, a, b);
+            here += f(a, id + j);
+            int at = here > goal ? id + j : -1;
+            here += f(b, id + j + 1);
+            if (at < 0 && here > goal) at = id + j + 1;
+            if (at >= 0) {
+              first.ctl.found = at;
+              break;
+            }
+          }
+        }
+        upto += __shfl_sync(kFull, scan, 31);
+        if (upto > goal) break;
+      }
     }
     sync();
     const int id = first.ctl.found;
@@ -835,7 +1046,8 @@ struct Sampler {
   __device__ __forceinline__ uint32_t* bin_words(int b) {
     return reinterpret_cast<uint32_t*>(&fine.bins_lo_hi[b]);
   }
-  __device__ __forceinline__ void histogram() {
+  // (counts: how many, too; only top_k asks for it)
+  __device__ __forceinline__ void histogram(bool counts) {
     for (int b = threadIdx.x; b < kBins; b += kThreads) fine.bins_lo_hi[b] = 0, fine.bins[b] = 0;
     __syncthreads();
     each([&](float z, int) {
@@ -846,16 +1058,22 @@ struct Sampler {
       const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(words, lo);
       const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u);
       if (hi) atomicAdd(words + 1, hi);
-      atomicAdd(&fine.bins[b], 1);
+      if (counts) atomicAdd(&fine.bins[b], 1);
     });
     sync();
     if (rank == 0 && ranks > 1) {
       for (int b = threadIdx.x; b < kBins; b += kThreads) {
-        for (int r = 1; r < ranks; ++r) {
+        uint64_t mass = fine.bins_lo_hi[b];
+        int count = fine.bins[b];
+#pragma unroll
+        for (int r = 1; r < kMaxRanks; ++r) {  // (all loads on their way together)
+          if (r >= ranks) break;
           const Fine& o = *cg::this_cluster().map_shared_rank(&fine, r);
-          fine.bins_lo_hi[b] += o.bins_lo_hi[b];
-          fine.bins[b] += o.bins[b];
+          mass += o.bins_lo_hi[b];
+          count += o.bins[b];
         }
+        fine.bins_lo_hi[b] = mass;
+        fine.bins[b] = count;
       }
     }
     __syncthreads();
@@ -874,9 +1092,10 @@ struct Sampler {
   }
   // Warp 0: what top_p has to reach of the sum of all weights, and how far that may be off.
   __device__ __forceinline__ void set_mass_goal() {
+    uint64_t before;
+    const uint64_t all = sum_of_ranks([&](int r) { return of(r).mine.mass; }, before);
+    const uint64_t light = sum_of_ranks([&](int r) { return of(r).mine.light; }, before);
     if (threadIdx.x == 0) {
-      uint64_t all = 0, light = 0;
-      for (int r = 0; r < ranks; ++r) all += of(r).mine.mass, light += of(r).mine.light;
       s.goal = static_cast<uint64_t>(ceil(p.top_p * static_cast<double>(all)));
       s.goal_error = static_cast<uint64_t>(kError * static_cast<double>(light)) + kRounding * ranks;
     }
@@ -929,66 +1148,53 @@ struct Sampler {
       sync();
       return;
     }
-    if (in_bin <= kCap) {
+    int listed = in_bin;  // (0 where they were not counted)
+    if (listed <= p.cap) {
       each([&](float z, int id) {
         if (bin_of(z) == bin) append(z, id);
       });
       sync();
+      listed = first.ctl.listed;
+    }
+    if (listed <= p.cap) {
       if (rank == 0) cut_in_list(goal);
       sync();
     } else {
       cut_in_bin(goal, bin);
     }
   }
+  // Largest top_k that is tried with a list.
+  __device__ __forceinline__ int list_k() const { return p.cap - p.cap / 4; }
   __device__ __forceinline__ void append(float z, int id) {
     const int at = atomicAdd(&first.ctl.listed, 1);
-    if (at < kCap) first.keys[at] = static_cast<uint64_t>(~order_of(z)) << 32 | static_cast<uint32_t>(id);
+    if (at < p.cap) first_keys[at] = static_cast<uint64_t>(~order_of(z)) << 32 | static_cast<uint32_t>(id);
   }
-  // Sort keys[0, n) rising (n <= kCap; the rest up to a power of two is filled up).
   __device__ __forceinline__ void sort_list(int n) {
-    int size = 2;
-    while (size < n) size *= 2;
-    for (int k = n + threadIdx.x; k < size; k += kThreads) s.keys[k] = ~uint64_t{0};
     __syncthreads();
-    for (int len = 2; len <= size; len *= 2) {
-      for (int d = len / 2; d > 0; d /= 2) {
-        for (int k = threadIdx.x; k < size / 2; k += kThreads) {
-          const int i = 2 * d * (k / d) + k % d, j = i + d;
-          const uint64_t a = s.keys[i], b = s.keys[j];
-          if ((a > b) == ((i & len) == 0)) s.keys[i] = b, s.keys[j] = a;
-        }
-        __syncthreads();
-      }
-    }
+    sort_keys(keys, n);
   }
   __device__ __forceinline__ float listed_z(int k) const {
-    return of_order(~static_cast<uint32_t>(s.keys[k] >> 32));
+    return of_order(~static_cast<uint32_t>(keys[k] >> 32));
   }
-  __device__ __forceinline__ int listed_id(int k) const { return static_cast<int>(s.keys[k] & 0xFFFFFFFFu); }
+  __device__ __forceinline__ int listed_id(int k) const { return static_cast<int>(keys[k] & 0xFFFFFFFFu); }
 
   // First CTA: the cut among the listed candidates, behind ctl.before and ctl.count_before.
   __device__ __forceinline__ void cut_in_list(const Goal& goal) {
-    constexpr int kEach = kCap / kThreads;
-    const int n = min(s.ctl.listed, kCap);
+    const int n = min(s.ctl.listed, p.cap);
     sort_list(n);
-    uint64_t w[kEach], mass = 0;
-    int count = 0;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int at = threadIdx.x * kEach + k;
-      w[k] = at < n ? weight(listed_z(at)) : 0;
-      mass += w[k];
-      count += at < n ? 1 : 0;
-    }
+    const int each = (n + kThreads - 1) / kThreads, at0 = threadIdx.x * each, at1 = min(at0 + each, n);
+    uint64_t mass = 0;
+    int count = max(at1 - at0, 0);
+#pragma unroll 1
+    for (int at = at0; at < at1; ++at) mass += weight(listed_z(at));
     block_scan(mass, count);
     mass += s.ctl.before;
     count += s.ctl.count_before;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int at = threadIdx.x * kEach + k;
+#pragma unroll 1
+    for (int at = at0; at < at1; ++at) {
       const bool was = goal.reached(count, mass);
-      if (at < n) mass += w[k], ++count;
-      if (at < n && !was && goal.reached(count, mass)) {
+      mass += weight(listed_z(at));
+      if (!was && goal.reached(++count, mass)) {
         s.ctl.cut = Cut{listed_z(at), listed_id(at)};
         s.ctl.mass = mass;
       }
@@ -998,7 +1204,7 @@ struct Sampler {
 
   // The cut inside a bin of more candidates than are sorted: the value by bisection, then how many of
   // the candidates with that value.
-  __device__ __noinline__ void cut_in_bin(const Goal& goal, int bin) {
+  __device__ __forceinline__ void cut_in_bin(const Goal& goal, int bin) {
     // reached from lo on, not from hi on
     uint32_t lo = 0u, hi = 0xFFFFFFFFu;
     const uint64_t before = first.ctl.before;
@@ -1052,17 +1258,18 @@ struct Sampler {
       s.total[1] = y;
     }
     sync();
-    a = b = 0;
-    for (int r = 0; r < ranks; ++r) a += of(r).total[0], b += of(r).total[1];
+    uint64_t before;
+    a = sum_of_ranks([&](int r) { return of(r).total[0]; }, before);
+    b = sum_of_ranks([&](int r) { return of(r).total[1]; }, before);
   }
 
   // The token by passes over all weights, whatever the filters keep.
-  __device__ __noinline__ int draw_any(float u) {
+  __device__ __forceinline__ int draw_any(float u) {
     Cut cut{-INFINITY, INT_MAX};
     sync();  // what the chunks' sums were is overwritten
     const bool by_k = p.top_k < p.V, by_p = p.top_p < 1.0;
     if (by_k || by_p) {
-      histogram();
+      histogram(by_k);
       if (by_k) {
         find_cut(Goal{false, p.top_k, 0});
         cut = first.ctl.cut;
@@ -1111,7 +1318,7 @@ struct Sampler {
     else
       pass<true, false>();
     // top_k: the logits that all of k, and an even share of it, of this CTA's chunks reach
-    if (by_k && p.top_k <= kListK) {
+    if (by_k && p.top_k <= list_k()) {
       // (thread maxima will do where there are twice as many: they are as good as k chunks)
       if (m > -INFINITY) coarse_histogram<false>(m, p.top_k <= kThreads / 2);
       if (threadIdx.x < 32) {
@@ -1141,42 +1348,57 @@ struct Sampler {
     float t = -INFINITY;  // all that the filters keep is from this logit on
     uint64_t goal = 0, error = 0;
     bool reaches = true;  // the list is not cut short by min_p
+    bool sure = true;     // all that is kept is listed
     if (by_mass) {
       weigh_chunks<false>();
       if (!by_p) {
         sync();
-        int token = draw_whole<false>(u);
+        int token = draw_whole(u);
         if (token == -2) {
           weigh_chunks<true>();
           sync();
-          token = draw_whole<true>(u);
+          token = draw_whole(u);
         }
         return token;
       }
       coarse_histogram<true>(m, false);
       sync();
+      for (int b = threadIdx.x; b < kCoarseBins; b += kThreads) {
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r)  // (all loads on their way together)
+          if (r < ranks) n += of(r).coarse[b];
+        s.row_coarse[b] = n;
+      }
+      __syncthreads();
       if (threadIdx.x < 32) {
         set_mass_goal();
-        const float all = static_cast<float>(s.goal);
-        int b0, b1;
+        // the maxima that reach the mass, but no more of them than the list is likely to hold (the mass
+        // of all that is listed may reach it all the same)
+        int b0, b1, none;
         coarse_reach(
             [&](int b) {
-              int n = 0;
-              for (int r = 0; r < ranks; ++r) n += of(r).coarse[b];
-              return static_cast<float>(n) * ex2(b * (-1.f / kCoarse) - 12.f);
+              return static_cast<float>(s.row_coarse[b]) * ex2(b * (-1.f / kCoarse) - 12.f);
             },
-            all * 0x1.002p-42f, INFINITY, b0, b1);
-        if (threadIdx.x == 0) s.from = b0 < kCoarseBins ? logit_of(m, b0) : -INFINITY;
+            static_cast<float>(s.goal) * 0x1.002p-42f, INFINITY, b0, none);
+        coarse_reach([&](int b) { return static_cast<float>(s.row_coarse[b]) * (1.f / 3750.f); },
+                     static_cast<float>(p.cap / 4), INFINITY, b1, none);
+        if (threadIdx.x == 0) {
+          s.from = min(b0, b1) < kCoarseBins ? logit_of(m, min(b0, b1)) : -INFINITY;
+          s.sure = b0 <= b1;
+        }
       }
       __syncthreads();
       goal = s.goal;
       error = s.goal_error;
       t = fmaxf(s.from, least);
       reaches = s.from > least;
+      sure = s.sure || !reaches;
     } else if (by_k) {
-      if (p.top_k <= kListK) {
-        float some = INFINITY, all = -INFINITY;
-        for (int r = 0; r < ranks; ++r) some = fminf(some, of(r).mine.some), all = fmaxf(all, of(r).mine.all);
+      if (p.top_k <= list_k()) {
+        const int lane = threadIdx.x & 31;
+        const float some = -warp_max(lane < ranks ? -of(lane).mine.some : -INFINITY);
+        const float all = warp_max(lane < ranks ? of(lane).mine.all : -INFINITY);
         // what lies further below weighs nothing
         t = fmaxf(fmaxf(some, all), logit_of(m, kCoarseBins - 1));
       }
@@ -1184,44 +1406,65 @@ struct Sampler {
     } else {
       t = least;
     }
-    if (t > -INFINITY || p.V <= kCap) {
+    if (t > -INFINITY || p.V <= p.cap) {
       list_from(t);
       sync();
-      const int n = first.ctl.listed;
-      if (n > 0 && n <= kCap) {
-        if (rank == 0) {
-          const int token = n <= kFew ? draw_few(n, u, goal, error, least, reaches)
-                                      : listed(n, u, goal, error, least, reaches);
-          if (threadIdx.x == 0) s.ctl.hi = static_cast<uint32_t>(token);
+      int n = first.ctl.listed;
+      if (n > 0 && n <= p.cap) {
+        for (bool again = false;; again = true) {
+          if (rank == 0) {
+            bool whole = true;  // all that is kept is listed
+            if ((n > kFew || !sure) && (by_k || by_mass) && !again) {
+              n = tightened(n, by_k, goal + error);
+              whole = sure || s.from > -INFINITY;
+            }
+            const int token = !whole       ? -3
+                              : n <= kFew ? draw_few(n, u, goal, error, least, reaches)
+                                          : listed(n, u, goal, error, least, reaches);
+            if (threadIdx.x == 0) s.ctl.hi = static_cast<uint32_t>(token);
+          }
+          if (!by_mass || again) break;
+          sync();
+          if (static_cast<int>(first.ctl.hi) != -2) break;
+          // once more, with the sum of weights known better
+          weigh_chunks<true>();
+          sync();
+          if (threadIdx.x < 32) set_mass_goal();
+          __syncthreads();
+          goal = s.goal;
+          error = s.goal_error;
         }
-        if (!by_mass) return rank == 0 ? static_cast<int>(s.ctl.hi) : -1;
-        sync();
-        if (static_cast<int>(first.ctl.hi) != -2) return static_cast<int>(first.ctl.hi);
-        // once more, with the sum of weights known better
-        weigh_chunks<true>();
-        sync();
-        if (rank != 0) return -1;
-        if (threadIdx.x < 32) set_mass_goal();
-        __syncthreads();
-        goal = s.goal;
-        error = s.goal_error;
-        return n <= kFew ? draw_few(n, u, goal, error, least, reaches)
-                         : listed(n, u, goal, error, least, reaches);
+        return rank == 0 ? max(static_cast<int>(s.ctl.hi), -2) : -1;
       }
-      sync();
     }
-    if (by_mass) return -2;
-    return in_full(u);
+    return by_mass ? -2 : in_full(u);
+  }
+  // Functions of their own, of copies: so the members stay in registers here and there.
+  static __device__ __noinline__ int listed_of(const Sampler& x, int n, float u, uint64_t goal, uint64_t error,
+                                               float least, bool reaches) {
+    Sampler own(x);
+    return own.draw_listed(n, u, goal, error, least, reaches);
+  }
+  static __device__ __noinline__ int tightened_of(const Sampler& x, int n, bool by_k, uint64_t goal) {
+    const Sampler own(x);
+    return own.drop_behind(n, by_k, goal);
+  }
+  static __device__ __noinline__ int in_full_of(const Sampler& x, float u) {
+    Sampler own(x);
+    return own.draw_any(u);
   }
   __device__ __forceinline__ int listed(int n, float u, uint64_t goal, uint64_t error, float least,
                                         bool reaches) const {
-    Sampler copy(*this);
-    return copy.draw_listed(n, u, goal, error, least, reaches);
+    const Sampler copy(*this);
+    return listed_of(copy, n, u, goal, error, least, reaches);
   }
-  // (on a copy, so that the members stay in registers here)
+  __device__ __forceinline__ int tightened(int n, bool by_k, uint64_t goal) const {
+    const Sampler copy(*this);
+    return tightened_of(copy, n, by_k, goal);
+  }
   __device__ __forceinline__ int in_full(float u) const {
-    Sampler copy(*this);
-    return copy.draw_any(u);
+    const Sampler copy(*this);
+    return in_full_of(copy, u);
   }
 };
 
@@ -1245,18 +1488,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   Shared* first = &s;
   if constexpr (kCluster) first = cg::this_cluster().map_shared_rank(&s, 0);
   const char* logits = p.logits + r * p.row_stride_bytes;
-  Fine& fine = *reinterpret_cast<Fine*>(dyn + sizeof(Shared) + p.tops_bytes);
+  Fine& fine = *reinterpret_cast<Fine*>(dyn + sizeof(Shared));
   Sampler<DT, kCluster> x(p, s, *first, fine, logits);
-  x.rank = rank;
-  x.ranks = ranks;
-  const int tiles = (x.row.vecs + kTileVecs - 1) / kTileVecs;
-  x.tile0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / ranks);
-  x.tiles = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / ranks) - x.tile0;
-  x.groups = (x.tiles + (1 << p.span_log2) - 1) >> p.span_log2;
-  x.tops = reinterpret_cast<float*>(dyn + sizeof(Shared));
-  x.masses = reinterpret_cast<float*>(&fine);
-  x.refs = x.masses + x.groups * 32;
-  x.sums = reinterpret_cast<uint64_t*>(dyn + p.sums_at);
+  x.place(dyn, rank, ranks);
   const float u = fminf(fmaxf(p.uniform[r], 0.f), 0x1.fffffep-1f);
   const int token = x.draw(u);
   if (rank == 0 && threadIdx.x == 0) {
@@ -1275,7 +1509,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
 // The rows that sample_kernel left open, a cluster each: there are few of them or none, and in
 // sample_kernel one of them would hold a CTA ten times as long as its neighbours.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) sample_rest_kernel(const __grid_constant__ SampleParams p,
+__global__ void __launch_bounds__(kThreads, 3) sample_rest_kernel(const __grid_constant__ SampleParams p,
                                                                   int rows) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ unsigned open[kWarps];
@@ -1301,12 +1535,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rest_kernel(const __grid_c
       const char* logits = p.logits + r * p.row_stride_bytes;
       Sampler<DT, true> x(p, s, *cluster.map_shared_rank(&s, 0), *reinterpret_cast<Fine*>(dyn + sizeof(Shared)),
                           logits);
-      x.rank = rank;
-      x.ranks = ranks;
-      const int tiles = (x.row.vecs + kTileVecs - 1) / kTileVecs;
-      x.tile0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / ranks);
-      x.tiles = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / ranks) - x.tile0;
-      x.sums = reinterpret_cast<uint64_t*>(dyn + sizeof(Shared) + sizeof(Fine));
+      x.place(dyn, rank, ranks);
       x.m = p.out.row_max[r];
       const int token = x.draw_any(fminf(fmaxf(p.uniform[r], 0.f), 0x1.fffffep-1f));
       if (rank == 0 && threadIdx.x == 0) {
@@ -1314,26 +1543,42 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rest_kernel(const __grid_c
         p.out.conf[r] =
             token < 0 ? 0.f : ex2((load_logit(logits, DT, token) - x.m) * kLog2e) * p.out.conf[r];
       }
+      cluster.sync();  // nobody leaves, or goes on, while its shared memory may be read
     }
-    cluster.sync();  // nobody leaves, or looks again, while shared memory may be read
+    __syncthreads();
   }
 }
 
+// Shares a row of `tiles` tiles out to `ranks` CTAs; their shared memory.
+// in_full: for draw_any too.
+size_t lay_out(SampleParams& p, int64_t tiles, int ranks, bool in_full, int cap) {
+  const int64_t own = (tiles + ranks - 1) / ranks;
+  p.span_log2 = 0;
+  while ((own >> p.span_log2) >= kMaxGroups) ++p.span_log2;
+  const size_t groups = static_cast<size_t>((own >> p.span_log2) + 1);
+  p.cap = cap;
+  p.sums_at = static_cast<uint32_t>(
+      sizeof(Shared) + std::max(in_full ? sizeof(Fine) : 0, align_up(groups * (2 * 128 + 4), 16)));
+  p.keys_at = p.sums_at + static_cast<uint32_t>(in_full ? own * kLaneVecs : groups) * 8;
+  return p.keys_at + static_cast<size_t>(cap) * (8 + 2);
+}
+
 template <int DT>
-cudaError_t launch_rest(const SampleParams& p, int64_t rows, int64_t tiles, int sm_count,
+cudaError_t launch_rest(SampleParams p, int64_t rows, int64_t tiles, int sm_count,
                         cudaStream_t stream) {
-  constexpr int kRanks = 8;
+  int ranks = 1;  // a tile or more each
+  while (ranks < kMaxRanks && tiles > 2 * ranks) ranks *= 2;
   cudaError_t e = allow_smem<sample_rest_kernel<DT>>(200 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int64_t clusters = std::min<int64_t>(rows, std::max(1, 4 * sm_count / kRanks));
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kRanks));
+  const int64_t clusters = std::min<int64_t>(rows, std::max(1, 4 * sm_count / ranks));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared) + sizeof(Fine) + static_cast<size_t>(tiles / kRanks + 2) * 8;
+  cfg.dynamicSmemBytes = lay_out(p, tiles, ranks, true, kCap);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kRanks;
+  attr[0].val.clusterDim.x = ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -1385,17 +1630,12 @@ cudaError_t launch_sample(const void* logits, const dllm_shape& sh, const uint8_
   const int64_t rows = static_cast<int64_t>(sh.B) * sh.L;
   const int64_t tiles = (static_cast<int64_t>(sh.V) * es + 16 * kTileVecs - 1) / (16 * kTileVecs) + 1;
   int ranks = 1;
-  while (ranks < 8 && rows * ranks * 2 <= 4 * static_cast<int64_t>(sm_count) &&
+  while (ranks < kMaxRanks && rows * ranks * 2 <= 4 * static_cast<int64_t>(sm_count) &&
          tiles >= 2 * ranks)
     ranks *= 2;
-  // a CTA's tiles (rows may begin anywhere in a vector), in groups
-  const int64_t own = (tiles + ranks - 1) / ranks;
-  while ((own >> p.span_log2) >= kMaxGroups) ++p.span_log2;
-  const size_t groups = static_cast<size_t>((own >> p.span_log2) + 1);
-  p.tops_bytes = static_cast<uint32_t>(align_up(groups * 128, 16));
-  const size_t shared_part = std::max(sizeof(Fine), align_up(groups * 132, 16));
-  p.sums_at = static_cast<uint32_t>(sizeof(Shared) + p.tops_bytes + align_up(shared_part, 16));
-  const size_t smem = p.sums_at + static_cast<size_t>(own + 1) * 8;
+  // rows are left open only where the sum of all weights counts
+  const bool by_mass = p.top_k == p.V && (p.top_p < 1.0 || p.log_min_p == -INFINITY);
+  const size_t smem = lay_out(p, tiles, ranks, !by_mass, by_mass && p.top_p == 1.0 ? 0 : kCap);
   cudaError_t e;
   if (sh.dtype == DLLM_BF16)
     e = ranks > 1 ? launch<DLLM_BF16, true>(p, rows, ranks, smem, stream)
@@ -1403,8 +1643,6 @@ cudaError_t launch_sample(const void* logits, const dllm_shape& sh, const uint8_
   else
     e = ranks > 1 ? launch<DLLM_F32, true>(p, rows, ranks, smem, stream)
                   : launch<DLLM_F32, false>(p, rows, ranks, smem, stream);
-  // rows are left open only where the sum of all weights counts
-  const bool by_mass = p.top_k == p.V && (p.top_p < 1.0 || p.log_min_p == -INFINITY);
   if (e != cudaSuccess || !by_mass) return e;
   return sh.dtype == DLLM_BF16 ? launch_rest<DLLM_BF16>(p, rows, tiles, sm_count, stream)
                                : launch_rest<DLLM_F32>(p, rows, tiles, sm_count, stream);
