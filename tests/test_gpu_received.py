@@ -204,3 +204,18 @@ def test_larger_and_repeated(n, B):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("n", [8, 9, 16, 17, 32, 33])
+def test_few_and_many_rows(D, n):
+    """Rows around the numbers at which one kernel takes over from the other."""
+    cache, q, _ = setup(2, 6, 2, 48, D, n, 1, n)
+    lens = torch.tensor([257, 255], dtype=torch.int32, device="cuda")
+    check(cache, q, lens, 280, causal=n % 2 == 0)
+
+
+@pytest.mark.parametrize("scale", [1e-7, -1e-7])
+def test_scales_beyond_the_many_rows_form(scale):
+    cache, q, _ = setup(1, 8, 2, 64, 128, 50, 2, 13)
+    check(cache, q, None, 500, scale=scale, causal=True)

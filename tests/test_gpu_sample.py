@@ -257,3 +257,34 @@ def test_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(stats.argmax, want.argmax) and torch.equal(stats.conf, want.conf)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1, 100, 129, 300, 513, 700, 1500, 2047, 2049, 5000])
+def test_kept_by_number(dtype, size):
+    """Nuclei and top-k sets of as many candidates as lists hold, a few more and far more: `size` tokens
+    stand out of 9001, alone or with a few chunks full of them."""
+    V, R = 9001, 6
+    g = torch.Generator(device="cuda").manual_seed(size)
+    z = torch.randn(R, V, device="cuda", generator=g) - 12.0
+    up = torch.rand(R, size, device="cuda", generator=g)
+    at = torch.rand(R, V, device="cuda", generator=g).argsort(1)[:, :size]
+    at[R // 2:] = torch.arange(size, device="cuda") + 17
+    z.scatter_(1, at, up)
+    for i, how in enumerate([dict(top_p=0.9), dict(top_k=size), dict(top_k=size, top_p=0.95),
+                             dict(top_p=0.999, min_p=0.4), dict(min_p=0.2)]):
+        u = uniform(R, 100 * size + i)
+        stats, seen = call(z, dtype, u, temperature=1.0, **how)
+        check(stats, seen, u, temperature=1.0, **how)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V", [(2, 1000), (40, 5000), (330, 12345)])
+def test_flat_rows(dtype, R, V):
+    """Rows that the sums of chunks leave open: no token weighs more than their error."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = 0.3 * torch.randn(R, V, device="cuda", generator=g)
+    for i, how in enumerate([dict(), dict(top_p=0.9), dict(top_p=0.1), dict(top_k=V - 1, top_p=0.5)]):
+        u = uniform(R, V + i)
+        stats, seen = call(z, dtype, u, temperature=1.5, **how)
+        check(stats, seen, u, temperature=1.5, **how)
