@@ -2,6 +2,8 @@
 
     python -m diffusion_decoding_gb300.kernel_driver {stats|probs|gemm|step|fused} [n [B L]]
     python -m diffusion_decoding_gb300.kernel_driver {rope|cache|token|block|piece} [n]
+    python -m diffusion_decoding_gb300.kernel_driver {whole|nucleus|top_k} [n [B L]]
+    python -m diffusion_decoding_gb300.kernel_driver {token_weights|block_weights|piece_weights|evict} [n]
 
 The inputs have the smoothing-step sizes (B=16, L=64, V=126464 bf16 logits, d=2048 embedding
 table; about 0.8 GB on the device), so every launch reads more than the L2 holds; `stats`
@@ -15,6 +17,10 @@ The second line runs the operators of the KV refresh (below 0.5 GB on the device
 rotation of 16384 tokens, `cache` write and read of 32768 entries, `token` attention of single tokens
 over 32 sequences of 8192 entries, `block` of 64-token blocks over 16 of 4160, `piece` of 1024 tokens of
 a prompt over 2 of 16384.
+
+The third line draws tokens of a block: `whole` from the distribution at temperature 0.7, `nucleus` with
+top_p 0.9 too, `top_k` with top_k 50 at temperature 1.  The fourth runs the accumulated weights of the
+second line's three calls of attention, and `evict` cuts 32 sequences of 8192 entries to 4096.
 """
 import sys
 
@@ -44,7 +50,8 @@ def refresh_operator(what: str, n: int) -> None:
     B, m, heads, group, T, causal = {"cache": (8, 4096, 8, 1, 4096, False),
                                      "token": (32, 1, 8, 4, 8192, False),
                                      "block": (16, 64, 2, 8, 4160, False),
-                                     "piece": (2, 1024, 8, 4, 16384, True)}[what]
+                                     "evict": (32, 1, 8, 4, 8192, False),
+                                     "piece": (2, 1024, 8, 4, 16384, True)}[what.removesuffix("_weights")]
     cache = dd.Kv4Cache(B * (T // page), heads, page, D, B, T // page, dev)
     cache.table.copy_(torch.randperm(B * (T // page), device=dev).view(B, -1).to(torch.int32))
     for b in range(0, T, 1024):  # fill it, a stretch of entries at a time
@@ -59,8 +66,25 @@ def refresh_operator(what: str, n: int) -> None:
             dd.dllm_kv4_read(cache, k, v, pos)
         torch.cuda.synchronize()
         return
+    weights = torch.rand(B, T, device=dev)
+    if what == "evict":
+        lens = torch.empty(B, dtype=torch.int32, device=dev)
+        slots = torch.empty(B, T, dtype=torch.int32, device=dev)
+        ws = dd.workspace(dd.dllm_kv4_evict_workspace_bytes(cache, B, T), dev)
+        for _ in range(n):
+            dd.dllm_kv4_evict(cache, weights, None, T, T // 2, slots, lens, ws)
+        torch.cuda.synchronize()
+        return
     q = torch.randn(B, m, heads * group, D, device=dev).to(bf16)
     out = torch.empty_like(q)
+    if what.endswith("_weights"):
+        lse = torch.full((B, heads * group, m), 9.0, device=dev)  # about what such queries have
+        ws = dd.workspace(dd.dllm_attention_kv4_weights_workspace_bytes(cache, B, m, heads * group, T), dev)
+        for _ in range(n):
+            dd.dllm_attention_kv4_weights(q, cache, None, T, lse, weights, ws, causal=causal)
+        if dd.dllm_get_status(ws) != dd.DLLM_OK:
+            raise SystemExit("the accumulated weights reported a fault")
+        return
     ws = dd.workspace(dd.dllm_attention_kv4_workspace_bytes(cache, B, m, heads * group, T), dev)
     for _ in range(n):
         dd.dllm_attention_kv4(q, cache, None, T, out, ws, causal=causal)
@@ -71,12 +95,14 @@ def refresh_operator(what: str, n: int) -> None:
 def main(argv) -> None:
     what = argv[0] if argv else "step"
     n = int(argv[1]) if len(argv) > 1 else 4
-    if what in ("rope", "cache", "token", "block", "piece"):
+    if what in ("rope", "cache", "token", "block", "piece", "token_weights", "block_weights", "piece_weights",
+                "evict"):
         refresh_operator(what, n)
         return
-    if what not in ("stats", "probs", "gemm", "step", "fused"):
+    draws = {"whole": dict(temperature=0.7), "nucleus": dict(temperature=0.7, top_p=0.9), "top_k": dict(top_k=50)}
+    if what not in ("stats", "probs", "gemm", "step", "fused", *draws):
         raise SystemExit(f"unknown kernel family {what!r}")
-    B, L = (int(argv[2]), int(argv[3])) if what == "stats" and len(argv) > 3 else (B_, L_)
+    B, L = (int(argv[2]), int(argv[3])) if what in ("stats", *draws) and len(argv) > 3 else (B_, L_)
     dev = torch.device("cuda")
     g = torch.Generator(device=dev)
     g.manual_seed(7)
@@ -84,6 +110,13 @@ def main(argv) -> None:
     lg = torch.randn(B, L, V, device=dev, generator=g).mul_(2).to(torch.bfloat16)
     state, stats = dd.BlockState(B, L), dd.StatsBuffers(B * L)
     ws = dd.workspace(dd.dllm_workspace_bytes(shape))
+    if what in draws:
+        lg[..., :32] += 12.0 - torch.arange(32, device=dev) / 4  # a head over the bulk
+        uniform = torch.rand(B * L, device=dev, generator=g)
+        for _ in range(n):
+            dd.dllm_sample(lg, shape, None, uniform, stats, **draws[what])
+        torch.cuda.synchronize()
+        return
     if what == "stats":
         for _ in range(n):
             state.reset()
