@@ -10,6 +10,11 @@
 // sequence are laid out in shared memory as the fragments want them.  The sums over rows and heads stay
 // in the lanes, so nothing is joined.  Where there are few entries the warps of a CTA share out the heads
 // and add up at the end.
+//
+// Bound by instructions: 490 for 32 entries of a head of 128 channels (codes to bf16 more than a third),
+// the integer pipe is 53 % busy.  32 sequences of up to 8192 entries, 8 heads of 128, 4 rows each: 41 us,
+// 0.42 of the copy rate (with codes loaded to registers ahead instead of through the ring 43; a warp a head
+// with its queries in registers 54; CTAs of four warps 47).
 #include <algorithm>
 
 #include "attention.h"

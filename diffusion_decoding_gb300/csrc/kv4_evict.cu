@@ -9,8 +9,14 @@
 // sorted in one CTA (a bin of more entries than the list holds is narrowed down by the other bits, and
 // equal weights by counting in order), which gives the border: the last entry kept.  Kept and dropped
 // entries are then numbered by counting in order, and the moves left in the workspace.
-// kv4_evict_move_kernel copies 16 bytes of codes and a param word a thread and step, eight steps at a
-// time so that enough loads are under way, and finishes slots and weights of the entries it moves.
+// kv4_evict_move_kernel copies 16 bytes of codes and a param word a thread and move, two moves at a time and
+// the next two's loads before these are stored, and finishes slots and weights of the entries it moves.
+//
+// The selection is bound by its chain of barriers (one CTA a sequence 14 us for 8192 entries in registers;
+// clusters of smaller CTAs 24, as each reads the others' histograms), the copies by memory in sectors: an
+// entry's param words of a head are 8 bytes of a 32-byte sector.  32 sequences of up to 8192 entries cut to
+// 4096: 46 us in all, 127 + 52 MB of DRAM traffic in the copies (more moves a warp at a time 46 to 90); one
+// of 65536 cut to 16384 23 us; a short one 12, the host's time for two launches.
 #include <limits.h>
 
 #include <algorithm>
