@@ -13,13 +13,14 @@
 // to 2^-18 of what its chunks hold, and the row is settled where that error changes nothing; chunks that
 // weigh much are summed up exactly for a second try).  Without a filter the sums of chunks lead to the
 // token in the same way.  What stays open, or has more candidates than the list holds, goes through exact
-// passes over all weights: sample_rest_kernel, a cluster a row (or, with top_k, at once: in_full).
+// passes over all weights: sample_rest_kernel, a cluster a row (or, in clusters and with top_k, at once:
+// in_full).
 //
 // The one pass is bound by its special-function operations and by loads in flight: one exponential an
 // element at temperature 1, two at another, 64 KB of loads a CTA's turn at four CTAs an SM.  1024 rows of
 // 126464 bf16 logits: 60 us with top_k 50, 60 drawn from the whole distribution at 0.7 (80 with a few rows
 // left open), 69 with top_p 0.9 there: 4.3 and 3.8 TB/s; fp32 99 to 121 us (5.2 to 4.3 TB/s).  A single
-// row 9 to 15 us: launch, barriers and first fetches of code.  Clusters where the rows fill the GPU
+// row 8 to 13 us: launch, barriers and first fetches of code.  Clusters where the rows fill the GPU
 // anyway cost more than they even out (640 rows: 2 CTAs a row 56 to 70 us, one 48 to 55).
 #include <algorithm>
 #include <climits>
@@ -57,6 +58,7 @@ struct SampleParams {
   int span_log2;           // tiles of a group
   uint32_t sums_at, keys_at;  // in shared memory
   int cap;                 // candidates that are listed, a power of two
+  bool at_once;            // no row is left to sample_rest_kernel
   const uint8_t* masked;   // null: every row
   const float* uniform;
   dllm_stats out;
@@ -1373,6 +1375,7 @@ struct Sampler {
           sync();
           token = draw_whole(u);
         }
+        if (kCluster && p.at_once && token == -2) return in_full(u);
         return token;
       }
       coarse_histogram<true>(m, false);
@@ -1437,9 +1440,9 @@ struct Sampler {
                                           : listed(n, u, goal, error, least, reaches);
             if (threadIdx.x == 0) s.ctl.hi = static_cast<uint32_t>(token);
           }
-          if (!by_mass || again) break;
+          if (!by_mass || (!kCluster && again)) break;
           sync();
-          if (static_cast<int>(first.ctl.hi) != -2) break;
+          if (static_cast<int>(first.ctl.hi) != -2 || again) break;
           // once more, with the sum of weights known better
           weigh_chunks<true>();
           sync();
@@ -1448,10 +1451,14 @@ struct Sampler {
           goal = s.goal;
           error = s.goal_error;
         }
+        if (kCluster && by_mass) {
+          const int token = static_cast<int>(first.ctl.hi);
+          if (token == -3 || (token == -2 && p.at_once)) return in_full(u);
+        }
         return rank == 0 ? max(static_cast<int>(s.ctl.hi), -2) : -1;
       }
     }
-    return by_mass ? -2 : in_full(u);
+    return by_mass && !kCluster ? -2 : in_full(u);
   }
   // Functions of their own, of copies: so the members stay in registers here and there.
   static __device__ __noinline__ int listed_of(const Sampler& x, int n, float u, uint64_t goal, uint64_t error,
@@ -1647,9 +1654,14 @@ cudaError_t launch_sample(const void* logits, const dllm_shape& sh, const uint8_
   while (ranks < kMaxRanks && rows * ranks * 2 <= 4 * static_cast<int64_t>(sm_count) &&
          tiles >= 2 * ranks)
     ranks *= 2;
-  // rows are left open only where the sum of all weights counts
-  const bool by_mass = p.top_k == p.V && (p.top_p < 1.0 || p.log_min_p == -INFINITY);
-  const size_t smem = lay_out(p, tiles, ranks, !by_mass, by_mass && p.top_p == 1.0 ? 0 : kCap);
+  // Rows are left open only where the sum of all weights counts, and not by clusters of four and more or of
+  // whole rows: these take the exact passes at once (32 rows of 1500 to 120000, nothing open: 8 to 9 us, with
+  // the second kernel 10 to 11).  A CTA or two would take longer over a row than the second kernel's eight
+  // (200 rows of 120000 with a few open: 83 us, with it 46), except where all rows are open because they are
+  // flat: what clusters of two cannot list they do at once too (200 such rows: 319 us, else 482).
+  p.at_once = p.top_k < p.V || (p.top_p == 1.0 && p.log_min_p > -INFINITY) || ranks >= 4 ||
+              (ranks == 2 && tiles <= 4);
+  const size_t smem = lay_out(p, tiles, ranks, p.at_once || ranks > 1, !p.at_once && p.top_p == 1.0 ? 0 : kCap);
   cudaError_t e;
   if (sh.dtype == DLLM_BF16)
     e = ranks > 1 ? launch<DLLM_BF16, true>(p, rows, ranks, smem, stream)
@@ -1657,7 +1669,7 @@ cudaError_t launch_sample(const void* logits, const dllm_shape& sh, const uint8_
   else
     e = ranks > 1 ? launch<DLLM_F32, true>(p, rows, ranks, smem, stream)
                   : launch<DLLM_F32, false>(p, rows, ranks, smem, stream);
-  if (e != cudaSuccess || !by_mass) return e;
+  if (e != cudaSuccess || p.at_once) return e;
   return sh.dtype == DLLM_BF16 ? launch_rest<DLLM_BF16>(p, rows, tiles, sm_count, stream)
                                : launch_rest<DLLM_F32>(p, rows, tiles, sm_count, stream);
 }

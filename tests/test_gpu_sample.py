@@ -288,3 +288,17 @@ def test_flat_rows(dtype, R, V):
         u = uniform(R, V + i)
         stats, seen = call(z, dtype, u, temperature=1.5, **how)
         check(stats, seen, u, temperature=1.5, **how)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_flat_rows_by_two(dtype):
+    """The same where two CTAs share a row: borders in doubt go to the second kernel, long lists do not."""
+    R, V = 200, 15001
+    g = torch.Generator(device="cuda").manual_seed(4)
+    z = torch.randn(R, V, device="cuda", generator=g)
+    z[: R // 2] *= 0.2
+    z[::3, 77] += 9.0
+    for i, how in enumerate([dict(), dict(top_p=0.9), dict(top_p=0.3, min_p=0.001)]):
+        u = uniform(R, 50 + i)
+        stats, seen = call(z, dtype, u, temperature=1.2, **how)
+        check(stats, seen, u, temperature=1.2, **how)
