@@ -465,14 +465,15 @@ struct Sampler {
       return t;
     }
   }
-  // 2^(x k - ref k) is computed as 2^(x k - hi) * rest.
+  // 2^(x k - ref k) is computed as 2^(x k - hi) * rest, which needs a ref k that hi misses by little: both
+  // factors are within 2^(1/2) up to 2^24, and from 2^31 on one would be infinite and the other 0.
   struct Scale {
     float k, hi, rest;
     bool far;  // hi is no use
     __device__ __forceinline__ explicit Scale(float k_) : k(k_), hi(0.f), rest(1.f), far(false) {}
     __device__ __forceinline__ void set(float r) {
       hi = r * k;
-      far = !(fabsf(hi) < 0x1p100f);
+      far = !(fabsf(hi) < 0x1p24f);
       rest = ex2(-fmaf(r, k, -hi));
     }
   };
@@ -505,7 +506,7 @@ struct Sampler {
     unpack2(add2(s2[0], s2[1]), c, d);
     b = (c + d) * temp.rest;
   }
-  // (logits so large that ref * k overflows, or nearly)
+  // (logits so large that ref * k is off by one or more)
   template <bool kTwo>
   __device__ __forceinline__ void sums_far(const uint4 (&q)[kLaneVecs], float ref, float& a, float& b) const {
     a = b = 0.f;
