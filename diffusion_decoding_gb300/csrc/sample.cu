@@ -12,7 +12,7 @@
 // there on are listed, weighed exactly and ordered (the sum of all weights, which top_p needs, is known
 // to 2^-18 of what its chunks hold, and the row is settled where that error changes nothing; chunks that
 // weigh much are summed up exactly for a second try).  Without a filter the sums of chunks lead to the
-// token in the same way.  What stays open, or has more candidates than the list holds, goes through exact
+// token in the same way, and the second try walks the tiles that hold it by exact weights.  What stays open, or has more candidates than the list holds, goes through exact
 // passes over all weights: sample_rest_kernel, a cluster a row (or, in clusters and with top_k, at once:
 // in_full).
 //
@@ -944,6 +944,48 @@ struct Sampler {
       if (before > goal) break;
     }
   }
+  // The same by exact weights, in units: where the heavy chunks' sums are exact the guard is far below what
+  // sums in 32 bits are off by.
+  __device__ __forceinline__ void find_exactly(int t, int t1, uint64_t goal, uint64_t error) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t before = 0;
+    for (; t < t1; ++t) {
+      const int vec = (tile0 + t) * kTileVecs + 32 * warp + lane;
+      const uint4 q = row.load(vec);
+      uint4 left = q;
+      float a, b;
+      uint64_t sum = 0;
+#pragma unroll 1
+      for (int j = 0; j < Row<DT>::VEC; j += 2) {
+        Row<DT>::take2(left, a, b);
+        sum += weight(a) + weight(b);
+      }
+      uint64_t upto = warp_scan(sum);
+      if (lane == 31) s.warp_mass[warp] = upto;
+      __syncthreads();
+      uint64_t from = before;
+      for (int k = 0; k < kWarps; ++k) {
+        if (k == warp) from = before;
+        before += s.warp_mass[k];
+      }
+      upto += from;
+      if (upto > goal && !(upto - sum > goal)) {
+        uint64_t low = upto - sum;
+        int id = row.id(vec);
+        left = q;
+#pragma unroll 1
+        for (int j = 0; j < Row<DT>::VEC; j += 2, id += 2) {
+          Row<DT>::take2(left, a, b);
+          const uint64_t mid = low + weight(a), high = mid + weight(b);
+          if (low + error <= goal && mid > goal + error) first.ctl.found = id;
+          if (mid + error <= goal && high > goal + error) first.ctl.found = id + 1;
+          low = high;
+        }
+      }
+      __syncthreads();
+      if (before > goal) break;
+    }
+  }
   // Warp 0: the group in which the sum of sums[] exceeds goal, and the sum before it (there is
   // one).
   __device__ __forceinline__ void find_group(const uint64_t* of_group, int n, uint64_t before, uint64_t goal) {
@@ -960,8 +1002,9 @@ struct Sampler {
     }
   }
 
-  // No filter: the group of tiles, then the token in it, by the weights of chunks; -2 where their error
-  // leaves either open.
+  // No filter: the group of tiles by the weights of chunks, then the token in it; -2 where the error of
+  // sums in 32 bits leaves either open.  kAgain: behind weigh_chunks<true>.
+  template <bool kAgain>
   __device__ __forceinline__ int draw_whole(float u) {
     constexpr float kOfUnit = 1.f / static_cast<float>(int64_t{1} << kWeightBits);
     uint64_t before_own;
@@ -970,7 +1013,7 @@ struct Sampler {
     const uint64_t light = sum_of_ranks([&](int r) { return of(r).mine.light; }, none);
     if (threadIdx.x == 0) {
       s.goal = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(all));
-      // u * all, the sum before a tile and the sum in it
+      // u * all, the sum before a group and (in the first try) the sum in it
       s.goal_error = static_cast<uint64_t>(2.0 * kError * static_cast<double>(light)) + 2 * kRounding * ranks;
       s.group_before = before_own;
       if (rank == 0) s.ctl.found = -2;
@@ -981,9 +1024,12 @@ struct Sampler {
       __syncthreads();
       if (threadIdx.x < 32) find_group(sums, groups, before, goal);
       __syncthreads();
-      find_in_tiles(s.group << p.span_log2, min((s.group + 1) << p.span_log2, tiles),
-                    static_cast<float>(goal - s.group_before) * kOfUnit,
-                    static_cast<float>(s.goal_error) * kOfUnit);
+      const int t0 = s.group << p.span_log2, t1 = min((s.group + 1) << p.span_log2, tiles);
+      if (kAgain)
+        find_exactly(t0, t1, goal - s.group_before, s.goal_error);
+      else
+        find_in_tiles(t0, t1, static_cast<float>(goal - s.group_before) * kOfUnit,
+                      static_cast<float>(s.goal_error) * kOfUnit);
     }
     sync();
     return first.ctl.found;
@@ -1370,11 +1416,11 @@ struct Sampler {
       weigh_chunks<false>();
       if (!by_p) {
         sync();
-        int token = draw_whole(u);
+        int token = draw_whole<false>(u);
         if (token == -2) {
           weigh_chunks<true>();
           sync();
-          token = draw_whole(u);
+          token = draw_whole<true>(u);
         }
         if (kCluster && p.at_once && token == -2) return in_full(u);
         return token;

@@ -149,8 +149,8 @@ dllm_status dllm_decode_stats(const void* logits, const dllm_shape* shape, const
  *   probability under the model itself (no temperature, no filter).
  * The commit calls take these statistics with logits = NULL and so commit sampled tokens.
  * temperature 0 takes the most probable token (lowest id on ties), whatever the other fields.
- * Sums of weights are exact to 2^-36 of their terms, and weights below 2^-42 count as 0; the token
- * does not depend on how the work was split.  Rows with masked[r] = 0 are not read and get -inf,
+ * A weight is off by at most 2^-36 of itself and half of 2^-42, and counts as 0 below 2^-42; weights
+ * are summed exactly, so the token does not depend on how the work was split.  Rows with masked[r] = 0 are not read and get -inf,
  * -inf, 0, -1; so does a row without a finite logit, its lse and row_max being what they are.
  * masked: [B*L] uint8 or NULL (every row).  uniform: [B*L] fp32 in [0, 1) (others count as the
  * nearest in range, a NaN as 0).  temperature 0 or in [2^-10, 2^10]; top_k >= 0; 0 < top_p <= 1;
