@@ -150,8 +150,9 @@ dllm_status dllm_decode_stats(const void* logits, const dllm_shape* shape, const
  * The commit calls take these statistics with logits = NULL and so commit sampled tokens.
  * temperature 0 takes the most probable token (lowest id on ties), whatever the other fields.
  * A weight is off by at most 2^-36 of itself and half of 2^-42, and counts as 0 below 2^-42; weights
- * are summed exactly, so the token does not depend on how the work was split.  Rows with masked[r] = 0 are not read and get -inf,
- * -inf, 0, -1; so does a row without a finite logit, its lse and row_max being what they are.
+ * are summed exactly, so the token does not depend on how the work was split.  Rows with
+ * masked[r] = 0 are not read and get -inf, -inf, 0, -1; so does a row without a finite logit, its lse
+ * and row_max being what they are.
  * masked: [B*L] uint8 or NULL (every row).  uniform: [B*L] fp32 in [0, 1) (others count as the
  * nearest in range, a NaN as 0).  temperature 0 or in [2^-10, 2^10]; top_k >= 0; 0 < top_p <= 1;
  * 0 <= min_p <= 1; V <= 2^20.  Logits are finite or -inf.  No workspace.
@@ -568,8 +569,8 @@ dllm_status dllm_attention_kv4(const dllm_heads* q, const dllm_kv4_cache* cache,
  * weights and prior: fp32, row b from b * their stride on (strides >= max_len); they may be the same
  * memory with the same stride, and must not overlap otherwise; prior NULL: nothing is added, and keep
  * is not used.  Words of weights from len_b on are left as they are.  A query whose lse is -inf saw
- * nothing and adds nothing; a score that is NaN makes the weight of its entry NaN, a NaN of lse those
- * of all entries its query sees.  All in fp32, in a fixed order: repeated calls agree bit for bit.
+ * nothing and adds nothing, one whose lse is +inf adds 0 by the formula; a score that is NaN makes the
+ * weight of its entry NaN, a NaN of lse those of all entries its query sees.  All in fp32, in a fixed order: repeated calls agree bit for bit.
  * Limits as dllm_attention_kv4, and B * max_len <= 2^36.
  * ws: dllm_attention_kv4_weights_workspace_bytes(...) bytes (0 on invalid sizes).
  */
