@@ -206,12 +206,15 @@ __global__ void __launch_bounds__(256)
       w[0] = l != l ? 0x7FFFu : x.scale > 0.f ? 0xFF80u : 0x7F80u;
     } else {
       double rest = -static_cast<double>(l) / static_cast<double>(x.scale);
+      const float whole = static_cast<float>(rest);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t term = __float_as_uint(static_cast<float>(rest)) & 0xFFFF0000u;  // (cut: the rest follows)
         rest -= static_cast<double>(__uint_as_float(term));
         w[k >> 1] |= term >> (k & 1 ? 0 : 16);
       }
+      // (beyond the largest float the next terms would cancel it to NaN)
+      if (fabsf(whole) == INFINITY) w[0] = __float_as_uint(whole) >> 16, w[1] = 0u;
     }
     *reinterpret_cast<uint4*>(out + D * 128 + block_at(row, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(out + D * 128 + block_at(row, 8)) = make_uint4(0u, 0u, 0u, 0u);
