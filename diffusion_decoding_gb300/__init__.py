@@ -370,8 +370,20 @@ def dllm_workspace_bytes(shape: dllm_shape) -> int:
     return int(lib().dllm_workspace_bytes(ctypes.byref(shape)))
 
 
+def _check_stats(stats: StatsBuffers, rows: int) -> None:
+    """Calls write (or read) as many rows as the shape has, whatever the buffers hold."""
+    if stats.row_max.numel() < rows or stats.lse.numel() < rows or stats.conf.numel() < rows \
+            or stats.argmax.numel() < rows:
+        raise ValueError("the statistics buffers hold fewer than B*L rows")
+
+
+def _stats_c(stats: StatsBuffers, shape: dllm_shape) -> dllm_stats:
+    _check_stats(stats, shape.B * shape.L)
+    return stats.c()
+
+
 def dllm_decode_stats(logits, shape, masked, stats: StatsBuffers, ws, stream=None) -> None:
-    st = stats.c()
+    st = _stats_c(stats, shape)
     _check(lib().dllm_decode_stats(_ptr(logits), ctypes.byref(shape), _ptr(masked),
                                    ctypes.byref(st), _ptr(ws), _stream(stream)),
            "dllm_decode_stats")
@@ -388,6 +400,7 @@ def dllm_sample(logits, shape, masked, uniform, stats: StatsBuffers, temperature
         if masked.element_size() != 1 or masked.numel() != rows or not masked.is_contiguous():
             raise ValueError("masked must be [B*L] uint8, contiguous")
         open_ = masked.data_ptr()
+    _check_stats(stats, rows)
     out = _pack_stats(stats.row_max.data_ptr(), stats.lse.data_ptr(), stats.conf.data_ptr(),
                       stats.argmax.data_ptr())
     status = lib().dllm_sample(_ptr(logits), _byref(shape), open_, uniform.data_ptr(),
@@ -398,7 +411,7 @@ def dllm_sample(logits, shape, masked, uniform, stats: StatsBuffers, temperature
 
 def dllm_commit_threshold(logits, shape, stats: StatsBuffers, state: BlockState, tau: float,
                           eos_id: int, ws, stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_threshold(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                        ctypes.byref(bs), tau, eos_id, _ptr(ws), _stream(stream)),
            "dllm_commit_threshold")
@@ -407,7 +420,7 @@ def dllm_commit_threshold(logits, shape, stats: StatsBuffers, state: BlockState,
 def dllm_commit_hierarchical(logits, shape, stats: StatsBuffers, state: BlockState,
                              tau_low: float, min_width: int, eos_id: int, ws,
                              stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_hierarchical(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                           ctypes.byref(bs), tau_low, min_width, eos_id, _ptr(ws),
                                           _stream(stream)),
@@ -417,7 +430,7 @@ def dllm_commit_hierarchical(logits, shape, stats: StatsBuffers, state: BlockSta
 def dllm_commit_hierarchical_levels(logits, shape, stats: StatsBuffers, state: BlockState,
                                     tau_low: float, min_width: int, eos_id: int, ws,
                                     stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_hierarchical_levels(_ptr(logits), ctypes.byref(shape),
                                                  ctypes.byref(st), ctypes.byref(bs), tau_low,
                                                  min_width, eos_id, _ptr(ws), _stream(stream)),
@@ -427,7 +440,7 @@ def dllm_commit_hierarchical_levels(logits, shape, stats: StatsBuffers, state: B
 def dllm_commit_credit_tracked(logits, shape, stats: StatsBuffers, state: BlockState, K: int,
                                decay: float, boost: float, tau: float, eos_id: int, ws,
                                stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_credit_tracked(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                             ctypes.byref(bs), _ptr(state.cand_id),
                                             _ptr(state.cand_credit), K, decay, boost, tau, eos_id,
@@ -438,7 +451,7 @@ def dllm_commit_credit_tracked(logits, shape, stats: StatsBuffers, state: BlockS
 def dllm_commit_credit(logits, shape, stats: StatsBuffers, state: BlockState, K: int,
                        decay: float, boost: float, tau: float, eos_id: int, ws,
                        stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_credit(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                     ctypes.byref(bs), _ptr(state.cand_id),
                                     _ptr(state.cand_credit), K, decay, boost, tau, eos_id,
@@ -463,7 +476,7 @@ def dllm_smooth_workspace_bytes(shape: dllm_shape, d: int) -> int:
 
 def dllm_smooth_embed(logits, shape, stats: StatsBuffers, state: BlockState, Et, d: int, out,
                       row_ids, M, ws, stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_smooth_embed(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                    ctypes.byref(bs), _ptr(Et), d, _ptr(out), _ptr(row_ids),
                                    _ptr(M), _ptr(ws), ws.numel(), _stream(stream)),
@@ -473,7 +486,7 @@ def dllm_smooth_embed(logits, shape, stats: StatsBuffers, state: BlockState, Et,
 def dllm_commit_threshold_smooth(logits, shape, stats: StatsBuffers, state: BlockState,
                                  tau: float, eos_id: int, Et, d: int, out, row_ids, M, ws,
                                  stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_threshold_smooth(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                               ctypes.byref(bs), tau, eos_id, _ptr(Et), d,
                                               _ptr(out), _ptr(row_ids), _ptr(M), _ptr(ws),
@@ -490,7 +503,7 @@ def dllm_smooth_plan_info(shape, d: int) -> dict:
 
 def dllm_smooth_probs(logits, shape, stats: StatsBuffers, state: BlockState, d: int, row_ids, M,
                       ws, stream=None) -> None:
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_smooth_probs(_ptr(logits), ctypes.byref(shape), ctypes.byref(st),
                                    ctypes.byref(bs), d, _ptr(row_ids), _ptr(M), _ptr(ws),
                                    ws.numel(), _stream(stream)),
@@ -525,7 +538,7 @@ def dllm_commit_threshold_static(logits, shape, stats: StatsBuffers, state: Bloc
                                  eos_id: int, stream=None) -> None:
     """dllm_commit_threshold for callers that cannot allocate: no workspace argument, the
     scratch is a fixed static array inside the library (see include/dllm.h)."""
-    st, bs = stats.c(), state.c()
+    st, bs = _stats_c(stats, shape), state.c()
     _check(lib().dllm_commit_threshold_static(_ptr(logits), ctypes.byref(shape),
                                               ctypes.byref(st), ctypes.byref(bs), tau, eos_id,
                                               _stream(stream)),
