@@ -709,12 +709,13 @@ struct Sampler {
   // coarse bins tell; how many are left.  (The list began with what the largest of chunks alone reach.)
   __device__ __forceinline__ int drop_behind(int n, bool by_k, uint64_t goal) const {
     constexpr int kEach = kCap / kThreads;
-    int* const low = s.coarse;   // of weights in a bin (or their number): the lower 21 bits' sum
+    int* const low = s.coarse;   // of weights in a bin (or their number): the sum of the lower 22 bits' half
     int* const high = s.row_coarse;
     for (int b = threadIdx.x; b < kCoarseBins; b += kThreads) low[b] = high[b] = 0;
     if (threadIdx.x == 0) s.queued = 0;
     __syncthreads();
-    static_assert(kCap <= 1 << 11 && kWeightBits - 21 + 11 <= 32, "sums of 2048 in 32 bits");
+    // (a weight is at most 2^42, that included; a unit that a half drops keeps a candidate more, at worst)
+    static_assert(kCap <= 1 << 11 && kWeightBits - 22 + 11 < 32 && 21 + 11 <= 32, "sums of 2048 in 32 bits");
 #pragma unroll 1
     for (int k = threadIdx.x; k < n; k += kThreads) {
       const float y = octaves_below(listed_z(k), m, p.t) * kCoarse;
@@ -724,8 +725,8 @@ struct Sampler {
         atomicAdd(low + b, 1);
       } else {
         const uint64_t w = weight(listed_z(k));
-        atomicAdd(reinterpret_cast<unsigned*>(low + b), static_cast<unsigned>(w & ((1u << 21) - 1)));
-        atomicAdd(reinterpret_cast<unsigned*>(high + b), static_cast<unsigned>(w >> 21));
+        atomicAdd(reinterpret_cast<unsigned*>(low + b), static_cast<unsigned>(w >> 1 & ((1u << 21) - 1)));
+        atomicAdd(reinterpret_cast<unsigned*>(high + b), static_cast<unsigned>(w >> 22));
       }
     }
     __syncthreads();
@@ -733,8 +734,8 @@ struct Sampler {
       int b0, b1;
       coarse_reach(
           [&](int b) {
-            return static_cast<float>(static_cast<unsigned>(low[b])) +
-                   static_cast<float>(static_cast<unsigned>(high[b])) * 0x1p21f;
+            const float sum = static_cast<float>(static_cast<unsigned>(low[b]));
+            return by_k ? sum : 2.f * sum + static_cast<float>(static_cast<unsigned>(high[b])) * 0x1p22f;
           },
           by_k ? static_cast<float>(p.top_k) : static_cast<float>(goal) * 1.0001f, INFINITY, b0, b1);
       if (threadIdx.x == 0) s.from = b0 < kCoarseBins ? logit_of(m, b0) : -INFINITY;
