@@ -439,13 +439,14 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv4_evict_move_kernel(const _
   const int steps = min(kSteps, 1 << p.lanes_log2);  // of a round
   const int moves = p.rounds * steps * together;
   const int64_t k0 = task * moves;
-  const int count = __ldg(p.e.count + b);
+  // (no __ldg of what the kernel before has written: a load of constants may be moved before the wait)
+  const int count = p.e.count[b];
   if (k0 >= count) return;
   const int here = static_cast<int>(min(static_cast<int64_t>(moves), count - k0));
   int64_t row[2] = {-1, -1};  // group 0 of head 0 of the lane's move, from and to
   if (lane < here) {
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
-    const int j0 = __ldg(p.e.from + b * p.e.most + k0 + lane), j1 = __ldg(p.e.to + b * p.e.most + k0 + lane);
+    const int j0 = p.e.from[b * p.e.most + k0 + lane], j1 = p.e.to[b * p.e.most + k0 + lane];
     const int t0 = j0 / p.page_size, t1 = j1 / p.page_size;
     const int page0 = __ldg(table + t0), page1 = __ldg(table + t1);
     p.e.slots[b * p.e.slots_stride + j0] = j1;
