@@ -12,15 +12,16 @@
 // there on are listed, weighed exactly and ordered (the sum of all weights, which top_p needs, is known
 // to 2^-18 of what its chunks hold, and the row is settled where that error changes nothing; chunks that
 // weigh much are summed up exactly for a second try).  Without a filter the sums of chunks lead to the
-// token in the same way, and the second try walks the tiles that hold it by exact weights.  What stays open, or has more candidates than the list holds, goes through exact
-// passes over all weights: sample_rest_kernel, a cluster a row (or, in clusters and with top_k, at once:
-// in_full).
+// token in the same way, and the second try walks the tiles that hold it by exact weights.  What stays
+// open, or has more candidates than the list holds, goes through exact passes over all weights:
+// sample_rest_kernel, a cluster a row (or, in clusters and with top_k, at once: in_full).
 //
-// The one pass is bound by its special-function operations and by loads in flight: one exponential an
-// element at temperature 1, two at another, 64 KB of loads a CTA's turn at four CTAs an SM.  1024 rows of
-// 126464 bf16 logits: 60 us with top_k 50, 60 drawn from the whole distribution at 0.7 (80 with a few rows
-// left open), 69 with top_p 0.9 there: 4.3 and 3.8 TB/s; fp32 99 to 121 us (5.2 to 4.3 TB/s).  A single
-// row 8 to 13 us: launch, barriers and first fetches of code.  Clusters where the rows fill the GPU
+// The one pass takes its time for special-function operations, one exponential an element at temperature 1 and
+// two at another, and for loads in flight: 64 KB of them a CTA's turn at four CTAs an SM.  1024 rows of
+// 126464 bf16 logits in a captured graph: 59 us with top_k 50, 57 drawn from the whole distribution at 0.7
+// (77 to 84 with a few rows left open), 67 with top_p 0.9 there: 4.5 and 3.9 TB/s; fp32 119 to 122 us
+// (4.4 TB/s).  Neither DRAM nor the special-function pipe is full (36 to 45 and 24 to 51 % of an ncu run).  A
+// single row 8 to 13 us: launch, barriers and first fetches of code.  Clusters where the rows fill the GPU
 // anyway cost more than they even out (640 rows: 2 CTAs a row 56 to 70 us, one 48 to 55).
 #include <algorithm>
 #include <climits>
@@ -215,7 +216,7 @@ __device__ __forceinline__ T warp_scan(T x) {  // inclusive
 }
 
 // Bitonic sort of kThreads * E keys, E a thread, rising: neighbours in a thread's registers, then lanes of
-// a warp by shuffles, then warps through `keys`.  (A row of 1500 with top_k 900, two sorts: 33 us; with
+// a warp by shuffles, then warps through `keys`.  (A row of 1500 with top_k 900, two sorts: 26 us; with
 // every step through shared memory 63.)
 template <int E>
 __device__ __noinline__ void sort_block(uint64_t* keys, int n) {
@@ -709,7 +710,7 @@ struct Sampler {
   // coarse bins tell; how many are left.  (The list began with what the largest of chunks alone reach.)
   __device__ __forceinline__ int drop_behind(int n, bool by_k, uint64_t goal) const {
     constexpr int kEach = kCap / kThreads;
-    int* const low = s.coarse;   // of weights in a bin (or their number): the sum of the lower 22 bits' half
+    int* const low = s.coarse;   // of halved weights in a bin (or their number): the lower 21 bits' sum
     int* const high = s.row_coarse;
     for (int b = threadIdx.x; b < kCoarseBins; b += kThreads) low[b] = high[b] = 0;
     if (threadIdx.x == 0) s.queued = 0;
@@ -734,10 +735,10 @@ struct Sampler {
       int b0, b1;
       coarse_reach(
           [&](int b) {
-            const float sum = static_cast<float>(static_cast<unsigned>(low[b]));
-            return by_k ? sum : 2.f * sum + static_cast<float>(static_cast<unsigned>(high[b])) * 0x1p22f;
+            return static_cast<float>(static_cast<unsigned>(low[b])) +
+                   static_cast<float>(static_cast<unsigned>(high[b])) * 0x1p21f;
           },
-          by_k ? static_cast<float>(p.top_k) : static_cast<float>(goal) * 1.0001f, INFINITY, b0, b1);
+          by_k ? static_cast<float>(p.top_k) : static_cast<float>(goal) * 0.50005f, INFINITY, b0, b1);
       if (threadIdx.x == 0) s.from = b0 < kCoarseBins ? logit_of(m, b0) : -INFINITY;
     }
     uint64_t mine[kEach];
@@ -1004,9 +1005,8 @@ struct Sampler {
   }
 
   // No filter: the group of tiles by the weights of chunks, then the token in it; -2 where the error of
-  // sums in 32 bits leaves either open.  kAgain: behind weigh_chunks<true>.
-  template <bool kAgain>
-  __device__ __forceinline__ int draw_whole(float u) {
+  // sums in 32 bits leaves either open.  again: behind weigh_chunks<true>.
+  __device__ __forceinline__ int draw_whole(float u, bool again) {
     constexpr float kOfUnit = 1.f / static_cast<float>(int64_t{1} << kWeightBits);
     uint64_t before_own;
     uint64_t none;
@@ -1026,7 +1026,7 @@ struct Sampler {
       if (threadIdx.x < 32) find_group(sums, groups, before, goal);
       __syncthreads();
       const int t0 = s.group << p.span_log2, t1 = min((s.group + 1) << p.span_log2, tiles);
-      if (kAgain)
+      if (again)
         find_exactly(t0, t1, goal - s.group_before, s.goal_error);
       else
         find_in_tiles(t0, t1, static_cast<float>(goal - s.group_before) * kOfUnit,
@@ -1416,12 +1416,13 @@ struct Sampler {
     if (by_mass) {
       weigh_chunks<false>();
       if (!by_p) {
-        sync();
-        int token = draw_whole<false>(u);
-        if (token == -2) {
-          weigh_chunks<true>();
+        int token;
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          if (again) weigh_chunks<true>();
           sync();
-          token = draw_whole<true>(u);
+          token = draw_whole(u, again);
+          if (token != -2 || again) break;
         }
         if (kCluster && p.at_once && token == -2) return in_full(u);
         return token;
