@@ -894,7 +894,7 @@ size_t dllm_attention_kv4_weights_workspace_bytes(const dllm_kv4_cache* cache, i
   if (check_attention(cache, B, n, q_heads, max_len) != DLLM_OK || check_entries(B, max_len) != DLLM_OK)
     return 0;
   return dllm::attention_weights_ws_bytes(B, n, q_heads / cache->heads, cache->heads, cache->head_dim,
-                                          max_len, sm_count());
+                                          max_len);
 }
 
 dllm_status dllm_attention_kv4_weights(const dllm_heads* q, const dllm_kv4_cache* cache,
@@ -923,7 +923,7 @@ dllm_status dllm_attention_kv4_weights(const dllm_heads* q, const dllm_kv4_cache
   if (prior == weights && prior_stride != weights_stride && B > 1)
     return fail(DLLM_ERR_INVALID_ARG, "prior and weights are one memory with two strides");
   const size_t need = dllm::attention_weights_ws_bytes(B, n, q->heads / cache->heads, cache->heads,
-                                                       cache->head_dim, max_len, sm_count());
+                                                       cache->head_dim, max_len);
   if (ws_bytes < need)
     return fail(DLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
                 need);

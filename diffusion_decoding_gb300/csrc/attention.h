@@ -70,14 +70,14 @@ struct AttnWeights {
   Divisor by_page;
   int ctas_per_seq, split_log2, heads_at_once, tiles_per_warp;  // few rows: attention_weights.cu
 };
-size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
+size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len);
 cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, void* ws, int sm_count,
                                      cudaStream_t stream);
 
 // Many rows per cache head (attention_weights_tc.cu).
 bool weights_tc_scale(float scale);  // whether it can have this scale
 bool weights_tc_takes(int B, int n, int G, int heads, int D, int max_len);
-size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count);
+size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len);
 cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,
                               cudaStream_t stream);
 

@@ -11,10 +11,11 @@
 // in the lanes, so nothing is joined.  Where there are few entries the warps of a CTA share out the heads
 // and add up at the end.
 //
-// Bound by instructions: 490 for 32 entries of a head of 128 channels (codes to bf16 more than a third),
-// the integer pipe is 53 % busy.  32 sequences of up to 8192 entries, 8 heads of 128, 4 rows each: 41 us,
-// 0.42 of the copy rate (with codes loaded to registers ahead instead of through the ring 43; a warp a head
-// with its queries in registers 54; CTAs of four warps 47).
+// Nothing is full: 0.42 of the copy rate, and 490 instructions for 32 entries of a head of 128 channels
+// (codes to bf16 more than a third), which are half of the issue slots, the integer pipe 53 % busy.  The 24
+// warps an SM that the registers leave room for do not fill the other half.  32 sequences of up to 8192
+// entries, 8 heads of 128, 4 rows each: 41 us (with codes loaded to registers ahead instead of through the
+// ring 43; a warp a head with its queries in registers 54; CTAs of four warps 47).
 #include <algorithm>
 
 #include "attention.h"
@@ -376,10 +377,9 @@ cudaError_t launch(const AttnParams& p, const AttnWeights& x, int sm_count, cuda
 
 }  // namespace
 
-size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
-  return weights_tc_takes(B, n, G, heads, D, max_len)
-             ? weights_tc_ws_bytes(B, n, G, heads, D, max_len, sm_count)
-             : kWsHeader;
+size_t attention_weights_ws_bytes(int B, int n, int G, int heads, int D, int max_len) {
+  return weights_tc_takes(B, n, G, heads, D, max_len) ? weights_tc_ws_bytes(B, n, G, heads, D, max_len)
+                                                      : kWsHeader;
 }
 
 cudaError_t launch_attention_weights(const AttnParams& p, AttnWeights x, int D, void* ws, int sm_count,

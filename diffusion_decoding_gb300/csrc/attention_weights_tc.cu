@@ -18,8 +18,8 @@
 // which codes come out).  Sums of an entry over heads and halves are partial results that
 // weights_join_kernel adds in order.
 //
-// Bound by the exchange between the products and the threads that add up: 1080 cycles for 256 entries x 64
-// rows of 128 channels, of which the products take 52 % and the exponentials 47 % (32 a cycle and SM).  2
+// What it loses: products and exponentials hardly overlap.  256 entries x 64 rows of 128 channels take 1080
+// cycles, the products 52 % of them and the exponentials (32 a cycle and SM) 47 %; neither pipe is full.  2
 // sequences of up to 16384 entries, 8 heads, 4096 rows, causal: 271 us, 0.93 PFLOP/s; 16 of 4160, 2 heads,
 // 512 rows: 31 us.  Eight sum warps, one thread an entry, took 420 for the first; log-sum-exps added by the
 // threads 371; exponentials computed by polynomials in part, or scores loaded ahead, no less.
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(256)
   put_weight(x, b, j, v);
 }
 
-WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int page_size, int sm_count) {
+WeightsPlan make_plan(int B, int n, int G, int heads, int max_len, int page_size) {
   WeightsPlan f{};
   f.rows = n * G;
   f.chunks = (f.rows + kChunk - 1) / kChunk;
@@ -564,22 +564,23 @@ bool weights_tc_scale(float scale) { return fabsf(scale) >= 0x1p-20f && fabsf(sc
 // x entries, sequences in brackets: 12 rows of 256 channels, 8 x 2000 (8) 16 and 26; 9 of 192 14 and 24;
 // 8 of 256, 8 x 4096 (32) 79 and 66; 16 of 128, 8 x 2000 (8) 13 and 9; 17 of 128, 8 x 4000 (8) 19.3 and 18.8, 48 of
 // 128 19.5 and 33; 17 of 128, 8 x 777 (1) 7.8 and 11; 20 of 64, 8 x 2000 (32) 27 and 16; 33 of 64, 6 x 777 (3)
-// 8.1 and 10).
+// 8.1 and 10).  The times are of a captured graph: three launches take the host longer than one, so that the
+// smallest calls made one by one are slower here (the last of these 16.5 and 12.3).
 bool weights_tc_takes(int B, int n, int G, int heads, int D, int max_len) {
   const int64_t rows = static_cast<int64_t>(n) * G;
   return rows > (D == 64 ? 32 : D == 128 ? 16 : 8) &&
          static_cast<int64_t>(B) * heads * (static_cast<int64_t>(max_len) + kPair) <= (int64_t{1} << 34);
 }
 
-size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len, int sm_count) {
-  const WeightsPlan f = make_plan(B, n, G, heads, max_len, 1, sm_count);
+size_t weights_tc_ws_bytes(int B, int n, int G, int heads, int D, int max_len) {
+  const WeightsPlan f = make_plan(B, n, G, heads, max_len, 1);
   return sums_at(f, B, heads, D) +
          static_cast<size_t>(B) * heads * 2 * static_cast<size_t>(f.pairs) * kPair * 4;
 }
 
 cudaError_t launch_weights_tc(const AttnParams& p, const AttnWeights& x, int D, void* ws, int sm_count,
                               cudaStream_t stream) {
-  WeightsPlan f = make_plan(p.B, p.n, p.G, p.heads, p.max_len, p.page_size, sm_count);
+  WeightsPlan f = make_plan(p.B, p.n, p.G, p.heads, p.max_len, p.page_size);
   f.status = static_cast<int32_t*>(ws);
   f.queries = static_cast<uint8_t*>(ws) + kWsHeader;
   f.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sums_at(f, p.B, p.heads, D));
